@@ -73,6 +73,9 @@ typedef enum pkv_kv_dtype {
 #define PKV_DEVERR_CONTEXT_LEN 0x2u /* a context length was < k (1 for one query token) or > max_context_len */
 #define PKV_DEVERR_SLOT 0x4u        /* a slot_mapping entry was >= num_blocks * 16               */
 #define PKV_DEVERR_TIMEOUT 0x8u     /* an asynchronous copy did not arrive within the time limit */
+#define PKV_DEVERR_CAPACITY 0x10u   /* pkv_reserve_slots: too few free blocks, table entries or slots */
+#define PKV_DEVERR_POSITION 0x20u   /* a position was < 0 or >= the rows of the rotation table       */
+#define PKV_DEVERR_PREFIX 0x40u     /* a group's first sequence or prefix length was invalid         */
 
 /* Opaque, host-owned pool descriptor. */
 typedef struct pkv_pool pkv_pool;
@@ -231,6 +234,27 @@ PKV_API pkv_status pkv_block_manager_release_before(pkv_block_manager* manager, 
  */
 PKV_API pkv_status pkv_block_manager_tables(const pkv_block_manager* manager, const int* seqs,
                                             int n, int32_t* block_tables, int32_t* context_lens);
+
+/*
+ * The first n blocks that the manager would hand out next, in order (for pkv_reserve_slots):
+ * ids (host, int32 [n]).  Nothing is taken; an append with the same growth takes the same blocks.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CAPACITY (fewer than n blocks are free).
+ */
+PKV_API pkv_status pkv_block_manager_free_list(const pkv_block_manager* manager, int n, int32_t* ids);
+
+/*
+ * Groups of neighbouring sequences among seqs[0..n) that share leading blocks, for
+ * pkv_shared_prefix_decode with num_queries query tokens: group_starts (host, int32 [n + 1]) and
+ * prefix_lens (host, int32 [n]) receive *num_groups groups that cover all n in order.  A prefix is
+ * the whole blocks that all of a group's tables have in common, at most what every query sees.
+ * A sequence joins the group before it where that does not lower the number of blocks saved,
+ * (sequences - 1) * (prefix blocks); sharing that is not between neighbours is not found.
+ * Released blocks (pkv_block_manager_release_before) are not shared.
+ * Errors: PKV_ERR_INVALID_ARG (unknown sequence, num_queries outside 1 .. 16).
+ */
+PKV_API pkv_status pkv_block_manager_prefix_groups(const pkv_block_manager* manager, const int* seqs, int n,
+                                                   int num_queries, int32_t* group_starts,
+                                                   int32_t* prefix_lens, int* num_groups);
 
 /* Free blocks and live sequences (either pointer may be NULL). */
 PKV_API pkv_status pkv_block_manager_stats(const pkv_block_manager* manager, int64_t* free_blocks,
@@ -408,6 +432,142 @@ PKV_API pkv_status pkv_paged_attention_decode_static_scratch(
  * PKV_ERR_CUDA it names the status only; pkv_last_cuda_error() has the CUDA text.
  */
 PKV_API const char* pkv_static_scratch_error(void);
+
+/*
+ * Reserve cache slots for new tokens on the device: what pkv_block_manager_append computes on
+ * the host (without its copy on write), from lengths that are already on the GPU, with no copy
+ * or wait in between.  Sequence b holds L_b = context_lens[b] tokens, in the first ceil(L_b / 16)
+ * entries of its block-table row, and grows by c_b = num_new_tokens[b].  Blocks come from a list of
+ * free ids in the order given, sequence after sequence, so that a list in a block manager's
+ * hand-out order (pkv_block_manager_free_list) gives the blocks that manager would give.
+ *   block_tables   (device, in and out): int32 [num_seqs, max_blocks_per_seq]; the new blocks'
+ *                  entries are written, all others are left as they are.  A sequence whose last
+ *                  block is partly filled must own that block (nothing is copied).
+ *   context_lens, num_new_tokens (device): int32 [num_seqs].
+ *   free_blocks    (device): int32 [num_free] distinct ids.
+ *   free_used      (device): int32 [1], how many of them are already handed out; NULL: none.
+ *   max_tokens:    entries of slot_mapping and positions, < 2^30.
+ *   slot_mapping   (device, out): int32 [max_tokens], the slot of each new token in (sequence,
+ *                  position) order; -1 past the last one (pkv_reshape_and_cache skips those).
+ *   positions      (device, out): int32 [max_tokens], each new token's position; 0 past the last.
+ *   query_starts   (device, out): int32 [num_seqs + 1], each sequence's first entry in these; the
+ *                  last is the number of new tokens.
+ *   new_context_lens (device, out): int32 [num_seqs], L_b + c_b; may be context_lens itself.
+ *   new_free_used  (device, out): int32 [1]; may be free_used itself.
+ * No other outputs and inputs may overlap.  All or nothing: where the free blocks, a table row
+ * or max_tokens do not suffice (PKV_DEVERR_CAPACITY), or a length or count is negative
+ * (PKV_DEVERR_CONTEXT_LEN), tables, lengths and free_used stay as they were, every slot is -1
+ * and query_starts is all 0.  A block id outside the pool gives its tokens slot -1 and sets
+ * PKV_DEVERR_BLOCK_ID.  Errors: PKV_ERR_INVALID_ARG (also when the pool's device is not
+ * current), PKV_ERR_UNSUPPORTED (more than 16384 sequences, a pool of 2^27 blocks or more),
+ * PKV_ERR_CUDA.
+ */
+PKV_API pkv_status pkv_reserve_slots(const pkv_pool* pool, int32_t* block_tables, int max_blocks_per_seq,
+                                     const int32_t* context_lens, const int32_t* num_new_tokens, int num_seqs,
+                                     const int32_t* free_blocks, int num_free, const int32_t* free_used,
+                                     int max_tokens, int32_t* slot_mapping, int32_t* positions,
+                                     int32_t* query_starts, int32_t* new_context_lens, int32_t* new_free_used,
+                                     void* stream);
+
+/*
+ * Arguments of pkv_norm_rope_and_cache.  Zero-initialise and set what you need.
+ *   q, k, v   (device): bf16 rows of the step's new tokens; token t's heads are contiguous
+ *             ([num_q_heads or kv_heads, head_dim]) at element t * stride, so that slices of one
+ *             projection's output can be passed.  16-byte aligned, strides multiples of 8.
+ *   q_weight, k_weight (device): bf16 [head_dim] weights of the norm of each query and key head,
+ *             16-byte aligned; NULL: that kind is not normalised.
+ *   cos_sin   (device): fp32 [max_position, rot_dim], each position's rot_dim / 2 cosines and then
+ *             its sines (pkv_rope_table), 16-byte aligned; NULL: no rotation.
+ *   positions (device): int32 [num_tokens], used with cos_sin only.
+ *   slot_mapping (device): int32 [num_tokens], as for pkv_reshape_and_cache.
+ *   q_out     (device, out): bf16 rows like q's at q_out_stride; may be q itself, at q's stride.
+ *   rot_dim:  rotated values of each head, a multiple of 16 up to head_dim.
+ *   interleaved: 0: pair i is values (i, i + rot_dim / 2); else (2 i, 2 i + 1).
+ *   eps:      added to the mean square, >= 0.
+ */
+typedef struct pkv_norm_rope {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos_sin;
+  const int32_t* positions;
+  const int32_t* slot_mapping;
+  void* q_out;
+  int64_t q_out_stride;
+  int64_t num_tokens;
+  int num_q_heads;
+  int rot_dim;
+  int max_position;
+  int interleaved;
+  float eps;
+  int reserved;
+} pkv_norm_rope;
+
+/*
+ * A step's new tokens on their way from the projection to attention, in one pass: every query
+ * and key head is normalised, y = x / sqrt(mean(x^2) + eps) * weight, and rotated by its
+ * token's position, (y_a, y_b) <- (y_a c - y_b s, y_b c + y_a s); queries go to q_out, keys and
+ * values to their slots as pkv_reshape_and_cache writes them.  All of it is computed in fp32
+ * and rounded once: a quantised pool's codes and scales are formed from the unrounded keys.
+ * A negative slot skips the token's cache write, not its queries.  A slot past the pool does
+ * so too and sets PKV_DEVERR_SLOT.  A position outside the table gives zero queries and no
+ * cache write and sets PKV_DEVERR_POSITION.  Slots must be distinct among a call's tokens.
+ * num_tokens == 0 is a no-op.  Errors: PKV_ERR_INVALID_ARG (also when the pool's device is not
+ * current), PKV_ERR_UNSUPPORTED (rot_dim not a multiple of 16), PKV_ERR_CUDA.
+ */
+PKV_API pkv_status pkv_norm_rope_and_cache(const pkv_pool* pool, const pkv_norm_rope* args, void* stream);
+
+/*
+ * The rotation table of pkv_norm_rope_and_cache: cos_sin (device, fp32 [max_position, rot_dim])
+ * receives cos(p * base^(-2 i / rot_dim)) at [p][i] and the sine at [p][rot_dim / 2 + i], formed
+ * in 64 bits.  Runs on the current device.  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED
+ * (rot_dim not a multiple of 16), PKV_ERR_CUDA.
+ */
+PKV_API pkv_status pkv_rope_table(float* cos_sin, int64_t max_position, int rot_dim, double base, void* stream);
+
+/*
+ * Bytes of device workspace that pkv_shared_prefix_decode needs.  options may be NULL.
+ */
+PKV_API pkv_status pkv_shared_prefix_workspace_bytes(const pkv_pool* pool, int num_seqs, int num_q_heads,
+                                                     int num_groups, int max_prefix_len, int max_suffix_len,
+                                                     const pkv_decode_options* options, size_t* bytes);
+
+/*
+ * pkv_paged_attention_decode for a batch whose groups of sequences share a prefix (sequences
+ * made by pkv_block_manager_fork, or requests behind one system prompt; "Efficient AI Lecture
+ * 13", section "PagedAttention"): each group's prefix is read once per kv head for all the group's
+ * queries, not once per sequence.  The result is that of pkv_paged_attention_decode.
+ *   group_starts (device): int32 [num_groups + 1], not decreasing, within [0, num_seqs]: group g is
+ *                sequences group_starts[g] .. group_starts[g + 1] - 1 (it may be empty).  Sequences
+ *                outside every group share nothing.
+ *   prefix_lens  (device): int32 [num_groups]: the group's sequences have the same first
+ *                prefix_lens[g] tokens.  A multiple of 16, 0 .. max_prefix_len.  The blocks are
+ *                read through the group's first sequence's table row; other rows' entries for
+ *                them are not read.
+ *   max_prefix_len, max_suffix_len (host): upper bounds on the prefix lengths and on each
+ *                sequence's own tokens, context_lens[b] - prefix; they size the workspace.
+ *   context_lens (device): whole lengths, prefix included.  Every query must see the whole prefix:
+ *                context_lens[b] - (k - 1) >= prefix_lens[g].
+ *   workspace    (device): at least pkv_shared_prefix_workspace_bytes(...) bytes, 16-byte aligned.
+ *   options      may be NULL; num_queries works as in pkv_paged_attention_decode_ex, the plan
+ *                knobs apply to the pass over the sequences' own tokens, window must be 0.
+ * The other arguments are as for pkv_paged_attention_decode.  A sequence whose length is out of
+ * range gets a zero output and sets PKV_DEVERR_CONTEXT_LEN; an invalid group_starts or
+ * prefix_lens entry sets PKV_DEVERR_PREFIX and gives the whole call a zero output (with
+ * PKV_DEVERR_CONTEXT_LEN); a block id out of range is skipped and sets PKV_DEVERR_BLOCK_ID.
+ * num_seqs == 0 is a no-op.  Errors: PKV_ERR_INVALID_ARG (also when the pool's device is not
+ * current), PKV_ERR_UNSUPPORTED (a window, more than 4096 groups), PKV_ERR_WORKSPACE, PKV_ERR_CUDA.
+ */
+PKV_API pkv_status pkv_shared_prefix_decode(const pkv_pool* pool, const void* q, const int32_t* block_tables,
+                                            int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                                            int num_q_heads, const int32_t* group_starts,
+                                            const int32_t* prefix_lens, int num_groups, int max_prefix_len,
+                                            int max_suffix_len, float scale, void* out, void* workspace,
+                                            size_t workspace_bytes, const pkv_decode_options* options,
+                                            void* stream);
 
 /*
  * Read and clear the pool's device error word (PKV_DEVERR_* bits).  Waits for the work

@@ -12,18 +12,26 @@ from .api import (  # noqa: F401
     decode_workspace_bytes,
     get_device_error,
     launch_count,
+    norm_rope_and_cache,
     paged_attention_decode,
     pool_bytes,
     pool_create,
     pool_destroy,
+    reserve_slots,
     reshape_and_cache,
+    rope_table,
     selftest_bounded_wait,
+    shared_prefix_decode,
+    shared_prefix_workspace_bytes,
     version,
 )
 from ._lib import (  # noqa: F401
     BLOCK_SIZE,
     DEVERR_BLOCK_ID,
+    DEVERR_CAPACITY,
     DEVERR_CONTEXT_LEN,
+    DEVERR_POSITION,
+    DEVERR_PREFIX,
     DEVERR_SLOT,
     DEVERR_TIMEOUT,
     PagedKVError,

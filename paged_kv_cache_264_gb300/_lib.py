@@ -27,6 +27,9 @@ DEVERR_BLOCK_ID = 0x1
 DEVERR_CONTEXT_LEN = 0x2
 DEVERR_SLOT = 0x4
 DEVERR_TIMEOUT = 0x8
+DEVERR_CAPACITY = 0x10
+DEVERR_POSITION = 0x20
+DEVERR_PREFIX = 0x40
 
 # Every function the header declares, with (restype, argtypes).
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -50,6 +53,13 @@ class DecodeOptions(ctypes.Structure):
                 ("window", ctypes.c_int), ("reserved", ctypes.c_int * 1)]
 
 
+class NormRope(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64),
+                ("q_weight", _vp), ("k_weight", _vp), ("cos_sin", _vp), ("positions", _vp), ("slot_mapping", _vp),
+                ("q_out", _vp), ("q_out_stride", _i64), ("num_tokens", _i64), ("num_q_heads", _i32),
+                ("rot_dim", _i32), ("max_position", _i32), ("interleaved", _i32), ("eps", _f32), ("reserved", _i32)]
+
+
 SIGNATURES = {
     "pkv_status_string": (ctypes.c_char_p, [_i32]),
     "pkv_last_cuda_error": (ctypes.c_char_p, []),
@@ -64,6 +74,15 @@ SIGNATURES = {
     "pkv_paged_attention_decode": (_i32, [_vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _f32, _vp, _vp, _sz, _vp]),
     "pkv_paged_attention_decode_ex": (_i32, [_vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _f32, _vp, _vp, _sz,
                                              ctypes.POINTER(DecodeOptions), _vp]),
+    "pkv_reserve_slots": (_i32, [_vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "pkv_norm_rope_and_cache": (_i32, [_vp, ctypes.POINTER(NormRope), _vp]),
+    "pkv_rope_table": (_i32, [_vp, _i64, _i32, ctypes.c_double, _vp]),
+    "pkv_shared_prefix_workspace_bytes": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(DecodeOptions),
+                                                 _psz]),
+    "pkv_shared_prefix_decode": (_i32, [_vp, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _f32, _vp,
+                                        _vp, _sz, ctypes.POINTER(DecodeOptions), _vp]),
+    "pkv_block_manager_free_list": (_i32, [_vp, _i32, _vp]),
+    "pkv_block_manager_prefix_groups": (_i32, [_vp, _vp, _i32, _i32, _vp, _vp, _pi32]),
     "pkv_get_device_error": (_i32, [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]),
     "pkv_launch_count": (ctypes.c_uint64, []),
     "pkv_paged_attention_decode_static_scratch": (_i32, [_vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _f32,

@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import BLOCK_SIZE, DecodeOptions, PKV_KV_BF16, PKV_KV_FP8_E4M3, PKV_KV_INT8, check
+from ._lib import BLOCK_SIZE, DecodeOptions, NormRope, PKV_KV_BF16, PKV_KV_FP8_E4M3, PKV_KV_INT8, check
 
 _DTYPES = {"bf16": PKV_KV_BF16, "int8": PKV_KV_INT8, "fp8": PKV_KV_FP8_E4M3}
 _CODE_DTYPES = {"bf16": torch.bfloat16, "int8": torch.int8, "fp8": torch.uint8}
@@ -40,6 +40,29 @@ def _need(t: torch.Tensor, dtype, name: str, ndim: int | None = None) -> None:
         raise ValueError(f"{name} must be contiguous")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+
+
+def _same_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, is on {t.device}")
+
+
+class _on_device:
+    """Make the pool's device current for a call (its stream and launches go there)."""
+
+    def __init__(self, pool):
+        self.index = pool.k_cache.device.index
+        self.guard = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 _KERNELS = {0: 0, "auto": 0, 1: 1, "cuda_core": 1, 2: 2, "tensor_core": 2}
@@ -118,6 +141,36 @@ class PagedKVPool:
             self.handle = pool_create(num_blocks, kv_heads, head_dim, dtype, self.k_cache,
                                       self.v_cache, self.k_scale, self.v_scale)
 
+    @classmethod
+    def from_tensors(cls, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor | None = None,
+                     v_scale: torch.Tensor | None = None) -> "PagedKVPool":
+        """A pool over tensors that the caller holds: K and V [num_blocks, kv_heads, 16, head_dim]
+        of bfloat16, int8 or uint8 (E4M3 codes), the latter two with fp32 scales
+        [num_blocks, kv_heads, 16]."""
+        names = {t: n for n, t in _CODE_DTYPES.items()}
+        if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in names:
+            raise TypeError("k_cache must be a bfloat16, int8 or uint8 torch.Tensor")
+        dtype = names[k_cache.dtype]
+        _need(k_cache, k_cache.dtype, "k_cache", 4)
+        _need(v_cache, k_cache.dtype, "v_cache", 4)
+        if v_cache.shape != k_cache.shape or k_cache.shape[2] != BLOCK_SIZE:
+            raise ValueError(f"k_cache and v_cache must be [num_blocks, kv_heads, {BLOCK_SIZE}, head_dim] alike")
+        if (dtype == "bf16") != (k_scale is None) or (dtype == "bf16") != (v_scale is None):
+            raise ValueError("k_scale and v_scale come with int8 and uint8 caches, and only with them")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                _need(t, torch.float32, name, 3)
+                if t.shape != k_cache.shape[:3]:
+                    raise ValueError(f"{name} must be {tuple(k_cache.shape[:3])}")
+        _same_device(k_cache.device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+        pool = cls.__new__(cls)
+        pool.num_blocks, pool.kv_heads, _, pool.head_dim = k_cache.shape
+        pool.dtype, pool.k_cache, pool.v_cache, pool.k_scale, pool.v_scale = dtype, k_cache, v_cache, k_scale, v_scale
+        with torch.cuda.device(k_cache.device):
+            pool.handle = pool_create(pool.num_blocks, pool.kv_heads, pool.head_dim, dtype, k_cache, v_cache, k_scale,
+                                      v_scale)
+        return pool
+
     def close(self) -> None:
         if getattr(self, "handle", None) is not None:
             pool_destroy(self.handle)
@@ -140,6 +193,17 @@ class PagedKVPool:
                                       out=out, workspace=workspace, partition_blocks=partition_blocks,
                                       kernel=kernel, schedule=schedule, stages=stages,
                                       blocks_per_stage=blocks_per_stage, window=window, stream=stream)
+
+    def reserve_slots(self, block_tables, context_lens, num_new_tokens, free_blocks, max_tokens, **kwargs):
+        return reserve_slots(self, block_tables, context_lens, num_new_tokens, free_blocks, max_tokens, **kwargs)
+
+    def norm_rope_and_cache(self, q, k, v, positions, slot_mapping, cos_sin=None, q_weight=None, k_weight=None, **kwargs):
+        return norm_rope_and_cache(self, q, k, v, positions, slot_mapping, cos_sin, q_weight, k_weight, **kwargs)
+
+    def decode_shared_prefix(self, q, block_tables, context_lens, group_starts, prefix_lens, scale, max_prefix_len,
+                             max_suffix_len, **kwargs):
+        return shared_prefix_decode(self, q, block_tables, context_lens, group_starts, prefix_lens, scale,
+                                    max_prefix_len, max_suffix_len, **kwargs)
 
     def device_error(self, stream=None) -> int:
         return get_device_error(self, stream)
@@ -241,6 +305,193 @@ def paged_attention_decode(pool: PagedKVPool, q: torch.Tensor, block_tables: tor
         int(max_context_len), float(scale), _ptr(out), _ptr(workspace), ws_bytes,
         _options(partition_blocks, kernel, schedule, stages, blocks_per_stage, nq, window), _stream(stream)),
         "paged_attention_decode")
+    return out
+
+
+def reserve_slots(pool: PagedKVPool, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                  num_new_tokens: torch.Tensor, free_blocks: torch.Tensor, max_tokens: int,
+                  free_used: torch.Tensor | None = None, slot_mapping: torch.Tensor | None = None,
+                  positions: torch.Tensor | None = None, query_starts: torch.Tensor | None = None,
+                  new_context_lens: torch.Tensor | None = None, new_free_used: torch.Tensor | None = None,
+                  stream=None):
+    """Reserve cache slots for num_new_tokens (int32 [B]) more tokens of each sequence on the
+    GPU, as ``BlockManager.append`` does on the host.  New blocks are entries of free_blocks
+    (int32 [F], after the first free_used[0] of them) and are written into block_tables
+    (int32 [B, max_blocks]) in place.  Returns (slot_mapping [max_tokens], positions
+    [max_tokens], query_starts [B + 1], new_context_lens [B], new_free_used [1]), all int32;
+    slots past the last new token are -1.  Outputs not given are allocated; new_context_lens may
+    be context_lens and new_free_used may be free_used.  All or nothing: a call that does not
+    fit changes nothing, returns slots of -1 and sets DEVERR_CAPACITY."""
+    i32 = torch.int32
+    _need(block_tables, i32, "block_tables", 2)
+    _need(context_lens, i32, "context_lens", 1)
+    _need(num_new_tokens, i32, "num_new_tokens", 1)
+    _need(free_blocks, i32, "free_blocks", 1)
+    max_tokens = int(max_tokens)
+    b, device = context_lens.shape[0], context_lens.device
+    if block_tables.shape[0] != b or num_new_tokens.shape[0] != b:
+        raise ValueError("block_tables, context_lens and num_new_tokens disagree in shape")
+    if max_tokens < 0:
+        raise ValueError("max_tokens must not be negative")
+    if free_used is not None:
+        _need(free_used, i32, "free_used", 1)
+        if free_used.shape[0] != 1:
+            raise ValueError("free_used must be [1]")
+    outs = []
+    for name, t, n in (("slot_mapping", slot_mapping, max_tokens), ("positions", positions, max_tokens),
+                       ("query_starts", query_starts, b + 1), ("new_context_lens", new_context_lens, b),
+                       ("new_free_used", new_free_used, 1)):
+        if t is None:
+            t = torch.empty(n, dtype=i32, device=device)
+        else:
+            _need(t, i32, name, 1)
+            if t.shape[0] != n:
+                raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+        outs.append(t)
+    _same_device(pool.k_cache.device, block_tables=block_tables, context_lens=context_lens,
+                 num_new_tokens=num_new_tokens, free_blocks=free_blocks, free_used=free_used,
+                 **dict(zip(("slot_mapping", "positions", "query_starts", "new_context_lens", "new_free_used"), outs)))
+    with _on_device(pool):
+        check(_lib.load().pkv_reserve_slots(
+            _handle(pool), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), _ptr(num_new_tokens), b,
+            _ptr(free_blocks), free_blocks.shape[0], _ptr(free_used), max_tokens, *map(_ptr, outs), _stream(stream)),
+            "reserve_slots")
+    return tuple(outs)
+
+
+def _head_rows(t: torch.Tensor, name: str, n: int | None, heads: int | None, head_dim: int) -> int:
+    """Check a bf16 [N, heads, head_dim] tensor whose tokens may lie apart; its token stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dim() != 3 or t.shape[2] != head_dim or (n is not None and t.shape[0] != n) or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [{'N' if n is None else n}, {'Hq' if heads is None else heads}, {head_dim}], "
+                         f"got {tuple(t.shape)}")
+    token, head, value = t.stride()
+    if t.shape[0] <= 1:
+        token = t.shape[1] * head_dim  # a size of one says nothing about its stride
+    if value != 1 or (head != head_dim and t.shape[1] > 1) or token % 8:
+        raise ValueError(f"{name}'s heads must be contiguous, its tokens a multiple of 8 values apart; strides {t.stride()}")
+    return token
+
+
+def norm_rope_and_cache(pool: PagedKVPool, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        positions: torch.Tensor | None, slot_mapping: torch.Tensor,
+                        cos_sin: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                        k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Normalise and rotate the heads of new tokens' q [N, Hq, d] and k [N, Hkv, d] (bf16) and
+    write k and v [N, Hkv, d] to the pool slots slot_mapping (int32 [N]), in one pass; returns
+    the new q, bf16 [N, Hq, d].  q, k and v may be slices of one projection's output: their heads
+    are contiguous, their tokens any multiple of 8 values apart.
+
+    ``q_weight``, ``k_weight`` (bf16 [d]): y = x / sqrt(mean(x^2) + eps) * weight per head; None:
+    no norm.  ``cos_sin`` (fp32 [max_position, rot_dim], see ``rope_table``) rotates each head's
+    first rot_dim values by ``positions`` (int32 [N]): pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1)
+    when ``interleaved``; None: no rotation, positions are not used.  ``out`` may be q itself.
+    A negative slot skips a token's cache write only."""
+    qs = _head_rows(q, "q", None, None, pool.head_dim)
+    n, hq, d = q.shape
+    ks = _head_rows(k, "k", n, pool.kv_heads, d)
+    vs = _head_rows(v, "v", n, pool.kv_heads, d)
+    _need(slot_mapping, torch.int32, "slot_mapping", 1)
+    if slot_mapping.shape[0] != n:
+        raise ValueError("q and slot_mapping disagree in shape")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need(w, torch.bfloat16, name, 1)
+            if w.shape[0] != d:
+                raise ValueError(f"{name} must be [{d}]")
+    if cos_sin is not None:
+        _need(cos_sin, torch.float32, "cos_sin", 2)
+        _need(positions, torch.int32, "positions", 1)
+        if positions.shape[0] != n:
+            raise ValueError("q and positions disagree in shape")
+        if cos_sin.numel() == 0:  # its NULL pointer would mean no rotation
+            raise ValueError("cos_sin must not be empty")
+    if out is None:
+        out = torch.empty(n, hq, d, dtype=q.dtype, device=q.device)
+    outs = _head_rows(out, "out", n, hq, d)
+    _same_device(pool.k_cache.device, q=q, k=k, v=v, slot_mapping=slot_mapping, positions=positions, cos_sin=cos_sin,
+                 q_weight=q_weight, k_weight=k_weight, out=out)
+    a = NormRope(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+                 0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
+                 0 if cos_sin is None else cos_sin.data_ptr(), 0 if cos_sin is None else positions.data_ptr(),
+                 slot_mapping.data_ptr(), out.data_ptr(), outs, n, hq,
+                 0 if cos_sin is None else cos_sin.shape[1], 0 if cos_sin is None else cos_sin.shape[0],
+                 1 if interleaved else 0, float(eps), 0)
+    with _on_device(pool):
+        check(_lib.load().pkv_norm_rope_and_cache(_handle(pool), ctypes.byref(a), _stream(stream)),
+              "norm_rope_and_cache")
+    return out
+
+
+def rope_table(max_position: int, rot_dim: int, base: float = 10000.0, device=None, stream=None) -> torch.Tensor:
+    """Cosines and sines for ``norm_rope_and_cache``: fp32 [max_position, rot_dim], row p holding
+    cos(p * base^(-2 i / rot_dim)) for each pair i and then the sines, formed in 64 bits."""
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):
+        out = torch.empty(int(max_position), int(rot_dim), dtype=torch.float32, device=device)
+        check(_lib.load().pkv_rope_table(_ptr(out), out.shape[0], out.shape[1], float(base), _stream(stream)), "rope_table")
+    return out
+
+
+def shared_prefix_workspace_bytes(pool: PagedKVPool, num_seqs: int, num_q_heads: int, num_groups: int,
+                                  max_prefix_len: int, max_suffix_len: int, num_queries: int = 1,
+                                  partition_blocks: int = 0) -> int:
+    n = ctypes.c_size_t()
+    check(_lib.load().pkv_shared_prefix_workspace_bytes(
+        _handle(pool), num_seqs, num_q_heads, num_groups, int(max_prefix_len), int(max_suffix_len),
+        _options(partition_blocks, num_queries=num_queries), ctypes.byref(n)), "shared_prefix_workspace_bytes")
+    return n.value
+
+
+def shared_prefix_decode(pool: PagedKVPool, q: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                         group_starts: torch.Tensor, prefix_lens: torch.Tensor, scale: float, max_prefix_len: int,
+                         max_suffix_len: int, out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, partition_blocks: int = 0,
+                         stream=None) -> torch.Tensor:
+    """``paged_attention_decode`` for a batch in which groups of neighbouring sequences share
+    their first tokens: each shared prefix is read once for its whole group.
+
+    Group g is sequences group_starts[g] .. group_starts[g + 1] - 1 (int32 [G + 1]) and shares
+    prefix_lens[g] tokens (int32 [G], multiples of 16), whose blocks the group's first sequence's
+    table row names; ``BlockManager.prefix_groups`` finds both.  max_prefix_len bounds the prefix
+    lengths, max_suffix_len every sequence's own tokens, context_lens[b] - prefix.  q is
+    [B, Hq, d], or [B, k, Hq, d] for k draft tokens per sequence, all of which see the whole prefix.
+    ``workspace`` (a uint8 CUDA tensor) is allocated here when not given."""
+    _need(q, torch.bfloat16, "q", 4 if q.dim() == 4 else 3)
+    _need(block_tables, torch.int32, "block_tables", 2)
+    _need(context_lens, torch.int32, "context_lens", 1)
+    _need(group_starts, torch.int32, "group_starts", 1)
+    _need(prefix_lens, torch.int32, "prefix_lens", 1)
+    if out is not None:
+        _need(out, torch.bfloat16, "out", q.dim())
+    b, nq, hq = check_decode_shapes(pool.head_dim, q.shape, block_tables.shape, context_lens.shape,
+                                    None if out is None else out.shape)
+    groups = prefix_lens.shape[0]
+    if group_starts.shape[0] != groups + 1:
+        raise ValueError("group_starts must have one entry more than prefix_lens")
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        workspace = torch.empty(
+            shared_prefix_workspace_bytes(pool, b, hq, groups, max_prefix_len, max_suffix_len, nq, partition_blocks),
+            dtype=torch.uint8, device=q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    _same_device(pool.k_cache.device, q=q, block_tables=block_tables, context_lens=context_lens,
+                 group_starts=group_starts, prefix_lens=prefix_lens, out=out, workspace=workspace)
+    with _on_device(pool):
+        check(_lib.load().pkv_shared_prefix_decode(
+            _handle(pool), _ptr(q), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), b, hq,
+            _ptr(group_starts), _ptr(prefix_lens), groups, int(max_prefix_len), int(max_suffix_len), float(scale),
+            _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _options(partition_blocks, num_queries=nq), _stream(stream)), "shared_prefix_decode")
     return out
 
 
@@ -360,6 +611,25 @@ class BlockManager:
         cl = torch.empty(max(len(seqs), 1), dtype=torch.int32)
         check(self.lib.pkv_block_manager_tables(self.handle, arr, len(seqs), _ptr(bt), _ptr(cl)), "tables")
         return bt[:len(seqs)], cl[:len(seqs)]
+
+    def free_list(self, n: int) -> torch.Tensor:
+        """The next n blocks the manager would hand out, in order (int32 [n], host): the list that
+        ``reserve_slots`` takes new blocks from.  Nothing is taken."""
+        ids = torch.empty(max(n, 1), dtype=torch.int32)
+        check(self.lib.pkv_block_manager_free_list(self.handle, n, _ptr(ids)), "free_list")
+        return ids[:n]
+
+    def prefix_groups(self, seqs, num_queries: int = 1):
+        """Groups of neighbouring sequences that share leading blocks, for ``shared_prefix_decode``
+        with num_queries query tokens: (group_starts int32 [G + 1], prefix_lens int32 [G], both on
+        the host)."""
+        arr = (ctypes.c_int * len(seqs))(*seqs)
+        starts = torch.empty(len(seqs) + 1, dtype=torch.int32)
+        lens = torch.empty(max(len(seqs), 1), dtype=torch.int32)
+        g = ctypes.c_int()
+        check(self.lib.pkv_block_manager_prefix_groups(self.handle, arr, len(seqs), num_queries, _ptr(starts),
+                                                       _ptr(lens), ctypes.byref(g)), "prefix_groups")
+        return starts[:g.value + 1], lens[:g.value]
 
     def stats(self) -> tuple[int, int]:
         fb, ls = ctypes.c_int64(), ctypes.c_int()

@@ -270,6 +270,108 @@ pkv_status check_decode_shape(const pkv_pool* pool, int num_seqs, int num_q_head
   return PKV_OK;
 }
 
+// The kernels' parameters for a planned decode (workspace pointers left NULL).
+pkv::DecodeParams decode_params(const pkv_pool* pool, const Plan& plan, const void* q,
+                                const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                int max_context_len, float scale, void* out) {
+  pkv::DecodeParams p{};
+  p.q = q;
+  p.k_cache = pool->k_cache;
+  p.v_cache = pool->v_cache;
+  p.k_scale = pool->k_scale;
+  p.v_scale = pool->v_scale;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.out = out;
+  p.err = pool->d_err;
+  p.sched = pool->d_err + 1;
+  p.persistent = plan.persistent;
+  const int64_t items = int64_t(plan.max_parts) * num_seqs * pool->kv_heads * plan.chunks;
+  const int64_t resident = int64_t(pool->sm_count) * plan.ctas_per_sm;
+  p.grid = static_cast<int>(items < resident ? items : resident);
+  p.num_blocks = pool->num_blocks;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.kv_heads = pool->kv_heads;
+  p.group = num_q_heads / pool->kv_heads;
+  p.group_log2 = -1;
+  for (int l = 0; l < 31; ++l)
+    if ((1 << l) == p.group) p.group_log2 = l;
+  p.num_queries = plan.num_queries;
+  p.window = plan.window;
+  p.chunks = plan.chunks;
+  p.head_dim = pool->head_dim;
+  p.max_context_len = max_context_len;
+  p.partition_blocks = plan.partition_blocks;
+  p.max_parts = plan.max_parts;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.min_len = plan.num_queries;
+  p.partials = 0;
+  return p;
+}
+
+cudaError_t launch_decode(const pkv_pool* pool, const Plan& plan, const pkv::DecodeParams& p, cudaStream_t s) {
+  if (plan.kernel == PKV_KERNEL_TENSOR_CORE)
+    return pkv::launch_decode_mma(p, &pool->tmap_k, &pool->tmap_v, static_cast<pkv::KvType>(pool->dtype),
+                                  plan.cols, plan.shape, s);
+  return pool->dtype == PKV_KV_INT8       ? pkv::launch_decode_int8(p, plan.cols, s)
+         : pool->dtype == PKV_KV_FP8_E4M3 ? pkv::launch_decode_fp8(p, plan.cols, s)
+                                          : pkv::launch_decode_bf16(p, plan.cols, s);
+}
+
+// Whether the pool's device is the current one: a launch on another device's stream fails,
+// and the kernels' attributes are per device.
+bool on_pool_device(const pkv_pool* pool) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == pool->device;
+}
+
+// Layout of a shared-prefix call's workspace and the plan of its suffix pass.
+struct PrefixPlan {
+  Plan suffix;
+  int grid;
+  int suffix_blocks;
+  size_t lens, tables, acc, ml, suffix_acc, suffix_ml, bytes;  // offsets (the descriptors sit at 0), size
+};
+
+pkv_status make_prefix_plan(const pkv_pool* pool, int num_seqs, int num_q_heads, int num_groups, int max_prefix_len,
+                            int max_suffix_len, const pkv_decode_options* opt, PrefixPlan* x) {
+  pkv_status st = check_decode_shape(pool, num_seqs, num_q_heads, max_suffix_len);
+  if (st != PKV_OK) return st;
+  if (num_groups < 0 || max_prefix_len < 0 || max_prefix_len >= pkv::kNoWindow) return PKV_ERR_INVALID_ARG;
+  if (num_groups > pkv::kMaxPrefixGroups) return PKV_ERR_UNSUPPORTED;
+  if (opt && opt->window != 0) return opt->window < 0 ? PKV_ERR_INVALID_ARG : PKV_ERR_UNSUPPORTED;
+  const int nq = num_queries_of(opt);
+  if (nq < 1) return PKV_ERR_INVALID_ARG;
+  const int group = num_q_heads / pool->kv_heads;
+  if (int64_t(num_seqs) * nq * num_q_heads > INT32_MAX / 4) return PKV_ERR_UNSUPPORTED;
+  // the prefix pass reads the pool through its tensor maps
+  if (!pool->has_tmaps) return PKV_ERR_UNSUPPORTED;
+  st = make_plan(pool, num_seqs, num_q_heads, max_suffix_len < nq ? nq : max_suffix_len, opt, &x->suffix);
+  if (st != PKV_OK) return st;
+  x->grid = pool->sm_count;
+  x->suffix_blocks = static_cast<int>(ceil_div(max_suffix_len, pkv::kBlockSize));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at = (at + bytes + 255) / 256 * 256;
+    return o;
+  };
+  const size_t rows = size_t(num_seqs) * nq * num_q_heads;
+  const size_t pre = 2 * size_t(num_seqs) * nq * group * pool->kv_heads + size_t(x->grid) * pkv::kPrefixRows;
+  take(size_t(num_seqs) * sizeof(pkv::PrefixSeq));
+  x->lens = take(size_t(num_seqs) * 4);
+  x->tables = take(size_t(num_seqs) * x->suffix_blocks * 4);
+  x->acc = take(pre * pool->head_dim * 4);
+  x->ml = take(pre * 8);
+  x->suffix_acc = take(rows * x->suffix.max_parts * pool->head_dim * 4);
+  x->suffix_ml = take(rows * x->suffix.max_parts * 8);
+  x->bytes = at;
+  return PKV_OK;
+}
+
 }  // namespace
 
 namespace pkv {
@@ -488,54 +590,15 @@ pkv_status pkv_paged_attention_decode_ex(const pkv_pool* pool, const void* q,
     if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
   }
 
-  pkv::DecodeParams p{};
-  p.q = q;
-  p.k_cache = pool->k_cache;
-  p.v_cache = pool->v_cache;
-  p.k_scale = pool->k_scale;
-  p.v_scale = pool->v_scale;
-  p.block_tables = block_tables;
-  p.context_lens = context_lens;
-  p.out = out;
+  pkv::DecodeParams p = decode_params(pool, plan, q, block_tables, max_blocks_per_seq, context_lens, num_seqs,
+                                      num_q_heads, max_context_len, scale, out);
   p.ws_acc = plan.ws_bytes ? static_cast<float*>(workspace) : nullptr;
   p.ws_ml = plan.ws_bytes
                 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.ws_ml_offset)
                 : nullptr;
-  p.err = pool->d_err;
-  p.sched = pool->d_err + 1;
-  p.persistent = plan.persistent;
-  {
-    const int64_t items = int64_t(plan.max_parts) * num_seqs * pool->kv_heads * plan.chunks;
-    const int64_t resident = int64_t(pool->sm_count) * plan.ctas_per_sm;
-    p.grid = static_cast<int>(items < resident ? items : resident);
-  }
-  p.num_blocks = pool->num_blocks;
-  p.max_blocks_per_seq = max_blocks_per_seq;
-  p.num_seqs = num_seqs;
-  p.num_q_heads = num_q_heads;
-  p.kv_heads = pool->kv_heads;
-  p.group = num_q_heads / pool->kv_heads;
-  p.group_log2 = -1;
-  for (int l = 0; l < 31; ++l)
-    if ((1 << l) == p.group) p.group_log2 = l;
-  p.num_queries = plan.num_queries;
-  p.window = plan.window;
-  p.chunks = plan.chunks;
-  p.head_dim = pool->head_dim;
-  p.max_context_len = max_context_len;
-  p.partition_blocks = plan.partition_blocks;
-  p.max_parts = plan.max_parts;
-  p.scale_log2 = scale * 1.4426950408889634f;
 
   auto s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (plan.kernel == PKV_KERNEL_TENSOR_CORE)
-    e = pkv::launch_decode_mma(p, &pool->tmap_k, &pool->tmap_v,
-                               static_cast<pkv::KvType>(pool->dtype), plan.cols, plan.shape, s);
-  else
-    e = pool->dtype == PKV_KV_INT8       ? pkv::launch_decode_int8(p, plan.cols, s)
-        : pool->dtype == PKV_KV_FP8_E4M3 ? pkv::launch_decode_fp8(p, plan.cols, s)
-                                         : pkv::launch_decode_bf16(p, plan.cols, s);
+  cudaError_t e = launch_decode(pool, plan, p, s);
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention_decode launch");
   g_launches.fetch_add(1, std::memory_order_relaxed);
   if (plan.max_parts > 1) {
@@ -554,6 +617,191 @@ pkv_status pkv_paged_attention_decode(const pkv_pool* pool, const void* q,
   return pkv_paged_attention_decode_ex(pool, q, block_tables, max_blocks_per_seq, context_lens,
                                        num_seqs, num_q_heads, max_context_len, scale, out,
                                        workspace, workspace_bytes, nullptr, stream);
+}
+
+pkv_status pkv_reserve_slots(const pkv_pool* pool, int32_t* block_tables, int max_blocks_per_seq,
+                             const int32_t* context_lens, const int32_t* num_new_tokens, int num_seqs,
+                             const int32_t* free_blocks, int num_free, const int32_t* free_used, int max_tokens,
+                             int32_t* slot_mapping, int32_t* positions, int32_t* query_starts,
+                             int32_t* new_context_lens, int32_t* new_free_used, void* stream) {
+  if (!pool || num_seqs < 0 || num_free < 0 || max_tokens < 0 || max_tokens >= (1 << 30)) return PKV_ERR_INVALID_ARG;
+  if (!query_starts || !new_free_used || (max_tokens > 0 && (!slot_mapping || !positions))) return PKV_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!block_tables || !context_lens || !num_new_tokens || !new_context_lens || max_blocks_per_seq < 1))
+    return PKV_ERR_INVALID_ARG;
+  if (num_free > 0 && !free_blocks) return PKV_ERR_INVALID_ARG;
+  // positions and slots are int32
+  if (int64_t(max_blocks_per_seq) * pkv::kBlockSize > INT32_MAX) return PKV_ERR_INVALID_ARG;
+  if (num_seqs > pkv::kMaxSlotSeqs || pool->num_blocks * pkv::kBlockSize > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if (!on_pool_device(pool)) return PKV_ERR_INVALID_ARG;
+  pkv::SlotParams p{};
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.num_new = num_new_tokens;
+  p.free_blocks = free_blocks;
+  p.free_used = free_used;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.query_starts = query_starts;
+  p.new_lens = new_context_lens;
+  p.new_used = new_free_used;
+  p.err = pool->d_err;
+  p.counter = pool->d_err + 3;
+  p.num_blocks = pool->num_blocks;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_free = num_free;
+  p.max_tokens = max_tokens;
+  cudaError_t e = pkv::launch_reserve_slots(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "reserve_slots launch");
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PKV_OK;
+}
+
+pkv_status pkv_norm_rope_and_cache(const pkv_pool* pool, const pkv_norm_rope* a, void* stream) {
+  if (!pool || !a || a->num_tokens < 0 || a->num_q_heads < 1) return PKV_ERR_INVALID_ARG;
+  if (a->num_tokens == 0) return PKV_OK;
+  if (!a->q || !a->k || !a->v || !a->q_out || !a->slot_mapping) return PKV_ERR_INVALID_ARG;
+  if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->q_out) || !aligned16(a->q_weight) ||
+      !aligned16(a->k_weight) || !aligned16(a->cos_sin))
+    return PKV_ERR_INVALID_ARG;
+  if (a->q_stride % 8 || a->k_stride % 8 || a->v_stride % 8 || a->q_out_stride % 8) return PKV_ERR_INVALID_ARG;
+  if (!(a->eps >= 0.0f)) return PKV_ERR_INVALID_ARG;
+  if (a->cos_sin) {
+    if (!a->positions || a->max_position < 1 || a->rot_dim < 2 || a->rot_dim > pool->head_dim) return PKV_ERR_INVALID_ARG;
+    if (a->rot_dim % 16) return PKV_ERR_UNSUPPORTED;
+  }
+  if (int64_t(a->num_q_heads) + 2 * int64_t(pool->kv_heads) > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
+  if (!on_pool_device(pool)) return PKV_ERR_INVALID_ARG;
+  pkv::RopeParams p{};
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.q_weight = a->q_weight;
+  p.k_weight = a->k_weight;
+  p.cos_sin = a->cos_sin;
+  p.positions = a->positions;
+  p.slot_mapping = a->slot_mapping;
+  p.q_out = a->q_out;
+  p.k_cache = pool->k_cache;
+  p.v_cache = pool->v_cache;
+  p.k_scale = pool->k_scale;
+  p.v_scale = pool->v_scale;
+  p.err = pool->d_err;
+  p.q_stride = a->q_stride;
+  p.k_stride = a->k_stride;
+  p.v_stride = a->v_stride;
+  p.out_stride = a->q_out_stride;
+  p.num_tokens = a->num_tokens;
+  p.num_blocks = pool->num_blocks;
+  p.num_q_heads = a->num_q_heads;
+  p.kv_heads = pool->kv_heads;
+  p.head_dim = pool->head_dim;
+  p.rot_dim = a->cos_sin ? a->rot_dim : 0;
+  p.max_position = a->max_position;
+  p.interleaved = a->interleaved != 0;
+  p.eps = a->eps;
+  cudaError_t e = pkv::launch_norm_rope(p, static_cast<pkv::KvType>(pool->dtype), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "norm_rope_and_cache launch");
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PKV_OK;
+}
+
+pkv_status pkv_rope_table(float* cos_sin, int64_t max_position, int rot_dim, double base, void* stream) {
+  if (!cos_sin || !aligned16(cos_sin) || max_position < 1 || max_position > INT32_MAX || rot_dim < 2 || !(base > 0.0))
+    return PKV_ERR_INVALID_ARG;
+  if (rot_dim % 16) return PKV_ERR_UNSUPPORTED;
+  cudaError_t e = pkv::launch_rope_table(cos_sin, max_position, rot_dim, base, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope_table launch");
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PKV_OK;
+}
+
+pkv_status pkv_shared_prefix_workspace_bytes(const pkv_pool* pool, int num_seqs, int num_q_heads, int num_groups,
+                                             int max_prefix_len, int max_suffix_len,
+                                             const pkv_decode_options* options, size_t* bytes) {
+  if (!bytes) return PKV_ERR_INVALID_ARG;
+  PrefixPlan plan;
+  const pkv_status st = make_prefix_plan(pool, num_seqs, num_q_heads, num_groups, max_prefix_len, max_suffix_len,
+                                         options, &plan);
+  if (st != PKV_OK) return st;
+  *bytes = plan.bytes;
+  return PKV_OK;
+}
+
+pkv_status pkv_shared_prefix_decode(const pkv_pool* pool, const void* q, const int32_t* block_tables,
+                                    int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                                    int num_q_heads, const int32_t* group_starts, const int32_t* prefix_lens,
+                                    int num_groups, int max_prefix_len, int max_suffix_len, float scale, void* out,
+                                    void* workspace, size_t workspace_bytes, const pkv_decode_options* options,
+                                    void* stream) {
+  PrefixPlan plan;
+  const pkv_status st = make_prefix_plan(pool, num_seqs, num_q_heads, num_groups, max_prefix_len, max_suffix_len,
+                                         options, &plan);
+  if (st != PKV_OK) return st;
+  if (num_seqs == 0) return PKV_OK;
+  if (!q || !block_tables || !context_lens || !out || !aligned16(q) || !aligned16(out)) return PKV_ERR_INVALID_ARG;
+  if (num_groups > 0 && (!group_starts || !prefix_lens)) return PKV_ERR_INVALID_ARG;
+  if (max_blocks_per_seq < 1) return PKV_ERR_INVALID_ARG;
+  const int64_t capacity = int64_t(max_blocks_per_seq) * pkv::kBlockSize;
+  if (max_prefix_len > capacity || max_suffix_len > capacity) return PKV_ERR_INVALID_ARG;
+  if (!(scale == scale)) return PKV_ERR_INVALID_ARG;  // NaN
+  if (!workspace || workspace_bytes < plan.bytes) return PKV_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
+  if (!on_pool_device(pool)) return PKV_ERR_INVALID_ARG;
+  char* ws = static_cast<char*>(workspace);
+
+  pkv::PrefixParams x{};
+  x.q = q;
+  x.k_cache = pool->k_cache;
+  x.v_cache = pool->v_cache;
+  x.k_scale = pool->k_scale;
+  x.v_scale = pool->v_scale;
+  x.block_tables = block_tables;
+  x.context_lens = context_lens;
+  x.group_starts = group_starts;
+  x.prefix_lens = prefix_lens;
+  x.out = out;
+  x.seqs = reinterpret_cast<pkv::PrefixSeq*>(ws);
+  x.suffix_lens = reinterpret_cast<int32_t*>(ws + plan.lens);
+  x.suffix_tables = reinterpret_cast<int32_t*>(ws + plan.tables);
+  x.acc = reinterpret_cast<float*>(ws + plan.acc);
+  x.ml = reinterpret_cast<float2*>(ws + plan.ml);
+  x.suffix_acc = reinterpret_cast<const float*>(ws + plan.suffix_acc);
+  x.suffix_ml = reinterpret_cast<const float2*>(ws + plan.suffix_ml);
+  x.err = pool->d_err;
+  x.num_blocks = pool->num_blocks;
+  x.max_blocks_per_seq = max_blocks_per_seq;
+  x.num_seqs = num_seqs;
+  x.num_groups = num_groups;
+  x.num_q_heads = num_q_heads;
+  x.kv_heads = pool->kv_heads;
+  x.group = num_q_heads / pool->kv_heads;
+  x.num_queries = plan.suffix.num_queries;
+  x.head_dim = pool->head_dim;
+  x.max_prefix_len = max_prefix_len;
+  x.max_suffix_len = max_suffix_len;
+  x.suffix_blocks = plan.suffix_blocks;
+  x.suffix_partition = plan.suffix.partition_blocks;
+  x.suffix_parts = plan.suffix.max_parts;
+  x.grid = plan.grid;
+  x.scale_log2 = scale * 1.4426950408889634f;
+
+  pkv::DecodeParams p = decode_params(pool, plan.suffix, q, x.suffix_tables, plan.suffix_blocks, x.suffix_lens,
+                                      num_seqs, num_q_heads, max_suffix_len, scale, out);
+  p.ws_acc = reinterpret_cast<float*>(ws + plan.suffix_acc);
+  p.ws_ml = reinterpret_cast<float*>(ws + plan.suffix_ml);
+  p.min_len = 0;  // the prefix may cover every token a query sees
+  p.partials = 1;
+
+  auto s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = pkv::launch_prefix(x, static_cast<pkv::KvType>(pool->dtype), s);
+  if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
+  e = launch_decode(pool, plan.suffix, p, s);
+  if (e != cudaSuccess) return cuda_fail(e, "shared prefix: suffix launch");
+  e = pkv::launch_prefix_merge(x, s);
+  if (e != cudaSuccess) return cuda_fail(e, "shared prefix: merge launch");
+  g_launches.fetch_add(3, std::memory_order_relaxed);
+  return PKV_OK;
 }
 
 pkv_status pkv_get_device_error(const pkv_pool* pool, uint32_t* flags, void* stream) {

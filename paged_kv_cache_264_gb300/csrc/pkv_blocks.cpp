@@ -252,6 +252,56 @@ PKV_API pkv_status pkv_block_manager_tables(const pkv_block_manager* m, const in
   return PKV_OK;
 }
 
+PKV_API pkv_status pkv_block_manager_free_list(const pkv_block_manager* m, int n, int32_t* ids) {
+  if (!m || n < 0 || (n > 0 && !ids)) return PKV_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> lock(m->mu);
+  if (size_t(n) > m->free_blocks.size()) return PKV_ERR_CAPACITY;
+  std::copy_n(m->free_blocks.rbegin(), n, ids);  // allocation pops from the back
+  return PKV_OK;
+}
+
+PKV_API pkv_status pkv_block_manager_prefix_groups(const pkv_block_manager* m, const int* seqs, int n,
+                                                   int num_queries, int32_t* group_starts,
+                                                   int32_t* prefix_lens, int* num_groups) {
+  if (!m || n < 0 || (n > 0 && (!seqs || !prefix_lens)) || !group_starts || !num_groups || num_queries < 1 ||
+      num_queries > 16)
+    return PKV_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> lock(m->mu);
+  for (int i = 0; i < n; ++i)
+    if (!seq_ok(m, seqs[i])) return PKV_ERR_INVALID_ARG;
+  int groups = 0;
+  int64_t members = 0, prefix = 0;  // of the open group: sequences and common whole blocks
+  group_starts[0] = 0;
+  for (int i = 0; i < n; ++i) {
+    const auto& q = m->seqs[size_t(seqs[i])];
+    // whole blocks that each of the sequence's last num_queries positions sees
+    const int64_t whole = std::max(0, q.len - (num_queries - 1)) / kBlock;
+    int64_t common = 0;
+    if (members > 0) {
+      const auto& first = m->seqs[size_t(seqs[group_starts[groups]])].blocks;
+      const int64_t most = std::min(whole, prefix);
+      while (common < most && q.blocks[size_t(common)] >= 0 && q.blocks[size_t(common)] == first[size_t(common)]) ++common;
+    }
+    if (members > 0 && common > 0 && members * common >= (members - 1) * prefix) {
+      ++members;
+      prefix = common;
+    } else {
+      if (members > 0) {
+        prefix_lens[groups] = members > 1 ? int32_t(prefix * kBlock) : 0;
+        group_starts[++groups] = i;
+      }
+      members = 1;
+      prefix = whole;
+    }
+  }
+  if (members > 0) {
+    prefix_lens[groups] = members > 1 ? int32_t(prefix * kBlock) : 0;
+    group_starts[++groups] = n;
+  }
+  *num_groups = groups;
+  return PKV_OK;
+}
+
 PKV_API pkv_status pkv_block_manager_stats(const pkv_block_manager* m, int64_t* free_blocks,
                                            int* live_seqs) {
   if (!m) return PKV_ERR_INVALID_ARG;

@@ -233,7 +233,7 @@ __device__ __forceinline__ int first_block(const DecodeParams& p, int T) {
 }
 
 __device__ __forceinline__ int seq_parts(const DecodeParams& p, int T) {
-  if (T < p.num_queries || T > p.max_context_len) return 1;
+  if (T < p.min_len || T > p.max_context_len) return 1;
   const int nblk = (T + kBlockSize - 1) / kBlockSize - first_block(p, T);
   return partition_count(nblk, p.partition_blocks);
 }
@@ -344,7 +344,7 @@ __device__ __forceinline__ void locate_unit(const DecodeParams& p, const SchedSm
 // classic-grid slot.
 __device__ __forceinline__ bool locate_len(const DecodeParams& p, int T, ItemInfo& it) {
   it.T = T;
-  it.bad_len = it.T < p.num_queries || it.T > p.max_context_len;
+  it.bad_len = it.T < p.min_len || it.T > p.max_context_len;
   it.nparts = seq_parts(p, it.T);
   return it.part < it.nparts;
 }
@@ -457,7 +457,7 @@ __device__ __forceinline__ void merge_warp_records(const unsigned char* smem, si
     }
   }
   const size_t row = col_row(p, b, kvh, c0 + g);
-  if (nparts == 1) {
+  if (nparts == 1 && !p.partials) {
     auto* out = static_cast<__nv_bfloat16*>(p.out) + row * D + d0;
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     if constexpr (kE == 1) {
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(128) lse_reduce_kernel(const DecodeParams p) {
       }
     }
   }
-  if (T < p.num_queries || T > p.max_context_len) return;  // the decode kernel wrote zeros
+  if (T < p.min_len || T > p.max_context_len) return;  // the decode kernel wrote zeros
   const int nparts = seq_parts(p, T);
   if (nparts <= 1) return;  // written directly by the decode kernel
   if (lane >= nparts) mine = make_float2(-INFINITY, 0.0f);

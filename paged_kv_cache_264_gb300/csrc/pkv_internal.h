@@ -33,6 +33,9 @@ constexpr uint32_t kErrBlockId = 0x1u;
 constexpr uint32_t kErrContextLen = 0x2u;
 constexpr uint32_t kErrSlot = 0x4u;
 constexpr uint32_t kErrTimeout = 0x8u;
+constexpr uint32_t kErrCapacity = 0x10u;
+constexpr uint32_t kErrPosition = 0x20u;
+constexpr uint32_t kErrPrefix = 0x40u;
 
 enum class KvType : int { kBf16 = 0, kInt8 = 1, kFp8 = 2 };
 
@@ -82,7 +85,117 @@ struct DecodeParams {
   int partition_blocks;         // P: blocks per work item
   int max_parts;                // ceil(ceil(max_context_len / 16) / P)
   float scale_log2;             // softmax scale * log2(e)
+  int min_len;                  // shortest valid context (num_queries; 0 when another pass
+                                // covers the tokens before this call's context)
+  int partials;                 // 1: always leave (m, l, acc) in the workspace, never write out
 };
+
+// Reserving cache slots for new tokens on the device (pkv_slots.cu).
+struct SlotParams {
+  int32_t* block_tables;        // [B, max_blocks_per_seq], new entries written
+  const int32_t* context_lens;  // [B]
+  const int32_t* num_new;       // [B]
+  const int32_t* free_blocks;   // [num_free] ids in hand-out order
+  const int32_t* free_used;     // [1] entries already handed out; NULL: 0
+  int32_t* slot_mapping;        // [max_tokens]
+  int32_t* positions;           // [max_tokens]
+  int32_t* query_starts;        // [B + 1]
+  int32_t* new_lens;            // [B], may be context_lens
+  int32_t* new_used;            // [1], may be free_used
+  uint32_t* err;
+  unsigned* counter;            // CTAs that have read their inputs (zero between calls)
+  int64_t num_blocks;
+  int max_blocks_per_seq;
+  int num_seqs;
+  int num_free;
+  int max_tokens;
+};
+constexpr int kMaxSlotSeqs = 16384;  // three ints of shared memory per sequence
+cudaError_t launch_reserve_slots(const SlotParams& p, cudaStream_t stream);
+
+// Per-head norm, rotation and cache write of new tokens (pkv_rope.cu).
+struct RopeParams {
+  const void* q;                // bf16 rows of [Hq, D] at token stride q_stride, and so on
+  const void* k;
+  const void* v;
+  const void* q_weight;         // bf16 [D] or NULL: q is not normalised
+  const void* k_weight;
+  const float* cos_sin;         // [max_position, rot_dim]: cosines, then sines; NULL: no rotation
+  const int32_t* positions;     // [N]
+  const int32_t* slot_mapping;  // [N]
+  void* q_out;                  // bf16 rows of [Hq, D] at token stride out_stride
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  uint32_t* err;
+  int64_t q_stride, k_stride, v_stride, out_stride;  // elements
+  int64_t num_tokens;
+  int64_t num_blocks;
+  int num_q_heads;
+  int kv_heads;
+  int head_dim;
+  int rot_dim;
+  int max_position;
+  int interleaved;
+  float eps;
+};
+cudaError_t launch_norm_rope(const RopeParams& p, KvType kv, cudaStream_t stream);
+cudaError_t launch_rope_table(float* out, int64_t max_position, int rot_dim, double base, cudaStream_t stream);
+
+// Decode attention over shared prefixes (pkv_prefix.cu).  The prefix pass writes, besides
+// its partials, what the two later passes need: each sequence's descriptor, the length of
+// its own tokens and their slice of its block table.
+struct PrefixSeq {
+  int64_t w_base;     // first work tile of the sequence's group
+  int64_t row_base;   // first partial row of the group
+  int64_t total;      // work tiles of the whole call
+  int suffix_len;     // the sequence's own tokens; -1: its inputs are invalid
+  int tiles;          // 128-token tiles of its prefix
+  int first_row;      // its first query row among the group's (per kv head)
+  int rows;           // the group's query rows per kv head
+};
+struct PrefixParams {
+  const void* q;                // bf16 [B, k, Hq, D]
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* group_starts;  // [G + 1]
+  const int32_t* prefix_lens;   // [G]
+  void* out;
+  PrefixSeq* seqs;              // [B]
+  int32_t* suffix_lens;         // [B]
+  int32_t* suffix_tables;       // [B, suffix_blocks]
+  float* acc;                   // [rows, D] prefix partials
+  float2* ml;                   // [rows] running max (log2 units) and sum
+  const float* suffix_acc;      // [B, k, Hq, suffix_parts, D]
+  const float2* suffix_ml;
+  uint32_t* err;
+  int64_t num_blocks;
+  int max_blocks_per_seq;
+  int num_seqs;
+  int num_groups;
+  int num_q_heads;
+  int kv_heads;
+  int group;                    // query heads per kv head
+  int num_queries;
+  int head_dim;
+  int max_prefix_len;
+  int max_suffix_len;
+  int suffix_blocks;            // width of suffix_tables
+  int suffix_partition;         // the suffix pass's partition size and most partitions
+  int suffix_parts;
+  int grid;                     // CTAs of the prefix pass
+  float scale_log2;
+};
+constexpr int kMaxPrefixGroups = 4096;
+constexpr int kPrefixTile = 128;     // prefix tokens of one work tile
+constexpr int kPrefixRows = 256;     // query rows of one work unit (two 128-row tiles)
+cudaError_t launch_prefix(const PrefixParams& p, KvType kv, cudaStream_t stream);
+cudaError_t launch_prefix_merge(const PrefixParams& p, cudaStream_t stream);
 
 // Launch a kernel with programmatic stream serialisation (see griddep_wait in
 // pkv_device.cuh): its launch may overlap the tail of the previous kernel in the stream.

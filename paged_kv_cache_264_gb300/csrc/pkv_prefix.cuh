@@ -1,0 +1,216 @@
+// pkv_prefix.cuh -- the work line of shared-prefix decode attention, shared by its passes.
+//
+// Group g of the batch is sequences group_starts[g] .. group_starts[g + 1] - 1, whose first
+// prefix_lens[g] tokens (whole blocks) are the same.  A group has R = (sequences) * k * (query
+// heads per kv head) query rows per kv head, in units of up to 256 rows, and its prefix is cut
+// into tiles of 128 tokens.  All (kv head, unit, tile) triples of all groups, in that order,
+// form one line of work tiles, which the CTAs of the prefix pass share out in equal
+// contiguous stretches: every CTA gets the same number of tiles (to within one) whatever the
+// groups' sizes.  A stretch inside one (kv head, unit) leaves one partial (running max, sum,
+// accumulator) per row.
+//
+// Partial rows: CTA c's partial of a unit starts at row (rows of all units before it) + 256 c.
+// Going along the line either the unit or the CTA (or both) moves on, by that unit's rows or by
+// 256, so no two partials overlap.  A unit of up to 128 rows holds two rows of partials per
+// query row, since its even and its odd tiles are accumulated apart.
+#pragma once
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+// Rows of partials that a group of `rows` query rows takes per kv head.
+__host__ __device__ __forceinline__ int64_t partial_rows(int rows) {
+  return rows <= kPrefixRows / 2 ? 2 * int64_t(rows) : rows;
+}
+
+struct PrefixGroup {
+  int first_seq, rows, units, tiles;  // units per kv head
+  int64_t w_base, row_base;
+};
+
+// The scan of the groups, in scratch shared memory: base[g] = (first work tile, first partial
+// row) of group g.
+struct PrefixScan {
+  longlong2* base;   // [G + 1]
+  longlong2* warp;   // [32]
+};
+__host__ __device__ constexpr size_t prefix_scan_bytes(int groups) { return (size_t(groups) + 1 + 32) * 16; }
+
+// Sizes of group g; false where its description is invalid.
+__device__ __forceinline__ bool prefix_group(const PrefixParams& p, int g, PrefixGroup& x) {
+  const int s0 = __ldg(p.group_starts + g), s1 = __ldg(p.group_starts + g + 1), len = __ldg(p.prefix_lens + g);
+  const bool ok = s0 >= 0 && s1 >= s0 && s1 <= p.num_seqs && len >= 0 && len <= p.max_prefix_len && len % kBlockSize == 0;
+  x.first_seq = s0;
+  x.rows = ok ? (s1 - s0) * p.num_queries * p.group : 0;
+  x.units = (x.rows + kPrefixRows - 1) / kPrefixRows;
+  x.tiles = ok ? (len + kPrefixTile - 1) / kPrefixTile : 0;
+  return ok;
+}
+
+// Fill the scan (all NT threads of the CTA); returns the work tiles of the call, or -1 where
+// some group is invalid.  Ends with a barrier.
+template <int NT>
+__device__ __forceinline__ int64_t prefix_scan(const PrefixParams& p, const PrefixScan& sc) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = p.num_groups;
+  const int per = (G + NT - 1) / NT;
+  const int lo = min(G, tid * per), hi = min(G, lo + per);
+  int64_t w = 0, r = 0;
+  bool ok = true;
+  for (int g = lo; g < hi; ++g) {
+    PrefixGroup x;
+    ok &= prefix_group(p, g, x);
+    w += int64_t(x.units) * p.kv_heads * x.tiles;
+    r += partial_rows(x.rows) * p.kv_heads;
+  }
+  int64_t iw = w, ir = r;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t a = __shfl_up_sync(0xffffffffu, iw, o), b = __shfl_up_sync(0xffffffffu, ir, o);
+    if (lane >= o) {
+      iw += a;
+      ir += b;
+    }
+  }
+  if (lane == 31) sc.warp[warp] = make_longlong2(iw, ir);
+  ok = __syncthreads_and(ok);
+  int64_t bw = iw - w, br = ir - r, total = 0;
+  for (int i = 0; i < NT / 32; ++i) {
+    const longlong2 x = sc.warp[i];
+    if (i < warp) {
+      bw += x.x;
+      br += x.y;
+    }
+    total += x.x;
+  }
+  for (int g = lo; g < hi; ++g) {
+    PrefixGroup x;
+    prefix_group(p, g, x);
+    sc.base[g] = make_longlong2(bw, br);
+    bw += int64_t(x.units) * p.kv_heads * x.tiles;
+    br += partial_rows(x.rows) * p.kv_heads;
+  }
+  __syncthreads();
+  return ok ? total : -1;
+}
+
+// CTAs that take work: no more than there are tiles, so that none between a unit's first and
+// last CTA is without one (its partial would be read unwritten).
+__device__ __forceinline__ int stretch_ctas(int64_t total, int grid) { return int(min(total, int64_t(grid))); }
+// CTA c's stretch of `total` work tiles starts here.
+__device__ __forceinline__ int64_t stretch_start(int64_t total, int ctas, int c) { return total * c / ctas; }
+// The CTA whose stretch holds work tile w: the last one that starts at or before it.
+__device__ __forceinline__ int stretch_owner(int64_t total, int ctas, int64_t w) {
+  return int(((w + 1) * ctas - 1) / total);
+}
+
+// A walk along one CTA's stretch: one (kv head, unit) at a time.
+struct PrefixWalk {
+  PrefixGroup x;
+  int g, kvh, unit;      // group, kv head and unit of the group's rows
+  int tile0, tile1;      // this stretch's tiles of the unit
+  int row0, nrows;       // the unit's query rows within the group
+  int64_t partial;       // its first partial row
+  int64_t w, w_end;
+};
+
+__device__ __forceinline__ void walk_place(const PrefixParams& p, PrefixWalk& k, int cta) {
+  const int64_t in_group = k.w - k.x.w_base;
+  const int u = int(in_group / k.x.tiles);  // kv head * units + unit
+  k.tile0 = int(in_group - int64_t(u) * k.x.tiles);
+  k.tile1 = int(min(int64_t(k.x.tiles), k.tile0 + (k.w_end - k.w)));
+  k.kvh = u / k.x.units;
+  k.unit = u - k.kvh * k.x.units;
+  k.row0 = k.unit * kPrefixRows;
+  k.nrows = min(kPrefixRows, k.x.rows - k.row0);
+  k.partial = k.x.row_base + int64_t(k.kvh) * partial_rows(k.x.rows) + k.row0 + int64_t(cta) * kPrefixRows;
+}
+
+// The first piece of CTA `cta`'s stretch; false if it has none.
+__device__ __forceinline__ bool walk_begin(const PrefixParams& p, const PrefixScan& sc, int64_t total, int cta,
+                                           PrefixWalk& k) {
+  const int ctas = stretch_ctas(total, p.grid);
+  if (cta >= ctas) return false;
+  k.w = stretch_start(total, ctas, cta);
+  k.w_end = stretch_start(total, ctas, cta + 1);
+  int lo = 0, hi = p.num_groups;  // the last group that starts at or before w (empty ones share a start)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sc.base[mid].x <= k.w) lo = mid; else hi = mid;
+  }
+  k.g = lo;
+  prefix_group(p, lo, k.x);
+  k.x.w_base = sc.base[lo].x;
+  k.x.row_base = sc.base[lo].y;
+  walk_place(p, k, cta);
+  return true;
+}
+
+__device__ __forceinline__ bool walk_next(const PrefixParams& p, int cta, PrefixWalk& k) {
+  k.w += k.tile1 - k.tile0;
+  if (k.w >= k.w_end) return false;
+  int64_t group_end = k.x.w_base + int64_t(k.x.units) * p.kv_heads * k.x.tiles;
+  while (k.w >= group_end) {  // past this group and any without work
+    const int64_t rows = k.x.row_base + partial_rows(k.x.rows) * p.kv_heads;
+    ++k.g;
+    prefix_group(p, k.g, k.x);
+    k.x.w_base = group_end;
+    k.x.row_base = rows;
+    group_end += int64_t(k.x.units) * p.kv_heads * k.x.tiles;
+  }
+  walk_place(p, k, cta);
+  return true;
+}
+
+// Row of q and out (in units of head_dim values) of the group's query row r for kv head kvh:
+// rows run over the group's sequences, each one's query tokens, each one's heads of the group.
+__device__ __forceinline__ int64_t prefix_q_row(const PrefixParams& p, const PrefixGroup& x, int kvh, int r) {
+  const int tok = r / p.group, head = r - tok * p.group;
+  return (int64_t(x.first_seq) * p.num_queries + tok) * p.num_q_heads + int64_t(kvh) * p.group + head;
+}
+
+// What the suffix and merge passes need of this CTA's share of the sequences (all NT threads).
+template <int NT>
+__device__ __forceinline__ void prefix_describe(const PrefixParams& p, const PrefixScan& sc, int64_t total) {
+  const int lane = threadIdx.x & 31;
+  for (int b = blockIdx.x * (NT / 32) + (threadIdx.x >> 5); b < p.num_seqs; b += gridDim.x * (NT / 32)) {
+    const int T = __ldg(p.context_lens + b);
+    PrefixSeq d{};
+    PrefixGroup x{};
+    int len = 0;
+    if (total >= 0 && p.num_groups > 0) {
+      int lo = 0, hi = p.num_groups;
+      while (hi - lo > 1) {  // the last group that starts at or before b
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.group_starts + mid) <= b) lo = mid; else hi = mid;
+      }
+      if (b >= __ldg(p.group_starts + lo) && b < __ldg(p.group_starts + lo + 1)) {
+        prefix_group(p, lo, x);
+        len = __ldg(p.prefix_lens + lo);
+        d.w_base = sc.base[lo].x;
+        d.row_base = sc.base[lo].y;
+        d.tiles = x.tiles;
+        d.rows = x.rows;
+        d.first_row = (b - x.first_seq) * p.num_queries * p.group;
+      }
+    }
+    d.total = total;
+    d.suffix_len = T - len;
+    // every query sees the whole prefix, and the table holds the sequence
+    if (total < 0 || T < p.num_queries || T - (p.num_queries - 1) < len || T - len > p.max_suffix_len ||
+        T > int64_t(p.max_blocks_per_seq) * kBlockSize)
+      d.suffix_len = -1;
+    const int nblk = d.suffix_len < 0 ? 0 : (d.suffix_len + kBlockSize - 1) / kBlockSize;
+    const int32_t* row = p.block_tables + int64_t(b) * p.max_blocks_per_seq + len / kBlockSize;
+    int32_t* to = p.suffix_tables + int64_t(b) * p.suffix_blocks;
+    for (int j = lane; j < p.suffix_blocks; j += 32) to[j] = j < nblk ? __ldg(row + j) : -1;
+    if (lane == 0) {
+      p.seqs[b] = d;
+      p.suffix_lens[b] = d.suffix_len;
+    }
+  }
+  if (total < 0 && blockIdx.x == 0 && threadIdx.x == 0) set_error(p.err, kErrPrefix);
+}
+
+}  // namespace pkv
