@@ -794,7 +794,7 @@ pkv_status pkv_shared_prefix_decode(const pkv_pool* pool, const void* q, const i
   p.partials = 1;
 
   auto s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = pkv::launch_prefix(x, static_cast<pkv::KvType>(pool->dtype), s);
+  cudaError_t e = pkv::launch_prefix(x, pool->tmap_k, pool->tmap_v, static_cast<pkv::KvType>(pool->dtype), s);
   if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
   e = launch_decode(pool, plan.suffix, p, s);
   if (e != cudaSuccess) return cuda_fail(e, "shared prefix: suffix launch");

@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
 #pragma unroll 4
     for (int j = 0; j < min(32, n - i0); ++j) {
       const float w = __shfl_sync(kFull, f, j);
+      if (w == 0.0f) continue;  // a stream without tiles leaves no accumulator
       const int i = i0 + j;
       const float* src = i < nsuf ? sacc + int64_t(i) * D : p.acc + pre_row(i - nsuf) * D + lane * kDPV;
 #pragma unroll
@@ -185,11 +186,12 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
 
 }  // namespace
 
-cudaError_t launch_prefix(const PrefixParams& p, KvType kv, cudaStream_t stream) {
+cudaError_t launch_prefix(const PrefixParams& p, const CUtensorMap& tk, const CUtensorMap& tv, KvType kv,
+                          cudaStream_t stream) {
   const bool wide = p.head_dim == 128;
   switch (kv) {
     case KvType::kBf16:
-      return wide ? launch_prefix_simple<KvType::kBf16, 128>(p, stream) : launch_prefix_simple<KvType::kBf16, 64>(p, stream);
+      return launch_prefix_bf16(p, tk, tv, stream);
     case KvType::kInt8:
       return wide ? launch_prefix_simple<KvType::kInt8, 128>(p, stream) : launch_prefix_simple<KvType::kInt8, 64>(p, stream);
     case KvType::kFp8:
