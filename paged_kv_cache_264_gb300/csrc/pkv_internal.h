@@ -196,6 +196,8 @@ constexpr int kPrefixTile = 128;     // prefix tokens of one work tile
 constexpr int kPrefixRows = 256;     // query rows of one work unit (two 128-row tiles)
 cudaError_t launch_prefix(const PrefixParams& p, const CUtensorMap& tk, const CUtensorMap& tv, KvType kv,
                           cudaStream_t stream);
+cudaError_t launch_prefix_quant(const PrefixParams& p, const CUtensorMap& tk, const CUtensorMap& tv, KvType kv,
+                                cudaStream_t stream);
 cudaError_t launch_prefix_bf16(const PrefixParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const PrefixParams& p, cudaStream_t stream);
 

@@ -19,103 +19,6 @@
 namespace pkv {
 namespace {
 
-constexpr int kSimpleThreads = 256;
-
-// Value of element c of a pool row.
-template <KvType KV>
-__device__ __forceinline__ float pool_value(const void* cache, int64_t i) {
-  if constexpr (KV == KvType::kBf16) {
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(cache)[i]);
-  } else if constexpr (KV == KvType::kInt8) {
-    return float(static_cast<const int8_t*>(cache)[i]);
-  } else {
-    float f[4];
-    e4m3x4_to_f32(static_cast<const uint8_t*>(cache)[i], f);
-    return f[0];
-  }
-}
-
-// One warp per query row of the CTA's stretch: 32 tokens at a time, a lane to a token for the
-// logits and a lane to D / 32 values for the accumulator.
-template <KvType KV, int D>
-__global__ void __launch_bounds__(kSimpleThreads) prefix_simple_kernel(const PrefixParams p) {
-  constexpr uint32_t kFull = 0xffffffffu;
-  constexpr int kDPV = D / 32;
-  extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float qs[kSimpleThreads / 32][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  griddep_wait();
-  PrefixScan sc{reinterpret_cast<longlong2*>(smem) + 32, reinterpret_cast<longlong2*>(smem)};
-  const int64_t total = prefix_scan<kSimpleThreads>(p, sc);
-  prefix_describe<kSimpleThreads>(p, sc, total);
-  if (total <= 0) return;
-  PrefixWalk k;
-  for (bool more = walk_begin(p, sc, total, blockIdx.x, k); more; more = walk_next(p, blockIdx.x, k)) {
-    const int prefix = __ldg(p.prefix_lens + k.g);
-    const int32_t* table = p.block_tables + int64_t(k.x.first_seq) * p.max_blocks_per_seq;
-    for (int r = warp; r < k.nrows; r += kSimpleThreads / 32) {
-      const auto* q = static_cast<const __nv_bfloat16*>(p.q) + prefix_q_row(p, k.x, k.kvh, k.row0 + r) * D;
-      __syncwarp();
-      for (int c = lane; c < D; c += 32) qs[warp][c] = __bfloat162float(q[c]) * p.scale_log2;
-      __syncwarp();
-      float m = kMaxFloor, l = 0.0f, acc[kDPV] = {};
-      for (int t0 = k.tile0 * kPrefixTile; t0 < min(prefix, k.tile1 * kPrefixTile); t0 += 32) {
-        const int t = t0 + lane;
-        float x = -INFINITY, sv = 1.0f;
-        int64_t row = -1;
-        if (t < prefix) {
-          const int64_t block = __ldg(table + t / kBlockSize);
-          if (block < 0 || block >= p.num_blocks) {
-            set_error(p.err, kErrBlockId);
-          } else {
-            row = (block * p.kv_heads + k.kvh) * kBlockSize + t % kBlockSize;
-            x = 0.0f;
-            for (int c = 0; c < D; ++c) x = fmaf(qs[warp][c], pool_value<KV>(p.k_cache, row * D + c), x);
-            if constexpr (KV != KvType::kBf16) {
-              x *= p.k_scale[row];
-              sv = p.v_scale[row];
-            }
-          }
-        }
-        float mx = x;
-        for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-        const float mu = fmaxf(m, mx), f = fast_exp2(m - mu);
-        m = mu;
-        const float pr = row >= 0 ? fast_exp2(x - m) : 0.0f;
-        l = l * f + pr;
-        for (int i = 0; i < kDPV; ++i) acc[i] *= f;
-        for (int j = 0; j < 32; ++j) {
-          const float w = __shfl_sync(kFull, pr * sv, j);
-          const int64_t rj = __shfl_sync(kFull, row, j);
-          if (rj >= 0)
-            for (int i = 0; i < kDPV; ++i) acc[i] = fmaf(w, pool_value<KV>(p.v_cache, rj * D + lane + 32 * i), acc[i]);
-        }
-      }
-      for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-      const int64_t to = k.partial + r;
-      for (int i = 0; i < kDPV; ++i) p.acc[to * D + lane + 32 * i] = acc[i];
-      if (lane == 0) p.ml[to] = make_float2(m, l);
-      if (k.x.rows <= kPrefixRows / 2 && lane == 0) {
-        p.ml[to + k.x.rows] = make_float2(kMaxFloor, 0.0f);
-        // never weighted, but read
-      }
-      if (k.x.rows <= kPrefixRows / 2)
-        for (int i = 0; i < kDPV; ++i) p.acc[(to + k.x.rows) * D + lane + 32 * i] = 0.0f;
-    }
-  }
-}
-
-template <KvType KV, int D>
-cudaError_t launch_prefix_simple(const PrefixParams& p, cudaStream_t stream) {
-  const size_t smem = prefix_scan_bytes(p.num_groups);
-  if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(prefix_simple_kernel<KV, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(prefix_scan_bytes(kMaxPrefixGroups)));
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(prefix_simple_kernel<KV, D>, dim3(p.grid), dim3(kSimpleThreads), smem, stream, p);
-}
-
 // Join a row's partials: one warp per (sequence, query token, query head), a lane to D / 32
 // consecutive values.
 template <int D>
@@ -188,16 +91,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
 
 cudaError_t launch_prefix(const PrefixParams& p, const CUtensorMap& tk, const CUtensorMap& tv, KvType kv,
                           cudaStream_t stream) {
-  const bool wide = p.head_dim == 128;
-  switch (kv) {
-    case KvType::kBf16:
-      return launch_prefix_bf16(p, tk, tv, stream);
-    case KvType::kInt8:
-      return wide ? launch_prefix_simple<KvType::kInt8, 128>(p, stream) : launch_prefix_simple<KvType::kInt8, 64>(p, stream);
-    case KvType::kFp8:
-      return wide ? launch_prefix_simple<KvType::kFp8, 128>(p, stream) : launch_prefix_simple<KvType::kFp8, 64>(p, stream);
-  }
-  return cudaErrorInvalidValue;
+  return kv == KvType::kBf16 ? launch_prefix_bf16(p, tk, tv, stream) : launch_prefix_quant(p, tk, tv, kv, stream);
 }
 
 cudaError_t launch_prefix_merge(const PrefixParams& p, cudaStream_t stream) {

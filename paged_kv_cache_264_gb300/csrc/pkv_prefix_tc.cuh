@@ -14,16 +14,22 @@
 // logits pass its maximum by 2^8.  P enters the product as bf16, and the softmax sum adds the
 // same rounded weights, so that numerator and denominator agree.
 //
+// INT8 and FP8 pools: TMA brings codes and scales into a ring of their own, and a warpgroup turns
+// the codes into bf16 operand tiles, which holds every INT8 and E4M3 code exactly.  The scales stay
+// out of the operands: a token's K scale multiplies its fp32 logit, and its V scale goes into its
+// weight before that is rounded to bf16 (so the weights are rounded once, as in a bf16 pool; the
+// sum adds the unrounded ones, since the rounded ones carry the scale).
+//
 // Warps: two warpgroups of softmax (one per stream, which also load Q and write the partials),
 // one warp that fills the ring of K and V tiles by TMA (8 blocks to a tile, each wherever it lies
-// in the pool), one that issues the products.  Every wait is bounded; after one that gave up the
+// in the pool), one that issues the products, and the converting warpgroup for INT8 and FP8.  Every wait is bounded; after one that gave up the
 // CTA takes no further work, lets its copies and products land, frees its tensor memory and ends.
 //
 // A prefix ends at a block (16 tokens), not at a tile: the product over V takes only the steps of
 // 16 tokens that exist, so nothing has to be zeroed, and the logits behind them are masked.
 #pragma once
 
-#include "pkv_decode.cuh"
+#include "pkv_decode_mma.cuh"
 #include "pkv_prefix.cuh"
 #include "pkv_tcgen05.cuh"
 
@@ -31,15 +37,34 @@ namespace pkv {
 
 template <KvType KV, int D>
 struct PrefixCfg {
+  static constexpr bool kQuant = KvTraits<KV>::kQuant;
   static constexpr int kHalves = D / 64;                         // 128-byte spans of a 16-bit row
   static constexpr int kTileBytes = kPrefixTile * D * 2;         // one K, V or Q tile, 16-bit
   static constexpr int kHalfBytes = kPrefixTile * 128;           // one span of all its rows
-  static constexpr int kStages = D == 128 ? 5 : 10;
-  static constexpr int kThreads = 320;
-  static constexpr int kTmaWarp = 8, kMmaWarp = 9;
+  static constexpr int kStages = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+  // codes as they come from the pool, and beside K's the tile's K and V scales
+  static constexpr int kRawBytes = kPrefixTile * D;
+  static constexpr int kScaleBytes = 2 * kPrefixTile * 4;
+  static constexpr int kRawStages = kQuant ? (D == 128 ? 3 : 8) : 0;
+  // Scales of a tile wait in a slot until its softmax has used them.  The slot of tile n (in load
+  // order) is written again for tile n + kSlots, when K of that tile takes a ring stage; V of tile
+  // n lies at least 2 kSlots - 3 stages before it, so it has been released, and its product came
+  // after its softmax.
+  static constexpr int kSlots = kQuant ? (D == 128 ? 4 : 8) : 0;
+  static_assert(!kQuant || 2 * kSlots - 3 >= kStages, "a scale slot is free when it is written again");
+  static constexpr int kThreads = kQuant ? 512 : 384;
+  static constexpr int kTmaWarp = 8, kMmaWarp = 9, kConvertWarp = 12;
+  // Registers: the softmax threads hold a row of 128 logits; what the other warpgroups give up
+  // goes to them.  The shares' sum is checked against the kernel's own count before a launch.
+  static constexpr int kSoftmaxRegs = kQuant ? 184 : 200;
+  static constexpr int kIssueRegs = kQuant ? 64 : 96, kConvertRegs = 72;
+  static constexpr int kRegSum = 128 * (2 * kSoftmaxRegs + kIssueRegs + (kQuant ? kConvertRegs : 0));
   static constexpr int kMiscBytes = 1024;
   static constexpr int kRingOff = 2 * kTileBytes;                // Q tiles of both streams first
-  static constexpr int kSmemBytes = kMiscBytes + 1024 + kRingOff + kStages * kTileBytes;
+  static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kRawScaleOff = kRawOff + kRawStages * kRawBytes;
+  static constexpr int kSlotOff = kRawScaleOff + kRawStages * kScaleBytes;
+  static constexpr int kSmemBytes = kMiscBytes + 1024 + kSlotOff + kSlots * kScaleBytes;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(size_t(kStages) * kTileBytes >= prefix_scan_bytes(kMaxPrefixGroups), "the scan fits the ring");
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
@@ -47,12 +72,59 @@ struct PrefixCfg {
 
 // Barriers and flags of one CTA, at the start of its shared memory.
 struct PrefixSync {
-  uint64_t full[16], empty[16];        // ring stages
+  uint64_t full[16], empty[16];          // operand ring stages
+  uint64_t raw_full[8], raw_empty[8];    // code ring stages
+  uint64_t scales[8];                    // scale slots
   uint64_t q_ready[2], s_ready[2], p_ready[2], pv_done[2], o_free[2];  // per stream
   uint64_t drain;
   uint32_t tmem;
   uint32_t abort;
 };
+static_assert(sizeof(PrefixSync) <= 1008, "barriers fit their space");
+
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// The i-th load of a piece of n tiles: K and V of a tile in turn where every stream takes every
+// tile; K, K, V, V of a pair of tiles where the streams share them out.
+struct TileLoad {
+  int tile, which;
+  bool is_v;
+};
+__device__ __forceinline__ TileLoad tile_load(bool two, int n, int i) {
+  if (two) return {i >> 1, 0, bool(i & 1)};
+  const int pair = i >> 2, have = min(2, n - 2 * pair), j = i & 3;
+  const bool is_v = j >= have;
+  const int which = is_v ? j - have : j;
+  return {2 * pair + which, which, is_v};
+}
+
+// Two codes in the low bytes of each half of `v` (bits 0-7 and 16-23) -> two bf16, exactly: with
+// x = (low seven bits) - 128 (sign), 0x4300 | low bits is 128 + low bits, 0x4300 | sign bit is 128 or
+// 256, and their difference is x.
+__device__ __forceinline__ uint32_t bf16x2_from_i8(uint32_t v) {
+  const uint32_t a = (v & 0x007f007fu) | 0x43004300u, b = (v & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Four codes of a word -> four bf16 in two words.
+template <KvType KV>
+__device__ __forceinline__ void bf16x4_from_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (KV == KvType::kFp8) {
+    uint32_t a, b;
+    f16x2x2_from_e4m3x4(w, a, b);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    lo = pack_bf16x2(x.x, x.y);
+    hi = pack_bf16x2(y.x, y.y);
+  } else {
+    lo = bf16x2_from_i8(__byte_perm(w, 0u, 0x4140u));
+    hi = bf16x2_from_i8(__byte_perm(w, 0u, 0x4342u));
+  }
+}
 
 // Which of the 8 blocks of a tile exist, bit j for block j (the same on every lane of the warp);
 // lane j's id in `id`.  The blocks past the prefix are absent without being an error.
@@ -73,6 +145,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
                      const PrefixParams p) {
   using C = PrefixCfg<KV, D>;
   constexpr int S = C::kStages;
+  constexpr int kRaw = C::kQuant ? C::kRawStages : 1, kSlots = C::kQuant ? C::kSlots : 1;
   constexpr uint32_t kFull = 0xffffffffu;
   extern __shared__ unsigned char smem_raw[];
   auto* sy = reinterpret_cast<PrefixSync*>((reinterpret_cast<uintptr_t>(smem_raw) + 15) & ~uintptr_t(15));
@@ -83,9 +156,14 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(sy->full + i, 1);
+      mbar_init(sy->full + i, C::kQuant ? 128 : 1);
       mbar_init(sy->empty + i, 1);
     }
+    for (int i = 0; i < C::kRawStages; ++i) {
+      mbar_init(sy->raw_full + i, 1);
+      mbar_init(sy->raw_empty + i, 128);
+    }
+    for (int i = 0; i < C::kSlots; ++i) mbar_init(sy->scales + i, 128);
     for (int s = 0; s < 2; ++s) {
       mbar_init(sy->q_ready + s, 128);
       mbar_init(sy->s_ready + s, 1);
@@ -121,8 +199,17 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
   // two: the streams hold different rows; else they share the tiles out between them.
   auto steps_of = [&](bool two, int nrows, int n, int s) { return two ? (s == 0 || nrows > 128 ? n : 0) : (n + 1 - s) / 2; };
 
+  if (warp >= C::kTmaWarp && warp < C::kTmaWarp + 4) regs_down<C::kIssueRegs>();
   if (warp == C::kTmaWarp) {
     // ---------------------------------------------------------------- K and V tiles -> ring
+    constexpr int R = C::kQuant ? C::kRawStages : S;
+    uint64_t* full = C::kQuant ? sy->raw_full : sy->full;
+    uint64_t* empty = C::kQuant ? sy->raw_empty : sy->empty;
+    unsigned char* to = C::kQuant ? smem + C::kRawOff : ring;
+    constexpr int kStage = C::kQuant ? C::kRawBytes : C::kTileBytes;
+    constexpr int kBoxRows = C::kQuant && D == 64 ? kBlockSize / 2 : kBlockSize;  // pool rows of 128 bytes per block and span
+    constexpr int kSpans = C::kQuant ? 1 : C::kHalves;
+    constexpr int kSpanBytes = kPrefixTile / kBlockSize * kBoxRows * 128;
     fence_proxy_async_smem();  // the scan's accesses to the ring come before the copies' writes
     uint32_t it = 0;           // stages filled so far
     bool alive = true;
@@ -136,39 +223,41 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       int ids[2];
       uint32_t blocks[2];
       for (int i = 0; i < 2 * n; ++i, ++it) {
-        // order of the loads: K, V of a tile; with shared-out tiles K, K, V, V of a pair
-        int tile, which;
-        bool is_v;
-        if (two) {
-          tile = i >> 1;
-          is_v = i & 1;
-          which = 0;
-        } else {
-          const int pair = i >> 2, have = min(2, n - 2 * pair), j = i & 3;
-          is_v = j >= have;
-          which = is_v ? j - have : j;
-          tile = 2 * pair + which;
+        const TileLoad ld = tile_load(two, n, i);
+        if (!ld.is_v) {
+          const int j = ld.which;
+          int id;
+          const uint32_t have = tile_blocks(p, table, nblk, k.tile0 + ld.tile, lane, id, true);
+          if (j) { ids[1] = id; blocks[1] = have; } else { ids[0] = id; blocks[0] = have; }
         }
-        if (!is_v) blocks[which] = tile_blocks(p, table, nblk, k.tile0 + tile, lane, ids[which], true);
-        const uint32_t st = it % S;
-        if (it >= S) {
-          if (!wait_all(sy->empty + st, ((it / S) & 1) ^ 1)) {
+        const uint32_t st = it % R;
+        if (it >= R) {
+          if (!wait_all(empty + st, ((it / R) & 1) ^ 1)) {
             alive = false;
             break;
           }
         }
-        const uint32_t have = blocks[which];
+        const uint32_t have = ld.which ? blocks[1] : blocks[0];
+        const int id = ld.which ? ids[1] : ids[0];  // of block lane % 8
         if (lane == 0) {
-          if (have) mbar_arrive_expect_tx(sy->full + st, __popc(have) * (kBlockSize * D * 2));
-          else mbar_arrive(sy->full + st);
+          const int each = kSpans * kBoxRows * 128 + (C::kQuant && !ld.is_v ? 2 * kBlockSize * 4 : 0);
+          if (have) mbar_arrive_expect_tx(full + st, __popc(have) * each);
+          else mbar_arrive(full + st);
         }
         __syncwarp();
-        // lane = (span, block): one copy of 16 rows x 128 bytes each
-        const int block = lane & 7, half = lane >> 3;
-        const int id = __shfl_sync(kFull, ids[which], block);
-        if (half < C::kHalves && (have >> block & 1))
-          tma_load_2d(ring + st * C::kTileBytes + half * C::kHalfBytes + block * (kBlockSize * 128), is_v ? &tmap_v : &tmap_k,
-                      half * 64, (id * p.kv_heads + k.kvh) * kBlockSize, sy->full + st, policy);
+        // lane = (what, block): one copy each
+        const int block = lane & 7, what = lane >> 3;
+        const int tile = id * p.kv_heads + k.kvh;  // pools with tensor maps have < 2^27 tiles
+        if (have >> block & 1) {
+          if (what < kSpans) {
+            tma_load_2d(to + st * kStage + what * kSpanBytes + block * (kBoxRows * 128), ld.is_v ? &tmap_v : &tmap_k,
+                        what * 64, tile * kBoxRows, full + st, policy);
+          } else if (C::kQuant && !ld.is_v && what < 3) {
+            const float* src = (what == 1 ? p.k_scale : p.v_scale) + int64_t(tile) * kBlockSize;
+            bulk_copy_g2s(smem + C::kRawScaleOff + st * C::kScaleBytes + (what - 1) * (kPrefixTile * 4) + block * (kBlockSize * 4),
+                          src, kBlockSize * 4, full + st, policy);
+          }
+        }
       }
     }
     if (!alive) {
@@ -178,7 +267,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       }
     }
     // the copies in flight land before the CTA can end (the stages filled last)
-    for (uint32_t j = it > S ? it - S : 0; j < it; ++j) (void)mbar_wait_bounded(sy->full + j % S, (j / S) & 1);
+    for (uint32_t j = it > R ? it - R : 0; j < it; ++j) (void)mbar_wait_bounded(full + j % R, (j / R) & 1);
   } else if (warp == C::kMmaWarp) {
     // ---------------------------------------------------------------- products
     constexpr uint32_t kDescS = mma_bf16_desc(128, kPrefixTile, false), kDescO = mma_bf16_desc(128, D, true);
@@ -268,8 +357,58 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       __syncwarp();
       (void)mbar_wait_bounded(&sy->drain, 0);
     }
-  } else {
+  } else if (C::kQuant && warp >= C::kConvertWarp) {
+    // ---------------------------------------------------------------- codes -> operand tiles, a thread to a token
+    regs_down<C::kConvertRegs>();
+    const int t = threadIdx.x & 127;
+    uint32_t it = 0, tiles = 0;  // stages and tiles converted so far
+    bool alive = true;
+    for (; more && alive; more = walk_next(p, blockIdx.x, k)) {
+      const bool two = k.x.rows > 128;
+      const int n = k.tile1 - k.tile0;
+      for (int i = 0; i < 2 * n; ++i, ++it) {
+        const TileLoad ld = tile_load(two, n, i);
+        const uint32_t st = it % S, rs = it % kRaw;
+        if (!wait_all(sy->raw_full + rs, (it / kRaw) & 1) || (it >= S && !wait_all(sy->empty + st, ((it / S) & 1) ^ 1))) {
+          alive = false;
+          break;
+        }
+        const unsigned char* raw = smem + C::kRawOff + rs * C::kRawBytes;
+        unsigned char* dst = ring + st * C::kTileBytes + t * 128;
+        if (!ld.is_v) {
+          const uint32_t slot = (tiles + ld.tile) % kSlots;
+          const float* from = reinterpret_cast<const float*>(smem + C::kRawScaleOff + rs * C::kScaleBytes);
+          float* to = reinterpret_cast<float*>(smem + C::kSlotOff + slot * C::kScaleBytes);
+          to[t] = from[t];
+          to[kPrefixTile + t] = from[kPrefixTile + t];
+          mbar_arrive(sy->scales + slot);
+        }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {  // 16 codes -> 32 bytes
+          const int off = D == 128 ? t * 128 + ((c ^ (t & 7)) << 4) : swz_off_pair(t, c);
+          const uint4 w = *reinterpret_cast<const uint4*>(raw + off);
+          uint4 a, b;
+          bf16x4_from_codes<KV>(w.x, a.x, a.y);
+          bf16x4_from_codes<KV>(w.y, a.z, a.w);
+          bf16x4_from_codes<KV>(w.z, b.x, b.y);
+          bf16x4_from_codes<KV>(w.w, b.z, b.w);
+          unsigned char* half = dst + (c >> 2) * C::kHalfBytes;
+          *reinterpret_cast<uint4*>(half + ((((2 * c) & 7) ^ (t & 7)) << 4)) = a;
+          *reinterpret_cast<uint4*>(half + ((((2 * c + 1) & 7) ^ (t & 7)) << 4)) = b;
+        }
+        mbar_arrive(sy->raw_empty + rs);
+        fence_proxy_async_smem();
+        mbar_arrive(sy->full + st);
+      }
+      tiles += n;
+    }
+    if (!alive && lane == 0) {
+      *abort = 1;
+      set_error(p.err, kErrTimeout);
+    }
+  } else if (warp < C::kTmaWarp) {
     // ---------------------------------------------------------------- softmax, one thread per row
+    regs_up<C::kSoftmaxRegs>();
     const int s = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
@@ -280,12 +419,14 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);
     const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.0f ? 0u : ~0u;
     const uint64_t scale2 = f32x2(scale, scale);
-    uint32_t cnt = 0;
+    uint32_t cnt = 0, tiles = 0;  // this stream's steps and all tiles before this piece
     bool alive = true;
     for (; more && alive; more = walk_next(p, blockIdx.x, k)) {
       const bool two = k.x.rows > 128;
       const int n = k.tile1 - k.tile0;
       const int ns = steps_of(two, k.nrows, n, s);
+      const uint32_t tiles0 = tiles;
+      tiles += n;
       const int row0 = two ? s * 128 : 0;              // the stream's first row within the unit
       const int nrows = min(128, k.nrows - row0);      // its rows
       const int64_t to = k.partial + (two ? s * 128 : s * k.x.rows) + r;
@@ -318,12 +459,16 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       bool any = false;
       for (int i = 0; i < ns; ++i) {
         int id;
-        const uint32_t have = tile_blocks(p, table, nblk, k.tile0 + (two ? i : 2 * i + s), lane, id, false);
+        const int tile = two ? i : 2 * i + s;
+        const uint32_t have = tile_blocks(p, table, nblk, k.tile0 + tile, lane, id, false);
         const uint32_t c = cnt + i;
-        if (!wait_all(sy->s_ready + s, c & 1)) {
+        const uint32_t slot = C::kQuant ? (tiles0 + tile) % kSlots : 0;
+        if ((C::kQuant && !wait_all(sy->scales + slot, ((tiles0 + tile) / kSlots) & 1)) || !wait_all(sy->s_ready + s, c & 1)) {
           alive = false;
           break;
         }
+        const auto* ks = reinterpret_cast<const float4*>(smem + C::kSlotOff + slot * C::kScaleBytes);
+        const float4* vs = ks + kPrefixTile / 4;
         any |= have != 0;
         if (!idle) {
           tc_fence_after();
@@ -331,6 +476,13 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmem_ld32(s_addr + 32 * j, x + 32 * j);
           tmem_wait_ld();
+          if constexpr (C::kQuant) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float4 f = ks[j];
+              x[4 * j] *= f.x; x[4 * j + 1] *= f.y; x[4 * j + 2] *= f.z; x[4 * j + 3] *= f.w;
+            }
+          }
           if (have != 0xffu) {
 #pragma unroll
             for (int j = 0; j < 128; ++j)
@@ -365,8 +517,16 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
           for (int j = 0; j < 64; ++j) {
             float a, b;
             f32x2_parts(fma2(f32x2(x[2 * j], x[2 * j + 1]), scale2, neg), a, b);
-            w[j] = pack_bf16x2(fast_exp2(a), fast_exp2(b));
-            sum[j & 1] = add2(sum[j & 1], f32x2(bf16lo(w[j]), bf16hi(w[j])));
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            if constexpr (C::kQuant) {
+              sum[j & 1] = add2(sum[j & 1], f32x2(a, b));
+              const float2 f = reinterpret_cast<const float2*>(vs)[j];
+              w[j] = pack_bf16x2(a * f.x, b * f.y);
+            } else {
+              w[j] = pack_bf16x2(a, b);
+              sum[j & 1] = add2(sum[j & 1], f32x2(bf16lo(w[j]), bf16hi(w[j])));
+            }
           }
           float a, b;
           f32x2_parts(add2(sum[0], sum[1]), a, b);
@@ -427,8 +587,12 @@ cudaError_t launch_prefix_tc(const PrefixParams& p, const CUtensorMap& tk, const
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_done[dev].load(std::memory_order_relaxed)) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    cudaFuncAttributes a;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kern);
     if (e != cudaSuccess) return e;
+    // the warpgroups' register shares come out of what the CTA is launched with
+    if (a.numRegs * C::kThreads < C::kRegSum) return cudaErrorInvalidConfiguration;
     if (dev >= 0 && dev < 64) attr_done[dev].store(true, std::memory_order_relaxed);
   }
   return launch_pdl(kern, dim3(p.grid), dim3(C::kThreads), C::kSmemBytes, stream, tk, tv, p);
