@@ -126,17 +126,15 @@ __device__ __forceinline__ void bf16x4_from_codes(uint32_t w, uint32_t& lo, uint
   }
 }
 
-// Which of the 8 blocks of a tile exist, bit j for block j (the same on every lane of the warp);
-// lane j's id in `id`.  The blocks past the prefix are absent without being an error.
-__device__ __forceinline__ uint32_t tile_blocks(const PrefixParams& p, const int32_t* table, int nblk, int tile, int lane,
-                                                int& id, bool flag) {
-  id = -1;
+// Block id of lane % 8 of a tile; -1 past the prefix.  Roles ask for a tile's ids one step ahead
+// of their use: a table entry is a global-memory round trip away.
+__device__ __forceinline__ int tile_id(const int32_t* table, int nblk, int tile, int lane) {
   const int j = tile * (kPrefixTile / kBlockSize) + (lane & 7);
-  const bool inside = j < nblk;
-  if (inside) id = __ldg(table + j);
-  const bool ok = inside && id >= 0 && id < p.num_blocks;
-  if (flag && inside && !ok && lane < 8) set_error(p.err, kErrBlockId);
-  return __ballot_sync(0xffffffffu, ok) & 0xffu;
+  return j < nblk ? __ldg(table + j) : -1;
+}
+// Which of the tile's 8 blocks exist, bit j for block j (the same on every lane of the warp).
+__device__ __forceinline__ uint32_t tile_blocks(const PrefixParams& p, int id) {
+  return __ballot_sync(0xffffffffu, id >= 0 && id < p.num_blocks) & 0xffu;
 }
 
 template <KvType KV, int D>
@@ -220,15 +218,17 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       // tiles read again by the group's other units stay in L2; others are read once
       const uint64_t policy = k.x.units > 1 ? l2_evict_last_policy() : l2_evict_first_policy();
       const int n = k.tile1 - k.tile0;
-      int ids[2];
+      int ids[2], next = tile_id(table, nblk, k.tile0, lane);
       uint32_t blocks[2];
       for (int i = 0; i < 2 * n; ++i, ++it) {
         const TileLoad ld = tile_load(two, n, i);
         if (!ld.is_v) {
-          const int j = ld.which;
-          int id;
-          const uint32_t have = tile_blocks(p, table, nblk, k.tile0 + ld.tile, lane, id, true);
-          if (j) { ids[1] = id; blocks[1] = have; } else { ids[0] = id; blocks[0] = have; }
+          const int id = next;
+          const uint32_t have = tile_blocks(p, id);
+          const int j = (k.tile0 + ld.tile) * (kPrefixTile / kBlockSize) + lane;
+          if (lane < 8 && j < nblk && !(have >> lane & 1)) set_error(p.err, kErrBlockId);
+          if (ld.which) { ids[1] = id; blocks[1] = have; } else { ids[0] = id; blocks[0] = have; }
+          if (ld.tile + 1 < n) next = tile_id(table, nblk, k.tile0 + ld.tile + 1, lane);
         }
         const uint32_t st = it % R;
         if (it >= R) {
@@ -270,8 +270,10 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     for (uint32_t j = it > R ? it - R : 0; j < it; ++j) (void)mbar_wait_bounded(full + j % R, (j / R) & 1);
   } else if (warp == C::kMmaWarp) {
     // ---------------------------------------------------------------- products
+    // The whole warp runs this with warp-uniform values; one elected lane issues.
     constexpr uint32_t kDescS = mma_bf16_desc(128, kPrefixTile, false), kDescO = mma_bf16_desc(128, D, true);
-    const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
+    const uint64_t q_desc = smem_operand(smem_addr(smem), 16, 1024), k_desc = smem_operand(smem_addr(ring), 16, 1024);
+    const uint64_t v_desc = smem_operand(smem_addr(ring), C::kHalfBytes, 1024);
     uint32_t it = 0;                  // ring stages before this piece
     uint32_t cnt[2] = {0, 0};         // steps of each stream before this piece
     uint32_t seg[2] = {0, 0};         // pieces that had work for the stream
@@ -288,58 +290,70 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
         if (!alive) return;
         alive = wait_all(bar, parity);
       };
-      auto k_index = [&](int i, int s) { return two ? 2 * i : 4 * i + s; };
-      auto v_index = [&](int i, int s) { return two ? 2 * i + 1 : 4 * i + min(2, n - 2 * i) + s; };
       // S of stream s, step i
-      auto issue_s = [&](int i, int s) {
-        const uint32_t c = cnt[s] + i, idx = it + k_index(i, s);
-        wait(sy->full + idx % S, (idx / S) & 1);
+      auto issue_s = [&](int i, auto s_c) {
+        constexpr int s = decltype(s_c)::value;
+        const uint32_t c = cnt[s] + i, idx = it + (two ? 2 * i : 4 * i + s);
+        const uint32_t st = idx % S;
+        wait(sy->full + st, (idx / S) & 1);
         if (i == 0) wait(sy->q_ready + s, seg[s] & 1);
         if (c > 0) wait(sy->pv_done + s, (c - 1) & 1);  // P lies over S until its product is done
         if (!alive) return;
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t qd = smem_operand(q_addr + s * C::kTileBytes, 16, 1024);
-          const uint64_t kd = smem_operand(ring_addr + (idx % S) * C::kTileBytes, 16, 1024);
+        tc_fence_after();
+        const uint64_t qd = q_desc + s * (C::kTileBytes >> 4), kd = k_desc + st * (C::kTileBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
-            const uint32_t o = ((j >> 2) * C::kHalfBytes + (j & 3) * 32) >> 4;
-            tc_mma_ss(tmem + s * 128, qd + o, kd + o, kDescS, j > 0);
+            constexpr auto at = [](int j) { return uint64_t(((j >> 2) * C::kHalfBytes + (j & 3) * 32) >> 4); };
+            tc_mma_ss(tmem + s * 128, qd + at(j), kd + at(j), kDescS, j > 0);
           }
           tc_commit(sy->s_ready + s);
-          if (!two || s == last) tc_commit(sy->empty + idx % S);
+          if (!two || s == last) tc_commit(sy->empty + st);
         }
         __syncwarp();
       };
-      for (int s = 0; s < 2; ++s)
-        if (ns[s] > 0) issue_s(0, s);
-      for (int i = 0; i < ns[0] && alive; ++i) {
-        for (int s = 0; s < 2 && alive; ++s) {
-          if (i >= ns[s]) continue;
-          int id;
-          const uint32_t have = tile_blocks(p, table, nblk, k.tile0 + (two ? i : 2 * i + s), lane, id, false);
-          const uint32_t c = cnt[s] + i, idx = it + v_index(i, s);
-          wait(sy->p_ready + s, c & 1);
-          wait(sy->full + idx % S, (idx / S) & 1);
-          if (i == 0 && seg[s] > 0) wait(sy->o_free + s, (seg[s] - 1) & 1);
-          if (!alive) break;
-          if (lane == 0) {
-            tc_fence_after();
-            const uint64_t vd = smem_operand(ring_addr + (idx % S) * C::kTileBytes, C::kHalfBytes, 1024);
-            bool acc = !fresh[s];
+      int next[2];
 #pragma unroll
-            for (int j = 0; j < kPrefixTile / 16; ++j)
-              if (have >> j & 1) {
-                tc_mma_ts(tmem + 256 + s * D, tmem + s * 128 + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, acc);
-                acc = true;
-              }
+      for (int s = 0; s < 2; ++s) next[s] = ns[s] > 0 ? tile_id(table, nblk, k.tile0 + (two ? 0 : s), lane) : -1;
+      static_for<2>([&](auto s_c) {
+        if (ns[decltype(s_c)::value] > 0) issue_s(0, s_c);
+      });
+      for (int i = 0; i < ns[0] && alive; ++i) {
+        static_for<2>([&](auto s_c) {
+          constexpr int s = decltype(s_c)::value;
+          if (i >= ns[s] || !alive) return;
+          const uint32_t have = tile_blocks(p, next[s]);
+          if (i + 1 < ns[s]) next[s] = tile_id(table, nblk, k.tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
+          const uint32_t c = cnt[s] + i, idx = it + (two ? 2 * i + 1 : 4 * i + min(2, n - 2 * i) + s);
+          const uint32_t st = idx % S;
+          wait(sy->full + st, (idx / S) & 1);
+          if (i == 0 && seg[s] > 0) wait(sy->o_free + s, (seg[s] - 1) & 1);
+          wait(sy->p_ready + s, c & 1);
+          if (!alive) return;
+          tc_fence_after();
+          const uint64_t vd = v_desc + st * (C::kTileBytes >> 4);
+          constexpr uint32_t o = 256 + s * D, pc = s * 128;
+          if (elect_one()) {
+            if (have == 0xffu) {
+              tc_mma_ts(tmem + o, tmem + pc, vd, kDescO, !fresh[s]);
+#pragma unroll
+              for (int j = 1; j < kPrefixTile / 16; ++j)
+                tc_mma_ts(tmem + o, tmem + pc + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, true);
+            } else {  // the prefix ends in this tile, or a block is missing
+              bool acc = !fresh[s];
+              for (int j = 0; j < kPrefixTile / 16; ++j)
+                if (have >> j & 1) {
+                  tc_mma_ts(tmem + o, tmem + pc + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, acc);
+                  acc = true;
+                }
+            }
             tc_commit(sy->pv_done + s);
-            if (!two || s == last) tc_commit(sy->empty + idx % S);
+            if (!two || s == last) tc_commit(sy->empty + st);
           }
           if (have) fresh[s] = false;
           __syncwarp();
-          if (i + 1 < ns[s]) issue_s(i + 1, s);
-        }
+          if (i + 1 < ns[s]) issue_s(i + 1, s_c);
+        });
       }
       it += 2 * n;
       for (int s = 0; s < 2; ++s)
@@ -421,7 +435,21 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     const uint64_t scale2 = f32x2(scale, scale);
     uint32_t cnt = 0, tiles = 0;  // this stream's steps and all tiles before this piece
     bool alive = true;
-    for (; more && alive; more = walk_next(p, blockIdx.x, k)) {
+    // this thread's row of Q of the piece at k, ahead of its use
+    uint4 w[D / 8];
+    auto load_q = [&]() {
+      const int row = (k.x.rows > 128 ? s * 128 : 0) + r;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < k.nrows) {
+        const auto* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                       prefix_q_row(p, k.x, k.kvh, k.row0 + row) * D);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) w[c] = __ldg(q + c);
+      }
+    };
+    if (more) load_q();
+    while (more) {
       const bool two = k.x.rows > 128;
       const int n = k.tile1 - k.tile0;
       const int ns = steps_of(two, k.nrows, n, s);
@@ -429,23 +457,17 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       tiles += n;
       const int row0 = two ? s * 128 : 0;              // the stream's first row within the unit
       const int nrows = min(128, k.nrows - row0);      // its rows
-      const int64_t to = k.partial + (two ? s * 128 : s * k.x.rows) + r;
+      const int64_t to = k.partial + (two ? s * 128 : s * k.x.rows);
       if (ns == 0) {
-        if (r < nrows) p.ml[to] = make_float2(kMaxFloor, 0.0f);  // no tile of its own: weighs nothing
+        if (r < nrows) p.ml[to + r] = make_float2(kMaxFloor, 0.0f);  // no tile of its own: weighs nothing
+        more = walk_next(p, blockIdx.x, k);
+        if (more) load_q();
         continue;
       }
-      const int prefix = __ldg(p.prefix_lens + k.g), nblk = prefix / kBlockSize;
+      const int tile0 = k.tile0, nblk = __ldg(p.prefix_lens + k.g) / kBlockSize;
       const int32_t* table = p.block_tables + int64_t(k.x.first_seq) * p.max_blocks_per_seq;
+      int next = tile_id(table, nblk, tile0 + (two ? 0 : s), lane);
       {  // Q -> shared memory, swizzled; its last reader was the last step's S, which this thread saw
-        uint4 w[D / 8];
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < nrows) {
-          const auto* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                         prefix_q_row(p, k.x, k.kvh, k.row0 + row0 + r) * D);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) w[c] = __ldg(q + c);
-        }
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           w[c] = make_uint4((w[c].x ^ flip) & keep, (w[c].y ^ flip) & keep, (w[c].z ^ flip) & keep, (w[c].w ^ flip) & keep);
@@ -458,9 +480,9 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       float m = kMaxFloor, l = 0.0f;
       bool any = false;
       for (int i = 0; i < ns; ++i) {
-        int id;
         const int tile = two ? i : 2 * i + s;
-        const uint32_t have = tile_blocks(p, table, nblk, k.tile0 + tile, lane, id, false);
+        const uint32_t have = tile_blocks(p, next);
+        if (i + 1 < ns) next = tile_id(table, nblk, tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
         const uint32_t c = cnt + i;
         const uint32_t slot = C::kQuant ? (tiles0 + tile) % kSlots : 0;
         if ((C::kQuant && !wait_all(sy->scales + slot, ((tiles0 + tile) / kSlots) & 1)) || !wait_all(sy->s_ready + s, c & 1)) {
@@ -472,26 +494,37 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
         any |= have != 0;
         if (!idle) {
           tc_fence_after();
-          float x[128];
+          // 64 columns at a time: the upper half for its maximum alone, then the lower half, which
+          // stays in registers; its weights go over its own columns, and the upper half is read
+          // again.  Holding all 128 columns instead spills.
+          float x[64];
+          auto fetch = [&](int c0) {
+            tmem_ld32(s_addr + c0, x);
+            tmem_ld32(s_addr + c0 + 32, x + 32);
+            tmem_wait_ld();
+            if constexpr (C::kQuant) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tmem_ld32(s_addr + 32 * j, x + 32 * j);
-          tmem_wait_ld();
-          if constexpr (C::kQuant) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float4 f = ks[j];
-              x[4 * j] *= f.x; x[4 * j + 1] *= f.y; x[4 * j + 2] *= f.z; x[4 * j + 3] *= f.w;
+              for (int j = 0; j < 16; ++j) {
+                const float4 f = ks[c0 / 4 + j];
+                x[4 * j] *= f.x; x[4 * j + 1] *= f.y; x[4 * j + 2] *= f.z; x[4 * j + 3] *= f.w;
+              }
             }
-          }
-          if (have != 0xffu) {
+            if (have != 0xffu) {
 #pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (!(have >> (j / 16) & 1)) x[j] = -INFINITY;
-          }
-          float mx[4] = {x[0], x[1], x[2], x[3]};
+              for (int j = 0; j < 64; ++j)
+                if (!(have >> ((c0 + j) / 16) & 1)) x[j] = -INFINITY;
+            }
+          };
+          auto largest = [&]() {
+            float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int j = 4; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
-          const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+            for (int j = 4; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+            return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          };
+          fetch(64);
+          float bm = largest();
+          fetch(0);
+          bm = fmaxf(bm, largest()) * scale;
           const bool grow = bm > m + kMaxSlack;
           if (__any_sync(kFull, grow)) {
             const float mu = grow ? bm : m, f = fast_exp2(m - mu);
@@ -500,39 +533,43 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
             if (i > 0) {
               // the last product into O is done: S was issued after it
 #pragma unroll 1
-              for (int j = 0; j < D / 32; ++j) {
-                float o[32];
-                tmem_ld32(o_addr + 32 * j, o);
+              for (int j = 0; j < D / 16; ++j) {
+                float o[16];
+                tmem_ld16(o_addr + 16 * j, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= f;
-                tmem_st32(o_addr + 32 * j, reinterpret_cast<const uint32_t*>(o));
+                for (int e = 0; e < 16; ++e) o[e] *= f;
+                tmem_st16(o_addr + 16 * j, o);
               }
             }
           }
           const uint64_t neg = f32x2(-m, -m);
           uint64_t sum[2] = {0, 0};
-          uint32_t w[64];
+          auto weights = [&](int c0) {
+            uint32_t pw[32];
 #pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            float a, b;
-            f32x2_parts(fma2(f32x2(x[2 * j], x[2 * j + 1]), scale2, neg), a, b);
-            a = fast_exp2(a);
-            b = fast_exp2(b);
-            if constexpr (C::kQuant) {
-              sum[j & 1] = add2(sum[j & 1], f32x2(a, b));
-              const float2 f = reinterpret_cast<const float2*>(vs)[j];
-              w[j] = pack_bf16x2(a * f.x, b * f.y);
-            } else {
-              w[j] = pack_bf16x2(a, b);
-              sum[j & 1] = add2(sum[j & 1], f32x2(bf16lo(w[j]), bf16hi(w[j])));
+            for (int j = 0; j < 32; ++j) {
+              float a, b;
+              f32x2_parts(fma2(f32x2(x[2 * j], x[2 * j + 1]), scale2, neg), a, b);
+              a = fast_exp2(a);
+              b = fast_exp2(b);
+              if constexpr (C::kQuant) {
+                sum[j & 1] = add2(sum[j & 1], f32x2(a, b));
+                const float2 f = reinterpret_cast<const float2*>(vs)[c0 / 2 + j];
+                pw[j] = pack_bf16x2(a * f.x, b * f.y);
+              } else {
+                pw[j] = pack_bf16x2(a, b);
+                sum[j & 1] = add2(sum[j & 1], f32x2(bf16lo(pw[j]), bf16hi(pw[j])));
+              }
             }
-          }
+            tmem_st32(s_addr + c0 / 2, pw);
+          };
+          weights(0);
+          fetch(64);
+          weights(64);
           float a, b;
           f32x2_parts(add2(sum[0], sum[1]), a, b);
           l += a + b;
-          tmem_st32(s_addr, w);
-          tmem_st32(s_addr + 32, w + 32);
           tmem_wait_st();
           tc_fence_before();
         }
@@ -540,27 +577,45 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       }
       if (!alive) break;
       cnt += ns;
-      // ---- the piece's partial
+      more = walk_next(p, blockIdx.x, k);
+      if (more) load_q();  // on its way while this piece's partial is written
+      // ---- the piece's partial.  A thread holds a row, so its stores would touch 32 lines at a
+      // time; the warp turns its 32 rows through its part of the Q tile (free: every S is done),
+      // 64 values of each row at a time, and stores whole lines.
       if (!wait_all(sy->pv_done + s, (cnt - 1) & 1)) {
         alive = false;
         break;
       }
       if (!idle) {
         tc_fence_after();
-        float* dst = p.acc + to * D;
+        unsigned char* turn = qt + (warp & 3) * (C::kTileBytes / 4);
+        constexpr int kCols = C::kTileBytes / 4 / 32 / 4;  // columns per round: 64 (D = 128) or 32
+        constexpr int kChunks = kCols / 4;                 // 16-byte chunks of a row in a round
+        const int wrow = (warp & 3) * 32, live = min(32, nrows - wrow);
+        float* dst = p.acc + (to + wrow) * D;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += kCols) {
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          float o[32];
-          tmem_ld32(o_addr + 32 * j, o);
-          tmem_wait_ld();
-          if (r < nrows) {
+          for (int h = 0; h < kCols; h += 32) {
+            float o[32];
+            tmem_ld32(o_addr + c0 + h, o);
+            tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + 32 * j + e) =
-                  any ? make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(turn + lane * (kCols * 4) + (((h / 4 + e) ^ (lane % kChunks)) << 4)) =
+                  any ? make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           }
+          __syncwarp();
+#pragma unroll 4
+          for (int j = 0; j < kChunks; ++j) {
+            const int row = j * (32 / kChunks) + lane / kChunks, chunk = lane % kChunks;
+            if (row < live)
+              *reinterpret_cast<float4*>(dst + row * D + c0 + chunk * 4) =
+                  *reinterpret_cast<const float4*>(turn + row * (kCols * 4) + ((chunk ^ (row % kChunks)) << 4));
+          }
+          __syncwarp();
         }
-        if (r < nrows) p.ml[to] = make_float2(m, l);
+        if (r < nrows) p.ml[to + r] = make_float2(m, l);
         tc_fence_before();
       }
       mbar_arrive(sy->o_free + s);
