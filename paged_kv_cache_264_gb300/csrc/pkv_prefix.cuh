@@ -115,13 +115,9 @@ struct PrefixWalk {
   int64_t w, w_end;
 };
 
-__device__ __forceinline__ void walk_place(const PrefixParams& p, PrefixWalk& k, int cta) {
-  const int64_t in_group = k.w - k.x.w_base;
-  const int u = int(in_group / k.x.tiles);  // kv head * units + unit
-  k.tile0 = int(in_group - int64_t(u) * k.x.tiles);
+// The rest of a piece that starts at tile k.tile0 of (k.kvh, k.unit).
+__device__ __forceinline__ void walk_place(PrefixWalk& k, int cta) {
   k.tile1 = int(min(int64_t(k.x.tiles), k.tile0 + (k.w_end - k.w)));
-  k.kvh = u / k.x.units;
-  k.unit = u - k.kvh * k.x.units;
   k.row0 = k.unit * kPrefixRows;
   k.nrows = min(kPrefixRows, k.x.rows - k.row0);
   k.partial = k.x.row_base + int64_t(k.kvh) * partial_rows(k.x.rows) + k.row0 + int64_t(cta) * kPrefixRows;
@@ -143,23 +139,35 @@ __device__ __forceinline__ bool walk_begin(const PrefixParams& p, const PrefixSc
   prefix_group(p, lo, k.x);
   k.x.w_base = sc.base[lo].x;
   k.x.row_base = sc.base[lo].y;
-  walk_place(p, k, cta);
+  const int64_t in_group = k.w - k.x.w_base;
+  const int u = int(in_group / k.x.tiles);  // kv head * units + unit
+  k.tile0 = int(in_group - int64_t(u) * k.x.tiles);
+  k.kvh = u / k.x.units;
+  k.unit = u - k.kvh * k.x.units;
+  walk_place(k, cta);
   return true;
 }
 
 __device__ __forceinline__ bool walk_next(const PrefixParams& p, int cta, PrefixWalk& k) {
   k.w += k.tile1 - k.tile0;
   if (k.w >= k.w_end) return false;
-  int64_t group_end = k.x.w_base + int64_t(k.x.units) * p.kv_heads * k.x.tiles;
-  while (k.w >= group_end) {  // past this group and any without work
-    const int64_t rows = k.x.row_base + partial_rows(k.x.rows) * p.kv_heads;
-    ++k.g;
-    prefix_group(p, k.g, k.x);
-    k.x.w_base = group_end;
-    k.x.row_base = rows;
-    group_end += int64_t(k.x.units) * p.kv_heads * k.x.tiles;
+  // this CTA's stretch goes on, so the piece ended with its unit's last tile
+  k.tile0 = 0;
+  if (++k.unit == k.x.units) {
+    k.unit = 0;
+    if (++k.kvh == p.kv_heads) {
+      k.kvh = 0;
+      do {  // the next group that has work
+        const int64_t w = k.x.w_base + int64_t(k.x.units) * p.kv_heads * k.x.tiles;
+        const int64_t rows = k.x.row_base + partial_rows(k.x.rows) * p.kv_heads;
+        ++k.g;
+        prefix_group(p, k.g, k.x);
+        k.x.w_base = w;
+        k.x.row_base = rows;
+      } while (k.x.units == 0 || k.x.tiles == 0);
+    }
   }
-  walk_place(p, k, cta);
+  walk_place(k, cta);
   return true;
 }
 
@@ -170,11 +178,12 @@ __device__ __forceinline__ int64_t prefix_q_row(const PrefixParams& p, const Pre
   return (int64_t(x.first_seq) * p.num_queries + tok) * p.num_q_heads + int64_t(kvh) * p.group + head;
 }
 
-// What the suffix and merge passes need of this CTA's share of the sequences (all NT threads).
-template <int NT>
-__device__ __forceinline__ void prefix_describe(const PrefixParams& p, const PrefixScan& sc, int64_t total) {
+// What the suffix and merge passes need of this CTA's share of the sequences; run by `warps` of
+// its warps, this one the `warp`-th of them.
+__device__ __forceinline__ void prefix_describe(const PrefixParams& p, const PrefixScan& sc, int64_t total, int warp,
+                                                int warps) {
   const int lane = threadIdx.x & 31;
-  for (int b = blockIdx.x * (NT / 32) + (threadIdx.x >> 5); b < p.num_seqs; b += gridDim.x * (NT / 32)) {
+  for (int b = blockIdx.x * warps + warp; b < p.num_seqs; b += gridDim.x * warps) {
     const int T = __ldg(p.context_lens + b);
     PrefixSeq d{};
     PrefixGroup x{};
@@ -210,7 +219,7 @@ __device__ __forceinline__ void prefix_describe(const PrefixParams& p, const Pre
       p.suffix_lens[b] = d.suffix_len;
     }
   }
-  if (total < 0 && blockIdx.x == 0 && threadIdx.x == 0) set_error(p.err, kErrPrefix);
+  if (total < 0 && blockIdx.x == 0 && warp == 0 && lane == 0) set_error(p.err, kErrPrefix);
 }
 
 }  // namespace pkv

@@ -22,7 +22,8 @@
 //
 // Warps: two warpgroups of softmax (one per stream, which also load Q and write the partials),
 // one warp that fills the ring of K and V tiles by TMA (8 blocks to a tile, each wherever it lies
-// in the pool), one that issues the products, and the converting warpgroup for INT8 and FP8.  Every wait is bounded; after one that gave up the
+// in the pool), one warp per stream that issues its products (one for both let a stream's waits
+// hold up the other's products), and the converting warpgroup for INT8 and FP8.  Every wait is bounded; after one that gave up the
 // CTA takes no further work, lets its copies and products land, frees its tensor memory and ends.
 //
 // A prefix ends at a block (16 tokens), not at a tile: the product over V takes only the steps of
@@ -53,7 +54,7 @@ struct PrefixCfg {
   static constexpr int kSlots = kQuant ? (D == 128 ? 4 : 8) : 0;
   static_assert(!kQuant || 2 * kSlots - 3 >= kStages, "a scale slot is free when it is written again");
   static constexpr int kThreads = kQuant ? 512 : 384;
-  static constexpr int kTmaWarp = 8, kMmaWarp = 9, kConvertWarp = 12;
+  static constexpr int kTmaWarp = 8, kMmaWarp = 9, kDescribeWarp = 11, kConvertWarp = 12;  // 9 and 10: one per stream
   // Registers: the softmax threads hold a row of 128 logits; what the other warpgroups give up
   // goes to them.  The shares' sum is checked against the kernel's own count before a launch.
   static constexpr int kSoftmaxRegs = kQuant ? 184 : 200;
@@ -76,11 +77,13 @@ struct PrefixSync {
   uint64_t raw_full[8], raw_empty[8];    // code ring stages
   uint64_t scales[8];                    // scale slots
   uint64_t q_ready[2], s_ready[2], p_ready[2], pv_done[2], o_free[2];  // per stream
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem;
   uint32_t abort;
+  longlong2 base[25];                    // scan of a call of up to 24 groups
 };
 static_assert(sizeof(PrefixSync) <= 1008, "barriers fit their space");
+constexpr int kFewGroups = 24;
 
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(sy->full + i, C::kQuant ? 128 : 1);
-      mbar_init(sy->empty + i, 1);
+      mbar_init(sy->empty + i, 2);
     }
     for (int i = 0; i < C::kRawStages; ++i) {
       mbar_init(sy->raw_full + i, 1);
@@ -168,8 +171,8 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       mbar_init(sy->p_ready + s, 128);
       mbar_init(sy->pv_done + s, 1);
       mbar_init(sy->o_free + s, 128);
+      mbar_init(sy->drain + s, 1);
     }
-    mbar_init(&sy->drain, 1);
     sy->abort = 0;
     fence_barrier_init();
     prefetch_tensor_map(&tmap_k);
@@ -177,9 +180,12 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
   }
   if (warp == C::kMmaWarp) tmem_alloc(&sy->tmem, C::kTmemCols);
   griddep_wait();  // inputs may come from the previous kernel in the stream
-  PrefixScan sc{reinterpret_cast<longlong2*>(ring) + 32, reinterpret_cast<longlong2*>(ring)};
+  // The scan of a few groups stays, and a spare warp describes the sequences beside the work; that
+  // of many lies where the ring will be, and is used up first.
+  const bool few = p.num_groups <= kFewGroups;
+  PrefixScan sc{few ? sy->base : reinterpret_cast<longlong2*>(ring) + 32, reinterpret_cast<longlong2*>(ring)};
   const int64_t total = prefix_scan<C::kThreads>(p, sc);
-  prefix_describe<C::kThreads>(p, sc, total);
+  if (!few) prefix_describe(p, sc, total, warp, C::kThreads / 32);
   PrefixWalk k;
   bool more = total > 0 && walk_begin(p, sc, total, blockIdx.x, k);
   tc_fence_before();
@@ -268,109 +274,100 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     }
     // the copies in flight land before the CTA can end (the stages filled last)
     for (uint32_t j = it > R ? it - R : 0; j < it; ++j) (void)mbar_wait_bounded(full + j % R, (j / R) & 1);
-  } else if (warp == C::kMmaWarp) {
-    // ---------------------------------------------------------------- products
+  } else if (warp == C::kMmaWarp || warp == C::kMmaWarp + 1) {
+    // ---------------------------------------------------------------- products of stream s
     // The whole warp runs this with warp-uniform values; one elected lane issues.
     constexpr uint32_t kDescS = mma_bf16_desc(128, kPrefixTile, false), kDescO = mma_bf16_desc(128, D, true);
-    const uint64_t q_desc = smem_operand(smem_addr(smem), 16, 1024), k_desc = smem_operand(smem_addr(ring), 16, 1024);
-    const uint64_t v_desc = smem_operand(smem_addr(ring), C::kHalfBytes, 1024);
-    uint32_t it = 0;                  // ring stages before this piece
-    uint32_t cnt[2] = {0, 0};         // steps of each stream before this piece
-    uint32_t seg[2] = {0, 0};         // pieces that had work for the stream
+    const int s = warp - C::kMmaWarp;
+    const uint64_t q_desc = smem_operand(smem_addr(smem) + s * C::kTileBytes, 16, 1024);
+    const uint64_t k_desc = smem_operand(smem_addr(ring), 16, 1024), v_desc = smem_operand(smem_addr(ring), C::kHalfBytes, 1024);
+    const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * D;
+    uint32_t it = 0;   // ring stages before this piece
+    uint32_t cnt = 0;  // steps of the stream before this piece
+    uint32_t seg = 0;  // pieces that had work for it
     bool alive = true;
     for (; more && alive; more = walk_next(p, blockIdx.x, k)) {
       const bool two = k.x.rows > 128;
+      const int n = k.tile1 - k.tile0, ns = steps_of(two, k.nrows, n, s);
+      const bool shared = two && k.nrows > 128;  // both streams use every tile: a stage is free after both
+      const uint32_t it0 = it;
+      it += 2 * n;
+      if (ns == 0) continue;
       const int nblk = __ldg(p.prefix_lens + k.g) / kBlockSize;
       const int32_t* table = p.block_tables + int64_t(k.x.first_seq) * p.max_blocks_per_seq;
-      const int n = k.tile1 - k.tile0;
-      const int ns[2] = {steps_of(two, k.nrows, n, 0), steps_of(two, k.nrows, n, 1)};
-      const int last = ns[1] > 0 ? 1 : 0;  // the stream that uses a shared tile last
-      bool fresh[2] = {true, true};        // O holds nothing of this piece yet
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!alive) return;
-        alive = wait_all(bar, parity);
+      int next = tile_id(table, nblk, k.tile0 + (two ? 0 : s), lane);
+      auto release = [&](uint32_t st) {  // once the products so far are done
+        tc_commit(sy->empty + st);
+        if (!shared) mbar_arrive(sy->empty + st);
       };
-      // S of stream s, step i
-      auto issue_s = [&](int i, auto s_c) {
-        constexpr int s = decltype(s_c)::value;
-        const uint32_t c = cnt[s] + i, idx = it + (two ? 2 * i : 4 * i + s);
-        const uint32_t st = idx % S;
-        wait(sy->full + st, (idx / S) & 1);
-        if (i == 0) wait(sy->q_ready + s, seg[s] & 1);
-        if (c > 0) wait(sy->pv_done + s, (c - 1) & 1);  // P lies over S until its product is done
-        if (!alive) return;
+      // S of step i
+      auto issue_s = [&](int i) {
+        const uint32_t idx = it0 + (two ? 2 * i : 4 * i + s), st = idx % S;
+        if (!wait_all(sy->full + st, (idx / S) & 1) || (i == 0 && !wait_all(sy->q_ready + s, seg & 1))) return false;
+        // P lies over S until its product is done
+        if (cnt + i > 0 && !wait_all(sy->pv_done + s, (cnt + i - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t qd = q_desc + s * (C::kTileBytes >> 4), kd = k_desc + st * (C::kTileBytes >> 4);
+        const uint64_t kd = k_desc + st * (C::kTileBytes >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
-            constexpr auto at = [](int j) { return uint64_t(((j >> 2) * C::kHalfBytes + (j & 3) * 32) >> 4); };
-            tc_mma_ss(tmem + s * 128, qd + at(j), kd + at(j), kDescS, j > 0);
+            const uint64_t at = ((j >> 2) * C::kHalfBytes + (j & 3) * 32) >> 4;
+            tc_mma_ss(t_s, q_desc + at, kd + at, kDescS, j > 0);
           }
           tc_commit(sy->s_ready + s);
-          if (!two || s == last) tc_commit(sy->empty + st);
+          release(st);
         }
         __syncwarp();
+        return true;
       };
-      int next[2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) next[s] = ns[s] > 0 ? tile_id(table, nblk, k.tile0 + (two ? 0 : s), lane) : -1;
-      static_for<2>([&](auto s_c) {
-        if (ns[decltype(s_c)::value] > 0) issue_s(0, s_c);
-      });
-      for (int i = 0; i < ns[0] && alive; ++i) {
-        static_for<2>([&](auto s_c) {
-          constexpr int s = decltype(s_c)::value;
-          if (i >= ns[s] || !alive) return;
-          const uint32_t have = tile_blocks(p, next[s]);
-          if (i + 1 < ns[s]) next[s] = tile_id(table, nblk, k.tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
-          const uint32_t c = cnt[s] + i, idx = it + (two ? 2 * i + 1 : 4 * i + min(2, n - 2 * i) + s);
-          const uint32_t st = idx % S;
-          wait(sy->full + st, (idx / S) & 1);
-          if (i == 0 && seg[s] > 0) wait(sy->o_free + s, (seg[s] - 1) & 1);
-          wait(sy->p_ready + s, c & 1);
-          if (!alive) return;
-          tc_fence_after();
-          const uint64_t vd = v_desc + st * (C::kTileBytes >> 4);
-          constexpr uint32_t o = 256 + s * D, pc = s * 128;
-          if (elect_one()) {
-            if (have == 0xffu) {
-              tc_mma_ts(tmem + o, tmem + pc, vd, kDescO, !fresh[s]);
-#pragma unroll
-              for (int j = 1; j < kPrefixTile / 16; ++j)
-                tc_mma_ts(tmem + o, tmem + pc + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, true);
-            } else {  // the prefix ends in this tile, or a block is missing
-              bool acc = !fresh[s];
-              for (int j = 0; j < kPrefixTile / 16; ++j)
-                if (have >> j & 1) {
-                  tc_mma_ts(tmem + o, tmem + pc + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, acc);
-                  acc = true;
-                }
-            }
-            tc_commit(sy->pv_done + s);
-            if (!two || s == last) tc_commit(sy->empty + st);
-          }
-          if (have) fresh[s] = false;
-          __syncwarp();
-          if (i + 1 < ns[s]) issue_s(i + 1, s_c);
-        });
-      }
-      it += 2 * n;
-      for (int s = 0; s < 2; ++s)
-        if (ns[s] > 0) {
-          cnt[s] += ns[s];
-          ++seg[s];
+      bool fresh = true;  // O holds nothing of this piece yet
+      alive = issue_s(0);
+      for (int i = 0; i < ns && alive; ++i) {
+        const uint32_t have = tile_blocks(p, next);
+        if (i + 1 < ns) next = tile_id(table, nblk, k.tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
+        const uint32_t idx = it0 + (two ? 2 * i + 1 : 4 * i + min(2, n - 2 * i) + s), st = idx % S;
+        if (!wait_all(sy->full + st, (idx / S) & 1) || (i == 0 && seg > 0 && !wait_all(sy->o_free + s, (seg - 1) & 1)) ||
+            !wait_all(sy->p_ready + s, (cnt + i) & 1)) {
+          alive = false;
+          break;
         }
+        tc_fence_after();
+        const uint64_t vd = v_desc + st * (C::kTileBytes >> 4);
+        if (elect_one()) {
+          if (have == 0xffu) {
+            tc_mma_ts(t_o, t_s, vd, kDescO, !fresh);
+#pragma unroll
+            for (int j = 1; j < kPrefixTile / 16; ++j)
+              tc_mma_ts(t_o, t_s + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, true);
+          } else {  // the prefix ends in this tile, or a block is missing
+            bool acc = !fresh;
+            for (int j = 0; j < kPrefixTile / 16; ++j)
+              if (have >> j & 1) {
+                tc_mma_ts(t_o, t_s + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, acc);
+                acc = true;
+              }
+          }
+          tc_commit(sy->pv_done + s);
+          release(st);
+        }
+        if (have) fresh = false;
+        __syncwarp();
+        if (i + 1 < ns) alive = issue_s(i + 1);
+      }
+      cnt += ns;
+      ++seg;
     }
     if (!alive) {
       if (lane == 0) {
         *abort = 1;
         set_error(p.err, kErrTimeout);
-        tc_commit(&sy->drain);  // the products in flight end before their memory is given up
+        tc_commit(sy->drain + s);  // the products in flight end before their memory is given up
       }
       __syncwarp();
-      (void)mbar_wait_bounded(&sy->drain, 0);
+      (void)mbar_wait_bounded(sy->drain + s, 0);
     }
+  } else if (warp == C::kDescribeWarp) {
+    if (few) prefix_describe(p, sc, total, 0, 1);
   } else if (C::kQuant && warp >= C::kConvertWarp) {
     // ---------------------------------------------------------------- codes -> operand tiles, a thread to a token
     regs_down<C::kConvertRegs>();
