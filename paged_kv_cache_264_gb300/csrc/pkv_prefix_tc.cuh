@@ -7,9 +7,12 @@
 // take the even and the odd tiles, so that either way one stream's softmax runs under the other's
 // products.  Per stream and tile:
 //     S = Q K^T    128 x 128 x D, both operands in shared memory, S in tensor memory (fp32)
-//     P = 2^(S * scale - m)    a thread to a row, all 128 logits in registers: no shuffles
+//     P = 2^(S * scale - m)    a thread to a row, its logits in registers: no shuffles
 //     O += P V     128 x D x 128, P in tensor memory (bf16, over S's columns), V as it lies in the
 //                  pool (token-major, the contracted index outermost: an MN-major operand)
+// in halves of 64 tokens: while the softmax works on one half, the other half's product over V and
+// the next tile's S of that half run.  (Whole tiles at a time left each stream a chain of S, softmax
+// and product with only the other stream's to fill it.)
 // The running maximum is lazy (kMaxSlack): O is rescaled in tensor memory only when a row's
 // logits pass its maximum by 2^8.  P enters the product as bf16, and the softmax sum adds the
 // same rounded weights, so that numerator and denominator agree.
@@ -76,7 +79,8 @@ struct PrefixSync {
   uint64_t full[16], empty[16];          // operand ring stages
   uint64_t raw_full[8], raw_empty[8];    // code ring stages
   uint64_t scales[8];                    // scale slots
-  uint64_t q_ready[2], s_ready[2], p_ready[2], pv_done[2], o_free[2];  // per stream
+  uint64_t q_ready[2], o_free[2];                        // per stream
+  uint64_t s_ready[2][2], p_ready[2][2], pv_done[2][2];  // per stream and half of a tile
   uint64_t drain[2];
   uint32_t tmem;
   uint32_t abort;
@@ -167,9 +171,11 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     for (int i = 0; i < C::kSlots; ++i) mbar_init(sy->scales + i, 128);
     for (int s = 0; s < 2; ++s) {
       mbar_init(sy->q_ready + s, 128);
-      mbar_init(sy->s_ready + s, 1);
-      mbar_init(sy->p_ready + s, 128);
-      mbar_init(sy->pv_done + s, 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sy->s_ready[s][h], 1);
+        mbar_init(&sy->p_ready[s][h], 128);
+        mbar_init(&sy->pv_done[s][h], 1);
+      }
       mbar_init(sy->o_free + s, 128);
       mbar_init(sy->drain + s, 1);
     }
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
   } else if (warp == C::kMmaWarp || warp == C::kMmaWarp + 1) {
     // ---------------------------------------------------------------- products of stream s
     // The whole warp runs this with warp-uniform values; one elected lane issues.
-    constexpr uint32_t kDescS = mma_bf16_desc(128, kPrefixTile, false), kDescO = mma_bf16_desc(128, D, true);
+    constexpr uint32_t kDescS = mma_bf16_desc(128, kPrefixTile / 2, false), kDescO = mma_bf16_desc(128, D, true);
     const int s = warp - C::kMmaWarp;
     const uint64_t q_desc = smem_operand(smem_addr(smem) + s * C::kTileBytes, 16, 1024);
     const uint64_t k_desc = smem_operand(smem_addr(ring), 16, 1024), v_desc = smem_operand(smem_addr(ring), C::kHalfBytes, 1024);
@@ -300,59 +306,64 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
         tc_commit(sy->empty + st);
         if (!shared) mbar_arrive(sy->empty + st);
       };
-      // S of step i
-      auto issue_s = [&](int i) {
+      // S of half h of step i
+      auto issue_s = [&](int i, auto h_c) {
+        constexpr int h = decltype(h_c)::value;
         const uint32_t idx = it0 + (two ? 2 * i : 4 * i + s), st = idx % S;
-        if (!wait_all(sy->full + st, (idx / S) & 1) || (i == 0 && !wait_all(sy->q_ready + s, seg & 1))) return false;
+        if (h == 0 && !wait_all(sy->full + st, (idx / S) & 1)) return false;
         // P lies over S until its product is done
-        if (cnt + i > 0 && !wait_all(sy->pv_done + s, (cnt + i - 1) & 1)) return false;
+        if (cnt + i > 0 && !wait_all(&sy->pv_done[s][h], (cnt + i - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t kd = k_desc + st * (C::kTileBytes >> 4);
+        const uint64_t kd = k_desc + ((st * C::kTileBytes + h * (64 * 128)) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             const uint64_t at = ((j >> 2) * C::kHalfBytes + (j & 3) * 32) >> 4;
-            tc_mma_ss(t_s, q_desc + at, kd + at, kDescS, j > 0);
+            tc_mma_ss(t_s + h * 64, q_desc + at, kd + at, kDescS, j > 0);
           }
-          tc_commit(sy->s_ready + s);
-          release(st);
+          tc_commit(&sy->s_ready[s][h]);
+          if (h == 1) release(st);
         }
         __syncwarp();
         return true;
       };
       bool fresh = true;  // O holds nothing of this piece yet
-      alive = issue_s(0);
+      alive = wait_all(sy->q_ready + s, seg & 1) && issue_s(0, IntC<0>{}) && issue_s(0, IntC<1>{});
       for (int i = 0; i < ns && alive; ++i) {
         const uint32_t have = tile_blocks(p, next);
         if (i + 1 < ns) next = tile_id(table, nblk, k.tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
         const uint32_t idx = it0 + (two ? 2 * i + 1 : 4 * i + min(2, n - 2 * i) + s), st = idx % S;
-        if (!wait_all(sy->full + st, (idx / S) & 1) || (i == 0 && seg > 0 && !wait_all(sy->o_free + s, (seg - 1) & 1)) ||
-            !wait_all(sy->p_ready + s, (cnt + i) & 1)) {
+        if (!wait_all(sy->full + st, (idx / S) & 1) || (i == 0 && seg > 0 && !wait_all(sy->o_free + s, (seg - 1) & 1))) {
           alive = false;
           break;
         }
-        tc_fence_after();
-        const uint64_t vd = v_desc + st * (C::kTileBytes >> 4);
-        if (elect_one()) {
-          if (have == 0xffu) {
-            tc_mma_ts(t_o, t_s, vd, kDescO, !fresh);
+        static_for<2>([&](auto h_c) {
+          constexpr int h = decltype(h_c)::value;
+          alive = alive && wait_all(&sy->p_ready[s][h], (cnt + i) & 1);
+          if (!alive) return;
+          tc_fence_after();
+          const uint64_t vd = v_desc + ((st * C::kTileBytes + h * (64 * 128)) >> 4);
+          const uint32_t mine = have >> (4 * h) & 0xfu, t_p = t_s + h * 64;
+          if (elect_one()) {
+            if (mine == 0xfu) {
+              tc_mma_ts(t_o, t_p, vd, kDescO, !fresh);
 #pragma unroll
-            for (int j = 1; j < kPrefixTile / 16; ++j)
-              tc_mma_ts(t_o, t_s + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, true);
-          } else {  // the prefix ends in this tile, or a block is missing
-            bool acc = !fresh;
-            for (int j = 0; j < kPrefixTile / 16; ++j)
-              if (have >> j & 1) {
-                tc_mma_ts(t_o, t_s + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, acc);
-                acc = true;
-              }
+              for (int j = 1; j < 4; ++j) tc_mma_ts(t_o, t_p + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, true);
+            } else {  // the prefix ends in this half, or a block is missing
+              bool acc = !fresh;
+              for (int j = 0; j < 4; ++j)
+                if (mine >> j & 1) {
+                  tc_mma_ts(t_o, t_p + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, acc);
+                  acc = true;
+                }
+            }
+            tc_commit(&sy->pv_done[s][h]);
+            if (h == 1) release(st);
           }
-          tc_commit(sy->pv_done + s);
-          release(st);
-        }
-        if (have) fresh = false;
-        __syncwarp();
-        if (i + 1 < ns) alive = issue_s(i + 1);
+          if (mine) fresh = false;
+          __syncwarp();
+          if (i + 1 < ns) alive = issue_s(i + 1, h_c);
+        });
       }
       cnt += ns;
       ++seg;
@@ -480,69 +491,63 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
         const int tile = two ? i : 2 * i + s;
         const uint32_t have = tile_blocks(p, next);
         if (i + 1 < ns) next = tile_id(table, nblk, tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
-        const uint32_t c = cnt + i;
         const uint32_t slot = C::kQuant ? (tiles0 + tile) % kSlots : 0;
-        if ((C::kQuant && !wait_all(sy->scales + slot, ((tiles0 + tile) / kSlots) & 1)) || !wait_all(sy->s_ready + s, c & 1)) {
+        if (C::kQuant && !wait_all(sy->scales + slot, ((tiles0 + tile) / kSlots) & 1)) {
           alive = false;
           break;
         }
-        const auto* ks = reinterpret_cast<const float4*>(smem + C::kSlotOff + slot * C::kScaleBytes);
-        const float4* vs = ks + kPrefixTile / 4;
         any |= have != 0;
-        if (!idle) {
-          tc_fence_after();
-          // 64 columns at a time: the upper half for its maximum alone, then the lower half, which
-          // stays in registers; its weights go over its own columns, and the upper half is read
-          // again.  Holding all 128 columns instead spills.
-          float x[64];
-          auto fetch = [&](int c0) {
-            tmem_ld32(s_addr + c0, x);
-            tmem_ld32(s_addr + c0 + 32, x + 32);
+        static_for<2>([&](auto h_c) {
+          constexpr int h = decltype(h_c)::value;
+          alive = alive && wait_all(&sy->s_ready[s][h], (cnt + i) & 1);
+          if (!alive) return;
+          if (!idle) {
+            const auto* ks = reinterpret_cast<const float4*>(smem + C::kSlotOff + slot * C::kScaleBytes) + h * 16;
+            [[maybe_unused]] const auto* vs = reinterpret_cast<const float2*>(ks + kPrefixTile / 4);
+            const uint32_t mine = have >> (4 * h) & 0xfu;
+            tc_fence_after();
+            float x[64];
+            tmem_ld32(s_addr + h * 64, x);
+            tmem_ld32(s_addr + h * 64 + 32, x + 32);
             tmem_wait_ld();
             if constexpr (C::kQuant) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const float4 f = ks[c0 / 4 + j];
+                const float4 f = ks[j];
                 x[4 * j] *= f.x; x[4 * j + 1] *= f.y; x[4 * j + 2] *= f.z; x[4 * j + 3] *= f.w;
               }
             }
-            if (have != 0xffu) {
+            if (mine != 0xfu) {
 #pragma unroll
               for (int j = 0; j < 64; ++j)
-                if (!(have >> ((c0 + j) / 16) & 1)) x[j] = -INFINITY;
+                if (!(mine >> (j / 16) & 1)) x[j] = -INFINITY;
             }
-          };
-          auto largest = [&]() {
             float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
             for (int j = 4; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
-            return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          };
-          fetch(64);
-          float bm = largest();
-          fetch(0);
-          bm = fmaxf(bm, largest()) * scale;
-          const bool grow = bm > m + kMaxSlack;
-          if (__any_sync(kFull, grow)) {
-            const float mu = grow ? bm : m, f = fast_exp2(m - mu);
-            m = mu;
-            l *= f;
-            if (i > 0) {
-              // the last product into O is done: S was issued after it
+            const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+            const bool grow = bm > m + kMaxSlack;
+            if (__any_sync(kFull, grow)) {
+              const float mu = grow ? bm : m, f = fast_exp2(m - mu);
+              m = mu;
+              l *= f;
+              if (i > 0 || h > 0) {
+                // every product into O so far has to be done: the half's before this one is the last
+                alive = wait_all(&sy->pv_done[s][h ^ 1], (cnt + i - (h ^ 1)) & 1);
+                tc_fence_after();
 #pragma unroll 1
-              for (int j = 0; j < D / 16; ++j) {
-                float o[16];
-                tmem_ld16(o_addr + 16 * j, o);
-                tmem_wait_ld();
+                for (int j = 0; j < D / 16; ++j) {
+                  float o[16];
+                  tmem_ld16(o_addr + 16 * j, o);
+                  tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] *= f;
-                tmem_st16(o_addr + 16 * j, o);
+                  for (int e = 0; e < 16; ++e) o[e] *= f;
+                  tmem_st16(o_addr + 16 * j, o);
+                }
               }
             }
-          }
-          const uint64_t neg = f32x2(-m, -m);
-          uint64_t sum[2] = {0, 0};
-          auto weights = [&](int c0) {
+            const uint64_t neg = f32x2(-m, -m);
+            uint64_t sum[2] = {0, 0};
             uint32_t pw[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -552,25 +557,23 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
               b = fast_exp2(b);
               if constexpr (C::kQuant) {
                 sum[j & 1] = add2(sum[j & 1], f32x2(a, b));
-                const float2 f = reinterpret_cast<const float2*>(vs)[c0 / 2 + j];
+                const float2 f = vs[j];
                 pw[j] = pack_bf16x2(a * f.x, b * f.y);
               } else {
                 pw[j] = pack_bf16x2(a, b);
                 sum[j & 1] = add2(sum[j & 1], f32x2(bf16lo(pw[j]), bf16hi(pw[j])));
               }
             }
-            tmem_st32(s_addr + c0 / 2, pw);
-          };
-          weights(0);
-          fetch(64);
-          weights(64);
-          float a, b;
-          f32x2_parts(add2(sum[0], sum[1]), a, b);
-          l += a + b;
-          tmem_wait_st();
-          tc_fence_before();
-        }
-        mbar_arrive(sy->p_ready + s);
+            tmem_st32(s_addr + h * 64, pw);
+            float a, b;
+            f32x2_parts(add2(sum[0], sum[1]), a, b);
+            l += a + b;
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          mbar_arrive(&sy->p_ready[s][h]);
+        });
+        if (!alive) break;
       }
       if (!alive) break;
       cnt += ns;
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       // ---- the piece's partial.  A thread holds a row, so its stores would touch 32 lines at a
       // time; the warp turns its 32 rows through its part of the Q tile (free: every S is done),
       // 64 values of each row at a time, and stores whole lines.
-      if (!wait_all(sy->pv_done + s, (cnt - 1) & 1)) {
+      if (!wait_all(&sy->pv_done[s][1], (cnt - 1) & 1)) {
         alive = false;
         break;
       }
