@@ -284,10 +284,12 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     // ---------------------------------------------------------------- products of stream s
     // The whole warp runs this with warp-uniform values; one elected lane issues.
     constexpr uint32_t kDescS = mma_bf16_desc(128, kPrefixTile / 2, false), kDescO = mma_bf16_desc(128, D, true);
-    const int s = warp - C::kMmaWarp;
-    const uint64_t q_desc = smem_operand(smem_addr(smem) + s * C::kTileBytes, 16, 1024);
-    const uint64_t k_desc = smem_operand(smem_addr(ring), 16, 1024), v_desc = smem_operand(smem_addr(ring), C::kHalfBytes, 1024);
-    const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * D;
+    constexpr uint32_t kHi = smem_operand_hi(1024);
+    auto uniform = [](uint32_t x) { return __shfl_sync(kFull, x, 0); };  // tells the compiler that it is
+    const int s = uniform(warp - C::kMmaWarp);
+    const uint32_t q_desc = uniform(smem_operand(smem_addr(smem) + s * C::kTileBytes, 16));
+    const uint32_t k_desc = smem_operand(smem_addr(ring), 16), v_desc = smem_operand(smem_addr(ring), C::kHalfBytes);
+    const uint32_t t_s = uniform(tmem + s * 128), t_o = uniform(tmem + 256 + s * D);
     uint32_t it = 0;   // ring stages before this piece
     uint32_t cnt = 0;  // steps of the stream before this piece
     uint32_t seg = 0;  // pieces that had work for it
@@ -307,19 +309,18 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
         if (!shared) mbar_arrive(sy->empty + st);
       };
       // S of half h of step i
-      auto issue_s = [&](int i, auto h_c) {
-        constexpr int h = decltype(h_c)::value;
+      auto issue_s = [&](int i, int h) {
         const uint32_t idx = it0 + (two ? 2 * i : 4 * i + s), st = idx % S;
         if (h == 0 && !wait_all(sy->full + st, (idx / S) & 1)) return false;
         // P lies over S until its product is done
         if (cnt + i > 0 && !wait_all(&sy->pv_done[s][h], (cnt + i - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t kd = k_desc + ((st * C::kTileBytes + h * (64 * 128)) >> 4);
+        const uint32_t kd = uniform(k_desc + ((st * C::kTileBytes + h * (64 * 128)) >> 4)), d = uniform(t_s + h * 64);
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
-            const uint64_t at = ((j >> 2) * C::kHalfBytes + (j & 3) * 32) >> 4;
-            tc_mma_ss(t_s + h * 64, q_desc + at, kd + at, kDescS, j > 0);
+            const uint32_t at = ((j >> 2) * C::kHalfBytes + (j & 3) * 32) >> 4;
+            tc_mma_ss(d, q_desc + at, kd + at, kHi, kDescS, j > 0);
           }
           tc_commit(&sy->s_ready[s][h]);
           if (h == 1) release(st);
@@ -328,42 +329,46 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
         return true;
       };
       bool fresh = true;  // O holds nothing of this piece yet
-      alive = wait_all(sy->q_ready + s, seg & 1) && issue_s(0, IntC<0>{}) && issue_s(0, IntC<1>{});
-      for (int i = 0; i < ns && alive; ++i) {
-        const uint32_t have = tile_blocks(p, next);
-        if (i + 1 < ns) next = tile_id(table, nblk, k.tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
-        const uint32_t idx = it0 + (two ? 2 * i + 1 : 4 * i + min(2, n - 2 * i) + s), st = idx % S;
-        if (!wait_all(sy->full + st, (idx / S) & 1) || (i == 0 && seg > 0 && !wait_all(sy->o_free + s, (seg - 1) & 1))) {
-          alive = false;
-          break;
+      alive = wait_all(sy->q_ready + s, seg & 1);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) alive = alive && issue_s(0, h);
+      uint32_t have = 0, st = 0;
+      // one half of a tile at a time (rolled: the CTA's roles share one instruction cache)
+#pragma unroll 1
+      for (int g = 0; g < 2 * ns && alive; ++g) {
+        const int i = g >> 1, h = g & 1;
+        if (h == 0) {
+          have = tile_blocks(p, next);
+          if (i + 1 < ns) next = tile_id(table, nblk, k.tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
+          const uint32_t idx = it0 + (two ? 2 * i + 1 : 4 * i + min(2, n - 2 * i) + s);
+          st = idx % S;
+          alive = wait_all(sy->full + st, (idx / S) & 1) && (i > 0 || seg == 0 || wait_all(sy->o_free + s, (seg - 1) & 1));
         }
-        static_for<2>([&](auto h_c) {
-          constexpr int h = decltype(h_c)::value;
-          alive = alive && wait_all(&sy->p_ready[s][h], (cnt + i) & 1);
-          if (!alive) return;
-          tc_fence_after();
-          const uint64_t vd = v_desc + ((st * C::kTileBytes + h * (64 * 128)) >> 4);
-          const uint32_t mine = have >> (4 * h) & 0xfu, t_p = t_s + h * 64;
-          if (elect_one()) {
-            if (mine == 0xfu) {
-              tc_mma_ts(t_o, t_p, vd, kDescO, !fresh);
+        alive = alive && wait_all(&sy->p_ready[s][h], (cnt + i) & 1);
+        if (!alive) break;
+        tc_fence_after();
+        const uint32_t vd = uniform(v_desc + ((st * C::kTileBytes + h * (64 * 128)) >> 4)), t_p = uniform(t_s + h * 64);
+        const uint32_t mine = have >> (4 * h) & 0xfu;
+        if (elect_one()) {
+          if (mine == 0xfu) {
 #pragma unroll
-              for (int j = 1; j < 4; ++j) tc_mma_ts(t_o, t_p + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, true);
-            } else {  // the prefix ends in this half, or a block is missing
-              bool acc = !fresh;
-              for (int j = 0; j < 4; ++j)
-                if (mine >> j & 1) {
-                  tc_mma_ts(t_o, t_p + j * 8, vd + j * ((kBlockSize * 128) >> 4), kDescO, acc);
-                  acc = true;
-                }
-            }
-            tc_commit(&sy->pv_done[s][h]);
-            if (h == 1) release(st);
+            for (int j = 0; j < 4; ++j)
+              tc_mma_ts(t_o, t_p + j * 8, vd + j * ((kBlockSize * 128) >> 4), kHi, kDescO, j > 0 || !fresh);
+          } else {  // the prefix ends in this half, or a block is missing
+            bool acc = !fresh;
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j)
+              if (mine >> j & 1) {
+                tc_mma_ts(t_o, t_p + j * 8, vd + j * ((kBlockSize * 128) >> 4), kHi, kDescO, acc);
+                acc = true;
+              }
           }
-          if (mine) fresh = false;
-          __syncwarp();
-          if (i + 1 < ns) alive = issue_s(i + 1, h_c);
-        });
+          tc_commit(&sy->pv_done[s][h]);
+          if (h == 1) release(st);
+        }
+        if (mine) fresh = false;
+        __syncwarp();
+        if (i + 1 < ns) alive = issue_s(i + 1, h);
       }
       cnt += ns;
       ++seg;
@@ -487,20 +492,23 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       const bool idle = (warp & 3) * 32 >= nrows;  // none of the warp's rows exists
       float m = kMaxFloor, l = 0.0f;
       bool any = false;
-      for (int i = 0; i < ns; ++i) {
-        const int tile = two ? i : 2 * i + s;
-        const uint32_t have = tile_blocks(p, next);
-        if (i + 1 < ns) next = tile_id(table, nblk, tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
-        const uint32_t slot = C::kQuant ? (tiles0 + tile) % kSlots : 0;
-        if (C::kQuant && !wait_all(sy->scales + slot, ((tiles0 + tile) / kSlots) & 1)) {
-          alive = false;
-          break;
+      uint32_t have = 0, slot = 0;
+#pragma unroll 1
+      for (int g = 0; g < 2 * ns; ++g) {
+        const int i = g >> 1, h = g & 1;
+        if (h == 0) {
+          const int tile = two ? i : 2 * i + s;
+          have = tile_blocks(p, next);
+          any |= have != 0;
+          if (i + 1 < ns) next = tile_id(table, nblk, tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
+          if constexpr (C::kQuant) {
+            slot = (tiles0 + tile) % kSlots;
+            alive = wait_all(sy->scales + slot, ((tiles0 + tile) / kSlots) & 1);
+          }
         }
-        any |= have != 0;
-        static_for<2>([&](auto h_c) {
-          constexpr int h = decltype(h_c)::value;
-          alive = alive && wait_all(&sy->s_ready[s][h], (cnt + i) & 1);
-          if (!alive) return;
+        alive = alive && wait_all(&sy->s_ready[s][h], (cnt + i) & 1);
+        if (!alive) break;
+        {
           if (!idle) {
             const auto* ks = reinterpret_cast<const float4*>(smem + C::kSlotOff + slot * C::kScaleBytes) + h * 16;
             [[maybe_unused]] const auto* vs = reinterpret_cast<const float2*>(ks + kPrefixTile / 4);
@@ -531,7 +539,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
               const float mu = grow ? bm : m, f = fast_exp2(m - mu);
               m = mu;
               l *= f;
-              if (i > 0 || h > 0) {
+              if (g > 0) {
                 // every product into O so far has to be done: the half's before this one is the last
                 alive = wait_all(&sy->pv_done[s][h ^ 1], (cnt + i - (h ^ 1)) & 1);
                 tc_fence_after();
@@ -572,8 +580,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
             tc_fence_before();
           }
           mbar_arrive(&sy->p_ready[s][h]);
-        });
-        if (!alive) break;
+        }
       }
       if (!alive) break;
       cnt += ns;

@@ -35,30 +35,34 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
 // bytes from one group of 8 rows to the next.  `lbo`: for an operand whose contiguous index is
 // not the contracted one (MN-major), bytes from one 64-value span of that index to the next;
 // unused for K-major.
-__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return uint64_t((addr & 0x3ffffu) >> 4) | uint64_t((lbo & 0x3ffffu) >> 4) << 16 | uint64_t((sbo & 0x3ffffu) >> 4) << 32 |
-         uint64_t(1) << 46 | uint64_t(2) << 61;
+// The descriptor is in two words: the low one holds address and lbo (add a byte offset / 16 to it
+// to move the operand), the high one is the same for every operand of one sbo.
+__device__ __forceinline__ uint32_t smem_operand(uint32_t addr, uint32_t lbo) {
+  return (addr & 0x3ffffu) >> 4 | ((lbo & 0x3ffffu) >> 4) << 16;
 }
+constexpr uint32_t smem_operand_hi(uint32_t sbo) { return (sbo & 0x3ffffu) >> 4 | 1u << 14 | 2u << 29; }
 
 // Instruction descriptor: bf16 operands, fp32 accumulator, M x N; A K-major, B K-major or MN-major.
 constexpr uint32_t mma_bf16_desc(int m, int n, bool b_mn_major) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn_major ? 1u << 16 : 0u) | uint32_t(n >> 3) << 17 | uint32_t(m >> 4) << 24;
 }
 
-// D (+)= A B^T over 16 contracted values; A in shared memory.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// D (+)= A B^T over 16 contracted values; A and B in shared memory (low descriptor words).
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"(uint32_t(accumulate))
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"(uint32_t(accumulate)), "r"(hi)
       : "memory");
 }
 // The same with A in tensor memory (a lane to a row, two 16-bit values to a column).
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"(uint32_t(accumulate))
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"(uint32_t(accumulate)), "r"(hi)
       : "memory");
 }
 
