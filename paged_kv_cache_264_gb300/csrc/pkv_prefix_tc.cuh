@@ -24,8 +24,8 @@
 // sum adds the unrounded ones, since the rounded ones carry the scale).
 //
 // Warps: two warpgroups of softmax (one per stream, which also load Q and write the partials),
-// one warp that fills the ring of K and V tiles by TMA (8 blocks to a tile, each wherever it lies
-// in the pool), one warp per stream that issues its products (one for both let a stream's waits
+// two warps that fill the ring of K and of V tiles by TMA (8 blocks to a tile, each wherever it
+// lies in the pool), one warp per stream that issues its products (one for both let a stream's waits
 // hold up the other's products), and the converting warpgroup for INT8 and FP8.  Every wait is bounded; after one that gave up the
 // CTA takes no further work, lets its copies and products land, frees its tensor memory and ends.
 //
@@ -46,7 +46,7 @@ struct PrefixCfg {
   static constexpr int kTileBytes = kPrefixTile * D * 2;         // one K, V or Q tile, 16-bit
   static constexpr int kHalfBytes = kPrefixTile * 128;           // one span of all its rows
   static constexpr int kStages = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
-  // codes as they come from the pool, and beside K's the tile's K and V scales
+  // codes as they come from the pool
   static constexpr int kRawBytes = kPrefixTile * D;
   static constexpr int kScaleBytes = 2 * kPrefixTile * 4;
   static constexpr int kRawStages = kQuant ? (D == 128 ? 3 : 8) : 0;
@@ -57,17 +57,16 @@ struct PrefixCfg {
   static constexpr int kSlots = kQuant ? (D == 128 ? 4 : 8) : 0;
   static_assert(!kQuant || 2 * kSlots - 3 >= kStages, "a scale slot is free when it is written again");
   static constexpr int kThreads = kQuant ? 512 : 384;
-  static constexpr int kTmaWarp = 8, kMmaWarp = 9, kDescribeWarp = 11, kConvertWarp = 12;  // 9 and 10: one per stream
+  static constexpr int kLoadK = 8, kMmaWarp = 9, kLoadV = 11, kConvertWarp = 12;  // 9 and 10: one per stream
   // Registers: the softmax threads hold a row of 128 logits; what the other warpgroups give up
   // goes to them.  The shares' sum is checked against the kernel's own count before a launch.
   static constexpr int kSoftmaxRegs = kQuant ? 184 : 200;
-  static constexpr int kIssueRegs = kQuant ? 64 : 96, kConvertRegs = 72;
+  static constexpr int kIssueRegs = kQuant ? 64 : 96, kConvertRegs = 80;
   static constexpr int kRegSum = 128 * (2 * kSoftmaxRegs + kIssueRegs + (kQuant ? kConvertRegs : 0));
   static constexpr int kMiscBytes = 1024;
   static constexpr int kRingOff = 2 * kTileBytes;                // Q tiles of both streams first
   static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
-  static constexpr int kRawScaleOff = kRawOff + kRawStages * kRawBytes;
-  static constexpr int kSlotOff = kRawScaleOff + kRawStages * kScaleBytes;
+  static constexpr int kSlotOff = kRawOff + kRawStages * kRawBytes;
   static constexpr int kSmemBytes = kMiscBytes + 1024 + kSlotOff + kSlots * kScaleBytes;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(size_t(kStages) * kTileBytes >= prefix_scan_bytes(kMaxPrefixGroups), "the scan fits the ring");
@@ -88,6 +87,21 @@ struct PrefixSync {
 };
 static_assert(sizeof(PrefixSync) <= 1008, "barriers fit their space");
 constexpr int kFewGroups = 24;
+
+// A place in a ring of N stages: the stage, and the parity of the phase that its current use
+// completes.
+template <int N>
+struct RingPos {
+  uint32_t st, ph;
+  __device__ __forceinline__ void advance(uint32_t by) {
+    st += by;
+    while (st >= N) {
+      st -= N;
+      ph ^= 1u;
+    }
+  }
+  static __device__ __forceinline__ RingPos at(uint32_t index) { return {index % N, (index / N) & 1u}; }
+};
 
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -133,15 +147,24 @@ __device__ __forceinline__ void bf16x4_from_codes(uint32_t w, uint32_t& lo, uint
   }
 }
 
-// Block id of lane % 8 of a tile; -1 past the prefix.  Roles ask for a tile's ids one step ahead
-// of their use: a table entry is a global-memory round trip away.
+// A load that stays where it is written: the compiler would sink a plain one to its use, behind the
+// waits that are there to cover its latency.
+__device__ __forceinline__ int load_ahead(const void* at) {
+  int v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(at));
+  return v;
+}
+
+// Block id of lane % 8 of a tile (of the prefix's last block, past its end: tile_blocks tells).
+// Roles ask for a tile's ids one step ahead of their use: a table entry is a global-memory round trip
+// away, and any use of the loaded value here would wait for it.
 __device__ __forceinline__ int tile_id(const int32_t* table, int nblk, int tile, int lane) {
-  const int j = tile * (kPrefixTile / kBlockSize) + (lane & 7);
-  return j < nblk ? __ldg(table + j) : -1;
+  return load_ahead(table + min(tile * (kPrefixTile / kBlockSize) + (lane & 7), nblk - 1));
 }
 // Which of the tile's 8 blocks exist, bit j for block j (the same on every lane of the warp).
-__device__ __forceinline__ uint32_t tile_blocks(const PrefixParams& p, int id) {
-  return __ballot_sync(0xffffffffu, id >= 0 && id < p.num_blocks) & 0xffu;
+__device__ __forceinline__ uint32_t tile_blocks(const PrefixParams& p, int id, int nblk, int tile, int lane) {
+  const bool inside = tile * (kPrefixTile / kBlockSize) + (lane & 7) < nblk;
+  return __ballot_sync(0xffffffffu, inside && id >= 0 && id < p.num_blocks) & 0xffu;
 }
 
 template <KvType KV, int D>
@@ -199,29 +222,43 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sy->tmem;
   volatile uint32_t* abort = &sy->abort;
-  // A whole warp's wait: the same answer on every lane, false once any part of the CTA gave up.
+  // A whole warp's wait: the same answer on every lane; false after the time limit, or once another
+  // warp of the CTA gave up.  A barrier that is already there costs one test and a vote.
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = mbar_wait_bounded(bar, parity);
-    return bool(__all_sync(kFull, ok && *abort == 0));
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    bool ok = false;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t tries = 0; tries < (1u << 26); ++tries) {
+      if (__all_sync(kFull, mbar_try_wait(bar, parity))) {
+        ok = true;
+        break;
+      }
+      if ((tries & 63u) == 63u && __any_sync(kFull, *abort != 0 || global_timer_ns() - t0 > kWaitTimeoutNs)) break;
+    }
+    return ok;
   };
 
   // Steps of stream s over n tiles: which of the unit's tiles it takes, and how many.
   // two: the streams hold different rows; else they share the tiles out between them.
   auto steps_of = [&](bool two, int nrows, int n, int s) { return two ? (s == 0 || nrows > 128 ? n : 0) : (n + 1 - s) / 2; };
 
-  if (warp >= C::kTmaWarp && warp < C::kTmaWarp + 4) regs_down<C::kIssueRegs>();
-  if (warp == C::kTmaWarp) {
-    // ---------------------------------------------------------------- K and V tiles -> ring
+  if (warp >= C::kLoadK && warp < C::kLoadK + 4) regs_down<C::kIssueRegs>();
+  if (warp == C::kLoadK || warp == C::kLoadV) {
+    // ---------------------------------------------------------------- K (or V) tiles -> ring
+    // The whole warp runs this with warp-uniform values; one elected lane issues (a copy per lane
+    // costs about 85 cycles each, one after the other).
     constexpr int R = C::kQuant ? C::kRawStages : S;
     uint64_t* full = C::kQuant ? sy->raw_full : sy->full;
     uint64_t* empty = C::kQuant ? sy->raw_empty : sy->empty;
-    unsigned char* to = C::kQuant ? smem + C::kRawOff : ring;
     constexpr int kStage = C::kQuant ? C::kRawBytes : C::kTileBytes;
     constexpr int kBoxRows = C::kQuant && D == 64 ? kBlockSize / 2 : kBlockSize;  // pool rows of 128 bytes per block and span
     constexpr int kSpans = C::kQuant ? 1 : C::kHalves;
     constexpr int kSpanBytes = kPrefixTile / kBlockSize * kBoxRows * 128;
+    const bool is_v = __shfl_sync(kFull, warp, 0) == C::kLoadV;
+    const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
+    unsigned char* to = C::kQuant ? smem + C::kRawOff : ring;
     fence_proxy_async_smem();  // the scan's accesses to the ring come before the copies' writes
-    uint32_t it = 0;           // stages filled so far
+    uint32_t it = 0;           // stages of both kinds so far
     bool alive = true;
     for (; more && alive; more = walk_next(p, blockIdx.x, k)) {
       const bool two = k.x.rows > 128;
@@ -230,56 +267,48 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       // tiles read again by the group's other units stay in L2; others are read once
       const uint64_t policy = k.x.units > 1 ? l2_evict_last_policy() : l2_evict_first_policy();
       const int n = k.tile1 - k.tile0;
-      int ids[2], next = tile_id(table, nblk, k.tile0, lane);
-      uint32_t blocks[2];
+      int next = tile_id(table, nblk, k.tile0, lane);
       for (int i = 0; i < 2 * n; ++i, ++it) {
         const TileLoad ld = tile_load(two, n, i);
-        if (!ld.is_v) {
-          const int id = next;
-          const uint32_t have = tile_blocks(p, id);
+        if (ld.is_v != is_v) continue;
+        const int id = next;  // of block lane % 8
+        const uint32_t have = tile_blocks(p, id, nblk, k.tile0 + ld.tile, lane);
+        if (!is_v && have != 0xffu) {
           const int j = (k.tile0 + ld.tile) * (kPrefixTile / kBlockSize) + lane;
           if (lane < 8 && j < nblk && !(have >> lane & 1)) set_error(p.err, kErrBlockId);
-          if (ld.which) { ids[1] = id; blocks[1] = have; } else { ids[0] = id; blocks[0] = have; }
-          if (ld.tile + 1 < n) next = tile_id(table, nblk, k.tile0 + ld.tile + 1, lane);
         }
+        if (ld.tile + 1 < n) next = tile_id(table, nblk, k.tile0 + ld.tile + 1, lane);
         const uint32_t st = it % R;
-        if (it >= R) {
-          if (!wait_all(empty + st, ((it / R) & 1) ^ 1)) {
-            alive = false;
-            break;
-          }
+        if (it >= R && !wait_all(empty + st, ((it / R) & 1) ^ 1)) {
+          alive = false;
+          break;
         }
-        const uint32_t have = ld.which ? blocks[1] : blocks[0];
-        const int id = ld.which ? ids[1] : ids[0];  // of block lane % 8
-        if (lane == 0) {
-          const int each = kSpans * kBoxRows * 128 + (C::kQuant && !ld.is_v ? 2 * kBlockSize * 4 : 0);
-          if (have) mbar_arrive_expect_tx(full + st, __popc(have) * each);
+        const int tile = id * p.kv_heads + k.kvh;  // pools with tensor maps have < 2^27 tiles
+        int row[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) row[j] = __shfl_sync(kFull, tile, j) * kBoxRows;
+        if (elect_one()) {
+          if (have) mbar_arrive_expect_tx(full + st, __popc(have) * (kSpans * kBoxRows * 128));
           else mbar_arrive(full + st);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (have >> j & 1) {
+#pragma unroll
+              for (int x = 0; x < kSpans; ++x)
+                tma_load_2d(to + st * kStage + x * kSpanBytes + j * (kBoxRows * 128), map, x * 64, row[j], full + st, policy);
+            }
+          }
         }
         __syncwarp();
-        // lane = (what, block): one copy each
-        const int block = lane & 7, what = lane >> 3;
-        const int tile = id * p.kv_heads + k.kvh;  // pools with tensor maps have < 2^27 tiles
-        if (have >> block & 1) {
-          if (what < kSpans) {
-            tma_load_2d(to + st * kStage + what * kSpanBytes + block * (kBoxRows * 128), ld.is_v ? &tmap_v : &tmap_k,
-                        what * 64, tile * kBoxRows, full + st, policy);
-          } else if (C::kQuant && !ld.is_v && what < 3) {
-            const float* src = (what == 1 ? p.k_scale : p.v_scale) + int64_t(tile) * kBlockSize;
-            bulk_copy_g2s(smem + C::kRawScaleOff + st * C::kScaleBytes + (what - 1) * (kPrefixTile * 4) + block * (kBlockSize * 4),
-                          src, kBlockSize * 4, full + st, policy);
-          }
-        }
       }
     }
-    if (!alive) {
-      if (lane == 0) {
-        *abort = 1;
-        set_error(p.err, kErrTimeout);
-      }
+    if (!alive && lane == 0) {
+      *abort = 1;
+      set_error(p.err, kErrTimeout);
     }
     // the copies in flight land before the CTA can end (the stages filled last)
     for (uint32_t j = it > R ? it - R : 0; j < it; ++j) (void)mbar_wait_bounded(full + j % R, (j / R) & 1);
+    if (few && !is_v) prefix_describe(p, sc, total, 0, 1);
   } else if (warp == C::kMmaWarp || warp == C::kMmaWarp + 1) {
     // ---------------------------------------------------------------- products of stream s
     // The whole warp runs this with warp-uniform values; one elected lane issues.
@@ -308,14 +337,17 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
         tc_commit(sy->empty + st);
         if (!shared) mbar_arrive(sy->empty + st);
       };
-      // S of half h of step i
-      auto issue_s = [&](int i, int h) {
-        const uint32_t idx = it0 + (two ? 2 * i : 4 * i + s), st = idx % S;
-        if (h == 0 && !wait_all(sy->full + st, (idx / S) & 1)) return false;
+      // Loads of a step are 2 apart (K, V of a tile) or 4 (K, K, V, V of two tiles; the last pair may
+      // be one tile alone).
+      const uint32_t apart = two ? 2 : 4;
+      auto kp = RingPos<S>::at(it0 + (two ? 0 : s)), vp = RingPos<S>::at(it0 + (two ? 1 : min(2, n) + s));
+      // S of half h of the step at kp; c: steps of the stream before it
+      auto issue_s = [&](uint32_t c, int h) {
+        if (h == 0 && !wait_all(sy->full + kp.st, kp.ph)) return false;
         // P lies over S until its product is done
-        if (cnt + i > 0 && !wait_all(&sy->pv_done[s][h], (cnt + i - 1) & 1)) return false;
+        if (c > 0 && !wait_all(&sy->pv_done[s][h], (c - 1) & 1)) return false;
         tc_fence_after();
-        const uint32_t kd = uniform(k_desc + ((st * C::kTileBytes + h * (64 * 128)) >> 4)), d = uniform(t_s + h * 64);
+        const uint32_t kd = uniform(k_desc + kp.st * (C::kTileBytes >> 4) + h * ((64 * 128) >> 4)), d = uniform(t_s + h * 64);
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
@@ -323,31 +355,32 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
             tc_mma_ss(d, q_desc + at, kd + at, kHi, kDescS, j > 0);
           }
           tc_commit(&sy->s_ready[s][h]);
-          if (h == 1) release(st);
+          if (h == 1) release(kp.st);
         }
         __syncwarp();
+        if (h == 1) kp.advance(apart);
         return true;
       };
       bool fresh = true;  // O holds nothing of this piece yet
       alive = wait_all(sy->q_ready + s, seg & 1);
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) alive = alive && issue_s(0, h);
-      uint32_t have = 0, st = 0;
+      for (int h = 0; h < 2; ++h) alive = alive && issue_s(cnt, h);
+      if (alive && seg > 0) alive = wait_all(sy->o_free + s, (seg - 1) & 1);
+      uint32_t have = 0;
       // one half of a tile at a time (rolled: the CTA's roles share one instruction cache)
 #pragma unroll 1
       for (int g = 0; g < 2 * ns && alive; ++g) {
         const int i = g >> 1, h = g & 1;
         if (h == 0) {
-          have = tile_blocks(p, next);
-          if (i + 1 < ns) next = tile_id(table, nblk, k.tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
-          const uint32_t idx = it0 + (two ? 2 * i + 1 : 4 * i + min(2, n - 2 * i) + s);
-          st = idx % S;
-          alive = wait_all(sy->full + st, (idx / S) & 1) && (i > 0 || seg == 0 || wait_all(sy->o_free + s, (seg - 1) & 1));
+          const int tile = two ? i : 2 * i + s;
+          have = tile_blocks(p, next, nblk, k.tile0 + tile, lane);
+          if (i + 1 < ns) next = tile_id(table, nblk, k.tile0 + tile + (two ? 1 : 2), lane);
+          alive = wait_all(sy->full + vp.st, vp.ph);
         }
         alive = alive && wait_all(&sy->p_ready[s][h], (cnt + i) & 1);
         if (!alive) break;
         tc_fence_after();
-        const uint32_t vd = uniform(v_desc + ((st * C::kTileBytes + h * (64 * 128)) >> 4)), t_p = uniform(t_s + h * 64);
+        const uint32_t vd = uniform(v_desc + vp.st * (C::kTileBytes >> 4) + h * ((64 * 128) >> 4)), t_p = uniform(t_s + h * 64);
         const uint32_t mine = have >> (4 * h) & 0xfu;
         if (elect_one()) {
           if (mine == 0xfu) {
@@ -364,11 +397,12 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
               }
           }
           tc_commit(&sy->pv_done[s][h]);
-          if (h == 1) release(st);
+          if (h == 1) release(vp.st);
         }
         if (mine) fresh = false;
         __syncwarp();
-        if (i + 1 < ns) alive = issue_s(i + 1, h);
+        if (h == 1) vp.advance(!two && n - 2 * i == 3 ? 3 : apart);  // V of a last tile alone is one place earlier
+        if (i + 1 < ns) alive = issue_s(cnt + i + 1, h);
       }
       cnt += ns;
       ++seg;
@@ -382,8 +416,6 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       __syncwarp();
       (void)mbar_wait_bounded(sy->drain + s, 0);
     }
-  } else if (warp == C::kDescribeWarp) {
-    if (few) prefix_describe(p, sc, total, 0, 1);
   } else if (C::kQuant && warp >= C::kConvertWarp) {
     // ---------------------------------------------------------------- codes -> operand tiles, a thread to a token
     regs_down<C::kConvertRegs>();
@@ -393,6 +425,22 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     for (; more && alive; more = walk_next(p, blockIdx.x, k)) {
       const bool two = k.x.rows > 128;
       const int n = k.tile1 - k.tile0;
+      const int nblk = __ldg(p.prefix_lens + k.g) / kBlockSize;
+      const int32_t* table = p.block_tables + int64_t(k.x.first_seq) * p.max_blocks_per_seq;
+      // this token's K and V scales of the tile to come, and its block of the tile after that
+      float ks = 0.0f, vs = 0.0f;
+      auto block_of = [&](int tile) {
+        const int j = (k.tile0 + tile) * (kPrefixTile / kBlockSize) + (t >> 4);
+        return load_ahead(table + min(j, nblk - 1));  // past the end: scales that nothing uses
+      };
+      auto fetch = [&](int id) {
+        id = max(0, min(id, int(p.num_blocks) - 1));  // a missing block's scales are not used either
+        const int64_t row = (int64_t(id) * p.kv_heads + k.kvh) * kBlockSize + (t & 15);
+        ks = __int_as_float(load_ahead(p.k_scale + row));
+        vs = __int_as_float(load_ahead(p.v_scale + row));
+      };
+      fetch(block_of(0));
+      int block = block_of(1);
       for (int i = 0; i < 2 * n; ++i, ++it) {
         const TileLoad ld = tile_load(two, n, i);
         const uint32_t st = it % S, rs = it % kRaw;
@@ -404,11 +452,12 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
         unsigned char* dst = ring + st * C::kTileBytes + t * 128;
         if (!ld.is_v) {
           const uint32_t slot = (tiles + ld.tile) % kSlots;
-          const float* from = reinterpret_cast<const float*>(smem + C::kRawScaleOff + rs * C::kScaleBytes);
           float* to = reinterpret_cast<float*>(smem + C::kSlotOff + slot * C::kScaleBytes);
-          to[t] = from[t];
-          to[kPrefixTile + t] = from[kPrefixTile + t];
+          to[t] = ks;
+          to[kPrefixTile + t] = vs;
           mbar_arrive(sy->scales + slot);
+          fetch(block);
+          block = block_of(ld.tile + 2);
         }
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {  // 16 codes -> 32 bytes
@@ -433,7 +482,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       *abort = 1;
       set_error(p.err, kErrTimeout);
     }
-  } else if (warp < C::kTmaWarp) {
+  } else if (warp < C::kLoadK) {
     // ---------------------------------------------------------------- softmax, one thread per row
     regs_up<C::kSoftmaxRegs>();
     const int s = warp >> 2;
@@ -498,7 +547,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
         const int i = g >> 1, h = g & 1;
         if (h == 0) {
           const int tile = two ? i : 2 * i + s;
-          have = tile_blocks(p, next);
+          have = tile_blocks(p, next, nblk, tile0 + tile, lane);
           any |= have != 0;
           if (i + 1 < ns) next = tile_id(table, nblk, tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
           if constexpr (C::kQuant) {
