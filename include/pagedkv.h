@@ -24,6 +24,8 @@
  *  - Layouts are row-major ("C order"); element sizes are those of the named types.
  *  - Calls on one pool must be ordered on one stream (or otherwise serialised): the
  *    pool's device error word and its scheduler counters are shared by its calls.
+ *  - pkv_reserve_slots, pkv_norm_rope_and_cache and pkv_shared_prefix_decode make the pool's
+ *    device current for the call; `stream` is a stream of that device.
  */
 #ifndef PAGEDKV_H_
 #define PAGEDKV_H_
@@ -458,8 +460,7 @@ PKV_API const char* pkv_static_scratch_error(void);
  * or max_tokens do not suffice (PKV_DEVERR_CAPACITY), or a length or count is negative
  * (PKV_DEVERR_CONTEXT_LEN), tables, lengths and free_used stay as they were, every slot is -1
  * and query_starts is all 0.  A block id outside the pool gives its tokens slot -1 and sets
- * PKV_DEVERR_BLOCK_ID.  Errors: PKV_ERR_INVALID_ARG (also when the pool's device is not
- * current), PKV_ERR_UNSUPPORTED (more than 16384 sequences, a pool of 2^27 blocks or more),
+ * PKV_DEVERR_BLOCK_ID.  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (more than 16384 sequences, a pool of 2^27 blocks or more),
  * PKV_ERR_CUDA.
  */
 PKV_API pkv_status pkv_reserve_slots(const pkv_pool* pool, int32_t* block_tables, int max_blocks_per_seq,
@@ -515,8 +516,7 @@ typedef struct pkv_norm_rope {
  * A negative slot skips the token's cache write, not its queries.  A slot past the pool does
  * so too and sets PKV_DEVERR_SLOT.  A position outside the table gives zero queries and no
  * cache write and sets PKV_DEVERR_POSITION.  Slots must be distinct among a call's tokens.
- * num_tokens == 0 is a no-op.  Errors: PKV_ERR_INVALID_ARG (also when the pool's device is not
- * current), PKV_ERR_UNSUPPORTED (rot_dim not a multiple of 16), PKV_ERR_CUDA.
+ * num_tokens == 0 is a no-op.  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (rot_dim not a multiple of 16), PKV_ERR_CUDA.
  */
 PKV_API pkv_status pkv_norm_rope_and_cache(const pkv_pool* pool, const pkv_norm_rope* args, void* stream);
 
@@ -558,8 +558,7 @@ PKV_API pkv_status pkv_shared_prefix_workspace_bytes(const pkv_pool* pool, int n
  * range gets a zero output and sets PKV_DEVERR_CONTEXT_LEN; an invalid group_starts or
  * prefix_lens entry sets PKV_DEVERR_PREFIX and gives the whole call a zero output (with
  * PKV_DEVERR_CONTEXT_LEN); a block id out of range is skipped and sets PKV_DEVERR_BLOCK_ID.
- * num_seqs == 0 is a no-op.  Errors: PKV_ERR_INVALID_ARG (also when the pool's device is not
- * current), PKV_ERR_UNSUPPORTED (a window, more than 4096 groups), PKV_ERR_WORKSPACE, PKV_ERR_CUDA.
+ * num_seqs == 0 is a no-op.  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (a window, more than 4096 groups), PKV_ERR_WORKSPACE, PKV_ERR_CUDA.
  */
 PKV_API pkv_status pkv_shared_prefix_decode(const pkv_pool* pool, const void* q, const int32_t* block_tables,
                                             int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,

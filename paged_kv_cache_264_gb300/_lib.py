@@ -123,6 +123,8 @@ class PagedKVError(RuntimeError):
 def load(path=None) -> ctypes.CDLL:
     """Load the built library (raises if it has not been built)."""
     global _LIB
+    if _LIB is not None and path is None:
+        return _LIB
     with _LOCK:
         if _LIB is not None and path is None:
             return _LIB

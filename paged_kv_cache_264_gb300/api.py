@@ -48,21 +48,23 @@ def _same_device(device, **tensors) -> None:
             raise ValueError(f"{name} must be on {device}, is on {t.device}")
 
 
-class _on_device:
-    """Make the pool's device current for a call (its stream and launches go there)."""
+def _check(t, dtype, name: str, ndim: int, pool) -> None:
+    """_need and the pool's device in one short test (a serving loop makes these calls every step);
+    the reason is looked for only where it fails."""
+    try:
+        if t.dtype is dtype and t.get_device() == pool.device_index and t.dim() == ndim and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _need(t, dtype, name, ndim)
+    _same_device(pool.k_cache.device, **{name: t})
 
-    def __init__(self, pool):
-        self.index = pool.k_cache.device.index
-        self.guard = None
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.index:
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _pool_stream(pool, stream) -> int:
+    """Handle of ``stream``, or of the current stream of the pool's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(pool.device_index)
 
 
 _KERNELS = {0: 0, "auto": 0, 1: 1, "cuda_core": 1, 2: 2, "tensor_core": 2}
@@ -137,6 +139,7 @@ class PagedKVPool:
             for t in (self.k_cache, self.v_cache, self.k_scale, self.v_scale):
                 if t is not None:
                     t.fill_(fill)
+        self.device_index = self.k_cache.get_device()
         with torch.cuda.device(device):
             self.handle = pool_create(num_blocks, kv_heads, head_dim, dtype, self.k_cache,
                                       self.v_cache, self.k_scale, self.v_scale)
@@ -166,6 +169,7 @@ class PagedKVPool:
         pool = cls.__new__(cls)
         pool.num_blocks, pool.kv_heads, _, pool.head_dim = k_cache.shape
         pool.dtype, pool.k_cache, pool.v_cache, pool.k_scale, pool.v_scale = dtype, k_cache, v_cache, k_scale, v_scale
+        pool.device_index = k_cache.get_device()
         with torch.cuda.device(k_cache.device):
             pool.handle = pool_create(pool.num_blocks, pool.kv_heads, pool.head_dim, dtype, k_cache, v_cache, k_scale,
                                       v_scale)
@@ -323,60 +327,71 @@ def reserve_slots(pool: PagedKVPool, block_tables: torch.Tensor, context_lens: t
     be context_lens and new_free_used may be free_used.  All or nothing: a call that does not
     fit changes nothing, returns slots of -1 and sets DEVERR_CAPACITY."""
     i32 = torch.int32
-    _need(block_tables, i32, "block_tables", 2)
-    _need(context_lens, i32, "context_lens", 1)
-    _need(num_new_tokens, i32, "num_new_tokens", 1)
-    _need(free_blocks, i32, "free_blocks", 1)
+    _check(block_tables, i32, "block_tables", 2, pool)
+    _check(context_lens, i32, "context_lens", 1, pool)
+    _check(num_new_tokens, i32, "num_new_tokens", 1, pool)
+    _check(free_blocks, i32, "free_blocks", 1, pool)
     max_tokens = int(max_tokens)
-    b, device = context_lens.shape[0], context_lens.device
-    if block_tables.shape[0] != b or num_new_tokens.shape[0] != b:
+    b = context_lens.shape[0]
+    rows, width = block_tables.shape
+    if rows != b or num_new_tokens.shape[0] != b:
         raise ValueError("block_tables, context_lens and num_new_tokens disagree in shape")
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
     if free_used is not None:
-        _need(free_used, i32, "free_used", 1)
+        _check(free_used, i32, "free_used", 1, pool)
         if free_used.shape[0] != 1:
             raise ValueError("free_used must be [1]")
-    outs = []
-    for name, t, n in (("slot_mapping", slot_mapping, max_tokens), ("positions", positions, max_tokens),
-                       ("query_starts", query_starts, b + 1), ("new_context_lens", new_context_lens, b),
-                       ("new_free_used", new_free_used, 1)):
+
+    def output(t, name, n):
         if t is None:
-            t = torch.empty(n, dtype=i32, device=device)
-        else:
-            _need(t, i32, name, 1)
-            if t.shape[0] != n:
-                raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
-        outs.append(t)
-    _same_device(pool.k_cache.device, block_tables=block_tables, context_lens=context_lens,
-                 num_new_tokens=num_new_tokens, free_blocks=free_blocks, free_used=free_used,
-                 **dict(zip(("slot_mapping", "positions", "query_starts", "new_context_lens", "new_free_used"), outs)))
-    with _on_device(pool):
-        check(_lib.load().pkv_reserve_slots(
-            _handle(pool), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), _ptr(num_new_tokens), b,
-            _ptr(free_blocks), free_blocks.shape[0], _ptr(free_used), max_tokens, *map(_ptr, outs), _stream(stream)),
-            "reserve_slots")
-    return tuple(outs)
+            return torch.empty(n, dtype=i32, device=context_lens.device)
+        _check(t, i32, name, 1, pool)
+        if t.shape[0] != n:
+            raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+        return t
+
+    slot_mapping = output(slot_mapping, "slot_mapping", max_tokens)
+    positions = output(positions, "positions", max_tokens)
+    query_starts = output(query_starts, "query_starts", b + 1)
+    new_context_lens = output(new_context_lens, "new_context_lens", b)
+    new_free_used = output(new_free_used, "new_free_used", 1)
+    st = _lib.load().pkv_reserve_slots(
+        pool.handle, block_tables.data_ptr(), width, context_lens.data_ptr(), num_new_tokens.data_ptr(), b,
+        free_blocks.data_ptr(), free_blocks.shape[0], 0 if free_used is None else free_used.data_ptr(), max_tokens,
+        slot_mapping.data_ptr(), positions.data_ptr(), query_starts.data_ptr(), new_context_lens.data_ptr(),
+        new_free_used.data_ptr(), _pool_stream(pool, stream))
+    if st:
+        check(st, "reserve_slots")
+    return slot_mapping, positions, query_starts, new_context_lens, new_free_used
 
 
-def _head_rows(t: torch.Tensor, name: str, n: int | None, heads: int | None, head_dim: int) -> int:
+def _head_rows(t: torch.Tensor, name: str, n, heads, pool) -> int:
     """Check a bf16 [N, heads, head_dim] tensor whose tokens may lie apart; its token stride."""
+    d = pool.head_dim
+    try:
+        if t.dtype is torch.bfloat16 and t.get_device() == pool.device_index and t.dim() == 3:
+            rows, h, width = t.shape
+            token, head, value = t.stride()
+            if (width == d and (n is None or rows == n) and (heads is None or h == heads) and value == 1
+                    and (head == d or h == 1) and not token % 8):
+                return token
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.dim() != 3 or t.shape[2] != head_dim or (n is not None and t.shape[0] != n) or \
-            (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [{'N' if n is None else n}, {'Hq' if heads is None else heads}, {head_dim}], "
+    _same_device(pool.k_cache.device, **{name: t})
+    if t.dim() != 3 or t.shape[2] != d or (n is not None and t.shape[0] != n) or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [{'N' if n is None else n}, {'Hq' if heads is None else heads}, {d}], "
                          f"got {tuple(t.shape)}")
     token, head, value = t.stride()
-    if t.shape[0] <= 1:
-        token = t.shape[1] * head_dim  # a size of one says nothing about its stride
-    if value != 1 or (head != head_dim and t.shape[1] > 1) or token % 8:
-        raise ValueError(f"{name}'s heads must be contiguous, its tokens a multiple of 8 values apart; strides {t.stride()}")
-    return token
+    if t.shape[0] <= 1 and value == 1 and (head == d or t.shape[1] == 1):
+        return t.shape[1] * d  # a size of one says nothing about its stride
+    raise ValueError(f"{name}'s heads must be contiguous, its tokens a multiple of 8 values apart; strides {t.stride()}")
 
 
 def norm_rope_and_cache(pool: PagedKVPool, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -394,39 +409,38 @@ def norm_rope_and_cache(pool: PagedKVPool, q: torch.Tensor, k: torch.Tensor, v: 
     first rot_dim values by ``positions`` (int32 [N]): pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1)
     when ``interleaved``; None: no rotation, positions are not used.  ``out`` may be q itself.
     A negative slot skips a token's cache write only."""
-    qs = _head_rows(q, "q", None, None, pool.head_dim)
+    qs = _head_rows(q, "q", None, None, pool)
     n, hq, d = q.shape
-    ks = _head_rows(k, "k", n, pool.kv_heads, d)
-    vs = _head_rows(v, "v", n, pool.kv_heads, d)
-    _need(slot_mapping, torch.int32, "slot_mapping", 1)
+    ks = _head_rows(k, "k", n, pool.kv_heads, pool)
+    vs = _head_rows(v, "v", n, pool.kv_heads, pool)
+    _check(slot_mapping, torch.int32, "slot_mapping", 1, pool)
     if slot_mapping.shape[0] != n:
         raise ValueError("q and slot_mapping disagree in shape")
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            _need(w, torch.bfloat16, name, 1)
+            _check(w, torch.bfloat16, name, 1, pool)
             if w.shape[0] != d:
                 raise ValueError(f"{name} must be [{d}]")
+    table = pos = max_position = rot_dim = 0
     if cos_sin is not None:
-        _need(cos_sin, torch.float32, "cos_sin", 2)
-        _need(positions, torch.int32, "positions", 1)
+        _check(cos_sin, torch.float32, "cos_sin", 2, pool)
+        _check(positions, torch.int32, "positions", 1, pool)
         if positions.shape[0] != n:
             raise ValueError("q and positions disagree in shape")
-        if cos_sin.numel() == 0:  # its NULL pointer would mean no rotation
+        max_position, rot_dim = cos_sin.shape
+        if not max_position or not rot_dim:  # its NULL pointer would mean no rotation
             raise ValueError("cos_sin must not be empty")
+        table, pos = cos_sin.data_ptr(), positions.data_ptr()
     if out is None:
         out = torch.empty(n, hq, d, dtype=q.dtype, device=q.device)
-    outs = _head_rows(out, "out", n, hq, d)
-    _same_device(pool.k_cache.device, q=q, k=k, v=v, slot_mapping=slot_mapping, positions=positions, cos_sin=cos_sin,
-                 q_weight=q_weight, k_weight=k_weight, out=out)
+    outs = _head_rows(out, "out", n, hq, pool)
     a = NormRope(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
                  0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
-                 0 if cos_sin is None else cos_sin.data_ptr(), 0 if cos_sin is None else positions.data_ptr(),
-                 slot_mapping.data_ptr(), out.data_ptr(), outs, n, hq,
-                 0 if cos_sin is None else cos_sin.shape[1], 0 if cos_sin is None else cos_sin.shape[0],
-                 1 if interleaved else 0, float(eps), 0)
-    with _on_device(pool):
-        check(_lib.load().pkv_norm_rope_and_cache(_handle(pool), ctypes.byref(a), _stream(stream)),
-              "norm_rope_and_cache")
+                 table, pos, slot_mapping.data_ptr(), out.data_ptr(), outs, n, hq, rot_dim, max_position,
+                 1 if interleaved else 0, float(eps))
+    st = _lib.load().pkv_norm_rope_and_cache(pool.handle, ctypes.byref(a), _pool_stream(pool, stream))
+    if st:
+        check(st, "norm_rope_and_cache")
     return out
 
 
@@ -464,34 +478,34 @@ def shared_prefix_decode(pool: PagedKVPool, q: torch.Tensor, block_tables: torch
     lengths, max_suffix_len every sequence's own tokens, context_lens[b] - prefix.  q is
     [B, Hq, d], or [B, k, Hq, d] for k draft tokens per sequence, all of which see the whole prefix.
     ``workspace`` (a uint8 CUDA tensor) is allocated here when not given."""
-    _need(q, torch.bfloat16, "q", 4 if q.dim() == 4 else 3)
-    _need(block_tables, torch.int32, "block_tables", 2)
-    _need(context_lens, torch.int32, "context_lens", 1)
-    _need(group_starts, torch.int32, "group_starts", 1)
-    _need(prefix_lens, torch.int32, "prefix_lens", 1)
-    if out is not None:
-        _need(out, torch.bfloat16, "out", q.dim())
-    b, nq, hq = check_decode_shapes(pool.head_dim, q.shape, block_tables.shape, context_lens.shape,
-                                    None if out is None else out.shape)
+    ndim = 4 if q.dim() == 4 else 3
+    _check(q, torch.bfloat16, "q", ndim, pool)
+    _check(block_tables, torch.int32, "block_tables", 2, pool)
+    _check(context_lens, torch.int32, "context_lens", 1, pool)
+    _check(group_starts, torch.int32, "group_starts", 1, pool)
+    _check(prefix_lens, torch.int32, "prefix_lens", 1, pool)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check(out, torch.bfloat16, "out", ndim, pool)
+    tables_shape = block_tables.shape
+    b, nq, hq = check_decode_shapes(pool.head_dim, q.shape, tables_shape, context_lens.shape, out.shape)
     groups = prefix_lens.shape[0]
     if group_starts.shape[0] != groups + 1:
         raise ValueError("group_starts must have one entry more than prefix_lens")
-    if out is None:
-        out = torch.empty_like(q)
     if workspace is None:
         workspace = torch.empty(
             shared_prefix_workspace_bytes(pool, b, hq, groups, max_prefix_len, max_suffix_len, nq, partition_blocks),
             dtype=torch.uint8, device=q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    _same_device(pool.k_cache.device, q=q, block_tables=block_tables, context_lens=context_lens,
-                 group_starts=group_starts, prefix_lens=prefix_lens, out=out, workspace=workspace)
-    with _on_device(pool):
-        check(_lib.load().pkv_shared_prefix_decode(
-            _handle(pool), _ptr(q), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), b, hq,
-            _ptr(group_starts), _ptr(prefix_lens), groups, int(max_prefix_len), int(max_suffix_len), float(scale),
-            _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _options(partition_blocks, num_queries=nq), _stream(stream)), "shared_prefix_decode")
+    elif workspace.get_device() != pool.device_index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the pool's device")
+    st = _lib.load().pkv_shared_prefix_decode(
+        pool.handle, q.data_ptr(), block_tables.data_ptr(), tables_shape[1], context_lens.data_ptr(), b, hq,
+        group_starts.data_ptr(), prefix_lens.data_ptr(), groups, int(max_prefix_len), int(max_suffix_len), float(scale),
+        out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _options(partition_blocks, num_queries=nq),
+        _pool_stream(pool, stream))
+    if st:
+        check(st, "shared_prefix_decode")
     return out
 
 

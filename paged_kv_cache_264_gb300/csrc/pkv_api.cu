@@ -321,12 +321,26 @@ cudaError_t launch_decode(const pkv_pool* pool, const Plan& plan, const pkv::Dec
                                           : pkv::launch_decode_bf16(p, plan.cols, s);
 }
 
-// Whether the pool's device is the current one: a launch on another device's stream fails,
-// and the kernels' attributes are per device.
-bool on_pool_device(const pkv_pool* pool) {
-  int dev = -1;
-  return cudaGetDevice(&dev) == cudaSuccess && dev == pool->device;
-}
+// Makes the pool's device current while it lives: a launch on another device's stream fails, and
+// the kernels' attributes are per device.
+class OnPoolDevice {
+ public:
+  explicit OnPoolDevice(const pkv_pool* pool) {
+    ok_ = cudaGetDevice(&before_) == cudaSuccess;
+    if (ok_ && before_ != pool->device) {
+      ok_ = cudaSetDevice(pool->device) == cudaSuccess;
+      switched_ = ok_;
+    }
+  }
+  ~OnPoolDevice() {
+    if (switched_) cudaSetDevice(before_);
+  }
+  explicit operator bool() const { return ok_; }
+
+ private:
+  int before_ = 0;
+  bool ok_ = false, switched_ = false;
+};
 
 // Layout of a shared-prefix call's workspace and the plan of its suffix pass.
 struct PrefixPlan {
@@ -632,7 +646,8 @@ pkv_status pkv_reserve_slots(const pkv_pool* pool, int32_t* block_tables, int ma
   // positions and slots are int32
   if (int64_t(max_blocks_per_seq) * pkv::kBlockSize > INT32_MAX) return PKV_ERR_INVALID_ARG;
   if (num_seqs > pkv::kMaxSlotSeqs || pool->num_blocks * pkv::kBlockSize > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-  if (!on_pool_device(pool)) return PKV_ERR_INVALID_ARG;
+  const OnPoolDevice device(pool);
+  if (!device) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
   pkv::SlotParams p{};
   p.block_tables = block_tables;
   p.context_lens = context_lens;
@@ -671,7 +686,8 @@ pkv_status pkv_norm_rope_and_cache(const pkv_pool* pool, const pkv_norm_rope* a,
     if (a->rot_dim % 16) return PKV_ERR_UNSUPPORTED;
   }
   if (int64_t(a->num_q_heads) + 2 * int64_t(pool->kv_heads) > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
-  if (!on_pool_device(pool)) return PKV_ERR_INVALID_ARG;
+  const OnPoolDevice device(pool);
+  if (!device) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
   pkv::RopeParams p{};
   p.q = a->q;
   p.k = a->k;
@@ -747,7 +763,8 @@ pkv_status pkv_shared_prefix_decode(const pkv_pool* pool, const void* q, const i
   if (!(scale == scale)) return PKV_ERR_INVALID_ARG;  // NaN
   if (!workspace || workspace_bytes < plan.bytes) return PKV_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
-  if (!on_pool_device(pool)) return PKV_ERR_INVALID_ARG;
+  const OnPoolDevice device(pool);
+  if (!device) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
   char* ws = static_cast<char*>(workspace);
 
   pkv::PrefixParams x{};
