@@ -24,6 +24,7 @@ namespace {
 template <int D>
 __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p) {
   constexpr int kDPV = D / 32;
+  constexpr int kAhead = 8;
   constexpr uint32_t kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   griddep_wait();
@@ -59,32 +60,55 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
   const int n = nsuf + npre;
   auto pre_row = [&](int i) { return first + int64_t(i >> twice) * kPrefixRows + (twice && (i & 1) ? d.rows : 0); };
   auto state = [&](int i) { return i < nsuf ? sml[i] : p.ml[pre_row(i - nsuf)]; };
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, state(i).x);
+  // lane i holds partials i, i + 32, ...; the first 32 stay in registers
+  const float2 mine = lane < n ? state(lane) : make_float2(-INFINITY, 0.0f);
+  float M = mine.x;
+  for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, state(i).x);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
   float L = 0.0f, a[kDPV] = {};
   for (int i0 = 0; i0 < n; i0 += 32) {
     float f = 0.0f;
     if (i0 + lane < n) {
-      const float2 s = state(i0 + lane);
+      const float2 s = i0 == 0 ? mine : state(i0 + lane);
       f = exp2f(s.x - M);
       L = fmaf(f, s.y, L);
     }
-#pragma unroll 4
-    for (int j = 0; j < min(32, n - i0); ++j) {
-      const float w = __shfl_sync(kFull, f, j);
-      if (w == 0.0f) continue;  // a stream without tiles leaves no accumulator
-      const int i = i0 + j;
-      const float* src = i < nsuf ? sacc + int64_t(i) * D : p.acc + pre_row(i - nsuf) * D + lane * kDPV;
+    const int here = min(32, n - i0);
+    for (int j0 = 0; j0 < here; j0 += kAhead) {  // kAhead accumulators on their way at a time
+      float v[kAhead][kDPV], w[kAhead];
 #pragma unroll
-      for (int e = 0; e < kDPV; ++e) a[e] = fmaf(w, src[e], a[e]);
+      for (int u = 0; u < kAhead; ++u) {
+        w[u] = __shfl_sync(kFull, f, (j0 + u) & 31);
+        if (j0 + u >= here) w[u] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kDPV; ++e) v[u][e] = 0.0f;
+        if (w[u] != 0.0f) {  // a stream without tiles leaves no accumulator
+          const int i = i0 + j0 + u;
+          const float* src = i < nsuf ? sacc + int64_t(i) * D : p.acc + pre_row(i - nsuf) * D + lane * kDPV;
+          if constexpr (kDPV == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            v[u][0] = x.x; v[u][1] = x.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int e = 0; e < kDPV; ++e) a[e] = fmaf(w[u], v[u][e], a[e]);
     }
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(kFull, L, o);
+  uint32_t packed[kDPV / 2];
 #pragma unroll
-  for (int i = 0; i < kDPV; ++i) out[i] = __float2bfloat16_rn(L == 0.0f ? 0.0f : a[i] / L);
+  for (int i = 0; i < kDPV / 2; ++i)
+    packed[i] = L == 0.0f ? 0u : pack_bf16x2(a[2 * i] / L, a[2 * i + 1] / L);
+  if constexpr (kDPV == 4) *reinterpret_cast<uint2*>(out) = make_uint2(packed[0], packed[1]);
+  else *reinterpret_cast<uint32_t*>(out) = packed[0];
 }
 
 }  // namespace

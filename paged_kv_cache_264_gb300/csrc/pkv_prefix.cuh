@@ -24,6 +24,12 @@ __host__ __device__ __forceinline__ int64_t partial_rows(int rows) {
   return rows <= kPrefixRows / 2 ? 2 * int64_t(rows) : rows;
 }
 
+// a / b for non-negative a and positive b: work lines are short enough for 32 bits as a rule, and a
+// 64-bit division is some hundred instructions.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
 struct PrefixGroup {
   int first_seq, rows, units, tiles;  // units per kv head
   int64_t w_base, row_base;
@@ -46,6 +52,42 @@ __device__ __forceinline__ bool prefix_group(const PrefixParams& p, int g, Prefi
   x.units = (x.rows + kPrefixRows - 1) / kPrefixRows;
   x.tiles = ok ? (len + kPrefixTile - 1) / kPrefixTile : 0;
   return ok;
+}
+
+// The scan of up to 32 groups, a lane to a group, by each warp for itself: no barrier, one round
+// trip to memory.
+constexpr int kFewGroups = 32;
+struct PrefixLanes {
+  PrefixGroup x;  // lane g's group
+};
+__device__ __forceinline__ int64_t prefix_scan_few(const PrefixParams& p, PrefixLanes& me) {
+  const int lane = threadIdx.x & 31;
+  me.x = PrefixGroup{};
+  bool ok = true;
+  if (lane < p.num_groups) ok = prefix_group(p, lane, me.x);
+  const int64_t w = int64_t(me.x.units) * p.kv_heads * me.x.tiles, r = partial_rows(me.x.rows) * p.kv_heads;
+  int64_t iw = w, ir = r;
+  for (int o = 1; o < p.num_groups; o <<= 1) {
+    const int64_t a = __shfl_up_sync(0xffffffffu, iw, o), b = __shfl_up_sync(0xffffffffu, ir, o);
+    if (lane >= o) {
+      iw += a;
+      ir += b;
+    }
+  }
+  me.x.w_base = iw - w;
+  me.x.row_base = ir - r;
+  const int64_t total = __shfl_sync(0xffffffffu, iw, p.num_groups > 0 ? p.num_groups - 1 : 0);
+  return __all_sync(0xffffffffu, ok) ? total : -1;
+}
+__device__ __forceinline__ PrefixGroup lane_group(const PrefixLanes& me, int g) {
+  PrefixGroup x;
+  x.first_seq = __shfl_sync(0xffffffffu, me.x.first_seq, g);
+  x.rows = __shfl_sync(0xffffffffu, me.x.rows, g);
+  x.units = __shfl_sync(0xffffffffu, me.x.units, g);
+  x.tiles = __shfl_sync(0xffffffffu, me.x.tiles, g);
+  x.w_base = __shfl_sync(0xffffffffu, me.x.w_base, g);
+  x.row_base = __shfl_sync(0xffffffffu, me.x.row_base, g);
+  return x;
 }
 
 // Fill the scan (all NT threads of the CTA); returns the work tiles of the call, or -1 where
@@ -99,10 +141,10 @@ __device__ __forceinline__ int64_t prefix_scan(const PrefixParams& p, const Pref
 // last CTA is without one (its partial would be read unwritten).
 __device__ __forceinline__ int stretch_ctas(int64_t total, int grid) { return int(min(total, int64_t(grid))); }
 // CTA c's stretch of `total` work tiles starts here.
-__device__ __forceinline__ int64_t stretch_start(int64_t total, int ctas, int c) { return total * c / ctas; }
+__device__ __forceinline__ int64_t stretch_start(int64_t total, int ctas, int c) { return div_pos(total * c, ctas); }
 // The CTA whose stretch holds work tile w: the last one that starts at or before it.
 __device__ __forceinline__ int stretch_owner(int64_t total, int ctas, int64_t w) {
-  return int(((w + 1) * ctas - 1) / total);
+  return int(div_pos((w + 1) * ctas - 1, total));
 }
 
 // A walk along one CTA's stretch: one (kv head, unit) at a time.
@@ -123,13 +165,26 @@ __device__ __forceinline__ void walk_place(PrefixWalk& k, int cta) {
   k.partial = k.x.row_base + int64_t(k.kvh) * partial_rows(k.x.rows) + k.row0 + int64_t(cta) * kPrefixRows;
 }
 
-// The first piece of CTA `cta`'s stretch; false if it has none.
-__device__ __forceinline__ bool walk_begin(const PrefixParams& p, const PrefixScan& sc, int64_t total, int cta,
-                                           PrefixWalk& k) {
+// This CTA's stretch; false if it has none.
+__device__ __forceinline__ bool walk_range(const PrefixParams& p, int64_t total, int cta, PrefixWalk& k) {
   const int ctas = stretch_ctas(total, p.grid);
-  if (cta >= ctas) return false;
+  if (total <= 0 || cta >= ctas) return false;
   k.w = stretch_start(total, ctas, cta);
   k.w_end = stretch_start(total, ctas, cta + 1);
+  return true;
+}
+// The first piece of the stretch, once k.g and k.x are the group that holds its first tile.
+__device__ __forceinline__ void walk_first(PrefixWalk& k, int cta) {
+  const int64_t in_group = k.w - k.x.w_base;
+  const int u = int(div_pos(in_group, k.x.tiles));  // kv head * units + unit
+  k.tile0 = int(in_group - int64_t(u) * k.x.tiles);
+  k.kvh = u / k.x.units;
+  k.unit = u - k.kvh * k.x.units;
+  walk_place(k, cta);
+}
+__device__ __forceinline__ bool walk_begin(const PrefixParams& p, const PrefixScan& sc, int64_t total, int cta,
+                                           PrefixWalk& k) {
+  if (!walk_range(p, total, cta, k)) return false;
   int lo = 0, hi = p.num_groups;  // the last group that starts at or before w (empty ones share a start)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -139,12 +194,16 @@ __device__ __forceinline__ bool walk_begin(const PrefixParams& p, const PrefixSc
   prefix_group(p, lo, k.x);
   k.x.w_base = sc.base[lo].x;
   k.x.row_base = sc.base[lo].y;
-  const int64_t in_group = k.w - k.x.w_base;
-  const int u = int(in_group / k.x.tiles);  // kv head * units + unit
-  k.tile0 = int(in_group - int64_t(u) * k.x.tiles);
-  k.kvh = u / k.x.units;
-  k.unit = u - k.kvh * k.x.units;
-  walk_place(k, cta);
+  walk_first(k, cta);
+  return true;
+}
+__device__ __forceinline__ bool walk_begin_few(const PrefixParams& p, const PrefixLanes& me, int64_t total, int cta,
+                                               PrefixWalk& k) {
+  if (!walk_range(p, total, cta, k)) return false;
+  const uint32_t at = __ballot_sync(0xffffffffu, int(threadIdx.x & 31) < p.num_groups && me.x.w_base <= k.w);
+  k.g = 31 - __clz(at);
+  k.x = lane_group(me, k.g);
+  walk_first(k, cta);
   return true;
 }
 
@@ -179,30 +238,23 @@ __device__ __forceinline__ int64_t prefix_q_row(const PrefixParams& p, const Pre
 }
 
 // What the suffix and merge passes need of this CTA's share of the sequences; run by `warps` of
-// its warps, this one the `warp`-th of them.
-__device__ __forceinline__ void prefix_describe(const PrefixParams& p, const PrefixScan& sc, int64_t total, int warp,
-                                                int warps) {
+// its warps, this one the `warp`-th of them.  group_of(b, x): the whole warp asks for sequence b's
+// group; false where it is in none.
+template <typename F>
+__device__ __forceinline__ void prefix_describe(const PrefixParams& p, int64_t total, int warp, int warps, F&& group_of) {
   const int lane = threadIdx.x & 31;
   for (int b = blockIdx.x * warps + warp; b < p.num_seqs; b += gridDim.x * warps) {
     const int T = __ldg(p.context_lens + b);
     PrefixSeq d{};
     PrefixGroup x{};
-    int len = 0;
-    if (total >= 0 && p.num_groups > 0) {
-      int lo = 0, hi = p.num_groups;
-      while (hi - lo > 1) {  // the last group that starts at or before b
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(p.group_starts + mid) <= b) lo = mid; else hi = mid;
-      }
-      if (b >= __ldg(p.group_starts + lo) && b < __ldg(p.group_starts + lo + 1)) {
-        prefix_group(p, lo, x);
-        len = __ldg(p.prefix_lens + lo);
-        d.w_base = sc.base[lo].x;
-        d.row_base = sc.base[lo].y;
-        d.tiles = x.tiles;
-        d.rows = x.rows;
-        d.first_row = (b - x.first_seq) * p.num_queries * p.group;
-      }
+    int len = 0, g = 0;
+    if (total >= 0 && p.num_groups > 0 && group_of(b, g, x)) {
+      len = __ldg(p.prefix_lens + g);
+      d.w_base = x.w_base;
+      d.row_base = x.row_base;
+      d.tiles = x.tiles;
+      d.rows = x.rows;
+      d.first_row = (b - x.first_seq) * p.num_queries * p.group;
     }
     d.total = total;
     d.suffix_len = T - len;
@@ -220,6 +272,32 @@ __device__ __forceinline__ void prefix_describe(const PrefixParams& p, const Pre
     }
   }
   if (total < 0 && blockIdx.x == 0 && warp == 0 && lane == 0) set_error(p.err, kErrPrefix);
+}
+__device__ __forceinline__ void prefix_describe_many(const PrefixParams& p, const PrefixScan& sc, int64_t total, int warp,
+                                                     int warps) {
+  prefix_describe(p, total, warp, warps, [&](int b, int& g, PrefixGroup& x) {
+    int lo = 0, hi = p.num_groups;
+    while (hi - lo > 1) {  // the last group that starts at or before b
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.group_starts + mid) <= b) lo = mid; else hi = mid;
+    }
+    if (b < __ldg(p.group_starts + lo) || b >= __ldg(p.group_starts + lo + 1)) return false;
+    g = lo;
+    prefix_group(p, lo, x);
+    x.w_base = sc.base[lo].x;
+    x.row_base = sc.base[lo].y;
+    return true;
+  });
+}
+__device__ __forceinline__ void prefix_describe_few(const PrefixParams& p, const PrefixLanes& me, int64_t total) {
+  prefix_describe(p, total, 0, 1, [&](int b, int& g, PrefixGroup& x) {
+    const int first = me.x.first_seq, n = me.x.rows / (p.num_queries * p.group);
+    const uint32_t at = __ballot_sync(0xffffffffu, b >= first && b < first + n);
+    if (at == 0) return false;
+    g = __ffs(at) - 1;
+    x = lane_group(me, g);
+    return true;
+  });
 }
 
 }  // namespace pkv

@@ -83,10 +83,8 @@ struct PrefixSync {
   uint64_t drain[2];
   uint32_t tmem;
   uint32_t abort;
-  longlong2 base[25];                    // scan of a call of up to 24 groups
 };
 static_assert(sizeof(PrefixSync) <= 1008, "barriers fit their space");
-constexpr int kFewGroups = 24;
 
 // A place in a ring of N stages: the stage, and the parity of the phase that its current use
 // completes.
@@ -209,14 +207,22 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
   }
   if (warp == C::kMmaWarp) tmem_alloc(&sy->tmem, C::kTmemCols);
   griddep_wait();  // inputs may come from the previous kernel in the stream
-  // The scan of a few groups stays, and a spare warp describes the sequences beside the work; that
-  // of many lies where the ring will be, and is used up first.
+  // The scan of up to 32 groups is each warp's own, and one describes the sequences beside the work;
+  // that of many lies where the ring will be, and is used up first.
   const bool few = p.num_groups <= kFewGroups;
-  PrefixScan sc{few ? sy->base : reinterpret_cast<longlong2*>(ring) + 32, reinterpret_cast<longlong2*>(ring)};
-  const int64_t total = prefix_scan<C::kThreads>(p, sc);
-  if (!few) prefix_describe(p, sc, total, warp, C::kThreads / 32);
+  PrefixLanes lanes;
   PrefixWalk k;
-  bool more = total > 0 && walk_begin(p, sc, total, blockIdx.x, k);
+  int64_t total;
+  bool more;
+  if (few) {
+    total = prefix_scan_few(p, lanes);
+    more = walk_begin_few(p, lanes, total, blockIdx.x, k);
+  } else {
+    PrefixScan sc{reinterpret_cast<longlong2*>(ring) + 32, reinterpret_cast<longlong2*>(ring)};
+    total = prefix_scan<C::kThreads>(p, sc);
+    prefix_describe_many(p, sc, total, warp, C::kThreads / 32);
+    more = walk_begin(p, sc, total, blockIdx.x, k);
+  }
   tc_fence_before();
   __syncthreads();  // the ring's memory is free again; the barriers and the tensor memory are there
   tc_fence_after();
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     }
     // the copies in flight land before the CTA can end (the stages filled last)
     for (uint32_t j = it > R ? it - R : 0; j < it; ++j) (void)mbar_wait_bounded(full + j % R, (j / R) & 1);
-    if (few && !is_v) prefix_describe(p, sc, total, 0, 1);
+    if (few && !is_v) prefix_describe_few(p, lanes, total);
   } else if (warp == C::kMmaWarp || warp == C::kMmaWarp + 1) {
     // ---------------------------------------------------------------- products of stream s
     // The whole warp runs this with warp-uniform values; one elected lane issues.
@@ -497,33 +503,79 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     const uint64_t scale2 = f32x2(scale, scale);
     uint32_t cnt = 0, tiles = 0;  // this stream's steps and all tiles before this piece
     bool alive = true;
-    // this thread's row of Q of the piece at k, ahead of its use
-    uint4 w[D / 8];
-    auto load_q = [&]() {
-      const int row = (k.x.rows > 128 ? s * 128 : 0) + r;
+    // The piece done last, whose partial is written while the next one's Q is on its way.
+    bool pending = false, any = false, idle = false;
+    int nrows = 0;
+    int64_t to = 0;
+    float m = kMaxFloor, l = 0.0f;
+    for (;;) {
+      uint4 w[D / 8];  // this thread's row of Q of the piece at k
+      if (more) {
+        const int row = (k.x.rows > 128 ? s * 128 : 0) + r;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (row < k.nrows) {
-        const auto* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                       prefix_q_row(p, k.x, k.kvh, k.row0 + row) * D);
+        for (int c = 0; c < D / 8; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < k.nrows) {
+          const auto* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                         prefix_q_row(p, k.x, k.kvh, k.row0 + row) * D);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) w[c] = __ldg(q + c);
+          for (int c = 0; c < D / 8; ++c) w[c] = __ldg(q + c);
+        }
       }
-    };
-    if (more) load_q();
-    while (more) {
+      if (pending) {
+        // ---- its partial.  A thread holds a row, so its stores would touch 32 lines at a time; the
+        // warp turns its 32 rows through its part of the Q tile (free: every S is done), 64 values
+        // of each row at a time (32 at head_dim 64), and stores whole lines.
+        if (!wait_all(&sy->pv_done[s][1], (cnt - 1) & 1)) {
+          alive = false;
+          break;
+        }
+        if (!idle) {
+          tc_fence_after();
+          unsigned char* turn = qt + (warp & 3) * (C::kTileBytes / 4);
+          constexpr int kCols = C::kTileBytes / 4 / 32 / 4;  // columns per round
+          constexpr int kChunks = kCols / 4;                 // 16-byte chunks of a row in a round
+          const int wrow = (warp & 3) * 32, live = min(32, nrows - wrow);
+          float* dst = p.acc + (to + wrow) * D;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += kCols) {
+#pragma unroll
+            for (int h = 0; h < kCols; h += 32) {
+              float o[32];
+              tmem_ld32(o_addr + c0 + h, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<float4*>(turn + lane * (kCols * 4) + (((h / 4 + e) ^ (lane % kChunks)) << 4)) =
+                    any ? make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int j = 0; j < kChunks; ++j) {
+              const int row = j * (32 / kChunks) + lane / kChunks, chunk = lane % kChunks;
+              if (row < live)
+                *reinterpret_cast<float4*>(dst + row * D + c0 + chunk * 4) =
+                    *reinterpret_cast<const float4*>(turn + row * (kCols * 4) + ((chunk ^ (row % kChunks)) << 4));
+            }
+            __syncwarp();
+          }
+          if (r < nrows) p.ml[to + r] = make_float2(m, l);
+          tc_fence_before();
+        }
+        mbar_arrive(sy->o_free + s);
+        pending = false;
+      }
+      if (!more) break;
       const bool two = k.x.rows > 128;
       const int n = k.tile1 - k.tile0;
       const int ns = steps_of(two, k.nrows, n, s);
       const uint32_t tiles0 = tiles;
       tiles += n;
-      const int row0 = two ? s * 128 : 0;              // the stream's first row within the unit
-      const int nrows = min(128, k.nrows - row0);      // its rows
-      const int64_t to = k.partial + (two ? s * 128 : s * k.x.rows);
+      const int row0 = two ? s * 128 : 0;         // the stream's first row within the unit
+      nrows = min(128, k.nrows - row0);           // its rows
+      to = k.partial + (two ? s * 128 : s * k.x.rows);
       if (ns == 0) {
         if (r < nrows) p.ml[to + r] = make_float2(kMaxFloor, 0.0f);  // no tile of its own: weighs nothing
         more = walk_next(p, blockIdx.x, k);
-        if (more) load_q();
         continue;
       }
       const int tile0 = k.tile0, nblk = __ldg(p.prefix_lens + k.g) / kBlockSize;
@@ -538,9 +590,10 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
         fence_proxy_async_smem();
         mbar_arrive(sy->q_ready + s);
       }
-      const bool idle = (warp & 3) * 32 >= nrows;  // none of the warp's rows exists
-      float m = kMaxFloor, l = 0.0f;
-      bool any = false;
+      idle = (warp & 3) * 32 >= nrows;  // none of the warp's rows exists
+      m = kMaxFloor;
+      l = 0.0f;
+      any = false;
       uint32_t have = 0, slot = 0;
 #pragma unroll 1
       for (int g = 0; g < 2 * ns; ++g) {
@@ -633,48 +686,8 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       }
       if (!alive) break;
       cnt += ns;
+      pending = true;
       more = walk_next(p, blockIdx.x, k);
-      if (more) load_q();  // on its way while this piece's partial is written
-      // ---- the piece's partial.  A thread holds a row, so its stores would touch 32 lines at a
-      // time; the warp turns its 32 rows through its part of the Q tile (free: every S is done),
-      // 64 values of each row at a time, and stores whole lines.
-      if (!wait_all(&sy->pv_done[s][1], (cnt - 1) & 1)) {
-        alive = false;
-        break;
-      }
-      if (!idle) {
-        tc_fence_after();
-        unsigned char* turn = qt + (warp & 3) * (C::kTileBytes / 4);
-        constexpr int kCols = C::kTileBytes / 4 / 32 / 4;  // columns per round: 64 (D = 128) or 32
-        constexpr int kChunks = kCols / 4;                 // 16-byte chunks of a row in a round
-        const int wrow = (warp & 3) * 32, live = min(32, nrows - wrow);
-        float* dst = p.acc + (to + wrow) * D;
-#pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += kCols) {
-#pragma unroll
-          for (int h = 0; h < kCols; h += 32) {
-            float o[32];
-            tmem_ld32(o_addr + c0 + h, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<float4*>(turn + lane * (kCols * 4) + (((h / 4 + e) ^ (lane % kChunks)) << 4)) =
-                  any ? make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          }
-          __syncwarp();
-#pragma unroll 4
-          for (int j = 0; j < kChunks; ++j) {
-            const int row = j * (32 / kChunks) + lane / kChunks, chunk = lane % kChunks;
-            if (row < live)
-              *reinterpret_cast<float4*>(dst + row * D + c0 + chunk * 4) =
-                  *reinterpret_cast<const float4*>(turn + row * (kCols * 4) + ((chunk ^ (row % kChunks)) << 4));
-          }
-          __syncwarp();
-        }
-        if (r < nrows) p.ml[to + r] = make_float2(m, l);
-        tc_fence_before();
-      }
-      mbar_arrive(sy->o_free + s);
     }
     if (!alive && lane == 0) {
       *abort = 1;
