@@ -10,9 +10,10 @@
 //     P = 2^(S * scale - m)    a thread to a row, its logits in registers: no shuffles
 //     O += P V     128 x D x 128, P in tensor memory (bf16, over S's columns), V as it lies in the
 //                  pool (token-major, the contracted index outermost: an MN-major operand)
-// in halves of 64 tokens: while the softmax works on one half, the other half's product over V and
-// the next tile's S of that half run.  (Whole tiles at a time left each stream a chain of S, softmax
-// and product with only the other stream's to fill it.)
+// The softmax hands P over in halves of 64 tokens, so that the first half's product over V runs under
+// the second half's softmax.  S is formed for whole tiles: its products read both operands from
+// shared memory, 8 KB for 64 cycles of arithmetic at 128 columns, which is what shared memory
+// delivers; at 64 columns they took as long for half the work.
 // The running maximum is lazy (kMaxSlack): O is rescaled in tensor memory only when a row's
 // logits pass its maximum by 2^8.  P enters the product as bf16, and the softmax sum adds the
 // same rounded weights, so that numerator and denominator agree.
@@ -24,9 +25,16 @@
 // sum adds the unrounded ones, since the rounded ones carry the scale).
 //
 // Warps: two warpgroups of softmax (one per stream, which also load Q and write the partials),
-// two warps that fill the ring of K and of V tiles by TMA (8 blocks to a tile, each wherever it
-// lies in the pool), one warp per stream that issues its products (one for both let a stream's waits
-// hold up the other's products), and the converting warpgroup for INT8 and FP8.  Every wait is bounded; after one that gave up the
+// one warp that fills the ring of K and V tiles by TMA (8 blocks to a tile, each wherever it lies
+// in the pool), one warp per stream that issues its products (one for both let a stream's waits
+// hold up the other's products), and the converting warpgroup for INT8 and FP8.
+//
+// A barrier's wait is for a parity, which tells a phase from the one before it only if the waiter
+// has seen that one complete.  So one warp fills the ring, and each issuing warp waits for and
+// releases every stage in ring order, those of the other stream's tiles too (a warp that filled
+// only K stages, or skipped stages, could run into one still in use).
+//
+// Every wait is bounded; after one that gave up the
 // CTA takes no further work, lets its copies and products land, frees its tensor memory and ends.
 //
 // A prefix ends at a block (16 tokens), not at a tile: the product over V takes only the steps of
@@ -57,7 +65,7 @@ struct PrefixCfg {
   static constexpr int kSlots = kQuant ? (D == 128 ? 4 : 8) : 0;
   static_assert(!kQuant || 2 * kSlots - 3 >= kStages, "a scale slot is free when it is written again");
   static constexpr int kThreads = kQuant ? 512 : 384;
-  static constexpr int kLoadK = 8, kMmaWarp = 9, kLoadV = 11, kConvertWarp = 12;  // 9 and 10: one per stream
+  static constexpr int kLoadWarp = 8, kMmaWarp = 9, kDescribeWarp = 11, kConvertWarp = 12;  // 9 and 10: one per stream
   // Registers: the softmax threads hold a row of 128 logits; what the other warpgroups give up
   // goes to them.  The shares' sum is checked against the kernel's own count before a launch.
   static constexpr int kSoftmaxRegs = kQuant ? 184 : 200;
@@ -78,8 +86,8 @@ struct PrefixSync {
   uint64_t full[16], empty[16];          // operand ring stages
   uint64_t raw_full[8], raw_empty[8];    // code ring stages
   uint64_t scales[8];                    // scale slots
-  uint64_t q_ready[2], o_free[2];                        // per stream
-  uint64_t s_ready[2][2], p_ready[2][2], pv_done[2][2];  // per stream and half of a tile
+  uint64_t q_ready[2], s_ready[2], o_free[2];   // per stream
+  uint64_t p_ready[2][2], pv_done[2][2];        // per stream and half of a tile
   uint64_t drain[2];
   uint32_t tmem;
   uint32_t abort;
@@ -192,8 +200,8 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     for (int i = 0; i < C::kSlots; ++i) mbar_init(sy->scales + i, 128);
     for (int s = 0; s < 2; ++s) {
       mbar_init(sy->q_ready + s, 128);
+      mbar_init(sy->s_ready + s, 1);
       for (int h = 0; h < 2; ++h) {
-        mbar_init(&sy->s_ready[s][h], 1);
         mbar_init(&sy->p_ready[s][h], 128);
         mbar_init(&sy->pv_done[s][h], 1);
       }
@@ -248,9 +256,9 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
   // two: the streams hold different rows; else they share the tiles out between them.
   auto steps_of = [&](bool two, int nrows, int n, int s) { return two ? (s == 0 || nrows > 128 ? n : 0) : (n + 1 - s) / 2; };
 
-  if (warp >= C::kLoadK && warp < C::kLoadK + 4) regs_down<C::kIssueRegs>();
-  if (warp == C::kLoadK || warp == C::kLoadV) {
-    // ---------------------------------------------------------------- K (or V) tiles -> ring
+  if (warp >= C::kLoadWarp && warp < C::kLoadWarp + 4) regs_down<C::kIssueRegs>();
+  if (warp == C::kLoadWarp) {
+    // ---------------------------------------------------------------- K and V tiles -> ring
     // The whole warp runs this with warp-uniform values; one elected lane issues (a copy per lane
     // costs about 85 cycles each, one after the other).
     constexpr int R = C::kQuant ? C::kRawStages : S;
@@ -260,11 +268,9 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     constexpr int kBoxRows = C::kQuant && D == 64 ? kBlockSize / 2 : kBlockSize;  // pool rows of 128 bytes per block and span
     constexpr int kSpans = C::kQuant ? 1 : C::kHalves;
     constexpr int kSpanBytes = kPrefixTile / kBlockSize * kBoxRows * 128;
-    const bool is_v = __shfl_sync(kFull, warp, 0) == C::kLoadV;
-    const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
     unsigned char* to = C::kQuant ? smem + C::kRawOff : ring;
     fence_proxy_async_smem();  // the scan's accesses to the ring come before the copies' writes
-    uint32_t it = 0;           // stages of both kinds so far
+    uint32_t it = 0;           // stages filled so far
     bool alive = true;
     for (; more && alive; more = walk_next(p, blockIdx.x, k)) {
       const bool two = k.x.rows > 128;
@@ -273,23 +279,27 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       // tiles read again by the group's other units stay in L2; others are read once
       const uint64_t policy = k.x.units > 1 ? l2_evict_last_policy() : l2_evict_first_policy();
       const int n = k.tile1 - k.tile0;
-      int next = tile_id(table, nblk, k.tile0, lane);
+      int ids[2] = {}, next = tile_id(table, nblk, k.tile0, lane);  // of block lane % 8
+      uint32_t blocks[2] = {};
       for (int i = 0; i < 2 * n; ++i, ++it) {
         const TileLoad ld = tile_load(two, n, i);
-        if (ld.is_v != is_v) continue;
-        const int id = next;  // of block lane % 8
-        const uint32_t have = tile_blocks(p, id, nblk, k.tile0 + ld.tile, lane);
-        if (!is_v && have != 0xffu) {
-          const int j = (k.tile0 + ld.tile) * (kPrefixTile / kBlockSize) + lane;
-          if (lane < 8 && j < nblk && !(have >> lane & 1)) set_error(p.err, kErrBlockId);
+        if (!ld.is_v) {
+          const uint32_t have = tile_blocks(p, next, nblk, k.tile0 + ld.tile, lane);
+          if (have != 0xffu) {
+            const int j = (k.tile0 + ld.tile) * (kPrefixTile / kBlockSize) + lane;
+            if (lane < 8 && j < nblk && !(have >> lane & 1)) set_error(p.err, kErrBlockId);
+          }
+          if (ld.which) { ids[1] = next; blocks[1] = have; } else { ids[0] = next; blocks[0] = have; }
+          if (ld.tile + 1 < n) next = tile_id(table, nblk, k.tile0 + ld.tile + 1, lane);
         }
-        if (ld.tile + 1 < n) next = tile_id(table, nblk, k.tile0 + ld.tile + 1, lane);
+        const int tile = (ld.which ? ids[1] : ids[0]) * p.kv_heads + k.kvh;  // pools with tensor maps have < 2^27 tiles
+        const uint32_t have = ld.which ? blocks[1] : blocks[0];
+        const CUtensorMap* map = ld.is_v ? &tmap_v : &tmap_k;
         const uint32_t st = it % R;
         if (it >= R && !wait_all(empty + st, ((it / R) & 1) ^ 1)) {
           alive = false;
           break;
         }
-        const int tile = id * p.kv_heads + k.kvh;  // pools with tensor maps have < 2^27 tiles
         int row[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) row[j] = __shfl_sync(kFull, tile, j) * kBoxRows;
@@ -314,63 +324,65 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     }
     // the copies in flight land before the CTA can end (the stages filled last)
     for (uint32_t j = it > R ? it - R : 0; j < it; ++j) (void)mbar_wait_bounded(full + j % R, (j / R) & 1);
-    if (few && !is_v) prefix_describe_few(p, lanes, total);
   } else if (warp == C::kMmaWarp || warp == C::kMmaWarp + 1) {
     // ---------------------------------------------------------------- products of stream s
     // The whole warp runs this with warp-uniform values; one elected lane issues.
-    constexpr uint32_t kDescS = mma_bf16_desc(128, kPrefixTile / 2, false), kDescO = mma_bf16_desc(128, D, true);
+    constexpr uint32_t kDescS = mma_bf16_desc(128, kPrefixTile, false), kDescO = mma_bf16_desc(128, D, true);
     constexpr uint32_t kHi = smem_operand_hi(1024);
     auto uniform = [](uint32_t x) { return __shfl_sync(kFull, x, 0); };  // tells the compiler that it is
     const int s = uniform(warp - C::kMmaWarp);
     const uint32_t q_desc = uniform(smem_operand(smem_addr(smem) + s * C::kTileBytes, 16));
     const uint32_t k_desc = smem_operand(smem_addr(ring), 16), v_desc = smem_operand(smem_addr(ring), C::kHalfBytes);
     const uint32_t t_s = uniform(tmem + s * 128), t_o = uniform(tmem + 256 + s * D);
-    uint32_t it = 0;   // ring stages before this piece
-    uint32_t cnt = 0;  // steps of the stream before this piece
-    uint32_t seg = 0;  // pieces that had work for it
+    RingPos<S> at{0, 0};  // the next stage in ring order
+    uint32_t cnt = 0;     // steps of the stream before this piece
+    uint32_t seg = 0;     // pieces that had work for it
     bool alive = true;
+    // Wait for the stage at `at`; pass over one that the other stream alone uses.
+    auto ready = [&]() { return wait_all(sy->full + at.st, at.ph); };
+    auto pass = [&](int stages) {
+      for (int j = 0; j < stages; ++j) {
+        if (!ready()) return false;
+        if (lane == 0) mbar_arrive(sy->empty + at.st);
+        at.advance(1);
+      }
+      return true;
+    };
     for (; more && alive; more = walk_next(p, blockIdx.x, k)) {
       const bool two = k.x.rows > 128;
       const int n = k.tile1 - k.tile0, ns = steps_of(two, k.nrows, n, s);
-      const bool shared = two && k.nrows > 128;  // both streams use every tile: a stage is free after both
-      const uint32_t it0 = it;
-      it += 2 * n;
-      if (ns == 0) continue;
+      if (ns == 0) {
+        alive = pass(2 * n);
+        continue;
+      }
       const int nblk = __ldg(p.prefix_lens + k.g) / kBlockSize;
       const int32_t* table = p.block_tables + int64_t(k.x.first_seq) * p.max_blocks_per_seq;
       int next = tile_id(table, nblk, k.tile0 + (two ? 0 : s), lane);
-      auto release = [&](uint32_t st) {  // once the products so far are done
-        tc_commit(sy->empty + st);
-        if (!shared) mbar_arrive(sy->empty + st);
-      };
-      // Loads of a step are 2 apart (K, V of a tile) or 4 (K, K, V, V of two tiles; the last pair may
-      // be one tile alone).
-      const uint32_t apart = two ? 2 : 4;
-      auto kp = RingPos<S>::at(it0 + (two ? 0 : s)), vp = RingPos<S>::at(it0 + (two ? 1 : min(2, n) + s));
-      // S of half h of the step at kp; c: steps of the stream before it
-      auto issue_s = [&](uint32_t c, int h) {
-        if (h == 0 && !wait_all(sy->full + kp.st, kp.ph)) return false;
-        // P lies over S until its product is done
-        if (c > 0 && !wait_all(&sy->pv_done[s][h], (c - 1) & 1)) return false;
+      // stages of the other stream around this one's K and V of a step: of two tiles' K, K, V, V this
+      // stream takes one each (the last tile may be alone)
+      auto others = [&](int i) { return two ? 0 : min(2, n - 2 * i) - 1; };
+      // S of step i
+      auto issue_s = [&](int i) {
+        if (s == 1 && !pass(others(i))) return false;
+        // P lies over S until its products are done
+        if (!ready() || (cnt + i > 0 && !wait_all(&sy->pv_done[s][1], (cnt + i - 1) & 1))) return false;
         tc_fence_after();
-        const uint32_t kd = uniform(k_desc + kp.st * (C::kTileBytes >> 4) + h * ((64 * 128) >> 4)), d = uniform(t_s + h * 64);
+        const uint32_t kd = uniform(k_desc + at.st * (C::kTileBytes >> 4));
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
-            const uint32_t at = ((j >> 2) * C::kHalfBytes + (j & 3) * 32) >> 4;
-            tc_mma_ss(d, q_desc + at, kd + at, kHi, kDescS, j > 0);
+            const uint32_t o = ((j >> 2) * C::kHalfBytes + (j & 3) * 32) >> 4;
+            tc_mma_ss(t_s, q_desc + o, kd + o, kHi, kDescS, j > 0);
           }
-          tc_commit(&sy->s_ready[s][h]);
-          if (h == 1) release(kp.st);
+          tc_commit(sy->s_ready + s);
+          tc_commit(sy->empty + at.st);  // K of the tile, once S is done
         }
         __syncwarp();
-        if (h == 1) kp.advance(apart);
-        return true;
+        at.advance(1);
+        return s == 1 || pass(others(i));
       };
       bool fresh = true;  // O holds nothing of this piece yet
-      alive = wait_all(sy->q_ready + s, seg & 1);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) alive = alive && issue_s(cnt, h);
+      alive = wait_all(sy->q_ready + s, seg & 1) && issue_s(0);
       if (alive && seg > 0) alive = wait_all(sy->o_free + s, (seg - 1) & 1);
       uint32_t have = 0;
       // one half of a tile at a time (rolled: the CTA's roles share one instruction cache)
@@ -381,12 +393,12 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
           const int tile = two ? i : 2 * i + s;
           have = tile_blocks(p, next, nblk, k.tile0 + tile, lane);
           if (i + 1 < ns) next = tile_id(table, nblk, k.tile0 + tile + (two ? 1 : 2), lane);
-          alive = wait_all(sy->full + vp.st, vp.ph);
+          alive = (s == 0 || pass(others(i))) && ready();
         }
         alive = alive && wait_all(&sy->p_ready[s][h], (cnt + i) & 1);
         if (!alive) break;
         tc_fence_after();
-        const uint32_t vd = uniform(v_desc + vp.st * (C::kTileBytes >> 4) + h * ((64 * 128) >> 4)), t_p = uniform(t_s + h * 64);
+        const uint32_t vd = uniform(v_desc + at.st * (C::kTileBytes >> 4) + h * ((64 * 128) >> 4)), t_p = uniform(t_s + h * 64);
         const uint32_t mine = have >> (4 * h) & 0xfu;
         if (elect_one()) {
           if (mine == 0xfu) {
@@ -403,13 +415,17 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
               }
           }
           tc_commit(&sy->pv_done[s][h]);
-          if (h == 1) release(vp.st);
+          if (h == 1) tc_commit(sy->empty + at.st);
         }
         if (mine) fresh = false;
         __syncwarp();
-        if (h == 1) vp.advance(!two && n - 2 * i == 3 ? 3 : apart);  // V of a last tile alone is one place earlier
-        if (i + 1 < ns) alive = issue_s(cnt + i + 1, h);
+        if (h == 1) {
+          at.advance(1);
+          alive = (s == 1 || pass(others(i))) && (i + 1 == ns || issue_s(i + 1));
+        }
       }
+      // streams that share the tiles out: the last tile is alone where n is odd, and stream 1 passes it
+      if (alive && !two && s == 1 && (n & 1)) alive = pass(2);
       cnt += ns;
       ++seg;
     }
@@ -422,6 +438,8 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       __syncwarp();
       (void)mbar_wait_bounded(sy->drain + s, 0);
     }
+  } else if (warp == C::kDescribeWarp) {
+    if (few) prefix_describe_few(p, lanes, total);
   } else if (C::kQuant && warp >= C::kConvertWarp) {
     // ---------------------------------------------------------------- codes -> operand tiles, a thread to a token
     regs_down<C::kConvertRegs>();
@@ -488,7 +506,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       *abort = 1;
       set_error(p.err, kErrTimeout);
     }
-  } else if (warp < C::kLoadK) {
+  } else if (warp < C::kLoadWarp) {
     // ---------------------------------------------------------------- softmax, one thread per row
     regs_up<C::kSoftmaxRegs>();
     const int s = warp >> 2;
@@ -605,15 +623,17 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
           if (i + 1 < ns) next = tile_id(table, nblk, tile0 + (two ? i + 1 : 2 * i + 2 + s), lane);
           if constexpr (C::kQuant) {
             slot = (tiles0 + tile) % kSlots;
-            alive = wait_all(sy->scales + slot, ((tiles0 + tile) / kSlots) & 1);
+            // after S, so that the slot's barrier is at this tile's phase: the stream does not see all
+            alive = wait_all(sy->s_ready + s, (cnt + i) & 1) && wait_all(sy->scales + slot, ((tiles0 + tile) / kSlots) & 1);
+          } else {
+            alive = wait_all(sy->s_ready + s, (cnt + i) & 1);
           }
+          if (!alive) break;
         }
-        alive = alive && wait_all(&sy->s_ready[s][h], (cnt + i) & 1);
-        if (!alive) break;
         {
           if (!idle) {
-            const auto* ks = reinterpret_cast<const float4*>(smem + C::kSlotOff + slot * C::kScaleBytes) + h * 16;
-            [[maybe_unused]] const auto* vs = reinterpret_cast<const float2*>(ks + kPrefixTile / 4);
+            const auto* ks = reinterpret_cast<const ulonglong2*>(smem + C::kSlotOff + slot * C::kScaleBytes) + h * 16;
+            [[maybe_unused]] const auto* vs = ks + kPrefixTile / 4;
             const uint32_t mine = have >> (4 * h) & 0xfu;
             tc_fence_after();
             float x[64];
@@ -623,8 +643,9 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
             if constexpr (C::kQuant) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const float4 f = ks[j];
-                x[4 * j] *= f.x; x[4 * j + 1] *= f.y; x[4 * j + 2] *= f.z; x[4 * j + 3] *= f.w;
+                const ulonglong2 f = ks[j];
+                f32x2_parts(mul2(f32x2(x[4 * j], x[4 * j + 1]), f.x), x[4 * j], x[4 * j + 1]);
+                f32x2_parts(mul2(f32x2(x[4 * j + 2], x[4 * j + 3]), f.y), x[4 * j + 2], x[4 * j + 3]);
               }
             }
             if (mine != 0xfu) {
@@ -660,18 +681,25 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
             uint64_t sum[2] = {0, 0};
             uint32_t pw[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float a, b;
-              f32x2_parts(fma2(f32x2(x[2 * j], x[2 * j + 1]), scale2, neg), a, b);
-              a = fast_exp2(a);
-              b = fast_exp2(b);
+            for (int j = 0; j < 32; j += 2) {  // four tokens at a time: one read of their V scales
+              float e[4];
+              f32x2_parts(fma2(f32x2(x[2 * j], x[2 * j + 1]), scale2, neg), e[0], e[1]);
+              f32x2_parts(fma2(f32x2(x[2 * j + 2], x[2 * j + 3]), scale2, neg), e[2], e[3]);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) e[u] = fast_exp2(e[u]);
               if constexpr (C::kQuant) {
-                sum[j & 1] = add2(sum[j & 1], f32x2(a, b));
-                const float2 f = vs[j];
-                pw[j] = pack_bf16x2(a * f.x, b * f.y);
-              } else {
-                pw[j] = pack_bf16x2(a, b);
-                sum[j & 1] = add2(sum[j & 1], f32x2(bf16lo(pw[j]), bf16hi(pw[j])));
+                const uint64_t p0 = f32x2(e[0], e[1]), p1 = f32x2(e[2], e[3]);
+                sum[0] = add2(sum[0], p0);
+                sum[1] = add2(sum[1], p1);
+                const ulonglong2 f = vs[j / 2];
+                f32x2_parts(mul2(p0, f.x), e[0], e[1]);
+                f32x2_parts(mul2(p1, f.y), e[2], e[3]);
+              }
+              pw[j] = pack_bf16x2(e[0], e[1]);
+              pw[j + 1] = pack_bf16x2(e[2], e[3]);
+              if constexpr (!C::kQuant) {
+                sum[0] = add2(sum[0], f32x2(bf16lo(pw[j]), bf16hi(pw[j])));
+                sum[1] = add2(sum[1], f32x2(bf16lo(pw[j + 1]), bf16hi(pw[j + 1])));
               }
             }
             tmem_st32(s_addr + h * 64, pw);
