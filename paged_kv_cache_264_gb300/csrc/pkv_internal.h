@@ -147,9 +147,9 @@ cudaError_t launch_rope_table(float* out, int64_t max_position, int rot_dim, dou
 // its partials, what the two later passes need: each sequence's descriptor, the length of
 // its own tokens and their slice of its block table.
 struct PrefixSeq {
-  int64_t w_base;     // first work tile of the sequence's group
+  int64_t w_base;     // first place of the sequence's group on the line of work
   int64_t row_base;   // first partial row of the group
-  int64_t total;      // work tiles of the whole call
+  int64_t total;      // places of the whole line
   int suffix_len;     // the sequence's own tokens; -1: its inputs are invalid
   int tiles;          // 128-token tiles of its prefix
   int first_row;      // its first query row among the group's (per kv head)

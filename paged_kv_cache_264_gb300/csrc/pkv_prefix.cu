@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
   if (d.tiles > 0) {
     const int r = d.first_row + qi * p.group + (h - kvh * p.group);
     const int units = (d.rows + kPrefixRows - 1) / kPrefixRows;
-    const int64_t w0 = d.w_base + (int64_t(kvh) * units + r / kPrefixRows) * d.tiles;
+    const int64_t w0 = d.w_base + (int64_t(kvh) * units + r / kPrefixRows) * (d.tiles + kUnitCost) + kUnitCost;  // first tile
     const int ctas = stretch_ctas(d.total, p.grid);
     const int c0 = stretch_owner(d.total, ctas, w0), c1 = stretch_owner(d.total, ctas, w0 + d.tiles - 1);
     twice = d.rows <= kPrefixRows / 2;

@@ -4,10 +4,11 @@
 // prefix_lens[g] tokens (whole blocks) are the same.  A group has R = (sequences) * k * (query
 // heads per kv head) query rows per kv head, in units of up to 256 rows, and its prefix is cut
 // into tiles of 128 tokens.  All (kv head, unit, tile) triples of all groups, in that order,
-// form one line of work tiles, which the CTAs of the prefix pass share out in equal
-// contiguous stretches: every CTA gets the same number of tiles (to within one) whatever the
-// groups' sizes.  A stretch inside one (kv head, unit) leaves one partial (running max, sum,
-// accumulator) per row.
+// form one line of work, which the CTAs of the prefix pass share out in equal contiguous
+// stretches, so that they end together whatever the groups' sizes.  Each unit takes kUnitCost places
+// on the line ahead of its tiles: what loading its queries and writing its partials costs, in
+// tiles.  A stretch's tiles of one (kv head, unit) are a piece; it leaves one partial (running max,
+// sum, accumulator) per row.
 //
 // Partial rows: CTA c's partial of a unit starts at row (rows of all units before it) + 256 c.
 // Going along the line either the unit or the CTA (or both) moves on, by that unit's rows or by
@@ -18,6 +19,8 @@
 #include "pkv_device.cuh"
 
 namespace pkv {
+
+constexpr int kUnitCost = 3;
 
 // Rows of partials that a group of `rows` query rows takes per kv head.
 __host__ __device__ __forceinline__ int64_t partial_rows(int rows) {
@@ -35,8 +38,13 @@ struct PrefixGroup {
   int64_t w_base, row_base;
 };
 
-// The scan of the groups, in scratch shared memory: base[g] = (first work tile, first partial
-// row) of group g.
+// Places of a group on the line.
+__device__ __forceinline__ int64_t group_line(const PrefixParams& p, const PrefixGroup& x) {
+  return x.tiles > 0 ? int64_t(x.units) * p.kv_heads * (x.tiles + kUnitCost) : 0;
+}
+
+// The scan of the groups, in scratch shared memory: base[g] = (first place on the line, first
+// partial row) of group g.
 struct PrefixScan {
   longlong2* base;   // [G + 1]
   longlong2* warp;   // [32]
@@ -65,7 +73,7 @@ __device__ __forceinline__ int64_t prefix_scan_few(const PrefixParams& p, Prefix
   me.x = PrefixGroup{};
   bool ok = true;
   if (lane < p.num_groups) ok = prefix_group(p, lane, me.x);
-  const int64_t w = int64_t(me.x.units) * p.kv_heads * me.x.tiles, r = partial_rows(me.x.rows) * p.kv_heads;
+  const int64_t w = group_line(p, me.x), r = partial_rows(me.x.rows) * p.kv_heads;
   int64_t iw = w, ir = r;
   for (int o = 1; o < p.num_groups; o <<= 1) {
     const int64_t a = __shfl_up_sync(0xffffffffu, iw, o), b = __shfl_up_sync(0xffffffffu, ir, o);
@@ -90,7 +98,7 @@ __device__ __forceinline__ PrefixGroup lane_group(const PrefixLanes& me, int g) 
   return x;
 }
 
-// Fill the scan (all NT threads of the CTA); returns the work tiles of the call, or -1 where
+// Fill the scan (all NT threads of the CTA); returns the line's places, or -1 where
 // some group is invalid.  Ends with a barrier.
 template <int NT>
 __device__ __forceinline__ int64_t prefix_scan(const PrefixParams& p, const PrefixScan& sc) {
@@ -103,7 +111,7 @@ __device__ __forceinline__ int64_t prefix_scan(const PrefixParams& p, const Pref
   for (int g = lo; g < hi; ++g) {
     PrefixGroup x;
     ok &= prefix_group(p, g, x);
-    w += int64_t(x.units) * p.kv_heads * x.tiles;
+    w += group_line(p, x);
     r += partial_rows(x.rows) * p.kv_heads;
   }
   int64_t iw = w, ir = r;
@@ -130,19 +138,19 @@ __device__ __forceinline__ int64_t prefix_scan(const PrefixParams& p, const Pref
     PrefixGroup x;
     prefix_group(p, g, x);
     sc.base[g] = make_longlong2(bw, br);
-    bw += int64_t(x.units) * p.kv_heads * x.tiles;
+    bw += group_line(p, x);
     br += partial_rows(x.rows) * p.kv_heads;
   }
   __syncthreads();
   return ok ? total : -1;
 }
 
-// CTAs that take work: no more than there are tiles, so that none between a unit's first and
-// last CTA is without one (its partial would be read unwritten).
+// CTAs that take work: no more than the line has places, so that none between a unit's first and
+// last tile is without one (its partial would be read unwritten).
 __device__ __forceinline__ int stretch_ctas(int64_t total, int grid) { return int(min(total, int64_t(grid))); }
-// CTA c's stretch of `total` work tiles starts here.
+// CTA c's stretch of the line starts here.
 __device__ __forceinline__ int64_t stretch_start(int64_t total, int ctas, int c) { return div_pos(total * c, ctas); }
-// The CTA whose stretch holds work tile w: the last one that starts at or before it.
+// The CTA whose stretch holds place w: the last one that starts at or before it.
 __device__ __forceinline__ int stretch_owner(int64_t total, int ctas, int64_t w) {
   return int(div_pos((w + 1) * ctas - 1, total));
 }
@@ -151,18 +159,39 @@ __device__ __forceinline__ int stretch_owner(int64_t total, int ctas, int64_t w)
 struct PrefixWalk {
   PrefixGroup x;
   int g, kvh, unit;      // group, kv head and unit of the group's rows
-  int tile0, tile1;      // this stretch's tiles of the unit
-  int row0, nrows;       // the unit's query rows within the group
-  int64_t partial;       // its first partial row
+  int at;                // place within the unit
   int64_t w, w_end;
 };
 
-// The rest of a piece that starts at tile k.tile0 of (k.kvh, k.unit).
-__device__ __forceinline__ void walk_place(PrefixWalk& k, int cta) {
-  k.tile1 = int(min(int64_t(k.x.tiles), k.tile0 + (k.w_end - k.w)));
-  k.row0 = k.unit * kPrefixRows;
-  k.nrows = min(kPrefixRows, k.x.rows - k.row0);
-  k.partial = k.x.row_base + int64_t(k.kvh) * partial_rows(k.x.rows) + k.row0 + int64_t(cta) * kPrefixRows;
+// A piece as the roles of a CTA see it (tiles == 0: there are no more).
+struct PrefixPiece {
+  int64_t partial;       // first partial row
+  int first_seq, nblk;   // the group's first sequence, the prefix's blocks
+  int tile0, tiles;
+  int kvh;
+  int row0, nrows;       // the unit's query rows within the group
+  int rows;              // all of the group's (up to 128: the streams share the tiles out)
+  int again;             // other units read the same tiles
+  int pad;
+};
+
+// The piece at the walk's place, if it has tiles; moves past the unit's part of the stretch.
+__device__ __forceinline__ bool walk_piece(const PrefixParams& p, PrefixWalk& k, int cta, PrefixPiece& x) {
+  const int all = k.x.tiles + kUnitCost;
+  const int len = int(min(int64_t(all - k.at), k.w_end - k.w));
+  x.tile0 = max(0, k.at - kUnitCost);
+  x.tiles = k.at + len - kUnitCost - x.tile0;
+  x.first_seq = k.x.first_seq;
+  x.kvh = k.kvh;
+  x.row0 = k.unit * kPrefixRows;
+  x.nrows = min(kPrefixRows, k.x.rows - x.row0);
+  x.rows = k.x.rows;
+  x.again = k.x.units > 1;
+  x.nblk = __ldg(p.prefix_lens + k.g) / kBlockSize;
+  x.partial = k.x.row_base + int64_t(k.kvh) * partial_rows(k.x.rows) + x.row0 + int64_t(cta) * kPrefixRows;
+  k.w += len;
+  k.at += len;
+  return x.tiles > 0;
 }
 
 // This CTA's stretch; false if it has none.
@@ -173,14 +202,14 @@ __device__ __forceinline__ bool walk_range(const PrefixParams& p, int64_t total,
   k.w_end = stretch_start(total, ctas, cta + 1);
   return true;
 }
-// The first piece of the stretch, once k.g and k.x are the group that holds its first tile.
-__device__ __forceinline__ void walk_first(PrefixWalk& k, int cta) {
+// Its first place, once k.g and k.x are the group that holds it.
+__device__ __forceinline__ void walk_first(PrefixWalk& k) {
   const int64_t in_group = k.w - k.x.w_base;
-  const int u = int(div_pos(in_group, k.x.tiles));  // kv head * units + unit
-  k.tile0 = int(in_group - int64_t(u) * k.x.tiles);
+  const int all = k.x.tiles + kUnitCost;
+  const int u = int(div_pos(in_group, all));  // kv head * units + unit
+  k.at = int(in_group - int64_t(u) * all);
   k.kvh = u / k.x.units;
   k.unit = u - k.kvh * k.x.units;
-  walk_place(k, cta);
 }
 __device__ __forceinline__ bool walk_begin(const PrefixParams& p, const PrefixScan& sc, int64_t total, int cta,
                                            PrefixWalk& k) {
@@ -194,7 +223,7 @@ __device__ __forceinline__ bool walk_begin(const PrefixParams& p, const PrefixSc
   prefix_group(p, lo, k.x);
   k.x.w_base = sc.base[lo].x;
   k.x.row_base = sc.base[lo].y;
-  walk_first(k, cta);
+  walk_first(k);
   return true;
 }
 __device__ __forceinline__ bool walk_begin_few(const PrefixParams& p, const PrefixLanes& me, int64_t total, int cta,
@@ -203,21 +232,20 @@ __device__ __forceinline__ bool walk_begin_few(const PrefixParams& p, const Pref
   const uint32_t at = __ballot_sync(0xffffffffu, int(threadIdx.x & 31) < p.num_groups && me.x.w_base <= k.w);
   k.g = 31 - __clz(at);
   k.x = lane_group(me, k.g);
-  walk_first(k, cta);
+  walk_first(k);
   return true;
 }
 
-__device__ __forceinline__ bool walk_next(const PrefixParams& p, int cta, PrefixWalk& k) {
-  k.w += k.tile1 - k.tile0;
+// On to the next unit once this one's part of the stretch is past; false at the stretch's end.
+__device__ __forceinline__ bool walk_next(const PrefixParams& p, PrefixWalk& k) {
   if (k.w >= k.w_end) return false;
-  // this CTA's stretch goes on, so the piece ended with its unit's last tile
-  k.tile0 = 0;
+  k.at = 0;
   if (++k.unit == k.x.units) {
     k.unit = 0;
     if (++k.kvh == p.kv_heads) {
       k.kvh = 0;
       do {  // the next group that has work
-        const int64_t w = k.x.w_base + int64_t(k.x.units) * p.kv_heads * k.x.tiles;
+        const int64_t w = k.x.w_base + group_line(p, k.x);
         const int64_t rows = k.x.row_base + partial_rows(k.x.rows) * p.kv_heads;
         ++k.g;
         prefix_group(p, k.g, k.x);
@@ -226,15 +254,14 @@ __device__ __forceinline__ bool walk_next(const PrefixParams& p, int cta, Prefix
       } while (k.x.units == 0 || k.x.tiles == 0);
     }
   }
-  walk_place(k, cta);
   return true;
 }
 
 // Row of q and out (in units of head_dim values) of the group's query row r for kv head kvh:
 // rows run over the group's sequences, each one's query tokens, each one's heads of the group.
-__device__ __forceinline__ int64_t prefix_q_row(const PrefixParams& p, const PrefixGroup& x, int kvh, int r) {
+__device__ __forceinline__ int64_t prefix_q_row(const PrefixParams& p, int first_seq, int kvh, int r) {
   const int tok = r / p.group, head = r - tok * p.group;
-  return (int64_t(x.first_seq) * p.num_queries + tok) * p.num_q_heads + int64_t(kvh) * p.group + head;
+  return (int64_t(first_seq) * p.num_queries + tok) * p.num_q_heads + int64_t(kvh) * p.group + head;
 }
 
 // What the suffix and merge passes need of this CTA's share of the sequences; run by `warps` of
