@@ -12,35 +12,32 @@
 // All of it is fp32 from the bf16 inputs to the one rounding at the end: a key is not
 // rounded to bf16 before it is quantised.
 //
-// A warp takes kRows rows (head rows of one token and one kind: query, key or value),
-// D / 8 lanes to a row, 16 bytes a lane; the rows' loads are issued together, ahead of the
-// arithmetic.  A lane holds its 8 values' cosines and sines, which all rows of the warp share.
-// The pass is bound by memory: it reads q, k and v once and writes each result once.
-#include "pkv_device.cuh"
+// A warp takes rows (heads) of one token and one kind: query, key or value; D / 8 lanes to a row,
+// so 2 or 4 rows at a time, kBatch such steps' loads ahead of the arithmetic.  A lane holds both values of
+// its four rotated pairs (two 8-byte pieces of the row, half the rotated part apart, or adjacent ones
+// when interleaved), so the rotation needs no exchange between lanes.  What is common to a
+// token's rows (weight times cosine or sine) is formed once per warp.  The pass is bound by memory:
+// it reads q, k and v once and writes each result once.
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kBatch = 4;  // steps whose rows are on their way together
 
-// One word of two bf16 values -> fp32.
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  x[0] = bf16lo(w.x); x[1] = bf16hi(w.x); x[2] = bf16lo(w.y); x[3] = bf16hi(w.y);
-  x[4] = bf16lo(w.z); x[5] = bf16hi(w.z); x[6] = bf16lo(w.w); x[7] = bf16hi(w.w);
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
-}
-
-// Write one row's 8 values of this lane to its slot: bf16, or codes with the row's scale.
+// Write this lane's 8 values (chunks c0 and c1 of 4) of a row to its slot: bf16, or codes with the
+// row's scale.
 template <KvType KV, int LPR>
-__device__ __forceinline__ void store_cache(const float (&x)[8], void* cache, float* scale, int64_t row, int lr,
-                                            bool write) {
+__device__ __forceinline__ void store_cache(const float (&x)[8], void* cache, float* scale, int64_t row, int c0, int c1,
+                                            bool write, bool first) {
   constexpr int D = LPR * 8;
   if constexpr (KV == KvType::kBf16) {
-    if (write) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + row * D + lr * 8) = pack8(x);
+    if (write) {
+      auto* to = static_cast<__nv_bfloat16*>(cache) + row * D;
+      *reinterpret_cast<uint2*>(to + c0 * 4) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+      *reinterpret_cast<uint2*>(to + c1 * 4) = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
   } else {
     float amax = 0.0f;
 #pragma unroll
@@ -64,119 +61,162 @@ __device__ __forceinline__ void store_cache(const float (&x)[8], void* cache, fl
       }
     }
     if (write) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D + lr * 8) = make_uint2(code[0], code[1]);
-      if (lr == 0) scale[row] = s;
+      auto* to = static_cast<uint8_t*>(cache) + row * D;
+      *reinterpret_cast<uint32_t*>(to + c0 * 4) = code[0];
+      *reinterpret_cast<uint32_t*>(to + c1 * 4) = code[1];
+      if (first) scale[row] = s;
     }
   }
 }
 
-template <KvType KV, int D, int STEPS>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParams p) {
+template <KvType KV, int D>
+__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParams p, int rows_per_unit) {
   constexpr int LPR = D / 8;              // lanes per row
   constexpr int RPS = 32 / LPR;           // rows per step of a warp
-  constexpr int kRows = RPS * STEPS;      // rows of one unit
   constexpr uint32_t kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   const int lr = lane % LPR, sub = lane / LPR;
   griddep_wait();  // the projection's output comes from the previous kernel in the stream
   griddep_launch_dependents();
-  const int uq = (p.num_q_heads + kRows - 1) / kRows, uk = (p.kv_heads + kRows - 1) / kRows;
+  const int uq = (p.num_q_heads + rows_per_unit - 1) / rows_per_unit, uk = (p.kv_heads + rows_per_unit - 1) / rows_per_unit;
   const int upt = uq + 2 * uk;  // units per token
-  const int64_t units = p.num_tokens * upt;
-  const int64_t stride = int64_t(gridDim.x) * (kRopeThreads / 32);
-  const int half = p.rot_dim >> 1;
-  const int hl = half >> 3;  // lanes that half of the rotated values take
-  for (int64_t u = int64_t(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5); u < units; u += stride) {
-    const int64_t t = u / upt;
-    const int v = int(u - t * upt);
-    const int kind = v < uq ? 0 : v < uq + uk ? 1 : 2;  // query, key, value
-    const int r0 = (kind == 0 ? v : kind == 1 ? v - uq : v - uq - uk) * kRows;
-    const int heads = kind == 0 ? p.num_q_heads : p.kv_heads;
-    const auto* src = static_cast<const __nv_bfloat16*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
-                      t * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride);
-    uint4 raw[STEPS];
+  const int64_t u = int64_t(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  if (u >= p.num_tokens * upt) return;
+  const int64_t t = u / upt;
+  const int v = int(u - t * upt);
+  const int kind = v < uq ? 0 : v < uq + uk ? 1 : 2;  // query, key, value
+  const int r0 = (kind == 0 ? v : kind == 1 ? v - uq : v - uq - uk) * rows_per_unit;
+  const int r1 = min(kind == 0 ? p.num_q_heads : p.kv_heads, r0 + rows_per_unit);
+  const auto* src = static_cast<const __nv_bfloat16*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
+                    t * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride);
+  // The lane's two chunks of 4 values: the two halves of 4 rotated pairs, or what lies past the
+  // rotated part, or (values, interleaved pairs) 8 neighbours.
+  const int half4 = p.rot_dim >> 3;  // chunks of half the rotated part
+  const bool apart = kind != 2 && !p.interleaved && p.rot_dim > 0;
+  const bool turns = kind != 2 && lr * 8 < p.rot_dim;  // half4 lanes hold pairs, whichever way they lie
+  int c0 = 2 * lr, c1 = 2 * lr + 1;
+  if (apart) {
+    c0 = lr < half4 ? lr : lr + half4;
+    c1 = lr < half4 ? lr + half4 : lr + half4 + (D / 8 - half4);
+  }
+  uint2 raw[kBatch][2];
+  auto load = [&](int r) {
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int h = r0 + i * RPS + sub;
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < heads) raw[i] = *reinterpret_cast<const uint4*>(src + int64_t(h) * D + lr * 8);
-    }
-    int64_t slot = -1;
-    if (kind != 0) {
-      slot = __ldg(p.slot_mapping + t);
-      if (slot >= p.num_blocks * kBlockSize) {
-        if (lane == 0 && r0 == 0 && kind == 1) set_error(p.err, kErrSlot);
-        slot = -1;
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = r + i * RPS + sub;
+      if (h < r1) {
+        raw[i][0] = *reinterpret_cast<const uint2*>(src + int64_t(h) * D + c0 * 4);
+        raw[i][1] = *reinterpret_cast<const uint2*>(src + int64_t(h) * D + c1 * 4);
       }
     }
-    bool ok = true;
-    float c[8], s[8];
-    if (p.cos_sin) {
-      const int pos = __ldg(p.positions + t);
-      ok = pos >= 0 && pos < p.max_position;
-      if (!ok && lane == 0 && v == 0) set_error(p.err, kErrPosition);
-      if (kind != 2 && ok && lr * 8 < p.rot_dim) {
-        const float* row = p.cos_sin + int64_t(pos) * p.rot_dim;
-        // a lane's 8 consecutive values belong to 8 pairs, or to 4 neighbouring ones
-        const float* cp = row + (p.interleaved ? lr * 4 : lr < hl ? lr * 8 : lr * 8 - half);
-        const float4 c0 = __ldg(reinterpret_cast<const float4*>(cp)), s0 = __ldg(reinterpret_cast<const float4*>(cp + half));
+  };
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
+  load(r0);
+  int64_t slot = -1;
+  if (kind != 0) {
+    slot = __ldg(p.slot_mapping + t);
+    if (slot >= p.num_blocks * kBlockSize) {
+      if (lane == 0 && r0 == 0 && kind == 1) set_error(p.err, kErrSlot);
+      slot = -1;
+    }
+  }
+  bool ok = true;
+  float4 c = make_float4(1.0f, 1.0f, 1.0f, 1.0f), s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (p.cos_sin) {
+    const int pos = __ldg(p.positions + t);
+    ok = pos >= 0 && pos < p.max_position;
+    if (!ok && lane == 0 && v == 0) set_error(p.err, kErrPosition);
+    if (ok && turns) {
+      const float4* row = reinterpret_cast<const float4*>(p.cos_sin + int64_t(pos) * p.rot_dim);
+      c = __ldg(row + lr);
+      s = __ldg(row + half4 + lr);
+    }
+  }
+  const void* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
+  float4 w0 = make_float4(1.0f, 1.0f, 1.0f, 1.0f), w1 = w0;
+  if (weight) {
+    const uint2 a = __ldg(static_cast<const uint2*>(weight) + c0), b = __ldg(static_cast<const uint2*>(weight) + c1);
+    w0 = make_float4(bf16lo(a.x), bf16hi(a.x), bf16lo(a.y), bf16hi(a.y));
+    w1 = make_float4(bf16lo(b.x), bf16hi(b.x), bf16lo(b.y), bf16hi(b.y));
+  }
+  // pairs (a, b) -> (a A - b B, b C + a E), two pairs to a register pair: A = w_a cos, B = w_b sin,
+  // C = w_b cos, E = w_a sin.  Pairs are (x0..3, x4..7), or neighbours when interleaved (x0 x1, ...).
+  uint64_t A[2], B[2], Cc[2], E[2];
+  if (p.interleaved && kind != 2) {  // a = x0 x2 | x4 x6
+    const float wa[4] = {w0.x, w0.z, w1.x, w1.z}, wb[4] = {w0.y, w0.w, w1.y, w1.w};
+    w0 = make_float4(wa[0], wa[1], wa[2], wa[3]);
+    w1 = make_float4(wb[0], wb[1], wb[2], wb[3]);
+  }
+  A[0] = f32x2(w0.x * c.x, w0.y * c.y); A[1] = f32x2(w0.z * c.z, w0.w * c.w);
+  B[0] = f32x2(-w1.x * s.x, -w1.y * s.y); B[1] = f32x2(-w1.z * s.z, -w1.w * s.w);
+  Cc[0] = f32x2(w1.x * c.x, w1.y * c.y); Cc[1] = f32x2(w1.z * c.z, w1.w * c.w);
+  E[0] = f32x2(w0.x * s.x, w0.y * s.y); E[1] = f32x2(w0.z * s.z, w0.w * s.w);
+
+  for (int r = r0; r < r1; r += kBatch * RPS) {
+    uint2 cur[kBatch][2];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      cur[i][0] = raw[i][0];
+      cur[i][1] = raw[i][1];
+    }
+    if (r + kBatch * RPS < r1) load(r + kBatch * RPS);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (r + i * RPS >= r1) break;  // the same for the whole warp
+      const int h = r + i * RPS + sub;
+      float x[8] = {bf16lo(cur[i][0].x), bf16hi(cur[i][0].x), bf16lo(cur[i][0].y), bf16hi(cur[i][0].y),
+                    bf16lo(cur[i][1].x), bf16hi(cur[i][1].x), bf16lo(cur[i][1].y), bf16hi(cur[i][1].y)};
+      if (kind != 2) {
+        uint64_t a[2], b[2];
         if (p.interleaved) {
-          c[0] = c[1] = c0.x; c[2] = c[3] = c0.y; c[4] = c[5] = c0.z; c[6] = c[7] = c0.w;
-          s[0] = s[1] = s0.x; s[2] = s[3] = s0.y; s[4] = s[5] = s0.z; s[6] = s[7] = s0.w;
+          a[0] = f32x2(x[0], x[2]); a[1] = f32x2(x[4], x[6]);
+          b[0] = f32x2(x[1], x[3]); b[1] = f32x2(x[5], x[7]);
         } else {
-          const float4 c1 = __ldg(reinterpret_cast<const float4*>(cp + 4)), s1 = __ldg(reinterpret_cast<const float4*>(cp + half + 4));
-          c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w; c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
-          s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w; s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
+          a[0] = f32x2(x[0], x[1]); a[1] = f32x2(x[2], x[3]);
+          b[0] = f32x2(x[4], x[5]); b[1] = f32x2(x[6], x[7]);
         }
-        // the first of a pair takes -s times its partner, the second +s
+        uint64_t inv2 = f32x2(1.0f, 1.0f);
+        if (weight) {
+          const uint64_t q2 = fma2(a[0], a[0], fma2(a[1], a[1], fma2(b[0], b[0], mul2(b[1], b[1]))));
+          float ss, hi;
+          f32x2_parts(q2, ss, hi);
+          ss += hi;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (p.interleaved ? !(e & 1) : lr < hl) s[e] = -s[e];
-      }
-    }
-    const void* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-    float w[8];
-    if (weight) unpack8(__ldg(static_cast<const uint4*>(weight) + lr), w);
+          for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+          const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
+          inv2 = f32x2(inv, inv);
+        }
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      if (r0 + i * RPS >= heads) break;  // the same for the whole warp
-      const int h = r0 + i * RPS + sub;
-      float x[8];
-      unpack8(raw[i], x);
-      if (weight) {
-        float ss = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-        const float inv = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= inv * w[e];
-      }
-      if (p.cos_sin && kind != 2) {
-        float y[8];  // each value's partner
+        for (int j = 0; j < 2; ++j) {
+          uint64_t ya = mul2(a[j], A[j]), yb = mul2(b[j], Cc[j]);
+          if (turns) {  // elsewhere sine is 0, but an infinity times 0 is not
+            ya = fma2(b[j], B[j], ya);
+            yb = fma2(a[j], E[j], yb);
+          }
+          a[j] = mul2(ya, inv2);
+          b[j] = mul2(yb, inv2);
+        }
         if (p.interleaved) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+          f32x2_parts(a[0], x[0], x[2]); f32x2_parts(a[1], x[4], x[6]);
+          f32x2_parts(b[0], x[1], x[3]); f32x2_parts(b[1], x[5], x[7]);
         } else {
-          const int from = (lane - lr) + (lr < hl ? lr + hl : lr < 2 * hl ? lr - hl : lr);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(kFull, x[e], from);
-        }
-        if (ok && lr * 8 < p.rot_dim) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], c[e], y[e] * s[e]);
+          f32x2_parts(a[0], x[0], x[1]); f32x2_parts(a[1], x[2], x[3]);
+          f32x2_parts(b[0], x[4], x[5]); f32x2_parts(b[1], x[6], x[7]);
         }
       }
       if (kind == 0) {
-        if (h < heads)
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.q_out) + t * p.out_stride + int64_t(h) * D + lr * 8) =
-              ok ? pack8(x) : make_uint4(0u, 0u, 0u, 0u);
+        if (h < r1) {
+          auto* to = static_cast<__nv_bfloat16*>(p.q_out) + t * p.out_stride + int64_t(h) * D;
+          const uint2 y0 = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+          const uint2 y1 = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+          *reinterpret_cast<uint2*>(to + c0 * 4) = ok ? y0 : make_uint2(0u, 0u);
+          *reinterpret_cast<uint2*>(to + c1 * 4) = ok ? y1 : make_uint2(0u, 0u);
+        }
       } else {
         const int64_t row = ((slot / kBlockSize) * p.kv_heads + h) * kBlockSize + slot % kBlockSize;
-        const bool write = ok && slot >= 0 && h < heads;
-        if (kind == 1) store_cache<KV, LPR>(x, p.k_cache, p.k_scale, row, lr, write);
-        else store_cache<KV, LPR>(x, p.v_cache, p.v_scale, row, lr, write);
+        store_cache<KV, LPR>(x, kind == 1 ? p.k_cache : p.v_cache, kind == 1 ? p.k_scale : p.v_scale, row, c0, c1,
+                             ok && slot >= 0 && h < r1, lr == 0);
       }
     }
   }
@@ -200,13 +240,16 @@ __global__ void __launch_bounds__(kRopeThreads)
 
 template <KvType KV, int D>
 cudaError_t launch_norm_rope_variant(const RopeParams& p, cudaStream_t stream) {
-  constexpr int kSteps = 4;
-  constexpr int kRows = 32 / (D / 8) * kSteps;
-  const int64_t units = p.num_tokens * ((p.num_q_heads + kRows - 1) / kRows + 2 * ((p.kv_heads + kRows - 1) / kRows));
-  const int64_t need = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  const int64_t cap = int64_t(1) << 30;
-  return launch_pdl(norm_rope_kernel<KV, D, kSteps>, dim3(unsigned(need < cap ? need : cap)), dim3(kRopeThreads), 0,
-                    stream, p);
+  constexpr int kWarps = kRopeThreads / 32;
+  constexpr int kFewRows = 32 / (D / 8) * kBatch;  // one batch of loads
+  // All of a token's heads to a warp where that fills the GPU (the token's position, table row and
+  // weights are then read once for all), one batch of rows otherwise.
+  const int most = p.num_q_heads > p.kv_heads ? p.num_q_heads : p.kv_heads;
+  const int rows = p.num_tokens * 3 >= 152 * 32 * 2 ? most : kFewRows;
+  const int64_t units = p.num_tokens * ((p.num_q_heads + rows - 1) / rows + 2 * ((p.kv_heads + rows - 1) / rows));
+  const int64_t grid = (units + kWarps - 1) / kWarps;
+  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch_pdl(norm_rope_kernel<KV, D>, dim3(unsigned(grid)), dim3(kRopeThreads), 0, stream, p, rows);
 }
 
 }  // namespace
