@@ -701,32 +701,33 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
               }
             }
             const uint64_t neg = f32x2(-m, -m);
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint64_t sum[2] = {0, 0};
+            // step by step over all 64: one value's chain of operations is long, and the warp has its
+            // scheduler nearly to itself
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f32x2_parts(fma2(f32x2(y[2 * j], y[2 * j + 1]), scale2, neg), y[2 * j], y[2 * j + 1]);
+#pragma unroll
+            for (int j = 0; j < 64; ++j) y[j] = fast_exp2(y[j]);
             uint32_t pw[32];
+            if constexpr (C::kQuant) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {  // four tokens at a time: one read of their V scales
-              float e[4];
-              f32x2_parts(fma2(f32x2(y[2 * j], y[2 * j + 1]), scale2, neg), e[0], e[1]);
-              f32x2_parts(fma2(f32x2(y[2 * j + 2], y[2 * j + 3]), scale2, neg), e[2], e[3]);
+              for (int j = 0; j < 32; ++j) sum[j & 1] = add2(sum[j & 1], f32x2(y[2 * j], y[2 * j + 1]));
 #pragma unroll
-              for (int u = 0; u < 4; ++u) e[u] = fast_exp2(e[u]);
-              if constexpr (C::kQuant) {
-                const uint64_t p0 = f32x2(e[0], e[1]), p1 = f32x2(e[2], e[3]);
-                f32x2_parts(add2(p0, f32x2(sum[0], sum[1])), sum[0], sum[1]);
-                f32x2_parts(add2(p1, f32x2(sum[2], sum[3])), sum[2], sum[3]);
-                const ulonglong2 f = vs[j / 2];
-                f32x2_parts(mul2(p0, f.x), e[0], e[1]);
-                f32x2_parts(mul2(p1, f.y), e[2], e[3]);
-              }
-              pw[j] = pack_bf16x2(e[0], e[1]);
-              pw[j + 1] = pack_bf16x2(e[2], e[3]);
-              if constexpr (!C::kQuant) {
-                add_bf16x2(sum[0], sum[1], pw[j]);
-                add_bf16x2(sum[2], sum[3], pw[j + 1]);
+              for (int j = 0; j < 16; ++j) {
+                const ulonglong2 f = vs[j];
+                f32x2_parts(mul2(f32x2(y[4 * j], y[4 * j + 1]), f.x), y[4 * j], y[4 * j + 1]);
+                f32x2_parts(mul2(f32x2(y[4 * j + 2], y[4 * j + 3]), f.y), y[4 * j + 2], y[4 * j + 3]);
               }
             }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              pw[j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+              if constexpr (!C::kQuant) sum[j & 1] = add2(sum[j & 1], f32x2(bf16lo(pw[j]), bf16hi(pw[j])));
+            }
             tmem_st32(s_addr + h * 64, pw);
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            float sum_lo, sum_hi;
+            f32x2_parts(add2(sum[0], sum[1]), sum_lo, sum_hi);
+            l += sum_lo + sum_hi;
             tmem_wait_st();
             tc_fence_before();
           }

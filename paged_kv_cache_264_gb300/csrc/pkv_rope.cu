@@ -17,14 +17,16 @@
 // its four rotated pairs (two 8-byte pieces of the row, half the rotated part apart, or adjacent ones
 // when interleaved), so the rotation needs no exchange between lanes.  What is common to a
 // token's rows (weight times cosine or sine) is formed once per warp.  The pass is bound by memory:
-// it reads q, k and v once and writes each result once.
+// it reads q, k and v once and writes each result once.  Measured on GB300, 16384 tokens of 32 + 8 + 8
+// heads of 128 into a bf16 pool (411 MB): 83 us, 4.9 TB/s, with 4 CTAs an SM and 2 steps ahead;
+// 3 CTAs and 4 steps 95 us, 2 and 8 128 us, 8 and 1 116 us.
 #include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kBatch = 4;  // steps whose rows are on their way together
+constexpr int kBatch = 2;  // steps whose rows are on their way together
 
 // Write this lane's 8 values (chunks c0 and c1 of 4) of a row to its slot: bf16, or codes with the
 // row's scale.
@@ -70,7 +72,7 @@ __device__ __forceinline__ void store_cache(const float (&x)[8], void* cache, fl
 }
 
 template <KvType KV, int D>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParams p, int rows_per_unit) {
+__global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const RopeParams p, int rows_per_unit) {
   constexpr int LPR = D / 8;              // lanes per row
   constexpr int RPS = 32 / LPR;           // rows per step of a warp
   constexpr uint32_t kFull = 0xffffffffu;

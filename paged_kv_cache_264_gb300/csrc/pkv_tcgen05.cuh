@@ -110,13 +110,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// acc + both bf16 values of a word, in fp32.
-__device__ __forceinline__ void add_bf16x2(float& acc0, float& acc1, uint32_t w) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
-      : "+f"(acc0), "+f"(acc1)
-      : "r"(w));
-}
-
 // Pairs of fp32 values in one 64-bit register.
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
   uint64_t r;
