@@ -7,11 +7,12 @@
 // take the even and the odd tiles, so that either way one stream's softmax runs under the other's
 // products.  Per stream and tile:
 //     S = Q K^T    128 x 128 x D, both operands in shared memory, S in tensor memory (fp32)
-//     P = 2^(S * scale - m)    a thread to a row, its logits in registers: no shuffles
+//     P = 2^(S * scale - m)    two threads to a row, 64 logits each in registers: no shuffles
 //     O += P V     128 x D x 128, P in tensor memory (bf16, over S's columns), V as it lies in the
 //                  pool (token-major, the contracted index outermost: an MN-major operand)
-// The softmax hands P over in halves of 64 tokens, so that the first half's product over V runs under
-// the second half's softmax.  S is formed for whole tiles: its products read both operands from
+// A row's two threads (of two warpgroups) exchange their halves' maxima and each hand their half of P
+// over: with one thread to a row its 128 logits were a chain twice as long, and nothing else was ready
+// to run.  S is formed for whole tiles: its products read both operands from
 // shared memory, 8 KB for 64 cycles of arithmetic at 128 columns, which is what shared memory
 // delivers; at 64 columns they took as long for half the work.
 // The running maximum is lazy (kMaxSlack): O is rescaled in tensor memory only when a row's
@@ -24,7 +25,7 @@
 // weight before that is rounded to bf16 (so the weights are rounded once, as in a bf16 pool; the
 // sum adds the unrounded ones, since the rounded ones carry the scale).
 //
-// Warps: two warpgroups of softmax (one per stream, which also load Q and write the partials),
+// Warps: four warpgroups of softmax (two per stream, which also load Q and write the partials),
 // one warp that fills the ring of K and V tiles by TMA (8 blocks to a tile, each wherever it lies
 // in the pool), one warp per stream that issues its products (one for both let a stream's waits
 // hold up the other's products), one that walks the CTA's stretch and hands its pieces to the others
@@ -67,14 +68,14 @@ struct PrefixCfg {
   // after its softmax.
   static constexpr int kSlots = kQuant ? (D == 128 ? 4 : 8) : 1;
   static_assert(!kQuant || 2 * kSlots - 3 >= kStages, "a scale slot is free when it is written again");
-  static constexpr int kThreads = kQuant ? 512 : 384;
-  static constexpr int kLoadWarp = 8, kMmaWarp = 9, kWalkWarp = 11, kConvertWarp = 12;  // 9 and 10: one per stream
+  static constexpr int kThreads = kQuant ? 768 : 640;
+  static constexpr int kLoadWarp = 16, kMmaWarp = 17, kWalkWarp = 19, kConvertWarp = 20;  // 17 and 18: one per stream
   static constexpr int kReaders = kThreads / 32 - 1;             // warps that take pieces from the queue
-  static constexpr int kMiscBytes = 1024;
   static constexpr int kRingOff = 2 * kTileBytes;                // Q tiles of both streams first
   static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
   static constexpr int kSlotOff = kRawOff + (kQuant ? kRawStages * kRawBytes : 0);
-  static constexpr int kSmemBytes = kMiscBytes + 1024 + kSlotOff + (kQuant ? kSlots * kScaleBytes : 0);
+  static constexpr int kMiscOff = kSlotOff + (kQuant ? kSlots * kScaleBytes : 0);
+  static constexpr int kSmemBytes = kMiscOff + 3072;             // barriers and flags, and the rows' exchange
   static constexpr uint32_t kTmemCols = 512;
   static_assert(size_t(kStages) * kTileBytes >= prefix_scan_bytes(kMaxPrefixGroups), "the scan fits the ring");
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
@@ -90,6 +91,7 @@ struct PrefixSync {
   uint64_t scales[8];                           // scale slots
   uint64_t q_ready[2], s_ready[2], o_free[2];   // per stream
   uint64_t p_ready[2][2], pv_done[2][2];        // per stream and half of a tile
+  uint64_t pair[2][4];                          // per stream and 32 rows: both halves' values are there
   uint64_t drain[2];
   uint64_t piece_full[kQueue], piece_empty[kQueue];
   PrefixPiece piece[kQueue];
@@ -97,7 +99,8 @@ struct PrefixSync {
   uint32_t tmem;
   uint32_t abort;
 };
-static_assert(sizeof(PrefixSync) <= 1008, "barriers fit their space");
+constexpr int kExchangeOff = 1024;  // float [stream][half][row] after the barriers
+static_assert(sizeof(PrefixSync) <= kExchangeOff, "barriers fit their space");
 
 template <int N>
 struct RingPos {  // a place in a ring of N stages: the stage, and the parity of the phase its current use completes
@@ -180,10 +183,8 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
   using C = PrefixCfg<KV, D>;
   constexpr int S = C::kStages;
   constexpr uint32_t kFull = 0xffffffffu;
-  extern __shared__ unsigned char smem_raw[];
-  auto* sy = reinterpret_cast<PrefixSync*>((reinterpret_cast<uintptr_t>(smem_raw) + 15) & ~uintptr_t(15));
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + C::kMiscBytes + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) unsigned char smem[];  // the swizzled tiles need its alignment
+  auto* sy = reinterpret_cast<PrefixSync*>(smem + C::kMiscOff);
   unsigned char* ring = smem + C::kRingOff;
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -198,13 +199,14 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     }
     for (int i = 0; i < C::kSlots; ++i) mbar_init(sy->scales + i, 128);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(sy->q_ready + s, 128);
+      mbar_init(sy->q_ready + s, 8);
+      for (int i = 0; i < 4; ++i) mbar_init(&sy->pair[s][i], 2);
       mbar_init(sy->s_ready + s, 1);
       for (int h = 0; h < 2; ++h) {
         mbar_init(&sy->p_ready[s][h], 4);
         mbar_init(&sy->pv_done[s][h], 1);
       }
-      mbar_init(sy->o_free + s, 4);
+      mbar_init(sy->o_free + s, 8);
       mbar_init(sy->drain + s, 1);
     }
     for (int i = 0; i < kQueue; ++i) {
@@ -217,6 +219,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     prefetch_tensor_map(&tmap_v);
   }
   if (warp == C::kMmaWarp) tmem_alloc(&sy->tmem, C::kTmemCols);
+  if (threadIdx.x == 0 && (smem_addr(smem) & 1023u)) set_error(p.err, kErrTimeout);  // never: the only shared memory
   griddep_wait();  // inputs may come from the previous kernel in the stream
   // The scan of up to 32 groups is the walking warp's own; that of many lies where the ring will be,
   // and all warps describe the sequences from it first.
@@ -521,17 +524,34 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       if (!alive) break;
     }
   } else if (warp < C::kLoadWarp) {
-    // ---------------------------------------------------------------- softmax, one thread per row
-    const int s = warp >> 2, wq = warp & 3;
+    // ---------------------------------------------------------------- softmax: rows of stream s, half h of each tile
+    const int s = warp >> 3, h = warp >> 2 & 1, wq = warp & 3;
     const int r = threadIdx.x & 127;
     const uint32_t lanes = uint32_t(wq) << 21;  // this warp's 32 lanes of tensor memory
-    const uint32_t s_addr = tmem + lanes + s * 128, o_addr = tmem + lanes + 256 + s * D;
+    const uint32_t s_addr = tmem + lanes + s * 128 + h * 64, o_addr = tmem + lanes + 256 + s * D + h * (D / 2);
     unsigned char* qt = smem + s * C::kTileBytes;
     // a negative scale goes into the sign of q, so that the largest product is the largest logit;
     // a scale of zero into a zero q, so that a masked logit stays -inf
     const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);
     const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.0f ? 0u : ~0u;
     const uint64_t scale2 = f32x2(scale, scale);
+    // The two warps of 32 rows meet; and exchange a value per row.  What was written last has to be
+    // read before the next is: a maximum is, as both halves' P go into the product that the next S
+    // waits for.
+    float* mine_at = reinterpret_cast<float*>(smem + C::kMiscOff + kExchangeOff) + (s * 2 + h) * 128 + r;
+    const float* other_at = mine_at + (h ? -128 : 128);
+    uint32_t pair = 0;
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sy->pair[s][wq]);
+      alive = wait_all(&sy->pair[s][wq], pair);
+      pair ^= 1u;
+    };
+    auto exchange = [&](float v) {
+      *mine_at = v;
+      meet();
+      return *other_at;
+    };
     uint32_t step = 0, tiles = 0;  // parity of the stream's step; all tiles before the next piece
     // The piece done last, whose partial is written while the next one's Q is on its way, and the
     // next one's rows of this stream.
@@ -546,15 +566,16 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       const int ns = x.tiles > 0 ? stream_steps(x, s) : 0;
       const int row0 = two ? s * 128 : 0;                           // the stream's first row within the unit
       next_rows = x.tiles > 0 ? max(0, min(128, x.nrows - row0)) : 0;  // its rows
-      uint4 w[D / 8];                                               // this thread's row of Q
+      constexpr int kChunksQ = D / 16;                              // this thread's half of its row of Q
+      uint4 w[kChunksQ];
       if (ns > 0) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < kChunksQ; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
         if (r < next_rows) {
           const auto* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                         prefix_q_row(p, x.first_seq, x.kvh, x.row0 + row0 + r) * D);
+                                                         prefix_q_row(p, x.first_seq, x.kvh, x.row0 + row0 + r) * D) + h * kChunksQ;
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) w[c] = __ldg(q + c);
+          for (int c = 0; c < kChunksQ; ++c) w[c] = __ldg(q + c);
         }
       }
       // Two things to do: Q -> shared memory, and the last piece's partial, which is turned through the
@@ -565,57 +586,65 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       for (int job = 0; job < 2 && alive; ++job) {
         if ((job == 0) == q_first) {
           if (ns == 0) continue;
+          if (!q_first) {  // the other warp of these rows has turned its half of them
+            meet();
+            if (!alive) break;
+          }
           if (!q_first || r < 64) {
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
+            for (int c = 0; c < kChunksQ; ++c) {
+              const int at = h * kChunksQ + c;
               w[c] = make_uint4((w[c].x ^ flip) & keep, (w[c].y ^ flip) & keep, (w[c].z ^ flip) & keep, (w[c].w ^ flip) & keep);
-              *reinterpret_cast<uint4*>(qt + (c >> 3) * C::kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[c];
+              *reinterpret_cast<uint4*>(qt + (at >> 3) * C::kHalfBytes + r * 128 + (((at & 7) ^ (r & 7)) << 4)) = w[c];
             }
           }
           fence_proxy_async_smem();
-          mbar_arrive(sy->q_ready + s);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sy->q_ready + s);
           continue;
         }
         if (!pending) continue;
-        // A thread holds a row, so its stores would touch 32 lines at a time; the warp turns its 32 rows
-        // through shared memory, 64 values of each row at a time (32 at head_dim 64), and stores whole
-        // lines.
-        if (!wait_all(&sy->pv_done[s][1], step ^ 1u)) {
-          alive = false;
-          break;
-        }
+        // A thread holds half a row, so its stores would touch 32 lines at a time; the warp turns its 32
+        // rows through shared memory, 32 values of each row at a time (16 at head_dim 64), and stores whole
+        // lines (half lines).
+        alive = wait_all(&sy->pv_done[s][0], step ^ 1u) && wait_all(&sy->pv_done[s][1], step ^ 1u);
+        if (!alive) break;
+        const float l_other = exchange(l);
+        if (alive) meet();  // both have read
+        if (!alive) break;
         const int live = min(32, nrows - wq * 32);
         if (live > 0) {
           tc_fence_after();
-          constexpr int kCols = C::kTileBytes / 4 / 32 / 4;  // columns per round
+          constexpr int kCols = C::kTileBytes / 8 / 32 / 4;  // columns per round
           constexpr int kChunks = kCols / 4;                 // 16-byte chunks of a row in a round
-          constexpr int kPart = C::kTileBytes / 4;
-          // a quarter of the tile for each warp, or of its rows 64 to 127 for the two that have rows
-          unsigned char* turn = qt + (!q_first ? wq * kPart : D == 128 ? wq * C::kHalfBytes + 8192 : 8192 + wq * kPart);
-          float* dst = p.acc + (to + wq * 32) * D;
+          // The warp's space in the Q tile: rows 32 wq + 16 h .. + 15 of each span where Q comes after, so
+          // that only its pair's Q rows lie there; a quarter of rows 64 to 127 where Q is there already
+          // (two quadrants have rows then).
+          float* dst = p.acc + (to + wq * 32) * D + h * (D / 2);
+          const int first = q_first ? 64 + (wq * 2 + h) * 16 : wq * 32 + h * 16;
+          // byte b of the warp's space: span b / 2048, 16 rows of 128 bytes in each
+          auto place = [&](int b) { return qt + (b >> 11) * C::kHalfBytes + first * 128 + (b & 2047); };
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += kCols) {
-#pragma unroll 1
-            for (int h = 0; h < kCols; h += 32) {
-              float o[32];
-              tmem_ld32(o_addr + c0 + h, o);
-              tmem_wait_ld();
+          for (int c0 = 0; c0 < D / 2; c0 += kCols) {
+            float o[kCols];
+            if constexpr (kCols == 32) tmem_ld32(o_addr + c0, o);
+            else tmem_ld16(o_addr + c0, o);
+            tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<float4*>(turn + lane * (kCols * 4) + (((h / 4 + e) ^ (lane % kChunks)) << 4)) =
-                    any ? make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            }
+            for (int e = 0; e < kChunks; ++e)
+              *reinterpret_cast<float4*>(place(lane * (kCols * 4) + ((e ^ (lane % kChunks)) << 4))) =
+                  any ? make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             __syncwarp();
 #pragma unroll 4
             for (int j = 0; j * (32 / kChunks) < live; ++j) {
               const int row = j * (32 / kChunks) + lane / kChunks, chunk = lane % kChunks;
               if (row < live)
                 *reinterpret_cast<float4*>(dst + row * D + c0 + chunk * 4) =
-                    *reinterpret_cast<const float4*>(turn + row * (kCols * 4) + ((chunk ^ (row % kChunks)) << 4));
+                    *reinterpret_cast<const float4*>(place(row * (kCols * 4) + ((chunk ^ (row % kChunks)) << 4)));
             }
             __syncwarp();
           }
-          if (lane < live) p.ml[to + wq * 32 + lane] = make_float2(m, l);
+          if (h == 0 && lane < live) p.ml[to + wq * 32 + lane] = make_float2(m, l + l_other);
           tc_fence_before();
         }
         __syncwarp();
@@ -628,7 +657,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       tiles += x.tiles;
       pending = ns > 0;
       if (ns == 0) {
-        if (r < nrows) p.ml[to + r] = make_float2(kMaxFloor, 0.0f);  // no tile of its own: weighs nothing
+        if (h == 0 && r < nrows) p.ml[to + r] = make_float2(kMaxFloor, 0.0f);  // no tile of its own: weighs nothing
         continue;
       }
       const bool idle = wq * 32 >= nrows;  // none of the warp's rows exists
@@ -648,93 +677,103 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
         // after S, so that the slot's barrier is at this tile's phase: the stream does not see all
         if constexpr (C::kQuant) alive = alive && wait_all(sy->scales + slot, ((tiles0 + tile) / C::kSlots) & 1);
         if (!alive) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int h = 0; h < 2 && alive; ++h) {
-          if (!idle) {
-            [[maybe_unused]] const auto* ks =
-                reinterpret_cast<const ulonglong2*>(smem + C::kSlotOff + slot * C::kScaleBytes) + h * 16;
-            [[maybe_unused]] const auto* vs = ks + kPrefixTile / 4;
-            const uint32_t mine = have >> (4 * h) & 0xfu;
-            float y[64];
-            tmem_ld32(s_addr + h * 64, y);
-            tmem_ld32(s_addr + h * 64 + 32, y + 32);
+        if (!idle) {
+          tc_fence_after();
+          [[maybe_unused]] const auto* ks =
+              reinterpret_cast<const ulonglong2*>(smem + C::kSlotOff + slot * C::kScaleBytes) + h * 16;
+          [[maybe_unused]] const auto* vs = ks + kPrefixTile / 4;
+          const uint32_t mine = have >> (4 * h) & 0xfu;
+          // 32 columns at a time: the upper ones for their maximum alone, then the lower ones, whose
+          // weights go over their own columns; the upper ones are read again
+          float y[32];
+          auto fetch = [&](int c) {
+            tmem_ld32(s_addr + 32 * c, y);
             tmem_wait_ld();
             if constexpr (C::kQuant) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const ulonglong2 f = ks[j];
+              for (int j = 0; j < 8; ++j) {
+                const ulonglong2 f = ks[8 * c + j];
                 f32x2_parts(mul2(f32x2(y[4 * j], y[4 * j + 1]), f.x), y[4 * j], y[4 * j + 1]);
                 f32x2_parts(mul2(f32x2(y[4 * j + 2], y[4 * j + 3]), f.y), y[4 * j + 2], y[4 * j + 3]);
               }
             }
             if (mine != 0xfu) {
 #pragma unroll
-              for (int j = 0; j < 64; ++j)
-                if (!(mine >> (j / 16) & 1)) y[j] = -INFINITY;
+              for (int j = 0; j < 32; ++j)
+                if (!(mine >> (2 * c + j / 16) & 1)) y[j] = -INFINITY;
             }
+          };
+          auto largest = [&]() {
             float mx[4] = {y[0], y[1], y[2], y[3]};
 #pragma unroll
-            for (int j = 4; j < 60; j += 8) {
+            for (int j = 4; j < 28; j += 8) {
 #pragma unroll
               for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], y[j + 2 * u], y[j + 2 * u + 1]);
             }
-            const float bm = max3(max3(mx[0], y[60], y[61]), max3(mx[1], y[62], y[63]), fmaxf(mx[2], mx[3])) * scale;
-            const bool grow = bm > m + kMaxSlack;
-            if (__any_sync(kFull, grow)) {
-              const float mu = grow ? bm : m, f = fast_exp2(m - mu);
-              m = mu;
-              l *= f;
-              if (i > 0 || h > 0) {
-                // every product into O so far has to be done: the half's before this one is the last
-                alive = wait_all(&sy->pv_done[s][h ^ 1], h == 0 ? step ^ 1u : step);
-                tc_fence_after();
+            return max3(max3(mx[0], y[28], y[29]), max3(mx[1], y[30], y[31]), fmaxf(mx[2], mx[3]));
+          };
+          fetch(1);
+          float bm = largest();
+          fetch(0);
+          bm = fmaxf(bm, largest()) * scale;
+          bm = fmaxf(bm, exchange(bm));
+          if (!alive) break;
+          const bool grow = bm > m + kMaxSlack;
+          if (__any_sync(kFull, grow)) {
+            const float mu = grow ? bm : m, f = fast_exp2(m - mu);
+            m = mu;
+            l *= f;
+            if (i > 0) {
+              // every product into O is done: S was issued after the last
 #pragma unroll 1
-                for (int j = 0; j < D / 16; ++j) {
-                  float o[16];
-                  tmem_ld16(o_addr + 16 * j, o);
-                  tmem_wait_ld();
+              for (int j = 0; j < D / 32; ++j) {
+                float o[16];
+                tmem_ld16(o_addr + 16 * j, o);
+                tmem_wait_ld();
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] *= f;
-                  tmem_st16(o_addr + 16 * j, o);
-                }
+                for (int e = 0; e < 16; ++e) o[e] *= f;
+                tmem_st16(o_addr + 16 * j, o);
               }
             }
-            const uint64_t neg = f32x2(-m, -m);
-            uint64_t sum[2] = {0, 0};
-            // step by step over all 64: one value's chain of operations is long, and the warp has its
-            // scheduler nearly to itself
+          }
+          const uint64_t neg = f32x2(-m, -m);
+          uint64_t sum[2] = {0, 0};
+          auto weights = [&](int c) {
+            // step by step over all 32: one value's chain of operations is long
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f32x2_parts(fma2(f32x2(y[2 * j], y[2 * j + 1]), scale2, neg), y[2 * j], y[2 * j + 1]);
+            for (int j = 0; j < 16; ++j) f32x2_parts(fma2(f32x2(y[2 * j], y[2 * j + 1]), scale2, neg), y[2 * j], y[2 * j + 1]);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) y[j] = fast_exp2(y[j]);
-            uint32_t pw[32];
+            for (int j = 0; j < 32; ++j) y[j] = fast_exp2(y[j]);
             if constexpr (C::kQuant) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) sum[j & 1] = add2(sum[j & 1], f32x2(y[2 * j], y[2 * j + 1]));
+              for (int j = 0; j < 16; ++j) sum[j & 1] = add2(sum[j & 1], f32x2(y[2 * j], y[2 * j + 1]));
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const ulonglong2 f = vs[j];
+              for (int j = 0; j < 8; ++j) {
+                const ulonglong2 f = vs[8 * c + j];
                 f32x2_parts(mul2(f32x2(y[4 * j], y[4 * j + 1]), f.x), y[4 * j], y[4 * j + 1]);
                 f32x2_parts(mul2(f32x2(y[4 * j + 2], y[4 * j + 3]), f.y), y[4 * j + 2], y[4 * j + 3]);
               }
             }
+            float pw[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              pw[j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
-              if constexpr (!C::kQuant) sum[j & 1] = add2(sum[j & 1], f32x2(bf16lo(pw[j]), bf16hi(pw[j])));
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t v = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+              pw[j] = __uint_as_float(v);
+              if constexpr (!C::kQuant) sum[j & 1] = add2(sum[j & 1], f32x2(bf16lo(v), bf16hi(v)));
             }
-            tmem_st32(s_addr + h * 64, pw);
-            float sum_lo, sum_hi;
-            f32x2_parts(add2(sum[0], sum[1]), sum_lo, sum_hi);
-            l += sum_lo + sum_hi;
-            tmem_wait_st();
-            tc_fence_before();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sy->p_ready[s][h]);
+            tmem_st16(s_addr + 16 * c, pw);
+          };
+          weights(0);
+          fetch(1);
+          weights(1);
+          float sum_lo, sum_hi;
+          f32x2_parts(add2(sum[0], sum[1]), sum_lo, sum_hi);
+          l += sum_lo + sum_hi;
+          tmem_wait_st();
+          tc_fence_before();
         }
-        if (!alive) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sy->p_ready[s][h]);
       }
       if (!alive) break;
     }
