@@ -20,7 +20,7 @@
 
 namespace pkv {
 
-constexpr int kUnitCost = 3;
+constexpr int kUnitCost = 4;
 
 // Rows of partials that a group of `rows` query rows takes per kv head.
 __host__ __device__ __forceinline__ int64_t partial_rows(int rows) {
