@@ -460,8 +460,8 @@ PKV_API const char* pkv_static_scratch_error(void);
  * or max_tokens do not suffice (PKV_DEVERR_CAPACITY), or a length or count is negative
  * (PKV_DEVERR_CONTEXT_LEN), tables, lengths and free_used stay as they were, every slot is -1
  * and query_starts is all 0.  A block id outside the pool gives its tokens slot -1 and sets
- * PKV_DEVERR_BLOCK_ID.  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (more than 16384 sequences, a pool of 2^27 blocks or more),
- * PKV_ERR_CUDA.
+ * PKV_DEVERR_BLOCK_ID.  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (more than 16384
+ * sequences, a pool of 2^27 blocks or more), PKV_ERR_CUDA.
  */
 PKV_API pkv_status pkv_reserve_slots(const pkv_pool* pool, int32_t* block_tables, int max_blocks_per_seq,
                                      const int32_t* context_lens, const int32_t* num_new_tokens, int num_seqs,
@@ -481,7 +481,8 @@ PKV_API pkv_status pkv_reserve_slots(const pkv_pool* pool, int32_t* block_tables
  *             its sines (pkv_rope_table), 16-byte aligned; NULL: no rotation.
  *   positions (device): int32 [num_tokens], used with cos_sin only.
  *   slot_mapping (device): int32 [num_tokens], as for pkv_reshape_and_cache.
- *   q_out     (device, out): bf16 rows like q's at q_out_stride; may be q itself, at q's stride.
+ *   q_out     (device, out): bf16 rows like q's at q_out_stride, at least a token's row apart; may
+ *             be q itself, at q's stride.
  *   rot_dim:  rotated values of each head, a multiple of 16 up to head_dim.
  *   interleaved: 0: pair i is values (i, i + rot_dim / 2); else (2 i, 2 i + 1).
  *   eps:      added to the mean square, >= 0.
@@ -516,7 +517,8 @@ typedef struct pkv_norm_rope {
  * A negative slot skips the token's cache write, not its queries.  A slot past the pool does
  * so too and sets PKV_DEVERR_SLOT.  A position outside the table gives zero queries and no
  * cache write and sets PKV_DEVERR_POSITION.  Slots must be distinct among a call's tokens.
- * num_tokens == 0 is a no-op.  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (rot_dim not a multiple of 16), PKV_ERR_CUDA.
+ * num_tokens == 0 is a no-op.  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (rot_dim not a
+ * multiple of 16), PKV_ERR_CUDA.
  */
 PKV_API pkv_status pkv_norm_rope_and_cache(const pkv_pool* pool, const pkv_norm_rope* args, void* stream);
 
@@ -558,7 +560,8 @@ PKV_API pkv_status pkv_shared_prefix_workspace_bytes(const pkv_pool* pool, int n
  * range gets a zero output and sets PKV_DEVERR_CONTEXT_LEN; an invalid group_starts or
  * prefix_lens entry sets PKV_DEVERR_PREFIX and gives the whole call a zero output (with
  * PKV_DEVERR_CONTEXT_LEN); a block id out of range is skipped and sets PKV_DEVERR_BLOCK_ID.
- * num_seqs == 0 is a no-op.  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (a window, more than 4096 groups), PKV_ERR_WORKSPACE, PKV_ERR_CUDA.
+ * num_seqs == 0 is a no-op.  Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (a window, more than
+ * 4096 groups, a pool of 2^31 or more rows of head_dim), PKV_ERR_WORKSPACE, PKV_ERR_CUDA.
  */
 PKV_API pkv_status pkv_shared_prefix_decode(const pkv_pool* pool, const void* q, const int32_t* block_tables,
                                             int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,

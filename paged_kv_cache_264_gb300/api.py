@@ -67,6 +67,15 @@ def _pool_stream(pool, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(pool.device_index)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for a call on ``stream``: taken from that stream's memory, so that it neither is still in
+    use by another stream's work nor goes to it while the call runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 _KERNELS = {0: 0, "auto": 0, 1: 1, "cuda_core": 1, 2: 2, "tensor_core": 2}
 _SCHEDULES = {0: 0, "auto": 0, 1: 1, "grid": 1, 2: 2, "persistent": 2}
 
@@ -324,8 +333,9 @@ def reserve_slots(pool: PagedKVPool, block_tables: torch.Tensor, context_lens: t
     (int32 [B, max_blocks]) in place.  Returns (slot_mapping [max_tokens], positions
     [max_tokens], query_starts [B + 1], new_context_lens [B], new_free_used [1]), all int32;
     slots past the last new token are -1.  Outputs not given are allocated; new_context_lens may
-    be context_lens and new_free_used may be free_used.  All or nothing: a call that does not
-    fit changes nothing, returns slots of -1 and sets DEVERR_CAPACITY."""
+    be context_lens and new_free_used may be free_used.  Nothing is copied: a sequence whose last
+    block is partly filled must own that block.  All or nothing: a call that does not fit changes
+    nothing, returns slots of -1 and sets DEVERR_CAPACITY."""
     i32 = torch.int32
     _check(block_tables, i32, "block_tables", 2, pool)
     _check(context_lens, i32, "context_lens", 1, pool)
@@ -345,7 +355,7 @@ def reserve_slots(pool: PagedKVPool, block_tables: torch.Tensor, context_lens: t
 
     def output(t, name, n):
         if t is None:
-            return torch.empty(n, dtype=i32, device=context_lens.device)
+            return _empty(n, i32, context_lens.device, stream)
         _check(t, i32, name, 1, pool)
         if t.shape[0] != n:
             raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
@@ -432,7 +442,7 @@ def norm_rope_and_cache(pool: PagedKVPool, q: torch.Tensor, k: torch.Tensor, v: 
             raise ValueError("cos_sin must not be empty")
         table, pos = cos_sin.data_ptr(), positions.data_ptr()
     if out is None:
-        out = torch.empty(n, hq, d, dtype=q.dtype, device=q.device)
+        out = _empty((n, hq, d), q.dtype, q.device, stream)
     outs = _head_rows(out, "out", n, hq, pool)
     a = NormRope(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
                  0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
@@ -449,7 +459,7 @@ def rope_table(max_position: int, rot_dim: int, base: float = 10000.0, device=No
     cos(p * base^(-2 i / rot_dim)) for each pair i and then the sines, formed in 64 bits."""
     device = torch.device(device or "cuda")
     with torch.cuda.device(device):
-        out = torch.empty(int(max_position), int(rot_dim), dtype=torch.float32, device=device)
+        out = _empty((int(max_position), int(rot_dim)), torch.float32, device, stream)
         check(_lib.load().pkv_rope_table(_ptr(out), out.shape[0], out.shape[1], float(base), _stream(stream)), "rope_table")
     return out
 
@@ -485,7 +495,7 @@ def shared_prefix_decode(pool: PagedKVPool, q: torch.Tensor, block_tables: torch
     _check(group_starts, torch.int32, "group_starts", 1, pool)
     _check(prefix_lens, torch.int32, "prefix_lens", 1, pool)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     else:
         _check(out, torch.bfloat16, "out", ndim, pool)
     tables_shape = block_tables.shape
@@ -494,9 +504,9 @@ def shared_prefix_decode(pool: PagedKVPool, q: torch.Tensor, block_tables: torch
     if group_starts.shape[0] != groups + 1:
         raise ValueError("group_starts must have one entry more than prefix_lens")
     if workspace is None:
-        workspace = torch.empty(
+        workspace = _empty(
             shared_prefix_workspace_bytes(pool, b, hq, groups, max_prefix_len, max_suffix_len, nq, partition_blocks),
-            dtype=torch.uint8, device=q.device)
+            torch.uint8, q.device, stream)
     elif workspace.get_device() != pool.device_index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the pool's device")
     st = _lib.load().pkv_shared_prefix_decode(

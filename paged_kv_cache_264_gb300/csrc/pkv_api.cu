@@ -686,6 +686,8 @@ pkv_status pkv_norm_rope_and_cache(const pkv_pool* pool, const pkv_norm_rope* a,
       !aligned16(a->k_weight) || !aligned16(a->cos_sin))
     return PKV_ERR_INVALID_ARG;
   if (a->q_stride % 8 || a->k_stride % 8 || a->v_stride % 8 || a->q_out_stride % 8) return PKV_ERR_INVALID_ARG;
+  // tokens' new queries must not lie on one another
+  if (a->num_tokens > 1 && std::abs(a->q_out_stride) < int64_t(a->num_q_heads) * pool->head_dim) return PKV_ERR_INVALID_ARG;
   if (!(a->eps >= 0.0f)) return PKV_ERR_INVALID_ARG;
   if (a->cos_sin) {
     if (!a->positions || a->max_position < 1 || a->rot_dim < 2 || a->rot_dim > pool->head_dim) return PKV_ERR_INVALID_ARG;

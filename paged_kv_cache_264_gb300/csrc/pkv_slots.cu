@@ -172,7 +172,7 @@ cudaError_t launch_reserve_slots(const SlotParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   const int64_t need = (int64_t(p.max_tokens) + kSlotThreads * kPerThread - 1) / (kSlotThreads * kPerThread);
-  const int grid = int(need < 1 ? 1 : need < 148 ? need : 148);
+  const int grid = int(need < 1 ? 1 : need < 152 ? need : 152);
   return launch_pdl(reserve_slots_kernel, dim3(grid), dim3(kSlotThreads), smem, stream, p);
 }
 
