@@ -12,109 +12,170 @@
 // All of it is fp32 from the bf16 inputs to the one rounding at the end: a key is not
 // rounded to bf16 before it is quantised.
 //
-// A warp takes rows (heads) of one token and one kind: query, key or value; D / 8 lanes to a row,
-// so 2 or 4 rows at a time, kBatch such steps' loads ahead of the arithmetic.  A lane holds both values of
-// its four rotated pairs (two 8-byte pieces of the row, half the rotated part apart, or adjacent ones
-// when interleaved), so the rotation needs no exchange between lanes.  What is common to a
-// token's rows (weight times cosine or sine) is formed once per warp.  The pass is bound by memory:
-// it reads q, k and v once and writes each result once.  Measured on GB300, 16384 tokens of 32 + 8 + 8
-// heads of 128 into a bf16 pool (411 MB): 83 us, 4.9 TB/s, with 4 CTAs an SM and 2 steps ahead;
-// 3 CTAs and 4 steps 95 us, 2 and 8 128 us, 8 and 1 116 us.
+// A warp takes rows (heads) of one token and one kind: query, key or value; D / 16 lanes to a row,
+// so 4 or 8 rows at a time.  A lane holds both values of its eight rotated pairs (two 16-byte pieces of
+// the row, half the rotated part apart when the pairs are), so the rotation needs no exchange between
+// lanes.  What is common to a token's rows (weight times cosine or sine) is formed once per warp.
+// The pass is bound by memory: it reads q, k and v once and writes each result once.  What it has on
+// its way at a time decides its rate, so each lane's pieces of the next kSlots - 1 steps are copied to
+// shared memory of its own (no registers held, no other lane to wait for).
+// All queries' warps come first, then the keys', then the values': mixed, a CTA waited for its
+// queries with half its warps done.  Measured on GB300, 16384 tokens of 32 + 8 + 8 heads of 128 into a
+// bf16 pool (411 MB): 72.8 us, 5.6 TB/s (mixed 80; 6 or 4 slots the same within 2%; 5 CTAs an SM 74.8, 7
+// 72.8 but slower when short); with loads of 8 bytes into registers, two steps ahead, it was 83.  Into an
+// INT8 pool 4096 tokens take 23 us, 3.9 TB/s: the arithmetic of keys' and values' codes is in the way.
 #include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kBatch = 2;  // steps whose rows are on their way together
+constexpr int kRopeThreads = 128;
+constexpr int kSlots = 3;    // steps whose rows have a place in shared memory
+constexpr int kMinCtas = 6;
 
-// Write this lane's 8 values (chunks c0 and c1 of 4) of a row to its slot: bf16, or codes with the
+__device__ __forceinline__ void copy_piece(uint4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_next_step() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but this thread's latest kSlots - 1 steps have landed.
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory"); }
+
+__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
+  x[0] = bf16lo(w.x); x[1] = bf16hi(w.x); x[2] = bf16lo(w.y); x[3] = bf16hi(w.y);
+  x[4] = bf16lo(w.z); x[5] = bf16hi(w.z); x[6] = bf16lo(w.w); x[7] = bf16hi(w.w);
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+
+// Codes of 16 values with scale s: the values divided by s, rounded, and rounded to a code, as
+// pkv_reshape_and_cache forms them.
+template <KvType KV>
+__device__ __forceinline__ void codes_by_division(const float (&x)[16], float s, uint32_t (&code)[4]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const float a = __fdiv_rn(x[i], s), b = __fdiv_rn(x[i + 1], s);
+    uint32_t two;
+    if constexpr (KV == KvType::kFp8) {
+      two = e4m3x2_from_f32(a, b);
+    } else {
+      const int ca = min(127, max(-127, __float2int_rn(a))), cb = min(127, max(-127, __float2int_rn(b)));
+      two = (uint32_t(ca) & 0xffu) | ((uint32_t(cb) & 0xffu) << 8);
+    }
+    code[i >> 2] = (i & 2) ? code[i >> 2] | two << 16 : two;
+  }
+}
+
+// The same codes, nearly always without a division per value.  With r = 1 / s to half a step
+// (2^-24), x * r (1 - 2^-21) and x * r (1 + 2^-21) lie on either side of the rounded quotient, whose
+// error is 2^-24 too, or are all too small for any code but 0.  Rounding to a code is monotone, so
+// where both give one code it is the quotient's; where they do not (about one lane in 2000), and for
+// NaN, this returns false.
+template <KvType KV>
+__device__ __forceinline__ bool codes_by_bounds(const float (&x)[16], float s, uint32_t (&code)[4]) {
+  if (!(s >= 0x1p-100f && s <= 0x1p100f)) return false;  // r is a normal number
+  const float r = __fdiv_rn(1.0f, s), r_lo = r * (1.0f - 0x1p-21f), r_hi = r * (1.0f + 0x1p-21f);
+  const uint64_t lo2 = f32x2(r_lo, r_lo), hi2 = f32x2(r_hi, r_hi);
+  bool same = true;
+  if constexpr (KV == KvType::kFp8) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const uint64_t v = f32x2(x[i], x[i + 1]);
+      float a, b, c, d;
+      f32x2_parts(mul2(v, lo2), a, b);
+      f32x2_parts(mul2(v, hi2), c, d);
+      const uint32_t two = e4m3x2_from_f32(a, b);
+      same = same && two == e4m3x2_from_f32(c, d);
+      code[i >> 2] = (i & 2) ? code[i >> 2] | two << 16 : two;
+    }
+  } else {
+    // adding 1.5 * 2^23 rounds to a whole number, which the sum's low byte then holds
+    const uint64_t magic = f32x2(12582912.0f, 12582912.0f);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      float a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const uint64_t v = f32x2(x[i + j], x[i + j + 1]);
+        f32x2_parts(fma2(v, lo2, magic), a[j], a[j + 1]);
+        f32x2_parts(fma2(v, hi2, magic), b[j], b[j + 1]);
+        same = same && a[j] == b[j] && a[j + 1] == b[j + 1];
+      }
+      code[i >> 2] = __byte_perm(__byte_perm(__float_as_uint(a[0]), __float_as_uint(a[1]), 0x0040u),
+                                 __byte_perm(__float_as_uint(a[2]), __float_as_uint(a[3]), 0x0040u), 0x5410u);
+    }
+  }
+  return same;
+}
+
+// Write this lane's 16 values (pieces c0 and c1 of 8) of a row to its slot: bf16, or codes with the
 // row's scale.
 template <KvType KV, int LPR>
-__device__ __forceinline__ void store_cache(const float (&x)[8], void* cache, float* scale, int64_t row, int c0, int c1,
+__device__ __forceinline__ void store_cache(const float (&x)[16], void* cache, float* scale, int64_t row, int c0, int c1,
                                             bool write, bool first) {
-  constexpr int D = LPR * 8;
+  constexpr int D = LPR * 16;
   if constexpr (KV == KvType::kBf16) {
     if (write) {
       auto* to = static_cast<__nv_bfloat16*>(cache) + row * D;
-      *reinterpret_cast<uint2*>(to + c0 * 4) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-      *reinterpret_cast<uint2*>(to + c1 * 4) = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+      *reinterpret_cast<uint4*>(to + c0 * 8) = pack8(x);
+      *reinterpret_cast<uint4*>(to + c1 * 8) = pack8(x + 8);
     }
   } else {
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
     for (int o = LPR / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float s = __fdiv_rn(amax, KV == KvType::kFp8 ? 448.0f : 127.0f);
-    uint32_t code[2] = {0u, 0u};
-    if (amax != 0.0f) {
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float a = __fdiv_rn(x[i], s), b = __fdiv_rn(x[i + 1], s);
-        uint32_t two;
-        if constexpr (KV == KvType::kFp8) {
-          two = e4m3x2_from_f32(a, b);
-        } else {
-          const int ca = min(127, max(-127, __float2int_rn(a))), cb = min(127, max(-127, __float2int_rn(b)));
-          two = (uint32_t(ca) & 0xffu) | ((uint32_t(cb) & 0xffu) << 8);
-        }
-        code[i >> 2] |= two << (8 * (i & 3));
-      }
-    }
+    uint32_t code[4];
+    if (!codes_by_bounds<KV>(x, s, code)) codes_by_division<KV>(x, s, code);
+    if (amax == 0.0f) code[0] = code[1] = code[2] = code[3] = 0u;
     if (write) {
       auto* to = static_cast<uint8_t*>(cache) + row * D;
-      *reinterpret_cast<uint32_t*>(to + c0 * 4) = code[0];
-      *reinterpret_cast<uint32_t*>(to + c1 * 4) = code[1];
+      *reinterpret_cast<uint2*>(to + c0 * 8) = make_uint2(code[0], code[1]);
+      *reinterpret_cast<uint2*>(to + c1 * 8) = make_uint2(code[2], code[3]);
       if (first) scale[row] = s;
     }
   }
 }
 
 template <KvType KV, int D>
-__global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const RopeParams p, int rows_per_unit) {
-  constexpr int LPR = D / 8;              // lanes per row
+__global__ void __launch_bounds__(kRopeThreads, kMinCtas) norm_rope_kernel(const RopeParams p, int rows_per_unit) {
+  constexpr int LPR = D / 16;             // lanes per row
   constexpr int RPS = 32 / LPR;           // rows per step of a warp
   constexpr uint32_t kFull = 0xffffffffu;
+  __shared__ uint4 stage[kSlots][2][kRopeThreads];
   const int lane = threadIdx.x & 31;
   const int lr = lane % LPR, sub = lane / LPR;
   griddep_wait();  // the projection's output comes from the previous kernel in the stream
   griddep_launch_dependents();
-  const int uq = (p.num_q_heads + rows_per_unit - 1) / rows_per_unit, uk = (p.kv_heads + rows_per_unit - 1) / rows_per_unit;
-  const int upt = uq + 2 * uk;  // units per token
+  // All units of queries, then those of keys, then those of values: a CTA's warps end together.
   const int64_t u = int64_t(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  if (u >= p.num_tokens * upt) return;
-  const int64_t t = u / upt;
-  const int v = int(u - t * upt);
-  const int kind = v < uq ? 0 : v < uq + uk ? 1 : 2;  // query, key, value
-  const int r0 = (kind == 0 ? v : kind == 1 ? v - uq : v - uq - uk) * rows_per_unit;
+  const int uq = (p.num_q_heads + rows_per_unit - 1) / rows_per_unit, uk = (p.kv_heads + rows_per_unit - 1) / rows_per_unit;
+  const int64_t nq = p.num_tokens * uq, nk = p.num_tokens * uk;
+  if (u >= nq + 2 * nk) return;
+  const int kind = u < nq ? 0 : u < nq + nk ? 1 : 2;  // query, key, value
+  const int64_t at = u - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk);
+  const int per = kind == 0 ? uq : uk;  // units per token
+  const int64_t t = (at >> 32) == 0 ? int64_t(uint32_t(at) / uint32_t(per)) : at / per;
+  const int r0 = int(at - t * per) * rows_per_unit;
   const int r1 = min(kind == 0 ? p.num_q_heads : p.kv_heads, r0 + rows_per_unit);
+  // The lane's two pieces of 8 values: the two halves of 8 rotated pairs, or what lies past the
+  // rotated part, or (values, interleaved pairs) any two.
+  const bool apart = kind != 2 && !p.interleaved;
+  const int half8 = apart ? p.rot_dim >> 4 : 0;  // pieces of half the rotated part
+  const int c0 = lr < half8 ? lr : lr + half8, c1 = lr < half8 ? lr + half8 : lr + LPR;
   const auto* src = static_cast<const __nv_bfloat16*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
                     t * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride);
-  // The lane's two chunks of 4 values: the two halves of 4 rotated pairs, or what lies past the
-  // rotated part, or (values, interleaved pairs) 8 neighbours.
-  const int half4 = p.rot_dim >> 3;  // chunks of half the rotated part
-  const bool apart = kind != 2 && !p.interleaved && p.rot_dim > 0;
-  const bool turns = kind != 2 && lr * 8 < p.rot_dim;  // half4 lanes hold pairs, whichever way they lie
-  int c0 = 2 * lr, c1 = 2 * lr + 1;
-  if (apart) {
-    c0 = lr < half4 ? lr : lr + half4;
-    c1 = lr < half4 ? lr + half4 : lr + half4 + (D / 8 - half4);
-  }
-  uint2 raw[kBatch][2];
-  auto load = [&](int r) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int h = r + i * RPS + sub;
-      if (h < r1) {
-        raw[i][0] = *reinterpret_cast<const uint2*>(src + int64_t(h) * D + c0 * 4);
-        raw[i][1] = *reinterpret_cast<const uint2*>(src + int64_t(h) * D + c1 * 4);
-      }
+  auto load = [&](int r, int st) {
+    if (r + sub < r1) {
+      copy_piece(&stage[st][0][threadIdx.x], src + int64_t(r + sub) * D + c0 * 8);
+      copy_piece(&stage[st][1][threadIdx.x], src + int64_t(r + sub) * D + c1 * 8);
     }
+    copies_next_step();
   };
 #pragma unroll
-  for (int i = 0; i < kBatch; ++i) raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
-  load(r0);
+  for (int i = 0; i < kSlots - 1; ++i) load(r0 + i * RPS, i);
   int64_t slot = -1;
   if (kind != 0) {
     slot = __ldg(p.slot_mapping + t);
@@ -123,103 +184,122 @@ __global__ void __launch_bounds__(kRopeThreads, 4) norm_rope_kernel(const RopePa
       slot = -1;
     }
   }
+  // whether pairs of the lane's first four and of its last four are rotated
+  const bool turns0 = kind != 2 && p.rot_dim > 0 && (apart ? lr < half8 : c0 * 8 < p.rot_dim);
+  const bool turns1 = kind != 2 && p.rot_dim > 0 && (apart ? lr < half8 : c1 * 8 < p.rot_dim);
   bool ok = true;
-  float4 c = make_float4(1.0f, 1.0f, 1.0f, 1.0f), s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float4 cs[2] = {make_float4(1.0f, 1.0f, 1.0f, 1.0f), make_float4(1.0f, 1.0f, 1.0f, 1.0f)};
+  float4 sn[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   if (p.cos_sin) {
     const int pos = __ldg(p.positions + t);
     ok = pos >= 0 && pos < p.max_position;
-    if (!ok && lane == 0 && v == 0) set_error(p.err, kErrPosition);
-    if (ok && turns) {
-      const float4* row = reinterpret_cast<const float4*>(p.cos_sin + int64_t(pos) * p.rot_dim);
-      c = __ldg(row + lr);
-      s = __ldg(row + half4 + lr);
+    if (!ok && lane == 0 && kind == 0 && r0 == 0) set_error(p.err, kErrPosition);
+    const float4* row = reinterpret_cast<const float4*>(p.cos_sin + int64_t(pos) * p.rot_dim);
+    const int half4 = p.rot_dim >> 3, i0 = apart ? 2 * lr : c0, i1 = apart ? 2 * lr + 1 : c1;
+    if (ok && turns0) {
+      cs[0] = __ldg(row + i0);
+      sn[0] = __ldg(row + half4 + i0);
+    }
+    if (ok && turns1) {
+      cs[1] = __ldg(row + i1);
+      sn[1] = __ldg(row + half4 + i1);
     }
   }
   const void* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-  float4 w0 = make_float4(1.0f, 1.0f, 1.0f, 1.0f), w1 = w0;
-  if (weight) {
-    const uint2 a = __ldg(static_cast<const uint2*>(weight) + c0), b = __ldg(static_cast<const uint2*>(weight) + c1);
-    w0 = make_float4(bf16lo(a.x), bf16hi(a.x), bf16lo(a.y), bf16hi(a.y));
-    w1 = make_float4(bf16lo(b.x), bf16hi(b.x), bf16lo(b.y), bf16hi(b.y));
-  }
   // pairs (a, b) -> (a A - b B, b C + a E), two pairs to a register pair: A = w_a cos, B = w_b sin,
-  // C = w_b cos, E = w_a sin.  Pairs are (x0..3, x4..7), or neighbours when interleaved (x0 x1, ...).
-  uint64_t A[2], B[2], Cc[2], E[2];
-  if (p.interleaved && kind != 2) {  // a = x0 x2 | x4 x6
-    const float wa[4] = {w0.x, w0.z, w1.x, w1.z}, wb[4] = {w0.y, w0.w, w1.y, w1.w};
-    w0 = make_float4(wa[0], wa[1], wa[2], wa[3]);
-    w1 = make_float4(wb[0], wb[1], wb[2], wb[3]);
-  }
-  A[0] = f32x2(w0.x * c.x, w0.y * c.y); A[1] = f32x2(w0.z * c.z, w0.w * c.w);
-  B[0] = f32x2(-w1.x * s.x, -w1.y * s.y); B[1] = f32x2(-w1.z * s.z, -w1.w * s.w);
-  Cc[0] = f32x2(w1.x * c.x, w1.y * c.y); Cc[1] = f32x2(w1.z * c.z, w1.w * c.w);
-  E[0] = f32x2(w0.x * s.x, w0.y * s.y); E[1] = f32x2(w0.z * s.z, w0.w * s.w);
-
-  for (int r = r0; r < r1; r += kBatch * RPS) {
-    uint2 cur[kBatch][2];
+  // C = w_b cos, E = w_a sin.  Pairs are a value of each piece, or neighbours when interleaved.
+  uint64_t A[4], B[4], Cc[4], E[4];
+  {
+    float w[16], wa[8], wb[8];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      cur[i][0] = raw[i][0];
-      cur[i][1] = raw[i][1];
+    for (int i = 0; i < 16; ++i) w[i] = 1.0f;
+    if (weight) {
+      unpack8(__ldg(static_cast<const uint4*>(weight) + c0), w);
+      unpack8(__ldg(static_cast<const uint4*>(weight) + c1), w + 8);
     }
-    if (r + kBatch * RPS < r1) load(r + kBatch * RPS);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (r + i * RPS >= r1) break;  // the same for the whole warp
-      const int h = r + i * RPS + sub;
-      float x[8] = {bf16lo(cur[i][0].x), bf16hi(cur[i][0].x), bf16lo(cur[i][0].y), bf16hi(cur[i][0].y),
-                    bf16lo(cur[i][1].x), bf16hi(cur[i][1].x), bf16lo(cur[i][1].y), bf16hi(cur[i][1].y)};
-      if (kind != 2) {
-        uint64_t a[2], b[2];
-        if (p.interleaved) {
-          a[0] = f32x2(x[0], x[2]); a[1] = f32x2(x[4], x[6]);
-          b[0] = f32x2(x[1], x[3]); b[1] = f32x2(x[5], x[7]);
-        } else {
-          a[0] = f32x2(x[0], x[1]); a[1] = f32x2(x[2], x[3]);
-          b[0] = f32x2(x[4], x[5]); b[1] = f32x2(x[6], x[7]);
-        }
-        uint64_t inv2 = f32x2(1.0f, 1.0f);
-        if (weight) {
-          const uint64_t q2 = fma2(a[0], a[0], fma2(a[1], a[1], fma2(b[0], b[0], mul2(b[1], b[1]))));
-          float ss, hi;
-          f32x2_parts(q2, ss, hi);
-          ss += hi;
+    for (int i = 0; i < 8; ++i) {
+      wa[i] = apart ? w[i] : w[2 * i];
+      wb[i] = apart ? w[8 + i] : w[2 * i + 1];
+    }
+    const float c[8] = {cs[0].x, cs[0].y, cs[0].z, cs[0].w, cs[1].x, cs[1].y, cs[1].z, cs[1].w};
+    const float s[8] = {sn[0].x, sn[0].y, sn[0].z, sn[0].w, sn[1].x, sn[1].y, sn[1].z, sn[1].w};
 #pragma unroll
-          for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-          const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
-          inv2 = f32x2(inv, inv);
-        }
+    for (int j = 0; j < 4; ++j) {
+      A[j] = f32x2(wa[2 * j] * c[2 * j], wa[2 * j + 1] * c[2 * j + 1]);
+      B[j] = f32x2(-wb[2 * j] * s[2 * j], -wb[2 * j + 1] * s[2 * j + 1]);
+      Cc[j] = f32x2(wb[2 * j] * c[2 * j], wb[2 * j + 1] * c[2 * j + 1]);
+      E[j] = f32x2(wa[2 * j] * s[2 * j], wa[2 * j + 1] * s[2 * j + 1]);
+    }
+  }
+
+  int st = 0;
+#pragma unroll 1
+  for (int r = r0; r < r1; r += RPS) {
+    const int h = r + sub;
+    load(r + (kSlots - 1) * RPS, st == 0 ? kSlots - 1 : st - 1);  // over the step before, whose values have all been used
+    copies_wait();
+    float x[16];
+    unpack8(stage[st][0][threadIdx.x], x);
+    unpack8(stage[st][1][threadIdx.x], x + 8);
+    if (++st == kSlots) st = 0;
+    if (kind != 2) {
+      uint64_t a[4], b[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint64_t ya = mul2(a[j], A[j]), yb = mul2(b[j], Cc[j]);
-          if (turns) {  // elsewhere sine is 0, but an infinity times 0 is not
-            ya = fma2(b[j], B[j], ya);
-            yb = fma2(a[j], E[j], yb);
-          }
-          a[j] = mul2(ya, inv2);
-          b[j] = mul2(yb, inv2);
-        }
-        if (p.interleaved) {
-          f32x2_parts(a[0], x[0], x[2]); f32x2_parts(a[1], x[4], x[6]);
-          f32x2_parts(b[0], x[1], x[3]); f32x2_parts(b[1], x[5], x[7]);
-        } else {
-          f32x2_parts(a[0], x[0], x[1]); f32x2_parts(a[1], x[2], x[3]);
-          f32x2_parts(b[0], x[4], x[5]); f32x2_parts(b[1], x[6], x[7]);
-        }
+      for (int j = 0; j < 4; ++j) {
+        a[j] = apart ? f32x2(x[2 * j], x[2 * j + 1]) : f32x2(x[4 * j], x[4 * j + 2]);
+        b[j] = apart ? f32x2(x[8 + 2 * j], x[9 + 2 * j]) : f32x2(x[4 * j + 1], x[4 * j + 3]);
       }
-      if (kind == 0) {
-        if (h < r1) {
-          auto* to = static_cast<__nv_bfloat16*>(p.q_out) + t * p.out_stride + int64_t(h) * D;
-          const uint2 y0 = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-          const uint2 y1 = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-          *reinterpret_cast<uint2*>(to + c0 * 4) = ok ? y0 : make_uint2(0u, 0u);
-          *reinterpret_cast<uint2*>(to + c1 * 4) = ok ? y1 : make_uint2(0u, 0u);
+      uint64_t inv2 = f32x2(1.0f, 1.0f);
+      if (weight) {
+        uint64_t q2 = mul2(a[0], a[0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) q2 = fma2(a[j], a[j], q2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q2 = fma2(b[j], b[j], q2);
+        float ss, hi;
+        f32x2_parts(q2, ss, hi);
+        ss += hi;
+#pragma unroll
+        for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+        const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
+        inv2 = f32x2(inv, inv);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint64_t ya = mul2(a[j], A[j]), yb = mul2(b[j], Cc[j]);
+        if (j < 2 ? turns0 : turns1) {  // elsewhere sine is 0, but an infinity times 0 is not
+          ya = fma2(b[j], B[j], ya);
+          yb = fma2(a[j], E[j], yb);
+        }
+        a[j] = mul2(ya, inv2);
+        b[j] = mul2(yb, inv2);
+      }
+      if (apart) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f32x2_parts(a[j], x[2 * j], x[2 * j + 1]);
+          f32x2_parts(b[j], x[8 + 2 * j], x[9 + 2 * j]);
         }
       } else {
-        const int64_t row = ((slot / kBlockSize) * p.kv_heads + h) * kBlockSize + slot % kBlockSize;
-        store_cache<KV, LPR>(x, kind == 1 ? p.k_cache : p.v_cache, kind == 1 ? p.k_scale : p.v_scale, row, c0, c1,
-                             ok && slot >= 0 && h < r1, lr == 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f32x2_parts(a[j], x[4 * j], x[4 * j + 2]);
+          f32x2_parts(b[j], x[4 * j + 1], x[4 * j + 3]);
+        }
       }
+    }
+    if (kind == 0) {
+      if (h < r1) {
+        auto* to = static_cast<__nv_bfloat16*>(p.q_out) + t * p.out_stride + int64_t(h) * D;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(to + c0 * 8) = ok ? pack8(x) : zero;
+        *reinterpret_cast<uint4*>(to + c1 * 8) = ok ? pack8(x + 8) : zero;
+      }
+    } else {
+      const int64_t row = ((slot / kBlockSize) * p.kv_heads + h) * kBlockSize + slot % kBlockSize;
+      store_cache<KV, LPR>(x, kind == 1 ? p.k_cache : p.v_cache, kind == 1 ? p.k_scale : p.v_scale, row, c0, c1,
+                           ok && slot >= 0 && h < r1, lr == 0);
     }
   }
 }
@@ -243,12 +323,18 @@ __global__ void __launch_bounds__(kRopeThreads)
 template <KvType KV, int D>
 cudaError_t launch_norm_rope_variant(const RopeParams& p, cudaStream_t stream) {
   constexpr int kWarps = kRopeThreads / 32;
-  constexpr int kFewRows = 32 / (D / 8) * kBatch;  // one batch of loads
-  // All of a token's heads to a warp where that fills the GPU (the token's position, table row and
-  // weights are then read once for all), one batch of rows otherwise.
+  // Rows of a unit: one step's, doubled (up to all of a token's heads) while that leaves 1.5 units for
+  // each warp the GPU holds at a time.  More rows share a token's position, table row and weights; fewer
+  // are done sooner.  Measured on GB300, 32 + 8 + 8 heads of 128 into a bf16 pool, 4 / 8 / 16 / 32 rows: 64
+  // tokens 2.3 / 2.5 / 3.1 / 4.4 us, 1024 9.9 / 7.5 / 7.3 / 11.2, 1536 14.0 / 10.1 / 9.0 / 11.1, 2048
+  // 17.7 / 12.8 / 11.5 / 10.8, 16384 142 / 97 / 80 / 72.7.
   const int most = p.num_q_heads > p.kv_heads ? p.num_q_heads : p.kv_heads;
-  const int rows = p.num_tokens * 3 >= 152 * 32 * 2 ? most : kFewRows;
-  const int64_t units = p.num_tokens * ((p.num_q_heads + rows - 1) / rows + 2 * ((p.kv_heads + rows - 1) / rows));
+  auto count = [&](int rows) {
+    return p.num_tokens * ((p.num_q_heads + int64_t(rows) - 1) / rows + 2 * ((p.kv_heads + int64_t(rows) - 1) / rows));
+  };
+  int rows = 32 / (D / 16);
+  while (rows < most && rows < (1 << 20) && count(2 * rows) * 2 >= 3 * 152 * kMinCtas * kWarps) rows *= 2;
+  const int64_t units = count(rows);
   const int64_t grid = (units + kWarps - 1) / kWarps;
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   return launch_pdl(norm_rope_kernel<KV, D>, dim3(unsigned(grid)), dim3(kRopeThreads), 0, stream, p, rows);

@@ -91,6 +91,36 @@ def test_memory_made_for_a_call_on_another_stream():
     pool.close()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kv", ["int8", "fp8"])
+def test_codes_are_those_of_reshape_and_cache(kv, d):
+    """Keys that are neither normalised nor rotated and values get the very codes and scales that
+    reshape_and_cache writes: random rows, quotients on a tie of two codes and next to one, rows of
+    tiny and of huge values, and rows with an infinity or a NaN."""
+    g = torch.Generator().manual_seed(d)
+    n, h = 4096, 2
+    x = torch.randn(n, h, d, generator=g)
+    x[512:1024] = (torch.randint(-254, 255, (512, h, d), generator=g) / 2.0).clamp(-127, 127)  # s = 1: halves are ties
+    x[512:1024, :, 0] = 127.0
+    x[1024:1536] = torch.randint(-448, 449, (512, h, d), generator=g).float()
+    x[1024:1536, :, 0] = 448.0
+    x[1536:2048] *= 2.0 ** torch.randint(-132, 120, (512, 1, 1), generator=g).float()
+    x[2048:2560] = (x[2048:2560] * 8).round() / 8  # few different values: quotients fall together
+    x = x.bfloat16()
+    x[2560, 0, 3], x[2561, 1, 5], x[2562, 0, :2], x[2563] = float("inf"), float("nan"), float("-inf"), 0.0
+    x = x.cuda()
+    v = x.flip(0).contiguous()
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    a, b = (pkv.PagedKVPool(n // 16, h, d, kv) for _ in range(2))
+    a.reshape_and_cache(x, v, slots)
+    b.norm_rope_and_cache(x, x, v, None, slots)
+    assert torch.equal(a.k_cache, b.k_cache) and torch.equal(a.v_cache, b.v_cache)
+    for s, t in ((a.k_scale, b.k_scale), (a.v_scale, b.v_scale)):
+        assert torch.equal(s.view(torch.int32), t.view(torch.int32))
+    for pool in (a, b):
+        pool.close()
+
+
 def test_queries_on_one_another_are_refused():
     pool = pkv.PagedKVPool(4, 2, 64)
     q = torch.randn(3, 4, 64, device="cuda").bfloat16()
