@@ -45,20 +45,23 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
   const float2* sml = p.suffix_ml + gw * p.suffix_parts;
   const float* sacc = p.suffix_acc + gw * p.suffix_parts * D + lane * kDPV;
   // prefix partials: rows 256 apart, one per CTA (two for a unit of up to 128 rows)
-  int npre = 0, twice = 0;
+  int npre = 0, twice = 0, rows = 0;
   int64_t first = 0;
   if (d.tiles > 0) {
     const int r = d.first_row + qi * p.group + (h - kvh * p.group);
-    const int units = (d.rows + kPrefixRows - 1) / kPrefixRows;
-    const int64_t w0 = d.w_base + (int64_t(kvh) * units + r / kPrefixRows) * (d.tiles + kUnitCost) + kUnitCost;  // first tile
+    const int units = (d.rows + kPrefixRows - 1) / kPrefixRows, u = r / kPrefixRows;
+    rows = unit_rows(d.rows, u);
+    twice = tiles_apart(rows);
+    // the places of the unit's steps
+    const int64_t w0 = d.w_base + kvh * head_line(d.rows, units, d.tiles) + int64_t(u) * unit_line(kPrefixRows, d.tiles) + unit_cost(rows);
+    const int64_t w1 = w0 + unit_steps(rows, d.tiles) - 1;
     const int ctas = stretch_ctas(d.total, p.grid);
-    const int c0 = stretch_owner(d.total, ctas, w0), c1 = stretch_owner(d.total, ctas, w0 + d.tiles - 1);
-    twice = d.rows <= kPrefixRows / 2;
+    const int c0 = stretch_owner(d.total, ctas, w0), c1 = stretch_owner(d.total, ctas, w1);
     npre = (c1 - c0 + 1) << twice;
     first = d.row_base + int64_t(kvh) * partial_rows(d.rows) + r + int64_t(c0) * kPrefixRows;
   }
   const int n = nsuf + npre;
-  auto pre_row = [&](int i) { return first + int64_t(i >> twice) * kPrefixRows + (twice && (i & 1) ? d.rows : 0); };
+  auto pre_row = [&](int i) { return first + int64_t(i >> twice) * kPrefixRows + (twice && (i & 1) ? rows : 0); };
   auto state = [&](int i) { return i < nsuf ? sml[i] : p.ml[pre_row(i - nsuf)]; };
   // lane i holds partials i, i + 32, ...; the first 32 stay in registers
   const float2 mine = lane < n ? state(lane) : make_float2(-INFINITY, 0.0f);

@@ -3,28 +3,45 @@
 // Group g of the batch is sequences group_starts[g] .. group_starts[g + 1] - 1, whose first
 // prefix_lens[g] tokens (whole blocks) are the same.  A group has R = (sequences) * k * (query
 // heads per kv head) query rows per kv head, in units of up to 256 rows, and its prefix is cut
-// into tiles of 128 tokens.  All (kv head, unit, tile) triples of all groups, in that order,
-// form one line of work, which the CTAs of the prefix pass share out in equal contiguous
-// stretches, so that they end together whatever the groups' sizes.  Each unit takes kUnitCost places
-// on the line ahead of its tiles: what loading its queries and writing its partials costs, in
-// tiles.  A stretch's tiles of one (kv head, unit) are a piece; it leaves one partial (running max,
-// sum, accumulator) per row.
+// into tiles of 128 tokens.  A unit of more than 128 rows takes a tile at a step, its rows in two
+// streams of 128; a unit of up to 128 rows (only a group's last can be) takes two, one per stream.
+// All (kv head, unit, step) triples of all groups, in that order, form one line of work, which the
+// CTAs of the prefix pass share out in equal contiguous stretches, so that they end together
+// whatever the groups' sizes.  Each unit takes places on the line ahead of its steps (unit_cost): what
+// loading its queries and writing its partials costs, in steps.  A stretch's steps of one (kv head,
+// unit) are a piece; it leaves one partial (running max, sum, accumulator) per row.
 //
 // Partial rows: CTA c's partial of a unit starts at row (rows of all units before it) + 256 c.
 // Going along the line either the unit or the CTA (or both) moves on, by that unit's rows or by
 // 256, so no two partials overlap.  A unit of up to 128 rows holds two rows of partials per
-// query row, since its even and its odd tiles are accumulated apart.
+// query row, since each stream accumulates its own tiles.
 #pragma once
 
 #include "pkv_device.cuh"
 
 namespace pkv {
 
-constexpr int kUnitCost = 4;
-
+// Query rows of unit u of a group of `rows`.
+__host__ __device__ __forceinline__ int unit_rows(int rows, int u) {
+  const int left = rows - u * kPrefixRows;
+  return left < kPrefixRows ? left : kPrefixRows;
+}
+// Whether a unit of n rows gives its streams tiles apart, and its steps over `tiles` tiles.
+__host__ __device__ __forceinline__ bool tiles_apart(int n) { return n <= kPrefixRows / 2; }
+__host__ __device__ __forceinline__ int unit_steps(int n, int tiles) { return tiles_apart(n) ? (tiles + 1) / 2 : tiles; }
+// Places ahead of a unit's steps: a piece's start and end, and its rows of partials.  Measured on GB300
+// with the same places for every unit (1 / 2 / 4 / 6), whole calls: 16 groups of 1 to 14 sequences
+// (MHA) 114.0 / 115.2 / 119.6 / 122.8 us, 2 groups of 384 rows a kv head (FP8, head_dim 64) 62.7 / 62.0 /
+// 59.9 / 62.3; with these 114.5 and 61.8.  With the last 128 of 384 rows as one stream's, on
+// every tile, the latter took 63.7.
+__host__ __device__ __forceinline__ int unit_cost(int n) {
+  return 1 + (tiles_apart(n) ? 2 * n : n) * 3 / kPrefixRows;
+}
+__host__ __device__ __forceinline__ int unit_line(int n, int tiles) { return unit_cost(n) + unit_steps(n, tiles); }
 // Rows of partials that a group of `rows` query rows takes per kv head.
 __host__ __device__ __forceinline__ int64_t partial_rows(int rows) {
-  return rows <= kPrefixRows / 2 ? 2 * int64_t(rows) : rows;
+  const int last = rows <= 0 ? 0 : (rows - 1) % kPrefixRows + 1;
+  return int64_t(rows) + (tiles_apart(last) ? last : 0);
 }
 
 // a / b for non-negative a and positive b: work lines are short enough for 32 bits as a rule, and a
@@ -34,13 +51,16 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
 }
 
 struct PrefixGroup {
-  int first_seq, rows, units, tiles;  // units per kv head
+  int first_seq, rows, units, nblk, tiles;  // units per kv head; blocks and tiles of the prefix
   int64_t w_base, row_base;
 };
 
-// Places of a group on the line.
+// Places on the line of one kv head of a group with work, and of the whole group.
+__device__ __forceinline__ int64_t head_line(int rows, int units, int tiles) {
+  return int64_t(units - 1) * unit_line(kPrefixRows, tiles) + unit_line(unit_rows(rows, units - 1), tiles);
+}
 __device__ __forceinline__ int64_t group_line(const PrefixParams& p, const PrefixGroup& x) {
-  return x.tiles > 0 ? int64_t(x.units) * p.kv_heads * (x.tiles + kUnitCost) : 0;
+  return x.tiles > 0 && x.rows > 0 ? p.kv_heads * head_line(x.rows, x.units, x.tiles) : 0;
 }
 
 // The scan of the groups, in scratch shared memory: base[g] = (first place on the line, first
@@ -58,6 +78,7 @@ __device__ __forceinline__ bool prefix_group(const PrefixParams& p, int g, Prefi
   x.first_seq = s0;
   x.rows = ok ? (s1 - s0) * p.num_queries * p.group : 0;
   x.units = (x.rows + kPrefixRows - 1) / kPrefixRows;
+  x.nblk = ok ? len / kBlockSize : 0;
   x.tiles = ok ? (len + kPrefixTile - 1) / kPrefixTile : 0;
   return ok;
 }
@@ -92,6 +113,7 @@ __device__ __forceinline__ PrefixGroup lane_group(const PrefixLanes& me, int g) 
   x.first_seq = __shfl_sync(0xffffffffu, me.x.first_seq, g);
   x.rows = __shfl_sync(0xffffffffu, me.x.rows, g);
   x.units = __shfl_sync(0xffffffffu, me.x.units, g);
+  x.nblk = __shfl_sync(0xffffffffu, me.x.nblk, g);
   x.tiles = __shfl_sync(0xffffffffu, me.x.tiles, g);
   x.w_base = __shfl_sync(0xffffffffu, me.x.w_base, g);
   x.row_base = __shfl_sync(0xffffffffu, me.x.row_base, g);
@@ -170,24 +192,23 @@ struct PrefixPiece {
   int tile0, tiles;
   int kvh;
   int row0, nrows;       // the unit's query rows within the group
-  int rows;              // all of the group's (up to 128: the streams share the tiles out)
   int again;             // other units read the same tiles
-  int pad;
+  int pad[2];
 };
 
 // The piece at the walk's place, if it has tiles; moves past the unit's part of the stretch.
 __device__ __forceinline__ bool walk_piece(const PrefixParams& p, PrefixWalk& k, int cta, PrefixPiece& x) {
-  const int all = k.x.tiles + kUnitCost;
+  x.row0 = k.unit * kPrefixRows;
+  x.nrows = unit_rows(k.x.rows, k.unit);
+  const int all = unit_line(x.nrows, k.x.tiles), cost = unit_cost(x.nrows), per = tiles_apart(x.nrows) ? 2 : 1;
   const int len = int(min(int64_t(all - k.at), k.w_end - k.w));
-  x.tile0 = max(0, k.at - kUnitCost);
-  x.tiles = k.at + len - kUnitCost - x.tile0;
+  const int step0 = max(0, k.at - cost), step1 = k.at + len - cost;
+  x.tile0 = step0 * per;
+  x.tiles = min(k.x.tiles, step1 * per) - x.tile0;
   x.first_seq = k.x.first_seq;
   x.kvh = k.kvh;
-  x.row0 = k.unit * kPrefixRows;
-  x.nrows = min(kPrefixRows, k.x.rows - x.row0);
-  x.rows = k.x.rows;
   x.again = k.x.units > 1;
-  x.nblk = __ldg(p.prefix_lens + k.g) / kBlockSize;
+  x.nblk = k.x.nblk;
   x.partial = k.x.row_base + int64_t(k.kvh) * partial_rows(k.x.rows) + x.row0 + int64_t(cta) * kPrefixRows;
   k.w += len;
   k.at += len;
@@ -198,18 +219,19 @@ __device__ __forceinline__ bool walk_piece(const PrefixParams& p, PrefixWalk& k,
 __device__ __forceinline__ bool walk_range(const PrefixParams& p, int64_t total, int cta, PrefixWalk& k) {
   const int ctas = stretch_ctas(total, p.grid);
   if (total <= 0 || cta >= ctas) return false;
-  k.w = stretch_start(total, ctas, cta);
-  k.w_end = stretch_start(total, ctas, cta + 1);
+  const int64_t at = stretch_start(total, ctas, cta + int(threadIdx.x & 1));  // one division for both
+  k.w = __shfl_sync(0xffffffffu, at, 0);
+  k.w_end = __shfl_sync(0xffffffffu, at, 1);
   return true;
 }
 // Its first place, once k.g and k.x are the group that holds it.
 __device__ __forceinline__ void walk_first(PrefixWalk& k) {
-  const int64_t in_group = k.w - k.x.w_base;
-  const int all = k.x.tiles + kUnitCost;
-  const int u = int(div_pos(in_group, all));  // kv head * units + unit
-  k.at = int(in_group - int64_t(u) * all);
-  k.kvh = u / k.x.units;
-  k.unit = u - k.kvh * k.x.units;
+  const int64_t in_group = k.w - k.x.w_base, head = head_line(k.x.rows, k.x.units, k.x.tiles);
+  k.kvh = int(div_pos(in_group, head));
+  const int64_t in_head = in_group - k.kvh * head;
+  const int all = unit_line(kPrefixRows, k.x.tiles);  // of every unit but the last
+  k.unit = k.x.units == 1 ? 0 : min(int(div_pos(in_head, all)), k.x.units - 1);
+  k.at = int(in_head - int64_t(k.unit) * all);
 }
 __device__ __forceinline__ bool walk_begin(const PrefixParams& p, const PrefixScan& sc, int64_t total, int cta,
                                            PrefixWalk& k) {

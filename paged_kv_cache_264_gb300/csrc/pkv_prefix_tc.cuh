@@ -2,10 +2,9 @@
 // core: up to 256 query rows of one (group, kv head) against a stretch of its prefix, a CTA per
 // SM, each with its stretch of the work line (pkv_prefix.cuh).
 //
-// Two streams of 128 rows run through the CTA.  With more than 128 rows in the group they hold
+// Two streams of 128 rows run through the CTA.  With more than 128 rows in the unit they hold
 // different rows and take every 128-token tile; with up to 128 rows both hold the same rows and
-// take the even and the odd tiles, so that either way one stream's softmax runs under the other's
-// products.  Per stream and tile:
+// take every other tile, so that either way one stream's softmax runs under the other's products.  Per stream and tile:
 //     S = Q K^T    128 x 128 x D, both operands in shared memory, S in tensor memory (fp32)
 //     P = 2^(S * scale - m)    two threads to a row, 64 logits each in registers: no shuffles
 //     O += P V     128 x D x 128, P in tensor memory (bf16, over S's columns), V as it lies in the
@@ -128,7 +127,7 @@ __device__ __forceinline__ TileLoad tile_load(bool two, int n, int i) {
 }
 // Tiles of a piece that stream s takes: all of them where the streams hold different rows.
 __device__ __forceinline__ int stream_steps(const PrefixPiece& x, int s) {
-  return x.rows > 128 ? (s == 0 || x.nrows > 128 ? x.tiles : 0) : (x.tiles + 1 - s) / 2;
+  return x.nrows > 128 ? x.tiles : (x.tiles + 1 - s) / 2;
 }
 
 // Two codes in the low bytes of each half of `v` (bits 0-7 and 16-23) -> two bf16, exactly: with
@@ -305,7 +304,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     uint32_t filled = 0, tiles = 0;
     PrefixPiece x;
     for (take(x); x.tiles > 0; take(x)) {
-      const bool two = x.rows > 128;
+      const bool two = x.nrows > 128;
       const int32_t* table = p.block_tables + int64_t(x.first_seq) * p.max_blocks_per_seq;
       // tiles read again by the group's other units stay in L2; others are read once
       const uint64_t policy = x.again ? l2_evict_last_policy() : l2_evict_first_policy();
@@ -373,7 +372,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     uint32_t step = 0;                     // parity of the stream's step
     PrefixPiece x;
     for (take(x); x.tiles > 0; take(x)) {
-      const bool two = x.rows > 128;
+      const bool two = x.nrows > 128;
       const int ns = stream_steps(x, s);
       bool fresh = true;  // O holds nothing of this piece yet
       if (ns > 0) alive = wait_all(sy->q_ready + s, seg & 1);
@@ -384,7 +383,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
           alive = false;
           break;
         }
-        if (two ? ns == 0 : ld.which != s) {  // the other stream's alone
+        if (!two && ld.which != s) {  // the other stream's alone
           if (lane == 0) mbar_arrive(sy->empty + at.st);
         } else if (!ld.is_v) {
           // S; P lies over it until the products of the step before are done
@@ -455,7 +454,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     uint32_t filled = 0;
     PrefixPiece x;
     for (take(x); x.tiles > 0; take(x)) {
-      const bool two = x.rows > 128;
+      const bool two = x.nrows > 128;
       const int32_t* table = p.block_tables + int64_t(x.first_seq) * p.max_blocks_per_seq;
       // this token's K and V scales of the tile to come, and its block of the tile after that
       // (past the end, or of a missing block: scales that nothing uses)
@@ -560,7 +559,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     PrefixPiece x;
     for (;;) {
       take(x);
-      const bool two = x.rows > 128;
+      const bool two = x.nrows > 128;
       const int ns = x.tiles > 0 ? stream_steps(x, s) : 0;
       const int row0 = two ? s * 128 : 0;                           // the stream's first row within the unit
       next_rows = x.tiles > 0 ? max(0, min(128, x.nrows - row0)) : 0;  // its rows
@@ -650,7 +649,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       }
       if (x.tiles == 0 || !alive) break;
       nrows = next_rows;
-      to = x.partial + (two ? s * 128 : s * x.rows);
+      to = x.partial + (two ? s * 128 : s * x.nrows);
       const uint32_t tiles0 = tiles;
       tiles += x.tiles;
       pending = ns > 0;
@@ -664,7 +663,7 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
       m = kMaxFloor;
       l = 0.0f;
       any = false;
-      const bool turning = D == 128 && x.rows > 128 && x.nrows > 128;
+      const bool turning = D == 128 && two;
 #pragma unroll 1
       for (int i = 0; i < ns; ++i, step ^= 1u) {
         const int tile = two ? i : 2 * i + s;
