@@ -2,6 +2,7 @@
 // decode plan (partition size), workspace layout and kernel dispatch.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdio>
 #include <cstring>
@@ -345,6 +346,7 @@ class OnPoolDevice {
 // Layout of a shared-prefix call's workspace and the plan of its suffix pass.
 struct PrefixPlan {
   Plan suffix;
+  bool join;  // the suffix pass joins the prefix's states itself: no merge pass
   int grid;
   int suffix_blocks;
   size_t lens, tables, acc, ml, suffix_acc, suffix_ml, bytes;  // offsets (the descriptors sit at 0), size
@@ -373,6 +375,15 @@ pkv_status make_prefix_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
   if (suffix_opt.partition_blocks == 0 && x->suffix_blocks <= 32) suffix_opt.partition_blocks = 32;
   st = make_plan(pool, num_seqs, num_q_heads, max_suffix_len < nq ? nq : max_suffix_len, &suffix_opt, &x->suffix);
   if (st != PKV_OK) return st;
+  // Each sequence one item, all on the GPU at once, and about 12 prefix states per row at most: the items
+  // join them.  Else a merge pass does.  Measured on GB300, whole calls, joined against merged: 32 items of
+  // 8 states 16.5 against 18.5 us, 384 of 10 57.1 against 61.7; 512 of 20 61.7 against 60.9, 3744 of 2 119.7
+  // against 114.1 (the loads' latency is paid per item).
+  const int64_t items = int64_t(num_seqs) * pool->kv_heads * x->suffix.chunks;
+  const int64_t states = std::min<int64_t>(ceil_div(max_prefix_len, pkv::kPrefixTile),
+                                           x->grid / (int64_t(pool->kv_heads) * std::max(num_groups, 1)) + 1);
+  x->join = x->suffix.kernel == PKV_KERNEL_TENSOR_CORE && x->suffix.shape == 0 && x->suffix.max_parts == 1 &&
+            items <= int64_t(pool->sm_count) * x->suffix.ctas_per_sm && states <= 12;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -816,16 +827,24 @@ pkv_status pkv_shared_prefix_decode(const pkv_pool* pool, const void* q, const i
   p.ws_acc = reinterpret_cast<float*>(ws + plan.suffix_acc);
   p.ws_ml = reinterpret_cast<float*>(ws + plan.suffix_ml);
   p.min_len = 0;  // the prefix may cover every token a query sees
-  p.partials = 1;
+  p.partials = !plan.join;
+  p.prefix_seqs = x.seqs;
+  p.prefix_acc = x.acc;
+  p.prefix_ml = x.ml;
+  p.prefix_grid = x.grid;
 
   auto s = static_cast<cudaStream_t>(stream);
   cudaError_t e = pkv::launch_prefix(x, pool->tmap_k, pool->tmap_v, static_cast<pkv::KvType>(pool->dtype), s);
   if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
-  e = launch_decode(pool, plan.suffix, p, s);
+  e = plan.join ? pkv::launch_decode_mma_join(p, &pool->tmap_k, &pool->tmap_v, static_cast<pkv::KvType>(pool->dtype),
+                                              plan.suffix.cols, s)
+                : launch_decode(pool, plan.suffix, p, s);
   if (e != cudaSuccess) return cuda_fail(e, "shared prefix: suffix launch");
+  g_launches.fetch_add(2, std::memory_order_relaxed);
+  if (plan.join) return PKV_OK;
   e = pkv::launch_prefix_merge(x, s);
   if (e != cudaSuccess) return cuda_fail(e, "shared prefix: merge launch");
-  g_launches.fetch_add(3, std::memory_order_relaxed);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
   return PKV_OK;
 }
 

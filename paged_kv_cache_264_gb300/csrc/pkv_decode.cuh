@@ -61,6 +61,7 @@
 #include <atomic>
 
 #include "pkv_device.cuh"
+#include "pkv_prefix.cuh"
 
 namespace pkv {
 
@@ -408,6 +409,113 @@ __device__ __forceinline__ void write_bad_len(const DecodeParams& p, const ItemI
   if (threadIdx.x == 0) set_error(p.err, kErrContextLen);
 }
 
+// Where an item's state goes when it joins the prefix pass's.
+struct JoinArgs {
+  const PrefixSeq* seq;
+  const float* acc;
+  const float2* ml;
+  __nv_bfloat16* out;  // of the item's sequence and kv head
+  int grid, kvh, group, num_q_heads, c0, ncols;
+};
+
+// Merge the NW per-warp states of one item, of a sequence's own tokens, and the prefix pass's partial states
+// of its rows, and write the result.  W of a column's lanes take one partial's maximum and sum each, then
+// all read the accumulators, kAhead at a time.  In kernels of their own: as a case of the decode kernels,
+// called or inlined, it took registers from their loops (INT8, 8 sequences of 20000 tokens: 72.6 -> 75.9 us).
+template <int NC, int D, int NW>
+__device__ __forceinline__ void join_warp_records(const unsigned char* smem, size_t warp_stride, JoinArgs p) {
+  constexpr int kThreads = NW * 32;
+  constexpr int kE = NC * D > kThreads ? NC * D / kThreads : 1;  // dims per thread
+  constexpr int kTpc = D / kE;                                    // threads per column
+  constexpr int W = kTpc < 32 ? kTpc : 32;
+  constexpr int kAhead = kE <= 4 ? 8 : 32 / kE;  // up to 32 values of accumulators in registers
+  static_assert(32 % W == 0, "a column's lanes are part of a warp, or whole warps");
+  const int g = threadIdx.x / kTpc, d0 = (threadIdx.x - g * kTpc) * kE;
+  if (g >= p.ncols) return;  // an inactive column, or a thread past NC * D
+  const PrefixSeq d = *p.seq;
+  float own = kMaxFloor, L = 0.0f, acc[kE];
+  float mw[NW];
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    mw[w] = reinterpret_cast<const float*>(smem + size_t(w) * warp_stride)[g * record_stride(D)];
+    own = fmaxf(own, mw[w]);
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const float* r = reinterpret_cast<const float*>(smem + size_t(w) * warp_stride) + g * record_stride(D);
+    const float f = fast_exp2(mw[w] - own);
+    L = fmaf(f, r[1], L);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] = fmaf(f, r[2 + d0 + e], acc[e]);
+  }
+  if (d.tiles > 0) {
+    const PrefixParts x(d, p.kvh, d.first_row + p.c0 + g, p.grid);
+    const int lane = threadIdx.x & 31, i = lane % W;
+    const uint32_t mask = (W == 32 ? ~0u : (1u << (W & 31)) - 1u) << (lane - i);
+    const float2 none = make_float2(kMaxFloor, 0.0f);
+    const float2 mine = i < x.count ? p.ml[x.row(i)] : none;  // the first W partials stay in registers
+    float M = fmaxf(own, mine.x);
+    for (int j = i + W; j < x.count; j += W) M = fmaxf(M, p.ml[x.row(j)].x);
+#pragma unroll
+    for (int o = W / 2; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(mask, M, o));
+    const float f = fast_exp2(own - M);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] *= f;
+    float sum = 0.0f;
+    for (int j0 = 0; j0 < x.count; j0 += W) {
+      const float2 s = j0 == 0 ? mine : j0 + i < x.count ? p.ml[x.row(j0 + i)] : none;
+      // a stream without tiles left a sum of 0 and no accumulator
+      const float w = s.y > 0.0f ? fast_exp2(s.x - M) : 0.0f;
+      sum = fmaf(w, s.y, sum);
+      const int here = min(W, x.count - j0);
+#pragma unroll 1
+      for (int u0 = 0; u0 < here; u0 += kAhead) {
+        float wu[kAhead], v[kAhead][kE];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          wu[u] = __shfl_sync(mask, w, (u0 + u) % W, W);
+          if (u0 + u >= here) wu[u] = 0.0f;
+#pragma unroll
+          for (int e = 0; e < kE; ++e) v[u][e] = 0.0f;
+          if (wu[u] != 0.0f) {
+            const float* src = p.acc + x.row(j0 + u0 + u) * D + d0;
+            if constexpr (kE % 4 == 0) {
+#pragma unroll
+              for (int e = 0; e < kE; e += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(src + e);
+                v[u][e] = q.x; v[u][e + 1] = q.y; v[u][e + 2] = q.z; v[u][e + 3] = q.w;
+              }
+            } else if constexpr (kE == 2) {
+              const float2 q = *reinterpret_cast<const float2*>(src);
+              v[u][0] = q.x; v[u][1] = q.y;
+            } else {
+              v[u][0] = src[0];
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+          for (int e = 0; e < kE; ++e) acc[e] = fmaf(wu[u], v[u][e], acc[e]);
+      }
+    }
+#pragma unroll
+    for (int o = W / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+    L = fmaf(L, f, sum);
+  }
+  const int c = p.c0 + g, qi = c / p.group;
+  auto* out = p.out + (int64_t(qi) * p.num_q_heads + (c - qi * p.group)) * D + d0;
+  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  if constexpr (kE == 1) {
+    out[0] = __float2bfloat16_rn(acc[0] * inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
 // Merge the NW per-warp states of one work item by log-sum-exp and write the bf16 output
 // (single-partition sequences) or the item's partial (m, l, acc) to the workspace.  Warp w's
 // record is [NC][record_stride(D)] floats (running max in log2 units, sum, accumulator) per query
@@ -415,10 +523,17 @@ __device__ __forceinline__ void write_bad_len(const DecodeParams& p, const ItemI
 // takes kE consecutive dims of one column, so that the column's weights 2^(m_w - M) are
 // formed once per thread and the reads and writes are vectors (out and the workspace are
 // 16-byte aligned, and kE divides D).
-template <int NC, int D, int NW>
+template <int NC, int D, int NW, bool kJoin = false>
 __device__ __forceinline__ void merge_warp_records(const unsigned char* smem, size_t warp_stride,
                                                    const DecodeParams& p, int b, int kvh, int c0,
                                                    int part, int nparts) {
+  if constexpr (kJoin) {
+    join_warp_records<NC, D, NW>(smem, warp_stride,
+                                 JoinArgs{p.prefix_seqs + b, p.prefix_acc, p.prefix_ml,
+                                          static_cast<__nv_bfloat16*>(p.out) + col_row(p, b, kvh, 0) * D, p.prefix_grid, kvh,
+                                          p.group, p.num_q_heads, c0, chunk_cols(p, c0, NC)});
+    return;
+  }
   constexpr int kThreads = NW * 32;
   constexpr int kE = NC * D > kThreads ? NC * D / kThreads : 1;  // dims per thread
   constexpr int kTpc = D / kE;                                    // threads per column

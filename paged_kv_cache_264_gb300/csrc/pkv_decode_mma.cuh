@@ -155,7 +155,8 @@ __device__ __forceinline__ void static_for(F&& f) {
 // INT8/FP8 tiles of up to 8 columns with one block per stage are held to 128 registers
 // (4 CTAs per SM), the compiler's own choice for most of them, which the 8-column tiles
 // otherwise exceed (168); every other variant keeps the compiler's choice.
-template <KvType KV, int D, int NC, int NW, int S, int BPS, bool kGen>
+// kJoin: the items, one per sequence, join a prefix pass's partial states with their own.
+template <KvType KV, int D, int NC, int NW, int S, int BPS, bool kGen, bool kJoin = false>
 __global__ void __launch_bounds__(NW * 32, (KvTraits<KV>::kQuant && NC <= 8 && BPS == 1) ? 4 : 0)
     paged_decode_mma_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             const __grid_constant__ CUtensorMap tmap_v, const DecodeParams p) {
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(NW * 32, (KvTraits<KV>::kQuant && NC <= 8 && B
     }
   }
   __syncthreads();
-  merge_warp_records<NC, D, NW>(smem, size_t(S) * C::kStageBytes, p, b, kvh, c0, part, nparts);
+  merge_warp_records<NC, D, NW, kJoin>(smem, size_t(S) * C::kStageBytes, p, b, kvh, c0, part, nparts);
   }  // valid context length
   }  // item located
   item = next_item(p, ss, ticket);
@@ -870,11 +871,11 @@ __global__ void __launch_bounds__(NW * 32, (KvTraits<KV>::kQuant && NC <= 8 && B
   finish_items(p);
 }
 
-template <KvType KV, int D, int NC, int NW, int S, int BPS, bool kGen>
+template <KvType KV, int D, int NC, int NW, int S, int BPS, bool kGen, bool kJoin = false>
 cudaError_t launch_mma_variant(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t stream) {
   using C = MmaCfg<KV, D, NC, NW, S, BPS>;
-  auto kern = paged_decode_mma_kernel<KV, D, NC, NW, S, BPS, kGen>;
+  auto kern = paged_decode_mma_kernel<KV, D, NC, NW, S, BPS, kGen, kJoin>;
   static std::atomic<bool> attr_done[64];  // per device: the shared-memory limit is raised
   int dev = 0;
   cudaGetDevice(&dev);
@@ -914,16 +915,16 @@ constexpr bool mma_record_fits(int nc) {
   return size_t(nc) * record_stride(D) * 4 <= size_t(S) * MmaCfg<KV, D, 2, kNwMma, S, BPS>::kStageBytes;
 }
 
-template <KvType KV, int D, int S, int BPS, bool kGen>
+template <KvType KV, int D, int S, int BPS, bool kGen, bool kJoin = false>
 cudaError_t launch_mma_cols(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                             int cols, cudaStream_t stream) {
   switch (cols) {
-    case 2: return launch_mma_variant<KV, D, 2, kNwMma, S, BPS, kGen>(p, tk, tv, stream);
-    case 4: return launch_mma_variant<KV, D, 4, kNwMma, S, BPS, kGen>(p, tk, tv, stream);
-    case 8: return launch_mma_variant<KV, D, 8, kNwMma, S, BPS, kGen>(p, tk, tv, stream);
+    case 2: return launch_mma_variant<KV, D, 2, kNwMma, S, BPS, kGen, kJoin>(p, tk, tv, stream);
+    case 4: return launch_mma_variant<KV, D, 4, kNwMma, S, BPS, kGen, kJoin>(p, tk, tv, stream);
+    case 8: return launch_mma_variant<KV, D, 8, kNwMma, S, BPS, kGen, kJoin>(p, tk, tv, stream);
     case 16:
       if constexpr (kGen && mma_record_fits<KV, D, S, BPS>(16))
-        return launch_mma_variant<KV, D, 16, kNwMma, S, BPS, kGen>(p, tk, tv, stream);
+        return launch_mma_variant<KV, D, 16, kNwMma, S, BPS, kGen, kJoin>(p, tk, tv, stream);
       return cudaErrorInvalidValue;
     default: return cudaErrorInvalidValue;
   }

@@ -54,6 +54,8 @@ struct CacheParams {
   int head_dim;
 };
 
+struct PrefixSeq;
+
 struct DecodeParams {
   const void* q;                // bf16 [B, k, Hq, D]  (k = num_queries)
   const void* k_cache;          // [NB, Hkv, 16, D]
@@ -88,6 +90,12 @@ struct DecodeParams {
   int min_len;                  // shortest valid context (num_queries; 0 when another pass
                                 // covers the tokens before this call's context)
   int partials;                 // 1: always leave (m, l, acc) in the workspace, never write out
+  // For the kernels that join a prefix pass's partial states (pkv_prefix.cuh): its descriptions
+  // of the sequences, its states and its CTAs.
+  const PrefixSeq* prefix_seqs;
+  const float* prefix_acc;
+  const float2* prefix_ml;
+  int prefix_grid;
 };
 
 // Reserving cache slots for new tokens on the device (pkv_slots.cu).
@@ -242,6 +250,8 @@ bool mma_supported(KvType kv, int head_dim, int cols);
 int mma_ring_shape(KvType kv, int head_dim, int stages, int blocks_per_stage);
 cudaError_t launch_decode_mma(const DecodeParams& p, const CUtensorMap* tk, const CUtensorMap* tv,
                               KvType kv, int cols, int shape, cudaStream_t stream);
+cudaError_t launch_decode_mma_join(const DecodeParams& p, const CUtensorMap* tk, const CUtensorMap* tv, KvType kv, int cols,
+                                   cudaStream_t stream);
 // gen: the variant with the general masks (several query tokens or a window).
 int mma_ctas_per_sm(KvType kv, int head_dim, int cols, int shape, bool gen);
 // Whether a tensor-core call takes the general-mask variant: some query has a causal cut

@@ -11,6 +11,8 @@
 // on the tail of its block table.  Both leave partial softmax states (running max m in log2
 // units, sum l, accumulator) per row, which (3) the merge pass joins:
 //     M = max_i m_i,  out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
+// Where each sequence's own tokens are one item and all items run at once, the items join the states
+// themselves (pkv_decode_mma_join.cu) and there is no third pass.
 #include <math.h>
 
 #include "pkv_decode.cuh"
@@ -44,25 +46,10 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
   const int nsuf = partition_count((d.suffix_len + kBlockSize - 1) / kBlockSize, p.suffix_partition);
   const float2* sml = p.suffix_ml + gw * p.suffix_parts;
   const float* sacc = p.suffix_acc + gw * p.suffix_parts * D + lane * kDPV;
-  // prefix partials: rows 256 apart, one per CTA (two for a unit of up to 128 rows)
-  int npre = 0, twice = 0, rows = 0;
-  int64_t first = 0;
-  if (d.tiles > 0) {
-    const int r = d.first_row + qi * p.group + (h - kvh * p.group);
-    const int units = (d.rows + kPrefixRows - 1) / kPrefixRows, u = r / kPrefixRows;
-    rows = unit_rows(d.rows, u);
-    twice = tiles_apart(rows);
-    // the places of the unit's steps
-    const int64_t w0 = d.w_base + kvh * head_line(d.rows, units, d.tiles) + int64_t(u) * unit_line(kPrefixRows, d.tiles) + unit_cost(rows);
-    const int64_t w1 = w0 + unit_steps(rows, d.tiles) - 1;
-    const int ctas = stretch_ctas(d.total, p.grid);
-    const int c0 = stretch_owner(d.total, ctas, w0), c1 = stretch_owner(d.total, ctas, w1);
-    npre = (c1 - c0 + 1) << twice;
-    first = d.row_base + int64_t(kvh) * partial_rows(d.rows) + r + int64_t(c0) * kPrefixRows;
-  }
-  const int n = nsuf + npre;
-  auto pre_row = [&](int i) { return first + int64_t(i >> twice) * kPrefixRows + (twice && (i & 1) ? rows : 0); };
-  auto state = [&](int i) { return i < nsuf ? sml[i] : p.ml[pre_row(i - nsuf)]; };
+  PrefixParts pre;
+  if (d.tiles > 0) pre = PrefixParts(d, kvh, d.first_row + qi * p.group + (h - kvh * p.group), p.grid);
+  const int n = nsuf + pre.count;
+  auto state = [&](int i) { return i < nsuf ? sml[i] : p.ml[pre.row(i - nsuf)]; };
   // lane i holds partials i, i + 32, ...; the first 32 stay in registers
   const float2 mine = lane < n ? state(lane) : make_float2(-INFINITY, 0.0f);
   float M = mine.x;
@@ -88,7 +75,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
         for (int e = 0; e < kDPV; ++e) v[u][e] = 0.0f;
         if (w[u] != 0.0f) {  // a stream without tiles leaves no accumulator
           const int i = i0 + j0 + u;
-          const float* src = i < nsuf ? sacc + int64_t(i) * D : p.acc + pre_row(i - nsuf) * D + lane * kDPV;
+          const float* src = i < nsuf ? sacc + int64_t(i) * D : p.acc + pre.row(i - nsuf) * D + lane * kDPV;
           if constexpr (kDPV == 4) {
             const float4 x = *reinterpret_cast<const float4*>(src);
             v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;

@@ -177,6 +177,29 @@ __device__ __forceinline__ int stretch_owner(int64_t total, int ctas, int64_t w)
   return int(div_pos((w + 1) * ctas - 1, total));
 }
 
+// The partial states that the prefix pass leaves for row r (of a group and kv head): rows 256 apart, one
+// per CTA that had steps of the row's unit (two where the streams took tiles apart).
+struct PrefixParts {
+  int count = 0, twice = 0, rows = 0;
+  int64_t first = 0;
+  PrefixParts() = default;
+  __device__ __forceinline__ PrefixParts(const PrefixSeq& d, int kvh, int r, int grid) {
+    const int units = (d.rows + kPrefixRows - 1) / kPrefixRows, u = r / kPrefixRows;
+    rows = unit_rows(d.rows, u);
+    twice = tiles_apart(rows);
+    // the places of the unit's steps
+    const int64_t w0 = d.w_base + kvh * head_line(d.rows, units, d.tiles) + int64_t(u) * unit_line(kPrefixRows, d.tiles) + unit_cost(rows);
+    const int64_t w1 = w0 + unit_steps(rows, d.tiles) - 1;
+    const int ctas = stretch_ctas(d.total, grid);
+    const int c0 = stretch_owner(d.total, ctas, w0), c1 = stretch_owner(d.total, ctas, w1);
+    count = (c1 - c0 + 1) << twice;
+    first = d.row_base + int64_t(kvh) * partial_rows(d.rows) + r + int64_t(c0) * kPrefixRows;
+  }
+  __device__ __forceinline__ int64_t row(int i) const {
+    return first + int64_t(i >> twice) * kPrefixRows + (twice && (i & 1) ? rows : 0);
+  }
+};
+
 // A walk along one CTA's stretch: one (kv head, unit) at a time.
 struct PrefixWalk {
   PrefixGroup x;
