@@ -15,15 +15,15 @@
 // A warp takes rows (heads) of one token and one kind: query, key or value; D / 16 lanes to a row,
 // so 4 or 8 rows at a time.  A lane holds both values of its eight rotated pairs (two 16-byte pieces of
 // the row, half the rotated part apart when the pairs are), so the rotation needs no exchange between
-// lanes.  What is common to a token's rows (weight times cosine or sine) is formed once per warp.
+// lanes.  What is common to a token's rows (weights, cosines, sines) is read once per warp.
 // The pass is bound by memory: it reads q, k and v once and writes each result once.  What it has on
 // its way at a time decides its rate, so each lane's pieces of the next kSlots - 1 steps are copied to
 // shared memory of its own (no registers held, no other lane to wait for).
 // All queries' warps come first, then the keys', then the values': mixed, a CTA waited for its
 // queries with half its warps done.  Measured on GB300, 16384 tokens of 32 + 8 + 8 heads of 128 into a
-// bf16 pool (411 MB): 72.8 us, 5.6 TB/s (mixed 80; 6 or 4 slots the same within 2%; 5 CTAs an SM 74.8, 7
+// bf16 pool (411 MB): 71.8 us, 5.7 TB/s (mixed 80; 6 or 4 slots the same within 2%; 5 CTAs an SM 74.8, 7
 // 72.8 but slower when short); with loads of 8 bytes into registers, two steps ahead, it was 83.  Into an
-// INT8 pool 4096 tokens take 23 us, 3.9 TB/s: the arithmetic of keys' and values' codes is in the way.
+// INT8 pool 4096 tokens (91 MB) take 24 us, 3.8 TB/s: the arithmetic of keys' and values' codes is in the way.
 #include "pkv_tcgen05.cuh"
 
 namespace pkv {
@@ -108,14 +108,16 @@ __device__ __forceinline__ bool codes_by_bounds(const float (&x)[16], float s, u
   return same;
 }
 
-// Write this lane's 16 values (pieces c0 and c1 of 8) of a row to its slot: bf16, or codes with the
-// row's scale.
+// Write this lane's 16 values (pieces c0 and c1 of 8), times the row's factor, to its slot: bf16, or codes
+// with the row's scale.  The factor cancels in a code's quotient and goes into the scale alone.
 template <KvType KV, int LPR>
-__device__ __forceinline__ void store_cache(const float (&x)[16], void* cache, float* scale, int64_t row, int c0, int c1,
+__device__ __forceinline__ void store_cache(float (&x)[16], float factor, void* cache, float* scale, int64_t row, int c0, int c1,
                                             bool write, bool first) {
   constexpr int D = LPR * 16;
   if constexpr (KV == KvType::kBf16) {
     if (write) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= factor;
       auto* to = static_cast<__nv_bfloat16*>(cache) + row * D;
       *reinterpret_cast<uint4*>(to + c0 * 8) = pack8(x);
       *reinterpret_cast<uint4*>(to + c1 * 8) = pack8(x + 8);
@@ -134,7 +136,7 @@ __device__ __forceinline__ void store_cache(const float (&x)[16], void* cache, f
       auto* to = static_cast<uint8_t*>(cache) + row * D;
       *reinterpret_cast<uint2*>(to + c0 * 8) = make_uint2(code[0], code[1]);
       *reinterpret_cast<uint2*>(to + c1 * 8) = make_uint2(code[2], code[3]);
-      if (first) scale[row] = s;
+      if (first) scale[row] = amax == 0.0f ? 0.0f : s * factor;
     }
   }
 }
@@ -206,11 +208,12 @@ __global__ void __launch_bounds__(kRopeThreads, kMinCtas) norm_rope_kernel(const
     }
   }
   const void* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-  // pairs (a, b) -> (a A - b B, b C + a E), two pairs to a register pair: A = w_a cos, B = w_b sin,
-  // C = w_b cos, E = w_a sin.  Pairs are a value of each piece, or neighbours when interleaved.
-  uint64_t A[4], B[4], Cc[4], E[4];
+  // Pairs (a, b) -> (w_a a cos - w_b b sin, w_b b cos + w_a a sin), two pairs to a register pair: a weight
+  // times a value is exact in fp32, so each result has two roundings.  Pairs are a value of each piece, or
+  // neighbours when interleaved.
+  uint64_t wa[4], wb[4], cos2[4], sin2[4];
   {
-    float w[16], wa[8], wb[8];
+    float w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = 1.0f;
     if (weight) {
@@ -218,18 +221,11 @@ __global__ void __launch_bounds__(kRopeThreads, kMinCtas) norm_rope_kernel(const
       unpack8(__ldg(static_cast<const uint4*>(weight) + c1), w + 8);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      wa[i] = apart ? w[i] : w[2 * i];
-      wb[i] = apart ? w[8 + i] : w[2 * i + 1];
-    }
-    const float c[8] = {cs[0].x, cs[0].y, cs[0].z, cs[0].w, cs[1].x, cs[1].y, cs[1].z, cs[1].w};
-    const float s[8] = {sn[0].x, sn[0].y, sn[0].z, sn[0].w, sn[1].x, sn[1].y, sn[1].z, sn[1].w};
-#pragma unroll
     for (int j = 0; j < 4; ++j) {
-      A[j] = f32x2(wa[2 * j] * c[2 * j], wa[2 * j + 1] * c[2 * j + 1]);
-      B[j] = f32x2(-wb[2 * j] * s[2 * j], -wb[2 * j + 1] * s[2 * j + 1]);
-      Cc[j] = f32x2(wb[2 * j] * c[2 * j], wb[2 * j + 1] * c[2 * j + 1]);
-      E[j] = f32x2(wa[2 * j] * s[2 * j], wa[2 * j + 1] * s[2 * j + 1]);
+      wa[j] = apart ? f32x2(w[2 * j], w[2 * j + 1]) : f32x2(w[4 * j], w[4 * j + 2]);
+      wb[j] = apart ? f32x2(w[8 + 2 * j], w[9 + 2 * j]) : f32x2(w[4 * j + 1], w[4 * j + 3]);
+      cos2[j] = j & 1 ? f32x2(cs[j >> 1].z, cs[j >> 1].w) : f32x2(cs[j >> 1].x, cs[j >> 1].y);
+      sin2[j] = j & 1 ? f32x2(sn[j >> 1].z, sn[j >> 1].w) : f32x2(sn[j >> 1].x, sn[j >> 1].y);
     }
   }
 
@@ -243,6 +239,7 @@ __global__ void __launch_bounds__(kRopeThreads, kMinCtas) norm_rope_kernel(const
     unpack8(stage[st][0][threadIdx.x], x);
     unpack8(stage[st][1][threadIdx.x], x + 8);
     if (++st == kSlots) st = 0;
+    float inv = 1.0f;  // of the row's norm
     if (kind != 2) {
       uint64_t a[4], b[4];
 #pragma unroll
@@ -250,7 +247,6 @@ __global__ void __launch_bounds__(kRopeThreads, kMinCtas) norm_rope_kernel(const
         a[j] = apart ? f32x2(x[2 * j], x[2 * j + 1]) : f32x2(x[4 * j], x[4 * j + 2]);
         b[j] = apart ? f32x2(x[8 + 2 * j], x[9 + 2 * j]) : f32x2(x[4 * j + 1], x[4 * j + 3]);
       }
-      uint64_t inv2 = f32x2(1.0f, 1.0f);
       if (weight) {
         uint64_t q2 = mul2(a[0], a[0]);
 #pragma unroll
@@ -262,18 +258,17 @@ __global__ void __launch_bounds__(kRopeThreads, kMinCtas) norm_rope_kernel(const
         ss += hi;
 #pragma unroll
         for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-        const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
-        inv2 = f32x2(inv, inv);
+        inv = rsqrtf(ss * (1.0f / D) + p.eps);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint64_t ya = mul2(a[j], A[j]), yb = mul2(b[j], Cc[j]);
+        a[j] = mul2(a[j], wa[j]);
+        b[j] = mul2(b[j], wb[j]);
         if (j < 2 ? turns0 : turns1) {  // elsewhere sine is 0, but an infinity times 0 is not
-          ya = fma2(b[j], B[j], ya);
-          yb = fma2(a[j], E[j], yb);
+          const uint64_t ya = fma2(b[j] ^ 0x8000000080000000ull, sin2[j], mul2(a[j], cos2[j]));
+          b[j] = fma2(a[j], sin2[j], mul2(b[j], cos2[j]));
+          a[j] = ya;
         }
-        a[j] = mul2(ya, inv2);
-        b[j] = mul2(yb, inv2);
       }
       if (apart) {
 #pragma unroll
@@ -291,6 +286,8 @@ __global__ void __launch_bounds__(kRopeThreads, kMinCtas) norm_rope_kernel(const
     }
     if (kind == 0) {
       if (h < r1) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] *= inv;
         auto* to = static_cast<__nv_bfloat16*>(p.q_out) + t * p.out_stride + int64_t(h) * D;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4*>(to + c0 * 8) = ok ? pack8(x) : zero;
@@ -298,7 +295,7 @@ __global__ void __launch_bounds__(kRopeThreads, kMinCtas) norm_rope_kernel(const
       }
     } else {
       const int64_t row = ((slot / kBlockSize) * p.kv_heads + h) * kBlockSize + slot % kBlockSize;
-      store_cache<KV, LPR>(x, kind == 1 ? p.k_cache : p.v_cache, kind == 1 ? p.k_scale : p.v_scale, row, c0, c1,
+      store_cache<KV, LPR>(x, inv, kind == 1 ? p.k_cache : p.v_cache, kind == 1 ? p.k_scale : p.v_scale, row, c0, c1,
                            ok && slot >= 0 && h < r1, lr == 0);
     }
   }
