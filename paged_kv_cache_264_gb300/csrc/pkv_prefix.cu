@@ -22,7 +22,8 @@ namespace pkv {
 namespace {
 
 // Join a row's partials: one warp per (sequence, query token, query head), a lane to D / 32
-// consecutive values.
+// consecutive values.  Bound by its chain of loads (description, states, accumulators): measured on GB300,
+// 2048 rows of 20 partials of 128 7 us, 8192 rows of up to 6 11 us.
 template <int D>
 __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p) {
   constexpr int kDPV = D / 32;
