@@ -368,8 +368,8 @@ pkv_status make_prefix_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
   x->grid = pool->sm_count;
   x->suffix_blocks = static_cast<int>(ceil_div(max_suffix_len, pkv::kBlockSize));
   // Sequences' own parts of up to 32 blocks run as one item each: measured on GB300, whole calls,
-  // against the plain plan's split: 4 sequences of up to 8 blocks 17.8 against 20.4 us, 64 of up to
-  // 19 56.8 against 60.8 us, 48 of up to 25 (4 queries, FP8) 60.7 against 66.5 us; 117 of up to 16
+  // against the plain plan's split: 4 sequences of up to 8 blocks 16.7 against 21.3 us, 64 of up to
+  // 19 60.7 against 64.9 us, 48 of up to 25 (4 queries, FP8) 56.7 against 66.8 us; 117 of up to 16
   // and 256 of up to 32 (INT8), where the plain plan splits nothing, the same.
   pkv_decode_options suffix_opt = opt ? *opt : pkv_decode_options{};
   if (suffix_opt.partition_blocks == 0 && x->suffix_blocks <= 32) suffix_opt.partition_blocks = 32;

@@ -550,8 +550,8 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     };
     // At head_dim 128 the softmaxes of streams that take the same tiles take turns: left alone the
     // streams fall into step, both in their softmax and then both waiting for their products.
-    // Measured on GB300: 64 sequences over 32768 tokens 59.9 us against 63.2, 256 over 16384 (INT8)
-    // 150 against 158; at head_dim 64, where the products are half as long, 66.2 against 63.8.
+    // Measured on GB300, whole calls: 64 sequences over 32768 tokens 60.7 us against 62.6, 256 over 16384
+    // (INT8) 148.4 against 160.1; at head_dim 64, where the products are half as long, 59.9 against 56.7.
     uint32_t turns = 0;  // before this piece
     auto turn_done = [&]() {
       if (lane == 0) mbar_arrive(sy->turn + s);
