@@ -57,6 +57,9 @@
 
 namespace pkv {
 
+constexpr int kExchangeOff = 1024;             // the rows' exchange, after the barriers and flags
+constexpr int kExchangeBytes = 2 * 2 * 128 * 4;  // float [stream][half][row]
+
 template <KvType KV, int D>
 struct PrefixCfg {
   static constexpr bool kQuant = KvTraits<KV>::kQuant;
@@ -81,7 +84,7 @@ struct PrefixCfg {
   static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
   static constexpr int kSlotOff = kRawOff + (kQuant ? kRawStages * kRawBytes : 0);
   static constexpr int kMiscOff = kSlotOff + (kQuant ? kSlots * kScaleBytes : 0);
-  static constexpr int kSmemBytes = kMiscOff + 3072;             // barriers and flags, and the rows' exchange
+  static constexpr int kSmemBytes = kMiscOff + kExchangeOff + kExchangeBytes;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(size_t(kStages) * kTileBytes >= prefix_scan_bytes(kMaxPrefixGroups), "the scan fits the ring");
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
@@ -105,7 +108,6 @@ struct PrefixSync {
   uint32_t tmem;
   uint32_t abort;
 };
-constexpr int kExchangeOff = 1024;  // float [stream][half][row] after the barriers
 static_assert(sizeof(PrefixSync) <= kExchangeOff, "barriers fit their space");
 
 template <int N>
