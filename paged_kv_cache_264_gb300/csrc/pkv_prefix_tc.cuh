@@ -40,9 +40,9 @@
 // What bounds it: each stream's chain of S, softmax and product over V, about 4600 cycles a step at
 // head_dim 128 (tensor memory is full, so the next S cannot lie beside this one's P), and some 9000 cycles
 // around each piece (roles' code that is not in the instruction cache, Q, the partials).  Measured on
-// GB300, this pass alone: 256 rows a kv head (8) over 32768 tokens 40 us, tensor pipe 36% busy; 16 groups of
-// 1 to 14 rows, 32 kv heads, 284 MB, 61 us, 4.7 TB/s; INT8, 1024 rows over 16384 tokens 104 us, 29% busy; FP8
-// at head_dim 64, 384 rows over 4000 and 8192 tokens 44 us, 15%.
+// GB300, this pass alone: 256 rows a kv head (8) over 32768 tokens 43 us, tensor pipe 36% busy; 16 groups of
+// 1 to 14 rows, 32 kv heads, 284 MB, 66 us, 4.3 TB/s; INT8, 1024 rows over 16384 tokens 101 us, 29% busy; FP8
+// at head_dim 64, 384 rows over 4000 and 8192 tokens 45 us, 15%.
 //
 // Every wait is bounded; after one that gave up the CTA takes no further work, lets its
 // copies and products land, frees its tensor memory and ends.
