@@ -50,6 +50,22 @@ def test_pool_past_32_bit_offsets(kv):
     x.pool.close()
 
 
+@pytest.mark.parametrize("kv,d,hq,k", [("bf16", 128, 1, 1), ("bf16", 128, 4, 1), ("bf16", 64, 7, 1), ("fp8", 64, 4, 4),
+                                        ("int8", 128, 8, 2), ("bf16", 128, 16, 1), ("int8", 64, 2, 1)])
+def test_many_partial_states_of_a_row(kv, d, hq, k):
+    """One kv head and one long prefix, so that nearly every CTA leaves a state for each row; the groups
+    behind it are empty.  The rows' states are joined by the items over the sequences' own tokens, and,
+    where those are split, by the merge pass."""
+    x = Batch([(20000 // 16 * 16, [40, 9, 300])] + [(0, [])] * 60 + [(16, [5])], hq, 1, d, kv, k=k, seed=13)
+    for args in ({}, {"partition_blocks": 2}):
+        launches = pkv.launch_count()
+        out = x.run(**args)
+        assert pkv.launch_count() - launches == (3 if args else 2)
+        assert x.pool.device_error() == 0
+        x.check(out)
+    x.pool.close()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.09, 0.5])
 @pytest.mark.parametrize("kv", ["bf16", "int8"])
 def test_scales(kv, scale):
