@@ -541,7 +541,9 @@ PKV_API pkv_status pkv_shared_prefix_workspace_bytes(const pkv_pool* pool, int n
  * pkv_paged_attention_decode for a batch whose groups of sequences share a prefix (sequences
  * made by pkv_block_manager_fork, or requests behind one system prompt; "Efficient AI Lecture
  * 13", section "PagedAttention"): each group's prefix is read once per kv head for all the group's
- * queries, not once per sequence.  The result is that of pkv_paged_attention_decode.
+ * queries, not once per sequence.  The result is that of pkv_paged_attention_decode, but for NaN:
+ * a NaN logit of any token that a query sees, or a NaN value, gives NaN here however the call is
+ * planned; pkv_paged_attention_decode gives 0 where it split the sequence.
  *   group_starts (device): int32 [num_groups + 1], not decreasing, within [0, num_seqs]: group g is
  *                sequences group_starts[g] .. group_starts[g + 1] - 1 (it may be empty).  Sequences
  *                outside every group share nothing.

@@ -487,7 +487,8 @@ def shared_prefix_decode(pool: PagedKVPool, q: torch.Tensor, block_tables: torch
     table row names; ``BlockManager.prefix_groups`` finds both.  max_prefix_len bounds the prefix
     lengths, max_suffix_len every sequence's own tokens, context_lens[b] - prefix.  q is
     [B, Hq, d], or [B, k, Hq, d] for k draft tokens per sequence, all of which see the whole prefix.
-    ``workspace`` (a uint8 CUDA tensor) is allocated here when not given."""
+    A NaN logit or value that a query sees gives NaN.  ``workspace`` (a uint8 CUDA tensor) is
+    allocated here when not given."""
     ndim = 4 if q.dim() == 4 else 3
     _check(q, torch.bfloat16, "q", ndim, pool)
     _check(block_tables, torch.int32, "block_tables", 2, pool)

@@ -466,9 +466,11 @@ __device__ __forceinline__ void join_warp_records(const unsigned char* smem, siz
     float sum = 0.0f;
     for (int j0 = 0; j0 < x.count; j0 += W) {
       const float2 s = j0 == 0 ? mine : j0 + i < x.count ? p.ml[x.row(j0 + i)] : none;
-      // a stream without tiles left a sum of 0 and no accumulator
-      const float w = s.y > 0.0f ? fast_exp2(s.x - M) : 0.0f;
-      sum = fmaf(w, s.y, sum);
+      // A state with a sum of 0 weighs nothing and may have no accumulator (a stream without tiles): -1
+      // stands for its weight.  A NaN sum, and a NaN accumulator under a weight of 0, go into the result.
+      const bool empty = s.y == 0.0f;
+      const float w = empty ? -1.0f : fast_exp2(s.x - M);
+      if (!empty) sum = fmaf(w, s.y, sum);
       const int here = min(W, x.count - j0);
 #pragma unroll 1
       for (int u0 = 0; u0 < here; u0 += kAhead) {
@@ -476,10 +478,11 @@ __device__ __forceinline__ void join_warp_records(const unsigned char* smem, siz
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           wu[u] = __shfl_sync(mask, w, (u0 + u) % W, W);
-          if (u0 + u >= here) wu[u] = 0.0f;
+          if (u0 + u >= here || wu[u] < 0.0f) {
+            wu[u] = 0.0f;
 #pragma unroll
-          for (int e = 0; e < kE; ++e) v[u][e] = 0.0f;
-          if (wu[u] != 0.0f) {
+            for (int e = 0; e < kE; ++e) v[u][e] = 0.0f;
+          } else {
             const float* src = p.acc + x.row(j0 + u0 + u) * D + d0;
             if constexpr (kE % 4 == 0) {
 #pragma unroll
@@ -507,7 +510,7 @@ __device__ __forceinline__ void join_warp_records(const unsigned char* smem, siz
   }
   const int c = p.c0 + g, qi = c / p.group;
   auto* out = p.out + (int64_t(qi) * p.num_q_heads + (c - qi * p.group)) * D + d0;
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;  // NaN stays NaN
   if constexpr (kE == 1) {
     out[0] = __float2bfloat16_rn(acc[0] * inv);
   } else {

@@ -59,11 +59,15 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
   float L = 0.0f, a[kDPV] = {};
   for (int i0 = 0; i0 < n; i0 += 32) {
-    float f = 0.0f;
+    // A state with a sum of 0 weighs nothing and may have no accumulator (a stream without tiles): -1 stands
+    // for its weight.  A NaN sum, and a NaN accumulator under a weight of 0, go into the result.
+    float f = -1.0f;
     if (i0 + lane < n) {
       const float2 s = i0 == 0 ? mine : state(i0 + lane);
-      f = exp2f(s.x - M);
-      L = fmaf(f, s.y, L);
+      if (s.y != 0.0f) {
+        f = exp2f(s.x - M);
+        L = fmaf(f, s.y, L);
+      }
     }
     const int here = min(32, n - i0);
     for (int j0 = 0; j0 < here; j0 += kAhead) {  // kAhead accumulators on their way at a time
@@ -71,10 +75,11 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         w[u] = __shfl_sync(kFull, f, (j0 + u) & 31);
-        if (j0 + u >= here) w[u] = 0.0f;
+        if (j0 + u >= here || w[u] < 0.0f) {
+          w[u] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < kDPV; ++e) v[u][e] = 0.0f;
-        if (w[u] != 0.0f) {  // a stream without tiles leaves no accumulator
+          for (int e = 0; e < kDPV; ++e) v[u][e] = 0.0f;
+        } else {
           const int i = i0 + j0 + u;
           const float* src = i < nsuf ? sacc + int64_t(i) * D : p.acc + pre.row(i - nsuf) * D + lane * kDPV;
           if constexpr (kDPV == 4) {
