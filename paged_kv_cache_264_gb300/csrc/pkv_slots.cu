@@ -30,7 +30,8 @@ constexpr int kSlotWarps = kSlotThreads / 32;
 constexpr int kPerThread = 4;         // consecutive tokens of one thread
 constexpr int kSumLimit = 1 << 30;    // sums saturate here (max_tokens is below it)
 
-__device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kSumLimit); }
+// Of values in 0 .. kSumLimit, whose plain sum would pass 2^31 - 1.
+__device__ __forceinline__ int sat_add(int a, int b) { return int(min(uint32_t(a) + uint32_t(b), uint32_t(kSumLimit))); }
 
 __global__ void __launch_bounds__(kSlotThreads) reserve_slots_kernel(const SlotParams p) {
   extern __shared__ int smem_slots[];
