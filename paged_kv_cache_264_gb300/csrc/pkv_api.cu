@@ -375,15 +375,35 @@ pkv_status make_prefix_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
   if (suffix_opt.partition_blocks == 0 && x->suffix_blocks <= 32) suffix_opt.partition_blocks = 32;
   st = make_plan(pool, num_seqs, num_q_heads, max_suffix_len < nq ? nq : max_suffix_len, &suffix_opt, &x->suffix);
   if (st != PKV_OK) return st;
-  // Each sequence one item, all on the GPU at once, and about 12 prefix states per row at most: the items
-  // join them.  Else a merge pass does.  Measured on GB300, whole calls, joined against merged: 32 items of
-  // 8 states 16.5 against 18.5 us, 384 of 10 57.1 against 61.7; 512 of 20 61.7 against 60.9, 3744 of 2 119.7
-  // against 114.1 (the loads' latency is paid per item).
-  const int64_t items = int64_t(num_seqs) * pool->kv_heads * x->suffix.chunks;
-  const int64_t states = std::min<int64_t>(ceil_div(max_prefix_len, pkv::kPrefixTile),
-                                           x->grid / (int64_t(pool->kv_heads) * std::max(num_groups, 1)) + 1);
-  x->join = x->suffix.kernel == PKV_KERNEL_TENSOR_CORE && x->suffix.shape == 0 && x->suffix.max_parts == 1 &&
-            items <= int64_t(pool->sm_count) * x->suffix.ctas_per_sm && states <= 12;
+  // Where each sequence is one item per kv head (and column chunk) and all run at once, the items join the
+  // prefix's states; else a merge pass does (3744 items, MHA: merged 114 us, joined 120).  Items of more than 4
+  // columns are halved while that leaves at most two an SM: a thread then holds fewer values of a state, and
+  // more CTAs share the states.  16 columns, 1 kv head, 4 sequences behind 20000
+  // tokens: 27 us, unhalved 60, merged 40; 40 sequences 33, 58, 43.  (Halved as long as all run at once, FP8, 4
+  // queries, 16 sequences: 27.3 for 23.9.)
+  const auto kv = static_cast<pkv::KvType>(pool->dtype);
+  auto items = [&](const Plan& s) { return int64_t(num_seqs) * pool->kv_heads * s.chunks; };
+  Plan join = x->suffix;
+  x->join = join.kernel == PKV_KERNEL_TENSOR_CORE && join.shape == 0 && join.max_parts == 1 &&
+            items(join) <= int64_t(pool->sm_count) * join.ctas_per_sm;
+  while (x->join && join.cols > 4) {
+    Plan half = join;
+    half.cols = join.cols / 2;
+    half.chunks = static_cast<int>(ceil_div(int64_t(group) * nq, half.cols));
+    half.ctas_per_sm = pkv::mma_ctas_per_sm(kv, pool->head_dim, half.cols, 0, pkv::mma_needs_general(nq, half.window, half.cols));
+    if (items(half) > int64_t(pool->sm_count) * std::min(half.ctas_per_sm, 2)) break;
+    join = half;
+  }
+  // States that a row may have at most, whatever the groups: its unit has up to one step per tile (or, with up
+  // to 128 rows, half as many of two states each), and every kv head's unit takes as many places on the line,
+  // so no more than grid / kv_heads + 2 stretches hold steps of one.  Items of 16 columns of 128 values join up
+  // to 33 of them: the last of many items to end, with 13 / 33 / 65 / 157 states, joined against merged, 27.7 /
+  // 32.0 / 36.9 / 46.9 against 30.7 / 31.1 / 34.1 / 40.3 us; with half as many values a thread 19.5 / 24.1 / 26.4
+  // / 31.5 against 21.7 / 26.1 / 29.1 / 34.1.
+  const int64_t states = std::min<int64_t>(ceil_div(max_prefix_len, pkv::kPrefixTile) + 1,
+                                           2 * (int64_t(x->grid) / pool->kv_heads + 2));
+  x->join = x->join && (join.cols * pool->head_dim <= 1024 || states <= 33);
+  if (x->join) x->suffix = join;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;

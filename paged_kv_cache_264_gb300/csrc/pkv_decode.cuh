@@ -420,8 +420,11 @@ struct JoinArgs {
 
 // Merge the NW per-warp states of one item, of a sequence's own tokens, and the prefix pass's partial states
 // of its rows, and write the result.  W of a column's lanes take one partial's maximum and sum each, then
-// all read the accumulators, kAhead at a time.  In kernels of their own: as a case of the decode kernels,
-// called or inlined, it took registers from their loops (INT8, 8 sequences of 20000 tokens: 72.6 -> 75.9 us).
+// all read the accumulators, kAhead at a time.  Each of the W lanes also finds its partial's place, and hands it
+// out with the weight: with every thread finding every place, calls of 4 sequences behind 20000 tokens (1 kv
+// head, some 150 states a row, items of 4 columns) took 49.0 us for 27.1.  In kernels of their own: as a case
+// of the decode kernels, called or inlined, it took registers from their loops (INT8, 8 sequences of 20000
+// tokens: 72.6 -> 75.9 us).
 template <int NC, int D, int NW>
 __device__ __forceinline__ void join_warp_records(const unsigned char* smem, size_t warp_stride, JoinArgs p) {
   constexpr int kThreads = NW * 32;
@@ -464,26 +467,33 @@ __device__ __forceinline__ void join_warp_records(const unsigned char* smem, siz
 #pragma unroll
     for (int e = 0; e < kE; ++e) acc[e] *= f;
     float sum = 0.0f;
+    const float* base = p.acc + x.first * D + d0;
     for (int j0 = 0; j0 < x.count; j0 += W) {
-      const float2 s = j0 == 0 ? mine : j0 + i < x.count ? p.ml[x.row(j0 + i)] : none;
-      // A state with a sum of 0 weighs nothing and may have no accumulator (a stream without tiles): -1
-      // stands for its weight.  A NaN sum, and a NaN accumulator under a weight of 0, go into the result.
+      const int j = j0 + i;
+      const float2 s = j0 == 0 ? mine : j < x.count ? p.ml[x.row(j)] : none;
+      // A state with a sum of 0 weighs nothing and may have no accumulator (a stream without tiles).  A NaN
+      // sum, and a NaN accumulator under a weight of 0, go into the result.
       const bool empty = s.y == 0.0f;
-      const float w = empty ? -1.0f : fast_exp2(s.x - M);
+      const float w = empty ? 0.0f : fast_exp2(s.x - M);
       if (!empty) sum = fmaf(w, s.y, sum);
+      // where its accumulator lies, from the first one (at most some 300 states of 256 rows apart)
+      const int at = empty ? -1 : int(x.row(j) - x.first) * D;
       const int here = min(W, x.count - j0);
 #pragma unroll 1
       for (int u0 = 0; u0 < here; u0 += kAhead) {
         float wu[kAhead], v[kAhead][kE];
+        int au[kAhead];  // lanes past the last state hold -1
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           wu[u] = __shfl_sync(mask, w, (u0 + u) % W, W);
-          if (u0 + u >= here || wu[u] < 0.0f) {
-            wu[u] = 0.0f;
+          au[u] = __shfl_sync(mask, at, (u0 + u) % W, W);
+        }
 #pragma unroll
-            for (int e = 0; e < kE; ++e) v[u][e] = 0.0f;
-          } else {
-            const float* src = p.acc + x.row(j0 + u0 + u) * D + d0;
+        for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) v[u][e] = 0.0f;
+          if (au[u] >= 0) {
+            const float* src = base + au[u];
             if constexpr (kE % 4 == 0) {
 #pragma unroll
               for (int e = 0; e < kE; e += 4) {
