@@ -343,6 +343,8 @@ class OnPoolDevice {
   bool ok_ = false, switched_ = false;
 };
 
+constexpr int kOneItemBlocks = 48;  // own parts of up to this many blocks are not split
+
 // Layout of a shared-prefix call's workspace and the plan of its suffix pass.
 struct PrefixPlan {
   Plan suffix;
@@ -367,12 +369,13 @@ pkv_status make_prefix_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
   if (!pool->has_tmaps) return PKV_ERR_UNSUPPORTED;
   x->grid = pool->sm_count;
   x->suffix_blocks = static_cast<int>(ceil_div(max_suffix_len, pkv::kBlockSize));
-  // Sequences' own parts of up to 32 blocks run as one item each: measured on GB300, whole calls,
-  // against the plain plan's split: 4 sequences of up to 8 blocks 16.7 against 21.3 us, 64 of up to
-  // 19 60.7 against 64.9 us, 48 of up to 25 (4 queries, FP8) 56.7 against 66.8 us; 117 of up to 16
-  // and 256 of up to 32 (INT8), where the plain plan splits nothing, the same.
+  // Sequences' own parts of up to kOneItemBlocks blocks run as one item each.  Measured on GB300, whole calls
+  // behind a prefix of 1024 tokens (32 query and 8 kv heads), one item against the plain plan's split, own
+  // parts of up to 16 / 33 / 48 / 64 blocks: 2 sequences 16.8 / 19.8 / 21.3 / 23.4 against 21.7 / 21.3 / 22.1 /
+  // 22.8 us (INT8 20.9 / 23.8 / 25.7 / 28.5 against 24.0 / 24.6 / 25.3 / 25.6), 48 sequences 22.0 / 26.4 / 36.6 /
+  // 41.9 against 33.5 / 37.6 / 45.9 / 49.1; 128, where the plain plan splits nothing, the same.
   pkv_decode_options suffix_opt = opt ? *opt : pkv_decode_options{};
-  if (suffix_opt.partition_blocks == 0 && x->suffix_blocks <= 32) suffix_opt.partition_blocks = 32;
+  if (suffix_opt.partition_blocks == 0 && x->suffix_blocks <= kOneItemBlocks) suffix_opt.partition_blocks = kOneItemBlocks;
   st = make_plan(pool, num_seqs, num_q_heads, max_suffix_len < nq ? nq : max_suffix_len, &suffix_opt, &x->suffix);
   if (st != PKV_OK) return st;
   // Where each sequence is one item per kv head (and column chunk) and all run at once, the items join the

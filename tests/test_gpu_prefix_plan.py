@@ -53,6 +53,14 @@ def test_items_of_fewer_columns(kv, d, hq, hkv, k, n):
     x.pool.close()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8", "fp8"])
+def test_own_parts_around_one_items_length(kv):
+    for own, expect in ((512, 2), (513, 2), (768, 2), (769, 3)):
+        x = Batch([(1024, [own, 3, own - 5, 1])], 32, 8, 128, kv, seed=own)
+        _run(x, expect)
+        x.pool.close()
+
+
 def test_bounds_given_as_capacities():
     """A captured step passes what its buffers hold, not what a batch needs."""
     x = Batch([(1024, [40, 9, 300]), (48, [7])], 32, 8, 128, "bf16", seed=1)
