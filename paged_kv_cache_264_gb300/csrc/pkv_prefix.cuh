@@ -30,10 +30,12 @@ __host__ __device__ __forceinline__ int unit_rows(int rows, int u) {
 __host__ __device__ __forceinline__ bool tiles_apart(int n) { return n <= kPrefixRows / 2; }
 __host__ __device__ __forceinline__ int unit_steps(int n, int tiles) { return tiles_apart(n) ? (tiles + 1) / 2 : tiles; }
 // Places ahead of a unit's steps: a piece's start and end, and its rows of partials.  Measured on GB300
-// with the same places for every unit (1 / 2 / 4 / 6), whole calls: 16 groups of 1 to 14 sequences
-// (MHA) 114.0 / 115.2 / 119.6 / 122.8 us, 2 groups of 384 rows a kv head (FP8, head_dim 64) 62.7 / 62.0 /
+// with the same places for every unit (1 / 2 / 4 / 6), whole calls: 16 groups of 1 to 13 sequences
+// (MHA) 114.0 / 115.2 / 119.6 / 122.8 us, 2 groups of 96 and 672 rows a kv head (FP8, head_dim 64) 62.7 / 62.0 /
 // 59.9 / 62.3; with these 114.5 and 61.8 (56.7 since the states are joined without a merge pass).
-// Had the last 128 of those 384 rows one stream, on every tile, it would be 63.7 for 61.8.
+// Had the 96 rows' unit one stream, on every tile, it would be 63.7 for 61.8.  Over 36 batches drawn at random
+// (1 to 41 groups, all types) a slope of 3 was on average 2.0% above each one's best of 0, 1, 2, 3, 5 and 8; 0
+// and 1 were 1.4%, 2 1.5%, 5 3.0%, 8 4.7%.
 __host__ __device__ __forceinline__ int unit_cost(int n) {
   return 1 + (tiles_apart(n) ? 2 * n : n) * 3 / kPrefixRows;
 }

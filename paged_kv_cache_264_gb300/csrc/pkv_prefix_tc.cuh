@@ -15,8 +15,9 @@
 // shared memory, 8 KB for 64 cycles of arithmetic at 128 columns, which is what shared memory
 // delivers; at 64 columns they took as long for half the work.
 // The running maximum is lazy (kMaxSlack): O is rescaled in tensor memory only when a row's
-// logits pass its maximum by 2^8.  P enters the product as bf16, and the softmax sum adds the
-// same rounded weights, so that numerator and denominator agree.
+// logits pass its maximum by 2^8.  P enters the product as bf16, which the product's other operand, V, sets
+// (2^-8 of each weight at most, as in the paged decode); on a bf16 pool the softmax sum adds the same rounded
+// weights, so that numerator and denominator agree.
 //
 // INT8 and FP8 pools: TMA brings codes and scales into a ring of their own, and a warpgroup turns
 // the codes into bf16 operand tiles, which holds every INT8 and E4M3 code exactly.  The scales stay
@@ -37,12 +38,15 @@
 // releases every stage in ring order, those of the other stream's tiles too (a warp that filled
 // only K stages, or skipped stages, could run into one still in use).
 //
-// What bounds it: each stream's chain of S, softmax and product over V, about 4600 cycles a step at
-// head_dim 128 (tensor memory is full, so the next S cannot lie beside this one's P), and some 9000 cycles
-// around each piece (roles' code that is not in the instruction cache, Q, the partials).  Measured on
-// GB300, this pass alone: 256 rows a kv head (8) over 32768 tokens 43 us, tensor pipe 36% busy; 16 groups of
-// 1 to 14 rows, 32 kv heads, 284 MB, 66 us, 4.3 TB/s; INT8, 1024 rows over 16384 tokens 101 us, 29% busy; FP8
-// at head_dim 64, 384 rows over 4000 and 8192 tokens 45 us, 15%.
+// What bounds it: each stream's chain of S, softmax and product over V.  At head_dim 128 S and O of two streams
+// fill tensor memory, so the next S cannot lie beside this one's P; at 64 a quarter of it is free and not
+// used.  Measured on GB300 with 256 rows a kv head (8), from passes of 16 and 32 steps a CTA: 3800 cycles a step
+// at head_dim 128 (INT8 6050, FP8 6130) and 3200 at 64 (INT8 5240, FP8 5030), and 26 to 40 thousand around them
+// (launch, the roles' code that is not in the instruction cache, Q, the partials of two or three pieces); the
+// tensor pipe is busy for 45% of the cycles at 32 steps (quantised 31%, head_dim 64 29%, quantised 18%).  This
+// pass alone: 256 rows over 32768 tokens 43 us, tensor pipe 37%; 16 groups of 1 to 13 rows, 32 kv heads, 284 MB,
+// 66 us, 4.3 TB/s; INT8, 1024 rows over 16384 tokens 101 us, 30%; FP8 at head_dim 64, 96 rows over 4000 and 672
+// over 8192 tokens 45 us, 15%.
 //
 // Every wait is bounded; after one that gave up the CTA takes no further work, lets its
 // copies and products land, frees its tensor memory and ends.

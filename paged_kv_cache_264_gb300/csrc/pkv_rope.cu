@@ -23,7 +23,9 @@
 // queries with half its warps done.  Measured on GB300, 16384 tokens of 32 + 8 + 8 heads of 128 into a
 // bf16 pool (411 MB): 71.8 us, 5.7 TB/s (mixed 80; 6 or 4 slots the same within 2%; 5 CTAs an SM 74.8, 7
 // 72.8 but slower when short); with loads of 8 bytes into registers, two steps ahead, it was 83.  Into an
-// INT8 pool 4096 tokens (91 MB) take 24 us, 3.8 TB/s: the arithmetic of keys' and values' codes is in the way.
+// INT8 pool 4096 tokens take 23.6 us and 16384 86.2 (FP8 23.5 and 85.8; 32 + 32 + 32 heads of 64, not normalised,
+// 26.4 and 94.4): the arithmetic of keys' and values' codes is in the way.  With the quotients' lower bound alone,
+// which is not enough for the code, these were 20.8 and 78.4 (MHA 20.0 and 74.6).
 #include "pkv_tcgen05.cuh"
 
 namespace pkv {
