@@ -543,14 +543,16 @@ PKV_API pkv_status pkv_shared_prefix_workspace_bytes(const pkv_pool* pool, int n
  * 13", section "PagedAttention"): each group's prefix is read once per kv head for all the group's
  * queries, not once per sequence.  The result is that of pkv_paged_attention_decode, but for NaN:
  * a NaN logit of any token that a query sees, or a NaN value, gives NaN here however the call is
- * planned; pkv_paged_attention_decode gives 0 where it split the sequence.
- * As there, softmax weights enter the product over V as bf16 (INT8 and FP8 pools: times V's scale), so
- * an output differs from the formula's by at most 2^-8 (sum of weight |v| + 2 |output|) and the fp32 sums'
- * rounding.  It has two passes to start where the plain decode has one, and works on tiles of 128 prefix
- * tokens.  On GB300, with heads of 128, it is the faster call from 2 sequences a group behind 4000 tokens
- * on (several groups of INT8 or FP8: from 4) and from 8 behind 1000 (one group of INT8 or FP8: from about
- * 32); behind one or a few blocks the plain decode is (8 sequences behind 128 tokens, 32 query and 8 kv
- * heads: 11 us against 16, INT8 11 against 20).
+ * planned; pkv_paged_attention_decode gives 0 where it split the sequence.  With several query tokens a
+ * NaN value (not a key) of the last num_queries - 1 tokens reaches all queries of its sequence, as there.
+ * Softmax weights enter the product over the prefix's V as bf16 (INT8 and FP8 pools: times V's scale),
+ * which moves an output by at most 2^-8 (sum of weight |v| + |output|) before its own rounding to bf16; own
+ * tokens are as in pkv_paged_attention_decode.
+ * The call has two passes to start where the plain decode has one, and works on tiles of 128 prefix tokens.
+ * On GB300, with heads of 128, it is the faster one from 2 sequences a group behind 4000 tokens on (several
+ * groups of INT8 or FP8: from 4) and from 8 behind 1000 (one group of INT8 or FP8: from about 32); behind
+ * one or a few blocks the plain decode is (8 sequences behind 128 tokens, 32 query and 8 kv heads: 11 us
+ * against 16, INT8 11 against 20).
  *   group_starts (device): int32 [num_groups + 1], not decreasing, within [0, num_seqs]: group g is
  *                sequences group_starts[g] .. group_starts[g + 1] - 1 (it may be empty).  Sequences
  *                outside every group share nothing.

@@ -16,7 +16,7 @@
 // delivers; at 64 columns they took as long for half the work.
 // The running maximum is lazy (kMaxSlack): O is rescaled in tensor memory only when a row's
 // logits pass its maximum by 2^8.  P enters the product as bf16, which the product's other operand, V, sets
-// (2^-8 of each weight at most, as in the paged decode); on a bf16 pool the softmax sum adds the same rounded
+// (2^-8 of each weight at most, as in the paged decode of a bf16 pool); on a bf16 pool the softmax sum adds the same rounded
 // weights, so that numerator and denominator agree.
 //
 // INT8 and FP8 pools: TMA brings codes and scales into a ring of their own, and a warpgroup turns
