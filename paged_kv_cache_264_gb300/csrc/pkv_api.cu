@@ -381,9 +381,8 @@ pkv_status make_prefix_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
   // Where each sequence is one item per kv head (and column chunk) and all run at once, the items join the
   // prefix's states; else a merge pass does (3744 items, MHA: merged 114 us, joined 120).  Items of more than 4
   // columns are halved while that leaves at most two an SM: a thread then holds fewer values of a state, and
-  // more CTAs share the states.  16 columns, 1 kv head, 4 sequences behind 20000
-  // tokens: 27 us, unhalved 60, merged 40; 40 sequences 33, 58, 43.  (Halved as long as all run at once, FP8, 4
-  // queries, 16 sequences: 27.3 for 23.9.)
+  // more CTAs share the states.  16 columns, 1 kv head, 4 sequences behind 20000 tokens: 27 us, unhalved 60, merged
+  // 40; 40 sequences 33, 58, 43.  (Halved as long as all run at once, FP8, 4 queries, 16 sequences: 27.3 for 23.9.)
   const auto kv = static_cast<pkv::KvType>(pool->dtype);
   auto items = [&](const Plan& s) { return int64_t(num_seqs) * pool->kv_heads * s.chunks; };
   Plan join = x->suffix;
