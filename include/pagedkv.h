@@ -24,8 +24,9 @@
  *  - Layouts are row-major ("C order"); element sizes are those of the named types.
  *  - Calls on one pool must be ordered on one stream (or otherwise serialised): the
  *    pool's device error word and its scheduler counters are shared by its calls.
- *  - pkv_reserve_slots, pkv_norm_rope_and_cache and pkv_shared_prefix_decode make the pool's
- *    device current for the call; `stream` is a stream of that device.
+ *  - pkv_reserve_slots, pkv_norm_rope_and_cache, pkv_shared_prefix_decode, pkv_paged_attention_prefill,
+ *    pkv_prompt_attention and pkv_gather_cache make the pool's device current for the call; `stream` is
+ *    a stream of that device.
  */
 #ifndef PAGEDKV_H_
 #define PAGEDKV_H_
@@ -78,6 +79,7 @@ typedef enum pkv_kv_dtype {
 #define PKV_DEVERR_CAPACITY 0x10u   /* pkv_reserve_slots: too few free blocks, table entries or slots */
 #define PKV_DEVERR_POSITION 0x20u   /* a position was < 0 or >= the rows of the rotation table       */
 #define PKV_DEVERR_PREFIX 0x40u     /* a group's first sequence or prefix length was invalid         */
+#define PKV_DEVERR_QUERY 0x80u      /* query_starts, key_starts or token_starts was not a row range  */
 
 /* Opaque, host-owned pool descriptor. */
 typedef struct pkv_pool pkv_pool;
@@ -581,6 +583,108 @@ PKV_API pkv_status pkv_shared_prefix_decode(const pkv_pool* pool, const void* q,
                                             int max_suffix_len, float scale, void* out, void* workspace,
                                             size_t workspace_bytes, const pkv_decode_options* options,
                                             void* stream);
+
+/*
+ * Arguments of pkv_paged_attention_prefill and pkv_prompt_attention.  Zero-initialise and set what you
+ * need; what belongs to the other call is not looked at.
+ *   q, out (device): bf16 rows of packed query tokens; token t's heads are contiguous
+ *             ([num_q_heads, head_dim]) at element t * stride, at least a token's row apart.  16-byte
+ *             aligned, strides multiples of 8.  out must not overlap any input.
+ *   query_starts (device): int32 [num_seqs + 1], not decreasing, within [0, num_tokens]: sequence b's
+ *             queries are rows query_starts[b] .. query_starts[b + 1] - 1 (pkv_reserve_slots forms it).
+ *             It may have none.  Rows outside all sequences are neither used nor written.
+ *   num_tokens: rows of q and out.
+ *   window:   as in pkv_decode_options: a query at position p attends to tokens p - window + 1 .. p; 0: none.
+ * pkv_paged_attention_prefill:
+ *   block_tables, max_blocks_per_seq, context_lens, max_context_len: as for pkv_paged_attention_decode;
+ *             context_lens[b] counts the sequence's query tokens, which are in the cache already.
+ * pkv_prompt_attention:
+ *   k, v (device): bf16 rows like q's, [kv_heads, head_dim] each.
+ *   key_starts (device): int32 [num_seqs + 1], not decreasing, within [0, num_keys]: sequence b's keys are
+ *             rows key_starts[b] .. key_starts[b + 1] - 1.  NULL: query_starts.
+ *   num_keys: rows of k and v.
+ *   bidirectional: 0: query i of n sees the keys t <= T - n + i of its sequence's T; else all of them
+ *             (window must be 0 then).
+ *   workspace (device): at least pkv_prefill_workspace_bytes(...) bytes, 16-byte aligned.
+ */
+typedef struct pkv_prefill {
+  const void* q;
+  void* out;
+  int64_t q_stride, out_stride;
+  const int32_t* query_starts;
+  int64_t num_tokens;
+  int num_seqs;
+  int num_q_heads;
+  float scale;
+  int window;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  int max_blocks_per_seq;
+  int max_context_len;
+  const void* k;
+  const void* v;
+  int64_t k_stride, v_stride;
+  const int32_t* key_starts;
+  int64_t num_keys;
+  int bidirectional;
+  int reserved;
+  void* workspace;
+  size_t workspace_bytes;
+} pkv_prefill;
+
+/*
+ * Bytes of device workspace that the two calls need: num_tokens rows of queries in num_seqs sequences
+ * of up to max_context_len tokens (pkv_prompt_attention: num_keys).  Its contents need no initialisation.
+ */
+PKV_API pkv_status pkv_prefill_workspace_bytes(const pkv_pool* pool, int num_seqs, int num_q_heads, int64_t num_tokens,
+                                               int max_context_len, size_t* bytes);
+
+/*
+ * Attention of a step's new tokens over the cache: whole prompts, the next chunk of a prompt and single
+ * tokens side by side, in one call ("Lesson 4", 4.2; pkv_paged_attention_decode's attention for packed
+ * queries, as many of each sequence as it has).  Query i of sequence b's n, at position p = T_b - n + i:
+ *   out[row][h][:] = sum_{t <= p} softmax_t(scale * q[row][h] . K_b[t]) V_b[t]
+ * with T_b = context_lens[b] >= n and query heads grouped as there.  INT8 and FP8 pools: K and V are the
+ * dequantised values s * value(code).  Accumulation is fp32, weights enter the product over V as bf16 (INT8 and
+ * FP8 pools: times V's scale), which moves an output by at most 2^-8 (sum of weight |v| + |output|) before its
+ * own rounding to bf16.
+ * A sequence whose T_b is out of range gets zero rows and sets PKV_DEVERR_CONTEXT_LEN; an invalid
+ * query_starts entry sets PKV_DEVERR_QUERY and nothing is written; a block id out of range is skipped and
+ * sets PKV_DEVERR_BLOCK_ID.  Cache slots that no query of the call sees may hold anything; a NaN or infinite
+ * value (not a key) of a token that only some of a sequence's queries see may reach the others.
+ * num_seqs == 0 or num_tokens == 0 is a no-op.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (2^30 rows or more, a pool of 2^31 or more rows of
+ * head_dim), PKV_ERR_WORKSPACE, PKV_ERR_CUDA.
+ */
+PKV_API pkv_status pkv_paged_attention_prefill(const pkv_pool* pool, const pkv_prefill* args, void* stream);
+
+/*
+ * The same over packed keys and values instead of the cache: prompts as they come out of the projection, or
+ * rows that pkv_gather_cache read back.  The pool gives the kv heads, head_dim, device and error word; its
+ * blocks are not touched, whatever their type.  Sequence b has T = key_starts[b + 1] - key_starts[b] keys and
+ * query i of its n is at position T - n + i among them; a query that sees no key gets a zero row.
+ * An invalid query_starts or key_starts entry sets PKV_DEVERR_QUERY and nothing is written.
+ * NaN, infinities, no-ops and errors as for pkv_paged_attention_prefill.
+ */
+PKV_API pkv_status pkv_prompt_attention(const pkv_pool* pool, const pkv_prefill* args, void* stream);
+
+/*
+ * Read cached tokens back: sequence b's tokens from position first_positions[b] (NULL: 0) on become rows
+ * token_starts[b] .. token_starts[b + 1] - 1 of k and v, as bf16 (INT8 and FP8 pools: s * value(code),
+ * rounded once).
+ *   block_tables (device): int32 [num_seqs, max_blocks_per_seq].
+ *   token_starts (device): int32 [num_seqs + 1], not decreasing, within [0, num_tokens].
+ *   k, v (device, out): bf16 rows of [kv_heads, head_dim], k_stride and v_stride elements apart (at least a
+ *                row, multiples of 8), 16-byte aligned; num_tokens rows.  Rows outside all sequences are not written.
+ * A token past the table's row, or at a negative position, becomes a row of zeros and sets
+ * PKV_DEVERR_CONTEXT_LEN; one whose block id is out of range does and sets PKV_DEVERR_BLOCK_ID; an invalid
+ * token_starts entry sets PKV_DEVERR_QUERY and nothing is written.  num_seqs == 0 or num_tokens == 0 is a no-op.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (2^30 rows or more), PKV_ERR_CUDA.
+ */
+PKV_API pkv_status pkv_gather_cache(const pkv_pool* pool, const int32_t* block_tables, int max_blocks_per_seq,
+                                    const int32_t* token_starts, const int32_t* first_positions, int num_seqs,
+                                    int64_t num_tokens, void* k, int64_t k_stride, void* v, int64_t v_stride,
+                                    void* stream);
 
 /*
  * Read and clear the pool's device error word (PKV_DEVERR_* bits).  Waits for the work

@@ -10,13 +10,17 @@ from .api import (  # noqa: F401
     copy_blocks,
     decode_plan,
     decode_workspace_bytes,
+    gather_cache,
     get_device_error,
     launch_count,
     norm_rope_and_cache,
     paged_attention_decode,
+    paged_attention_prefill,
     pool_bytes,
     pool_create,
     pool_destroy,
+    prefill_workspace_bytes,
+    prompt_attention,
     reserve_slots,
     reshape_and_cache,
     rope_table,
@@ -32,6 +36,7 @@ from ._lib import (  # noqa: F401
     DEVERR_CONTEXT_LEN,
     DEVERR_POSITION,
     DEVERR_PREFIX,
+    DEVERR_QUERY,
     DEVERR_SLOT,
     DEVERR_TIMEOUT,
     PagedKVError,

@@ -30,6 +30,7 @@ DEVERR_TIMEOUT = 0x8
 DEVERR_CAPACITY = 0x10
 DEVERR_POSITION = 0x20
 DEVERR_PREFIX = 0x40
+DEVERR_QUERY = 0x80
 
 # Every function the header declares, with (restype, argtypes).
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -60,6 +61,14 @@ class NormRope(ctypes.Structure):
                 ("rot_dim", _i32), ("max_position", _i32), ("interleaved", _i32), ("eps", _f32), ("reserved", _i32)]
 
 
+class Prefill(ctypes.Structure):
+    _fields_ = [("q", _vp), ("out", _vp), ("q_stride", _i64), ("out_stride", _i64), ("query_starts", _vp),
+                ("num_tokens", _i64), ("num_seqs", _i32), ("num_q_heads", _i32), ("scale", _f32), ("window", _i32),
+                ("block_tables", _vp), ("context_lens", _vp), ("max_blocks_per_seq", _i32), ("max_context_len", _i32),
+                ("k", _vp), ("v", _vp), ("k_stride", _i64), ("v_stride", _i64), ("key_starts", _vp), ("num_keys", _i64),
+                ("bidirectional", _i32), ("reserved", _i32), ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
 SIGNATURES = {
     "pkv_status_string": (ctypes.c_char_p, [_i32]),
     "pkv_last_cuda_error": (ctypes.c_char_p, []),
@@ -81,6 +90,10 @@ SIGNATURES = {
                                                  _psz]),
     "pkv_shared_prefix_decode": (_i32, [_vp, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _f32, _vp,
                                         _vp, _sz, ctypes.POINTER(DecodeOptions), _vp]),
+    "pkv_prefill_workspace_bytes": (_i32, [_vp, _i32, _i32, _i64, _i32, _psz]),
+    "pkv_paged_attention_prefill": (_i32, [_vp, ctypes.POINTER(Prefill), _vp]),
+    "pkv_prompt_attention": (_i32, [_vp, ctypes.POINTER(Prefill), _vp]),
+    "pkv_gather_cache": (_i32, [_vp, _vp, _i32, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _i64, _vp]),
     "pkv_block_manager_free_list": (_i32, [_vp, _i32, _vp]),
     "pkv_block_manager_prefix_groups": (_i32, [_vp, _vp, _i32, _i32, _vp, _vp, _pi32]),
     "pkv_get_device_error": (_i32, [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]),

@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import BLOCK_SIZE, DecodeOptions, NormRope, PKV_KV_BF16, PKV_KV_FP8_E4M3, PKV_KV_INT8, check
+from ._lib import BLOCK_SIZE, DecodeOptions, NormRope, Prefill, PKV_KV_BF16, PKV_KV_FP8_E4M3, PKV_KV_INT8, check
 
 _DTYPES = {"bf16": PKV_KV_BF16, "int8": PKV_KV_INT8, "fp8": PKV_KV_FP8_E4M3}
 _CODE_DTYPES = {"bf16": torch.bfloat16, "int8": torch.int8, "fp8": torch.uint8}
@@ -217,6 +217,15 @@ class PagedKVPool:
                              max_suffix_len, **kwargs):
         return shared_prefix_decode(self, q, block_tables, context_lens, group_starts, prefix_lens, scale,
                                     max_prefix_len, max_suffix_len, **kwargs)
+
+    def prefill(self, q, block_tables, context_lens, query_starts, scale, max_context_len, **kwargs):
+        return paged_attention_prefill(self, q, block_tables, context_lens, query_starts, scale, max_context_len, **kwargs)
+
+    def prompt_attention(self, q, k, v, query_starts, scale, **kwargs):
+        return prompt_attention(self, q, k, v, query_starts, scale, **kwargs)
+
+    def gather_cache(self, block_tables, token_starts, num_tokens, **kwargs):
+        return gather_cache(self, block_tables, token_starts, num_tokens, **kwargs)
 
     def device_error(self, stream=None) -> int:
         return get_device_error(self, stream)
@@ -518,6 +527,118 @@ def shared_prefix_decode(pool: PagedKVPool, q: torch.Tensor, block_tables: torch
     if st:
         check(st, "shared_prefix_decode")
     return out
+
+
+def prefill_workspace_bytes(pool: PagedKVPool, num_seqs: int, num_q_heads: int, num_tokens: int,
+                            max_context_len: int) -> int:
+    """Workspace of ``paged_attention_prefill`` and ``prompt_attention`` (there max_context_len is k's rows)."""
+    n = ctypes.c_size_t()
+    check(_lib.load().pkv_prefill_workspace_bytes(_handle(pool), num_seqs, num_q_heads, num_tokens, int(max_context_len),
+                                                  ctypes.byref(n)), "prefill_workspace_bytes")
+    return n.value
+
+
+def _prefill_args(pool, q, query_starts, scale, max_context_len, window, out, workspace, stream):
+    """The arguments that the calls over the cache and over packed keys have in common, and out."""
+    q_stride = _head_rows(q, "q", None, None, pool)
+    n, hq, d = q.shape
+    _check(query_starts, torch.int32, "query_starts", 1, pool)
+    b = query_starts.shape[0] - 1
+    if b < 0:
+        raise ValueError("query_starts must have one entry more than there are sequences")
+    if out is None:
+        out = _empty((n, hq, d), q.dtype, q.device, stream)
+    out_stride = _head_rows(out, "out", n, hq, pool)
+    if workspace is None:
+        workspace = _empty(prefill_workspace_bytes(pool, b, hq, n, max_context_len), torch.uint8, q.device, stream)
+    elif workspace.get_device() != pool.device_index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the pool's device")
+    a = Prefill()
+    a.q, a.q_stride, a.out, a.out_stride = q.data_ptr(), q_stride, out.data_ptr(), out_stride
+    a.query_starts, a.num_tokens, a.num_seqs, a.num_q_heads = query_starts.data_ptr(), n, b, hq
+    a.scale, a.window = float(scale), int(window)
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.nbytes
+    return a, out, workspace
+
+
+def paged_attention_prefill(pool: PagedKVPool, q: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                            query_starts: torch.Tensor, scale: float, max_context_len: int, window: int = 0,
+                            out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """Attention of a step's new tokens over the cache: whole prompts, chunks of prompts and single tokens side
+    by side.  q is bf16 [N, Hq, d], packed: sequence b's rows are query_starts[b] .. query_starts[b + 1] - 1
+    (int32 [B + 1]), its last tokens, which are in the cache already; context_lens (int32 [B]) counts them.  A query
+    at position p attends to the tokens up to p, with ``window`` W > 0 to the last W of them.  Returns out, bf16
+    [N, Hq, d]; its rows outside all sequences are not written.  q and out may be slices like those of
+    ``norm_rope_and_cache``.  ``workspace`` (a uint8 CUDA tensor) is allocated here when not given."""
+    _check(block_tables, torch.int32, "block_tables", 2, pool)
+    _check(context_lens, torch.int32, "context_lens", 1, pool)
+    a, out, workspace = _prefill_args(pool, q, query_starts, scale, max_context_len, window, out, workspace, stream)
+    rows, width = block_tables.shape
+    if rows != a.num_seqs or context_lens.shape[0] != rows:
+        raise ValueError("query_starts, block_tables and context_lens disagree in shape")
+    a.block_tables, a.context_lens = block_tables.data_ptr(), context_lens.data_ptr()
+    a.max_blocks_per_seq, a.max_context_len = width, int(max_context_len)
+    st = _lib.load().pkv_paged_attention_prefill(pool.handle, ctypes.byref(a), _pool_stream(pool, stream))
+    if st:
+        check(st, "paged_attention_prefill")
+    return out
+
+
+def prompt_attention(pool: PagedKVPool, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, query_starts: torch.Tensor,
+                     scale: float, key_starts: torch.Tensor | None = None, causal: bool = True, window: int = 0,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of packed prompts over keys and values that are not in the cache (yet): q bf16 [N, Hq, d], k and
+    v bf16 [M, Hkv, d], all possibly slices of one projection's output.  Sequence b's queries are rows
+    query_starts[b] .. query_starts[b + 1] - 1, its keys rows key_starts[b] .. key_starts[b + 1] - 1 (int32 [B + 1];
+    None: the queries' rows).  Query i of n sees the keys up to T - n + i of its sequence's T, with ``window`` W > 0
+    the last W of them; with ``causal`` false all T.  A query that sees none gets zeros.  The pool gives the kv heads,
+    head_dim and device; its blocks are not touched.  Returns out, bf16 [N, Hq, d]; its rows outside all sequences are
+    not written.  ``workspace`` (a uint8 CUDA tensor) is allocated here when not given."""
+    k_stride = _head_rows(k, "k", None, pool.kv_heads, pool)
+    v_stride = _head_rows(v, "v", k.shape[0], pool.kv_heads, pool)
+    if key_starts is not None:
+        _check(key_starts, torch.int32, "key_starts", 1, pool)
+        if key_starts.shape != query_starts.shape:
+            raise ValueError("query_starts and key_starts disagree in shape")
+    a, out, workspace = _prefill_args(pool, q, query_starts, scale, k.shape[0], window, out, workspace, stream)
+    a.k, a.v, a.k_stride, a.v_stride, a.num_keys = k.data_ptr(), v.data_ptr(), k_stride, v_stride, k.shape[0]
+    a.key_starts = None if key_starts is None else key_starts.data_ptr()
+    a.bidirectional = 0 if causal else 1
+    st = _lib.load().pkv_prompt_attention(pool.handle, ctypes.byref(a), _pool_stream(pool, stream))
+    if st:
+        check(st, "prompt_attention")
+    return out
+
+
+def gather_cache(pool: PagedKVPool, block_tables: torch.Tensor, token_starts: torch.Tensor, num_tokens: int,
+                 first_positions: torch.Tensor | None = None, k: torch.Tensor | None = None,
+                 v: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Read cached tokens back: sequence b's tokens from position first_positions[b] (int32 [B]; None: 0) on become
+    rows token_starts[b] .. token_starts[b + 1] - 1 (int32 [B + 1]) of k and v, bf16 [num_tokens, Hkv, d],
+    dequantised.  Returns (k, v), allocated here when not given; rows outside all sequences are not written."""
+    _check(block_tables, torch.int32, "block_tables", 2, pool)
+    _check(token_starts, torch.int32, "token_starts", 1, pool)
+    b, width = block_tables.shape
+    if token_starts.shape[0] != b + 1:
+        raise ValueError("token_starts must have one entry more than block_tables has rows")
+    if first_positions is not None:
+        _check(first_positions, torch.int32, "first_positions", 1, pool)
+        if first_positions.shape[0] != b:
+            raise ValueError("block_tables and first_positions disagree in shape")
+    num_tokens = int(num_tokens)
+    if num_tokens < 0:
+        raise ValueError("num_tokens must not be negative")
+    shape = (num_tokens, pool.kv_heads, pool.head_dim)
+    k, v = (_empty(shape, torch.bfloat16, block_tables.device, stream) if t is None else t for t in (k, v))
+    ks, vs = (_head_rows(t, name, num_tokens, pool.kv_heads, pool) for t, name in ((k, "k"), (v, "v")))
+    st = _lib.load().pkv_gather_cache(
+        pool.handle, block_tables.data_ptr(), width, token_starts.data_ptr(),
+        0 if first_positions is None else first_positions.data_ptr(), b, num_tokens, k.data_ptr(), ks, v.data_ptr(), vs,
+        _pool_stream(pool, stream))
+    if st:
+        check(st, "gather_cache")
+    return k, v
 
 
 def get_device_error(pool: PagedKVPool, stream=None) -> int:

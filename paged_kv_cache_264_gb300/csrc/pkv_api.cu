@@ -425,6 +425,161 @@ pkv_status make_prefix_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
   return PKV_OK;
 }
 
+// Heads of a row chunk of a group, so that 128 rows hold whole tokens: the whole group, or, where that
+// leaves more than a quarter of the rows without one, the split into up to four that leaves the fewest.
+// Measured on GB300: see pkv_prompt_tc.cuh.
+void prompt_heads(int group, int* heads, int* chunks) {
+  const int least = static_cast<int>(ceil_div(group, pkv::kRowTile));
+  double best = 0.0;
+  for (int c = least; c < least + 4 && c <= group; ++c) {
+    const int h = static_cast<int>(ceil_div(group, c));
+    if (ceil_div(group, h) != c) continue;
+    const double used = double(pkv::kRowTile / h) * group / (double(pkv::kRowTile) * c);
+    if (used > best) {
+      best = used;
+      *heads = h;
+      *chunks = c;
+    }
+    if (best >= 0.75) break;
+  }
+}
+
+// Layout of a prompt attention call's workspace, and its parameters that follow from the shape.
+struct PromptPlan {
+  int heads, chunks, units, stream_tokens, max_pieces, part_rows;
+  size_t list, joins, starts, cuts, acc, ml, bytes;  // offsets (the header sits at 0), size
+};
+
+pkv_status make_prompt_plan(const pkv_pool* pool, int num_seqs, int num_q_heads, int64_t num_tokens,
+                            int64_t max_context_len, PromptPlan* x) {
+  if (!pool || num_seqs < 0 || num_q_heads < 1 || num_tokens < 0 || max_context_len < 0) return PKV_ERR_INVALID_ARG;
+  if (num_q_heads % pool->kv_heads != 0) return PKV_ERR_INVALID_ARG;
+  if (num_tokens >= pkv::kNoWindow || max_context_len >= pkv::kNoWindow) return PKV_ERR_UNSUPPORTED;
+  prompt_heads(num_q_heads / pool->kv_heads, &x->heads, &x->chunks);
+  x->units = pool->kv_heads * x->chunks;
+  x->stream_tokens = pkv::kRowTile / x->heads;
+  const int64_t per = 2 * x->stream_tokens;
+  // Items are cut only where they are longer than a CTA's share of all (prompt_plan_kernel): with P
+  // pieces of at least L tiles, where L is at least two thirds of the share, P L <= 2 (tiles of the cut
+  // items) <= 2 (3 / 2 L) (CTAs) / units.
+  const int64_t tiles = ceil_div(max_context_len, pkv::kPromptTile);
+  x->max_pieces = tiles > pkv::kPromptMinPiece ? 3 * pool->sm_count / x->units : 0;
+  if (x->max_pieces < 2) x->max_pieces = 0;
+  x->part_rows = static_cast<int>(std::min(per, num_tokens)) * x->heads;
+  const int64_t items = num_seqs + num_tokens / per;
+  if ((items + x->max_pieces) * x->units > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at = (at + bytes + 255) / 256 * 256;
+    return o;
+  };
+  take(sizeof(pkv::PromptHeader));
+  x->list = take(size_t(items + x->max_pieces) * sizeof(pkv::PromptItem));
+  x->joins = take(size_t(x->max_pieces) * sizeof(pkv::PromptJoin));
+  x->starts = take(size_t(num_seqs) * 4);
+  x->cuts = take(size_t(items) * sizeof(int2));
+  const size_t rows = size_t(x->max_pieces) * x->units * x->part_rows;
+  x->acc = take(rows * pool->head_dim * 4);
+  x->ml = take(rows * 8);
+  x->bytes = at;
+  return PKV_OK;
+}
+
+// Rows of [heads, head_dim] at `stride`: aligned, and not on one another.
+bool valid_rows(const void* base, int64_t stride, int64_t rows, int64_t width) {
+  return base && aligned16(base) && (rows <= 1 || (stride % 8 == 0 && stride >= width && stride < (int64_t(1) << 38)));
+}
+
+pkv_status prompt_attention(const pkv_pool* pool, const pkv_prefill* a, bool paged, void* stream) {
+  if (!pool || !a) return PKV_ERR_INVALID_ARG;
+  if (!paged && a->num_keys < 0) return PKV_ERR_INVALID_ARG;
+  PromptPlan plan;
+  const pkv_status st = make_prompt_plan(pool, a->num_seqs, a->num_q_heads, a->num_tokens,
+                                         paged ? a->max_context_len : a->num_keys, &plan);
+  if (st != PKV_OK) return st;
+  if (a->window < 0 || !(a->scale == a->scale)) return PKV_ERR_INVALID_ARG;
+  if (!paged && a->bidirectional && a->window != 0) return PKV_ERR_INVALID_ARG;
+  if (a->num_seqs == 0 || a->num_tokens == 0) return PKV_OK;
+  const int64_t q_width = int64_t(a->num_q_heads) * pool->head_dim, k_width = int64_t(pool->kv_heads) * pool->head_dim;
+  if (!a->query_starts || !valid_rows(a->q, a->q_stride, a->num_tokens, q_width) ||
+      !valid_rows(a->out, a->out_stride, a->num_tokens, q_width))
+    return PKV_ERR_INVALID_ARG;
+  if (paged) {
+    if (!a->block_tables || !a->context_lens || a->max_context_len < 1 || a->max_blocks_per_seq < 1) return PKV_ERR_INVALID_ARG;
+    if (int64_t(a->max_context_len) > int64_t(a->max_blocks_per_seq) * pkv::kBlockSize) return PKV_ERR_INVALID_ARG;
+    if (!pool->has_tmaps) return PKV_ERR_UNSUPPORTED;
+  } else if (a->num_keys > 0 && (!valid_rows(a->k, a->k_stride, a->num_keys, k_width) ||
+                                 !valid_rows(a->v, a->v_stride, a->num_keys, k_width))) {
+    return PKV_ERR_INVALID_ARG;
+  }
+  if (!a->workspace || a->workspace_bytes < plan.bytes) return PKV_ERR_WORKSPACE;
+  if (!aligned16(a->workspace)) return PKV_ERR_INVALID_ARG;
+  const OnPoolDevice device(pool);
+  if (!device) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+  char* ws = static_cast<char*>(a->workspace);
+  pkv::PromptParams p{};
+  p.q = a->q;
+  p.out = a->out;
+  p.query_starts = a->query_starts;
+  p.err = pool->d_err;
+  p.q_stride = a->q_stride;
+  p.out_stride = a->out_stride;
+  p.num_tokens = static_cast<int>(a->num_tokens);
+  p.num_seqs = a->num_seqs;
+  p.num_q_heads = a->num_q_heads;
+  p.kv_heads = pool->kv_heads;
+  p.group = a->num_q_heads / pool->kv_heads;
+  p.head_dim = pool->head_dim;
+  p.window = a->window == 0 || a->window > pkv::kNoWindow ? pkv::kNoWindow : a->window;
+  p.causal = paged || !a->bidirectional;
+  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.paged = paged;
+  if (paged) {
+    p.k_cache = pool->k_cache;
+    p.v_cache = pool->v_cache;
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
+    p.block_tables = a->block_tables;
+    p.context_lens = a->context_lens;
+    p.num_blocks = pool->num_blocks;
+    p.max_blocks_per_seq = a->max_blocks_per_seq;
+    p.max_context_len = a->max_context_len;
+  } else {
+    p.k = a->k;
+    p.v = a->v;
+    p.key_starts = a->key_starts ? a->key_starts : a->query_starts;
+    p.k_stride = a->k_stride;
+    p.v_stride = a->v_stride;
+    p.num_keys = static_cast<int>(a->num_keys);
+  }
+  p.heads = plan.heads;
+  p.chunks = plan.chunks;
+  p.units = plan.units;
+  p.stream_tokens = plan.stream_tokens;
+  p.grid = pool->sm_count;
+  p.max_pieces = plan.max_pieces;
+  p.part_rows = plan.part_rows;
+  p.header = reinterpret_cast<pkv::PromptHeader*>(ws);
+  p.list = reinterpret_cast<pkv::PromptItem*>(ws + plan.list);
+  p.joins = reinterpret_cast<pkv::PromptJoin*>(ws + plan.joins);
+  p.tile_starts = reinterpret_cast<int*>(ws + plan.starts);
+  p.cuts = reinterpret_cast<int2*>(ws + plan.cuts);
+  p.acc = reinterpret_cast<float*>(ws + plan.acc);
+  p.ml = reinterpret_cast<float2*>(ws + plan.ml);
+  const auto s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = pkv::launch_prompt_plan(p, s);
+  if (e != cudaSuccess) return cuda_fail(e, "prompt attention: plan launch");
+  e = pkv::launch_prompt_simple(p, static_cast<pkv::KvType>(pool->dtype), s);
+  if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
+  g_launches.fetch_add(2, std::memory_order_relaxed);
+  if (plan.max_pieces == 0) return PKV_OK;
+  e = pkv::launch_prompt_join(p, s);
+  if (e != cudaSuccess) return cuda_fail(e, "prompt attention: join launch");
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PKV_OK;
+}
+
 }  // namespace
 
 namespace pkv {
@@ -866,6 +1021,60 @@ pkv_status pkv_shared_prefix_decode(const pkv_pool* pool, const void* q, const i
   if (plan.join) return PKV_OK;
   e = pkv::launch_prefix_merge(x, s);
   if (e != cudaSuccess) return cuda_fail(e, "shared prefix: merge launch");
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PKV_OK;
+}
+
+pkv_status pkv_prefill_workspace_bytes(const pkv_pool* pool, int num_seqs, int num_q_heads, int64_t num_tokens,
+                                       int max_context_len, size_t* bytes) {
+  if (!bytes) return PKV_ERR_INVALID_ARG;
+  PromptPlan plan;
+  const pkv_status st = make_prompt_plan(pool, num_seqs, num_q_heads, num_tokens, max_context_len, &plan);
+  if (st != PKV_OK) return st;
+  *bytes = plan.bytes;
+  return PKV_OK;
+}
+
+pkv_status pkv_paged_attention_prefill(const pkv_pool* pool, const pkv_prefill* args, void* stream) {
+  return prompt_attention(pool, args, true, stream);
+}
+
+pkv_status pkv_prompt_attention(const pkv_pool* pool, const pkv_prefill* args, void* stream) {
+  return prompt_attention(pool, args, false, stream);
+}
+
+pkv_status pkv_gather_cache(const pkv_pool* pool, const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* token_starts, const int32_t* first_positions, int num_seqs,
+                            int64_t num_tokens, void* k, int64_t k_stride, void* v, int64_t v_stride, void* stream) {
+  if (!pool || num_seqs < 0 || num_tokens < 0) return PKV_ERR_INVALID_ARG;
+  if (num_tokens >= pkv::kNoWindow) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+  if (!block_tables || max_blocks_per_seq < 1 || !token_starts) return PKV_ERR_INVALID_ARG;
+  const int64_t width = int64_t(pool->kv_heads) * pool->head_dim;
+  if (!valid_rows(k, k_stride, num_tokens, width) || !valid_rows(v, v_stride, num_tokens, width)) return PKV_ERR_INVALID_ARG;
+  const OnPoolDevice device(pool);
+  if (!device) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+  pkv::GatherParams p{};
+  p.k_cache = pool->k_cache;
+  p.v_cache = pool->v_cache;
+  p.k_scale = pool->k_scale;
+  p.v_scale = pool->v_scale;
+  p.block_tables = block_tables;
+  p.token_starts = token_starts;
+  p.first_positions = first_positions;
+  p.k = k;
+  p.v = v;
+  p.err = pool->d_err;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.num_blocks = pool->num_blocks;
+  p.num_tokens = static_cast<int>(num_tokens);
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.kv_heads = pool->kv_heads;
+  p.head_dim = pool->head_dim;
+  const cudaError_t e = pkv::launch_gather(p, static_cast<pkv::KvType>(pool->dtype), pool->sm_count, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gather_cache launch");
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return PKV_OK;
 }

@@ -36,6 +36,7 @@ constexpr uint32_t kErrTimeout = 0x8u;
 constexpr uint32_t kErrCapacity = 0x10u;
 constexpr uint32_t kErrPosition = 0x20u;
 constexpr uint32_t kErrPrefix = 0x40u;
+constexpr uint32_t kErrQuery = 0x80u;
 
 enum class KvType : int { kBf16 = 0, kInt8 = 1, kFp8 = 2 };
 
@@ -208,6 +209,99 @@ cudaError_t launch_prefix_quant(const PrefixParams& p, const CUtensorMap& tk, co
                                 cudaStream_t stream);
 cudaError_t launch_prefix_bf16(const PrefixParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream);
 cudaError_t launch_prefix_merge(const PrefixParams& p, cudaStream_t stream);
+
+// Attention of packed query tokens, over the paged cache or over packed keys and values
+// (pkv_prompt.cu).
+struct PromptItem {
+  int seq;
+  int row0, ntok;        // first row of q and out, tokens
+  int pos0;              // position of the first token (below 0 where a packed sequence has fewer keys than queries)
+  int len;               // tokens of the sequence that may be seen (0: its length is invalid, its rows become zero)
+  int key0;              // packed: first row of k and v
+  int tile0, tiles;      // 128-token tiles of this piece
+  int part;              // first partial of this piece's head units; -1: writes out
+  int pad[3];
+};
+struct PromptJoin {      // an item in several pieces
+  int row0, ntok, part, parts;
+};
+struct PromptHeader {    // of the workspace
+  unsigned ticket;       // work units handed out after each CTA's first
+  int items, joins;
+  int pad;
+};
+struct PromptParams {
+  const void* q;                // bf16 rows of [Hq, D] at token stride q_stride
+  void* out;
+  const int32_t* query_starts;  // [B + 1]
+  uint32_t* err;
+  int64_t q_stride, out_stride; // elements
+  int num_tokens;               // rows of q and out
+  int num_seqs;
+  int num_q_heads, kv_heads, group, head_dim;
+  int window;                   // tokens each query sees back from its own position (kNoWindow: all)
+  int causal;
+  float scale_log2;
+  // over the cache
+  int paged;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  int64_t num_blocks;
+  int max_blocks_per_seq;
+  int max_context_len;
+  // over packed rows
+  const void* k;                // bf16 rows of [Hkv, D]
+  const void* v;
+  const int32_t* key_starts;    // [B + 1]
+  int64_t k_stride, v_stride;
+  int num_keys;
+  // head units and items
+  int heads, chunks, units;     // heads of a chunk, chunks of a kv head, units = kv_heads * chunks
+  int stream_tokens;            // tokens of a stream's rows
+  int grid;
+  int max_pieces;               // pieces of split items that there is room for (0: nothing is split)
+  int part_rows;                // rows of a partial
+  // workspace
+  PromptHeader* header;
+  PromptItem* list;
+  PromptJoin* joins;
+  int* tile_starts;             // [B + 1] items before each sequence's
+  int2* cuts;                   // per item: pieces, first partial
+  float* acc;                   // [pieces * units, part_rows, D]
+  float2* ml;                   // running max (log2 units) and sum
+};
+constexpr int kPromptTile = 128;  // tokens of one tile
+constexpr int kRowTile = 128;     // rows of one stream
+constexpr int kPromptMinPiece = 4;  // tiles of a cut item's piece at least
+cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream);
+cudaError_t launch_prompt_join(const PromptParams& p, cudaStream_t stream);
+cudaError_t launch_prompt_simple(const PromptParams& p, KvType kv, cudaStream_t stream);
+
+// Cache rows of sequences' tokens, dequantised, to packed rows (pkv_gather.cu).
+struct GatherParams {
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_tables;
+  const int32_t* token_starts;    // [B + 1]
+  const int32_t* first_positions; // [B] or NULL: 0
+  void* k;                        // bf16 rows of [Hkv, D]
+  void* v;
+  uint32_t* err;
+  int64_t k_stride, v_stride;
+  int64_t num_blocks;
+  int num_tokens;
+  int max_blocks_per_seq;
+  int num_seqs;
+  int kv_heads;
+  int head_dim;
+};
+cudaError_t launch_gather(const GatherParams& p, KvType kv, int sms, cudaStream_t stream);
 
 // Launch a kernel with programmatic stream serialisation (see griddep_wait in
 // pkv_device.cuh): its launch may overlap the tail of the previous kernel in the stream.
