@@ -491,6 +491,22 @@ bool valid_rows(const void* base, int64_t stride, int64_t rows, int64_t width) {
   return base && aligned16(base) && (rows <= 1 || (stride % 8 == 0 && stride >= width && stride < (int64_t(1) << 38)));
 }
 
+// A tensor map of bf16 rows of [heads, head_dim] at `stride`: 128-byte boxes of box_heads heads of box_rows
+// rows, 128-byte swizzle.
+bool make_rows_tensor_map(CUtensorMap* map, const void* base, int head_dim, int heads, int64_t rows, int64_t stride,
+                          int box_heads, int box_rows) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  if (rows == 1) stride = int64_t(heads) * head_dim;
+  const cuuint64_t dims[3] = {cuuint64_t(head_dim), cuuint64_t(heads), cuuint64_t(rows)};
+  const cuuint64_t strides[2] = {cuuint64_t(head_dim) * 2, cuuint64_t(stride) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_rows)};
+  const cuuint32_t elem_strides[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem_strides,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 pkv_status prompt_attention(const pkv_pool* pool, const pkv_prefill* a, bool paged, void* stream) {
   if (!pool || !a) return PKV_ERR_INVALID_ARG;
   if (!paged && a->num_keys < 0) return PKV_ERR_INVALID_ARG;
@@ -567,10 +583,23 @@ pkv_status prompt_attention(const pkv_pool* pool, const pkv_prefill* a, bool pag
   p.cuts = reinterpret_cast<int2*>(ws + plan.cuts);
   p.acc = reinterpret_cast<float*>(ws + plan.acc);
   p.ml = reinterpret_cast<float2*>(ws + plan.ml);
+  CUtensorMap tq, tk, tv;
+  if (!make_rows_tensor_map(&tq, a->q, pool->head_dim, a->num_q_heads, a->num_tokens, a->q_stride, p.heads, p.stream_tokens))
+    return PKV_ERR_UNSUPPORTED;
+  if (paged) {
+    tk = pool->tmap_k;
+    tv = pool->tmap_v;
+  } else if (a->num_keys == 0) {
+    tk = tv = tq;  // never read
+  } else if (!make_rows_tensor_map(&tk, a->k, pool->head_dim, pool->kv_heads, a->num_keys, a->k_stride, 1, pkv::kPromptTile) ||
+             !make_rows_tensor_map(&tv, a->v, pool->head_dim, pool->kv_heads, a->num_keys, a->v_stride, 1, pkv::kPromptTile)) {
+    return PKV_ERR_UNSUPPORTED;
+  }
   const auto s = static_cast<cudaStream_t>(stream);
   cudaError_t e = pkv::launch_prompt_plan(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention: plan launch");
-  e = pkv::launch_prompt_simple(p, static_cast<pkv::KvType>(pool->dtype), s);
+  e = paged && pool->dtype != PKV_KV_BF16 ? pkv::launch_prompt_simple(p, static_cast<pkv::KvType>(pool->dtype), s)
+                                          : pkv::launch_prompt_bf16(p, tq, tk, tv, s);
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
   g_launches.fetch_add(2, std::memory_order_relaxed);
   if (plan.max_pieces == 0) return PKV_OK;

@@ -220,7 +220,8 @@ struct PromptItem {
   int key0;              // packed: first row of k and v
   int tile0, tiles;      // 128-token tiles of this piece
   int part;              // first partial of this piece's head units; -1: writes out
-  int pad[3];
+  int shared;            // other items read the same tiles
+  int pad[2];
 };
 struct PromptJoin {      // an item in several pieces
   int row0, ntok, part, parts;
@@ -279,6 +280,8 @@ constexpr int kRowTile = 128;     // rows of one stream
 constexpr int kPromptMinPiece = 4;  // tiles of a cut item's piece at least
 cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream);
 cudaError_t launch_prompt_join(const PromptParams& p, cudaStream_t stream);
+cudaError_t launch_prompt_bf16(const PromptParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               cudaStream_t stream);
 cudaError_t launch_prompt_simple(const PromptParams& p, KvType kv, cudaStream_t stream);
 
 // Cache rows of sequences' tokens, dequantised, to packed rows (pkv_gather.cu).

@@ -89,6 +89,7 @@ __device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, int at)
   x.pos0 = s.len - s.n + tok0;
   x.len = s.len;
   x.key0 = s.key0;
+  x.shared = s.n > per;
   span_tiles(prompt_span(p, x.pos0, x.pos0 + x.ntok - 1, s.len), x.tile0, x.tiles);
   return x;
 }
