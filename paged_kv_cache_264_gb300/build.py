@@ -21,7 +21,7 @@ SOURCES = ["pkv_api.cu", "pkv_cache.cu", "pkv_decode_bf16.cu", "pkv_decode_int8.
            "pkv_decode_fp8.cu", "pkv_decode_mma.cu", "pkv_decode_mma_bf16.cu", "pkv_decode_mma_int8.cu",
            "pkv_decode_mma_fp8.cu", "pkv_decode_mma_quant_d64.cu", "pkv_decode_mma_join.cu", "pkv_static_scratch.cu",
            "pkv_selftest.cu", "pkv_slots.cu", "pkv_rope.cu", "pkv_prefix.cu", "pkv_prefix_bf16.cu", "pkv_prefix_quant.cu",
-           "pkv_prompt.cu", "pkv_prompt_bf16.cu", "pkv_gather.cu", "pkv_blocks.cpp"]
+           "pkv_prompt.cu", "pkv_prompt_bf16.cu", "pkv_prompt_quant.cu", "pkv_gather.cu", "pkv_blocks.cpp"]
 
 
 def build_dir() -> Path:

@@ -427,7 +427,6 @@ pkv_status make_prefix_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
 
 // Heads of a row chunk of a group, so that 128 rows hold whole tokens: the whole group, or, where that
 // leaves more than a quarter of the rows without one, the split into up to four that leaves the fewest.
-// Measured on GB300: see pkv_prompt_tc.cuh.
 void prompt_heads(int group, int* heads, int* chunks) {
   const int least = static_cast<int>(ceil_div(group, pkv::kRowTile));
   double best = 0.0;
@@ -446,8 +445,8 @@ void prompt_heads(int group, int* heads, int* chunks) {
 
 // Layout of a prompt attention call's workspace, and its parameters that follow from the shape.
 struct PromptPlan {
-  int heads, chunks, units, stream_tokens, max_pieces, part_rows;
-  size_t list, joins, starts, cuts, acc, ml, bytes;  // offsets (the header sits at 0), size
+  int heads, chunks, units, stream_tokens, max_parts, part_rows;
+  size_t list, joins, ctas, starts, entries, acc, ml, bytes;  // offsets (the header sits at 0), size
 };
 
 pkv_status make_prompt_plan(const pkv_pool* pool, int num_seqs, int num_q_heads, int64_t num_tokens,
@@ -455,19 +454,17 @@ pkv_status make_prompt_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
   if (!pool || num_seqs < 0 || num_q_heads < 1 || num_tokens < 0 || max_context_len < 0) return PKV_ERR_INVALID_ARG;
   if (num_q_heads % pool->kv_heads != 0) return PKV_ERR_INVALID_ARG;
   if (num_tokens >= pkv::kNoWindow || max_context_len >= pkv::kNoWindow) return PKV_ERR_UNSUPPORTED;
+  if (pool->sm_count >= 1024) return PKV_ERR_UNSUPPORTED;  // the plan holds a value per CTA
   prompt_heads(num_q_heads / pool->kv_heads, &x->heads, &x->chunks);
   x->units = pool->kv_heads * x->chunks;
   x->stream_tokens = pkv::kRowTile / x->heads;
   const int64_t per = 2 * x->stream_tokens;
-  // Items are cut only where they are longer than a CTA's share of all (prompt_plan_kernel): with P
-  // pieces of at least L tiles, where L is at least two thirds of the share, P L <= 2 (tiles of the cut
-  // items) <= 2 (3 / 2 L) (CTAs) / units.
-  const int64_t tiles = ceil_div(max_context_len, pkv::kPromptTile);
-  x->max_pieces = tiles > pkv::kPromptMinPiece ? 3 * pool->sm_count / x->units : 0;
-  if (x->max_pieces < 2) x->max_pieces = 0;
+  // A CTA's stretch of the line holds pieces of at most two units that are cut.
+  const bool cut = ceil_div(max_context_len, pkv::kPromptTile) > pkv::kPromptWhole;
+  x->max_parts = cut ? 2 * pool->sm_count : 0;
   x->part_rows = static_cast<int>(std::min(per, num_tokens)) * x->heads;
-  const int64_t items = num_seqs + num_tokens / per;
-  if ((items + x->max_pieces) * x->units > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  const int64_t items = num_seqs + num_tokens / per, work = items * x->units;
+  if (work > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -475,11 +472,12 @@ pkv_status make_prompt_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
     return o;
   };
   take(sizeof(pkv::PromptHeader));
-  x->list = take(size_t(items + x->max_pieces) * sizeof(pkv::PromptItem));
-  x->joins = take(size_t(x->max_pieces) * sizeof(pkv::PromptJoin));
+  x->list = take(size_t(work + x->max_parts) * sizeof(pkv::PromptItem));
+  x->joins = take(size_t(x->max_parts) * sizeof(pkv::PromptJoin));
+  x->ctas = take(size_t(pool->sm_count + 1) * 4);
   x->starts = take(size_t(num_seqs) * 4);
-  x->cuts = take(size_t(items) * sizeof(int2));
-  const size_t rows = size_t(x->max_pieces) * x->units * x->part_rows;
+  x->entries = take(size_t(num_seqs) * 4);
+  const size_t rows = size_t(x->max_parts) * x->part_rows;
   x->acc = take(rows * pool->head_dim * 4);
   x->ml = take(rows * 8);
   x->bytes = at;
@@ -574,13 +572,14 @@ pkv_status prompt_attention(const pkv_pool* pool, const pkv_prefill* a, bool pag
   p.units = plan.units;
   p.stream_tokens = plan.stream_tokens;
   p.grid = pool->sm_count;
-  p.max_pieces = plan.max_pieces;
+  p.max_parts = plan.max_parts;
   p.part_rows = plan.part_rows;
   p.header = reinterpret_cast<pkv::PromptHeader*>(ws);
   p.list = reinterpret_cast<pkv::PromptItem*>(ws + plan.list);
   p.joins = reinterpret_cast<pkv::PromptJoin*>(ws + plan.joins);
-  p.tile_starts = reinterpret_cast<int*>(ws + plan.starts);
-  p.cuts = reinterpret_cast<int2*>(ws + plan.cuts);
+  p.cta_first = reinterpret_cast<int*>(ws + plan.ctas);
+  p.item_starts = reinterpret_cast<int*>(ws + plan.starts);
+  p.seq_entry = reinterpret_cast<int*>(ws + plan.entries);
   p.acc = reinterpret_cast<float*>(ws + plan.acc);
   p.ml = reinterpret_cast<float2*>(ws + plan.ml);
   CUtensorMap tq, tk, tv;
@@ -598,11 +597,11 @@ pkv_status prompt_attention(const pkv_pool* pool, const pkv_prefill* a, bool pag
   const auto s = static_cast<cudaStream_t>(stream);
   cudaError_t e = pkv::launch_prompt_plan(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention: plan launch");
-  e = paged && pool->dtype != PKV_KV_BF16 ? pkv::launch_prompt_simple(p, static_cast<pkv::KvType>(pool->dtype), s)
+  e = paged && pool->dtype != PKV_KV_BF16 ? pkv::launch_prompt_quant(p, tq, static_cast<pkv::KvType>(pool->dtype), s)
                                           : pkv::launch_prompt_bf16(p, tq, tk, tv, s);
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
   g_launches.fetch_add(2, std::memory_order_relaxed);
-  if (plan.max_pieces == 0) return PKV_OK;
+  if (plan.max_parts == 0) return PKV_OK;
   e = pkv::launch_prompt_join(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention: join launch");
   g_launches.fetch_add(1, std::memory_order_relaxed);

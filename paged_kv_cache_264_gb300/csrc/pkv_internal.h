@@ -219,17 +219,18 @@ struct PromptItem {
   int len;               // tokens of the sequence that may be seen (0: its length is invalid, its rows become zero)
   int key0;              // packed: first row of k and v
   int tile0, tiles;      // 128-token tiles of this piece
-  int part;              // first partial of this piece's head units; -1: writes out
+  int part;              // its partial; -1: writes out
   int shared;            // other items read the same tiles
-  int pad[2];
+  int unit;              // head unit; in a list of whole items: the sequence's first entry,
+  int count;             //   and its entries
 };
-struct PromptJoin {      // an item in several pieces
-  int row0, ntok, part, parts;
+struct PromptJoin {      // a unit of work in several pieces
+  int row0, ntok, unit, part, parts;
 };
 struct PromptHeader {    // of the workspace
-  unsigned ticket;       // work units handed out after each CTA's first
+  unsigned ticket;       // units of work handed out after each CTA's first
+  int line;              // 1: each CTA has its pieces in the list; 0: a list of whole items
   int items, joins;
-  int pad;
 };
 struct PromptParams {
   const void* q;                // bf16 rows of [Hq, D] at token stride q_stride
@@ -264,25 +265,27 @@ struct PromptParams {
   int heads, chunks, units;     // heads of a chunk, chunks of a kv head, units = kv_heads * chunks
   int stream_tokens;            // tokens of a stream's rows
   int grid;
-  int max_pieces;               // pieces of split items that there is room for (0: nothing is split)
+  int max_parts;                // partials that there is room for
   int part_rows;                // rows of a partial
   // workspace
   PromptHeader* header;
   PromptItem* list;
   PromptJoin* joins;
-  int* tile_starts;             // [B + 1] items before each sequence's
-  int2* cuts;                   // per item: pieces, first partial
-  float* acc;                   // [pieces * units, part_rows, D]
+  int* cta_first;               // [grid + 1] each CTA's first piece
+  int* item_starts;             // [B] items before each sequence's
+  int* seq_entry;               // [B] its first entry in a list of whole items
+  float* acc;                   // [max_parts, part_rows, D]
   float2* ml;                   // running max (log2 units) and sum
 };
 constexpr int kPromptTile = 128;  // tokens of one tile
 constexpr int kRowTile = 128;     // rows of one stream
-constexpr int kPromptMinPiece = 4;  // tiles of a cut item's piece at least
+constexpr int kPromptWhole = 3;   // units of up to this many tiles are not cut
+constexpr int kPromptWaves = 8;   // up to this many units of work a CTA are shared out piece by piece
 cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream);
 cudaError_t launch_prompt_join(const PromptParams& p, cudaStream_t stream);
 cudaError_t launch_prompt_bf16(const PromptParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t stream);
-cudaError_t launch_prompt_simple(const PromptParams& p, KvType kv, cudaStream_t stream);
+cudaError_t launch_prompt_quant(const PromptParams& p, const CUtensorMap& tq, KvType kv, cudaStream_t stream);
 
 // Cache rows of sequences' tokens, dequantised, to packed rows (pkv_gather.cu).
 struct GatherParams {

@@ -4,10 +4,15 @@
 //     out[i][h] = sum_t softmax_t(scale * q[i][h] . K[t]) V[t]   over the tokens t that query i sees
 //
 // in up to three launches.  (1) The plan: lengths are on the device, so one CTA forms the list of
-// items there (pkv_prompt.cuh), largest first, and cuts items that are longer than a CTA's share of
-// the whole call, as a few rows behind a long context are.  (2) The pass over the items.  Pieces of a cut
-// item leave partial softmax states (running max m in log2 units, sum l, accumulator) per row, which (3) joins:
+// work there.  (2) The pass over it (pkv_prompt_tc.cuh).  (3) Where units of work were cut, their pieces'
+// partial softmax states (running max m in log2 units, sum l, accumulator) are joined, row by row:
 //     M = max_i m_i,  out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
+//
+// The list takes one of two forms.  Few units of work, or one that is large beside a CTA's share of all: a line.
+// The units in order, each as long as its tiles and a fixed cost, make one line that the CTAs share out in equal
+// stretches, so that they end together; a unit on a border is cut there.  Many units: whole items, which
+// the CTAs take one after the other, longest sequences first, so that what is left at the end is
+// small.  A sequence's items of one head unit are neighbours there, and run together on their keys and values.
 #include "pkv_decode.cuh"
 #include "pkv_prompt.cuh"
 
@@ -15,9 +20,8 @@ namespace pkv {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 1024;  // of item sizes, for the order
-constexpr int kItemCost = 2;    // an item's start and end, in tiles
-
+constexpr int kBuckets = 1024;  // of sequences' sizes, for the order
+constexpr int kUnitCost = 2;    // a unit's start and end, in tiles
 template <typename T>
 __device__ __forceinline__ T warp_scan(T v) {  // inclusive
   const int lane = threadIdx.x & 31;
@@ -71,17 +75,19 @@ __device__ __forceinline__ bool prompt_seq(const PromptParams& p, int b, PromptS
   return s.key0 >= 0 && key1 >= s.key0 && key1 <= p.num_keys;
 }
 
-// Item `at` of the call: its sequence, rows and tiles.
-__device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, int at) {
+// Item `at` of the call: its sequence, rows and tiles; `index` of the sequence's `count`.
+__device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, int at, int items, int& index) {
   int lo = 0, hi = p.num_seqs;
   while (hi - lo > 1) {  // the last sequence whose items start at or before this one
     const int mid = (lo + hi) >> 1;
-    if (p.tile_starts[mid] <= at) lo = mid; else hi = mid;
+    if (p.item_starts[mid] <= at) lo = mid; else hi = mid;
   }
   PromptSeq s;
   bool bad;
   prompt_seq(p, lo, s, bad);
-  const int per = 2 * p.stream_tokens, tok0 = (at - p.tile_starts[lo]) * per;
+  const int per = 2 * p.stream_tokens, start = p.item_starts[lo];
+  index = at - start;
+  const int tok0 = index * per;
   PromptItem x{};
   x.seq = lo;
   x.row0 = s.row0 + tok0;
@@ -89,20 +95,44 @@ __device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, int at)
   x.pos0 = s.len - s.n + tok0;
   x.len = s.len;
   x.key0 = s.key0;
-  x.shared = s.n > per;
+  x.part = -1;
+  x.count = (lo + 1 < p.num_seqs ? p.item_starts[lo + 1] : items) - start;
+  x.shared = x.count > 1;
   span_tiles(prompt_span(p, x.pos0, x.pos0 + x.ntok - 1, s.len), x.tile0, x.tiles);
   return x;
+}
+
+// CTA c's stretch of a line of `total` places starts here; the CTA whose stretch holds place w.
+__device__ __forceinline__ int64_t line_start(int64_t total, int ctas, int c) { return total * c / ctas; }
+__device__ __forceinline__ int line_owner(int64_t total, int ctas, int64_t w) { return int(((w + 1) * ctas - 1) / total); }
+
+// A unit's pieces along the line: f(CTA, first tile, tiles) for each that has tiles, or once for a unit that has none.
+template <typename F>
+__device__ __forceinline__ void line_pieces(int64_t total, int ctas, int64_t at, int tiles, F&& f) {
+  const int cost = tiles + kUnitCost;
+  if (tiles <= kPromptWhole) {
+    f(line_owner(total, ctas, at + cost / 2), 0, tiles);
+    return;
+  }
+  const int c1 = line_owner(total, ctas, at + cost - 1);
+  for (int c = line_owner(total, ctas, at), t = 0; c <= c1; ++c) {
+    const int end = c == c1 ? tiles : int(max(line_start(total, ctas, c + 1) - at - kUnitCost, int64_t(0)));
+    if (end > t) {
+      f(c, t, end - t);
+      t = end;
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptParams p) {
   __shared__ int part[32];
   __shared__ int64_t part64[32];
-  __shared__ int hist[kBuckets];
-  __shared__ int s_most, s_parts, s_joins;
+  __shared__ int hist[kBuckets];  // sequences' sizes, or the CTAs' pieces
+  __shared__ int s_most, s_joins;
   const int tid = threadIdx.x;
   griddep_wait();
   griddep_launch_dependents();
-  if (tid == 0) s_most = s_parts = s_joins = 0;
+  if (tid == 0) s_most = s_joins = 0;
   hist[tid] = 0;
   // items of each sequence
   int items = 0;
@@ -120,7 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
     }
     int all;
     const int before = block_scan(n, part, all);
-    if (b < p.num_seqs) p.tile_starts[b] = items + before;
+    if (b < p.num_seqs) p.item_starts[b] = items + before;
     items += all;
   }
   if (!__syncthreads_and(ok)) {
@@ -132,10 +162,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
   }
   // the whole call's tiles, and the largest item's
   int64_t sum = 0;
-  int most = 0;
+  int most = 0, index;
   for (int i = tid; i < items; i += kPlanThreads) {
-    const int t = prompt_item(p, i).tiles;
-    sum += t + kItemCost;
+    const int t = prompt_item(p, i, items, index).tiles;
+    sum += t + kUnitCost;
     most = max(most, t);
   }
   int64_t total;
@@ -143,44 +173,79 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
   atomicMax(&s_most, most);
   __syncthreads();
   most = s_most;
-  // Items longer than a CTA's share are cut into equal pieces.
-  const int64_t share = (total * p.units + p.grid - 1) / p.grid;
-  const int limit = p.max_pieces > 0 ? int(min(max(share - kItemCost, int64_t(kPromptMinPiece)), int64_t(INT_MAX))) : INT_MAX;
-  most = min(most, limit);
-  auto bucket = [&](int tiles) { return kBuckets - 1 - int(int64_t(min(tiles, most)) * (kBuckets - 1) / max(most, 1)); };
-  for (int i = tid; i < items; i += kPlanThreads) {
-    const PromptItem x = prompt_item(p, i);
-    int2 cut = make_int2(1, -1);
-    if (x.tiles > limit) {
-      const int pieces = (x.tiles + limit - 1) / limit;
-      const int at = atomicAdd(&s_parts, pieces);
-      if (at + pieces <= p.max_pieces) {
-        cut = make_int2(pieces, at);
-        p.joins[atomicAdd(&s_joins, 1)] = PromptJoin{x.row0, x.ntok, at, pieces};
+  total *= p.units;
+  const int work = items * p.units;
+  const bool line = work <= kPromptWaves * p.grid || int64_t(most) * kPromptWaves > total / p.grid;
+  if (line) {
+    const int ctas = int(min(total, int64_t(p.grid)));
+    int64_t line0 = 0;
+    int entry0 = 0, part0 = 0;
+    for (int w0 = 0; w0 < work; w0 += kPlanThreads) {
+      // in order: sequences, their head units, their items
+      const int w = w0 + tid;
+      PromptItem x{};
+      int pieces = 0;
+      if (w < work) {
+        x = prompt_item(p, w / p.units, items, index);
+        const int in_seq = w - (w / p.units - index) * p.units, unit = in_seq / x.count;
+        x = prompt_item(p, w / p.units - index + in_seq - unit * x.count, items, index);
+        x.unit = unit;
+      }
+      int64_t all64;
+      const int64_t at = line0 + block_scan(int64_t(w < work ? x.tiles + kUnitCost : 0), part64, all64);
+      if (w < work)
+        line_pieces(total, ctas, at, x.tiles, [&](int c, int, int) {
+          atomicAdd(&hist[c], 1);
+          ++pieces;
+        });
+      int all_entries, all_parts;
+      int entry = entry0 + block_scan(pieces, part, all_entries);
+      const int first = part0 + block_scan(pieces > 1 ? pieces : 0, part, all_parts);
+      if (w < work) {
+        const int tile0 = x.tile0, tiles = x.tiles;
+        int to = first;
+        line_pieces(total, ctas, at, tiles, [&](int, int t, int n) {
+          x.tile0 = tile0 + t;
+          x.tiles = n;
+          x.part = pieces > 1 ? to++ : -1;
+          p.list[entry++] = x;
+        });
+        if (pieces > 1) p.joins[atomicAdd(&s_joins, 1)] = PromptJoin{x.row0, x.ntok, x.unit, first, pieces};
+      }
+      line0 += all64;
+      entry0 += all_entries;
+      part0 += all_parts;
+    }
+    __syncthreads();
+    int all;
+    const int before = block_scan(hist[tid], part, all);
+    if (tid <= p.grid) p.cta_first[tid] = before;
+  } else {
+    // sequences by the tiles of their last item, largest first
+    auto bucket = [&](int tiles) { return kBuckets - 1 - int(int64_t(tiles) * (kBuckets - 1) / max(most, 1)); };
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int b = tid; b < p.num_seqs; b += kPlanThreads) {
+        const int n = (b + 1 < p.num_seqs ? p.item_starts[b + 1] : items) - p.item_starts[b];
+        if (n == 0) continue;
+        int* at = &hist[bucket(prompt_item(p, p.item_starts[b] + n - 1, items, index).tiles)];
+        if (pass == 0) atomicAdd(at, n);
+        else p.seq_entry[b] = atomicAdd(at, n);
+      }
+      __syncthreads();
+      if (pass == 0) {
+        int all;
+        const int before = block_scan(hist[tid], part, all);
+        hist[tid] = before;
+        __syncthreads();
       }
     }
-    p.cuts[i] = cut;
-    atomicAdd(&hist[bucket((x.tiles + cut.x - 1) / cut.x)], cut.x);
-  }
-  __syncthreads();
-  int all;
-  const int before = block_scan(hist[tid], part, all);
-  hist[tid] = before;
-  __syncthreads();
-  for (int i = tid; i < items; i += kPlanThreads) {
-    PromptItem x = prompt_item(p, i);
-    const int2 cut = p.cuts[i];
-    const int tile0 = x.tile0, tiles = x.tiles;
-    int at = atomicAdd(&hist[bucket((tiles + cut.x - 1) / cut.x)], cut.x);
-    for (int j = 0; j < cut.x; ++j) {
-      const int t0 = int(int64_t(tiles) * j / cut.x), t1 = int(int64_t(tiles) * (j + 1) / cut.x);
-      x.tile0 = tile0 + t0;
-      x.tiles = t1 - t0;
-      x.part = cut.y < 0 ? -1 : cut.y + j;
-      p.list[at++] = x;
+    for (int i = tid; i < items; i += kPlanThreads) {
+      PromptItem x = prompt_item(p, i, items, index);
+      x.unit = p.seq_entry[x.seq];
+      p.list[x.unit + x.count - 1 - index] = x;
     }
   }
-  if (tid == 0) *p.header = PromptHeader{0u, all, s_joins, 0};
+  if (tid == 0) *p.header = PromptHeader{0u, line, items, s_joins};
 }
 
 // Join the pieces' states of cut items: a warp per row, a lane to D / 32 consecutive values.
@@ -191,17 +256,15 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) 
   const int lane = threadIdx.x & 31;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t rows = int64_t(p.header->joins) * p.units * p.part_rows;
+  const int64_t rows = int64_t(p.header->joins) * p.part_rows;
   const int64_t warps = int64_t(gridDim.x) * (blockDim.x / 32);
   for (int64_t w = int64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5); w < rows; w += warps) {
-    const int64_t ju = w / p.part_rows;
-    const int r = int(w - ju * p.part_rows);
-    const int j = int(ju / p.units), unit = int(ju - int64_t(j) * p.units);
+    const int j = int(w / p.part_rows), r = int(w - int64_t(j) * p.part_rows);
     const PromptJoin x = p.joins[j];
     const int tok = r / p.heads, h = r - tok * p.heads;
-    const int kvh = unit / p.chunks, head = (unit - kvh * p.chunks) * p.heads + h;
+    const int kvh = x.unit / p.chunks, head = (x.unit - kvh * p.chunks) * p.heads + h;
     if (tok >= x.ntok || head >= p.group) continue;
-    auto row = [&](int i) { return (int64_t(x.part + i) * p.units + unit) * p.part_rows + r; };
+    auto row = [&](int i) { return int64_t(x.part + i) * p.part_rows + r; };
     float M = kMaxFloor;
     for (int i = lane; i < x.parts; i += 32) M = fmaxf(M, p.ml[row(i)].x);
 #pragma unroll
@@ -226,106 +289,6 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) 
   }
 }
 
-// The pass over the items, one warp to a row: a lane to a token of 32 for the logits, to D / 32
-// values for the sums.
-template <KvType KV, int D, bool kPaged>
-__global__ void __launch_bounds__(256) prompt_simple_kernel(const PromptParams p) {
-  constexpr int kDPV = D / 32;
-  constexpr uint32_t kAll = 0xffffffffu;
-  __shared__ float qs[8][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int total = p.header->items * p.units;
-  auto value = [&](const void* base, const float* scale, int64_t row, int c) -> float {
-    if constexpr (KV == KvType::kBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[row * D + c]);
-    if constexpr (KV == KvType::kInt8) return scale[row] * float(static_cast<const int8_t*>(base)[row * D + c]);
-    uint32_t lo, hi;
-    f16x2x2_from_e4m3x4(static_cast<const uint8_t*>(base)[row * D + c], lo, hi);
-    return scale[row] * __half2float(__ushort_as_half(uint16_t(lo & 0xffffu)));
-  };
-  for (int w = blockIdx.x; w < total; w += gridDim.x) {
-    const PromptItem x = p.list[w / p.units];
-    const int unit = w % p.units, kvh = unit / p.chunks, chunk = unit - kvh * p.chunks;
-    for (int r = warp; r < x.ntok * p.heads; r += 8) {
-      const int tok = r / p.heads, head = chunk * p.heads + r - tok * p.heads;
-      if (head >= p.group) continue;
-      const auto* q = static_cast<const __nv_bfloat16*>(p.q) + int64_t(x.row0 + tok) * p.q_stride +
-                      (int64_t(kvh) * p.group + head) * D;
-      __syncwarp();
-      for (int c = lane; c < D; c += 32) qs[warp][c] = __bfloat162float(q[c]);
-      __syncwarp();
-      const PromptSpan span = prompt_span(p, x.pos0 + tok, x.pos0 + tok, x.len);
-      const int lo = max(span.lo, x.tile0 * kPromptTile), hi = min(span.hi, (x.tile0 + x.tiles) * kPromptTile);
-      float m = kMaxFloor, l = 0.0f, acc[kDPV] = {};
-      for (int t0 = lo / 32 * 32; t0 < hi; t0 += 32) {
-        const int t = t0 + lane;
-        // row of the token's K and V (in units of head_dim values); -1: not there
-        int64_t row = -1;
-        if (t >= lo && t < hi) {
-          if constexpr (kPaged) {
-            const int id = p.block_tables[int64_t(x.seq) * p.max_blocks_per_seq + t / kBlockSize];
-            if (id < 0 || id >= p.num_blocks) set_error(p.err, kErrBlockId);
-            else row = (int64_t(id) * p.kv_heads + kvh) * kBlockSize + t % kBlockSize;
-          } else {
-            row = t;
-          }
-        }
-        float y = -INFINITY;
-        if (row >= 0) {
-          float dot = 0.0f;
-          for (int c = 0; c < D; ++c) {
-            float k;
-            if constexpr (kPaged) k = value(p.k_cache, p.k_scale, row, c);
-            else k = __bfloat162float(static_cast<const __nv_bfloat16*>(p.k)[(x.key0 + row) * p.k_stride + kvh * D + c]);
-            dot = fmaf(qs[warp][c], k, dot);
-          }
-          y = dot * p.scale_log2;
-        }
-        float mx = y;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
-        const float m2 = fmaxf(m, mx), f = exp2f(m - m2), e = row >= 0 ? exp2f(y - m2) : 0.0f;
-        m = m2;
-        l = l * f + e;
-#pragma unroll
-        for (int i = 0; i < kDPV; ++i) acc[i] *= f;
-        for (int j = 0; j < 32; ++j) {
-          const int64_t rj = __shfl_sync(kAll, row, j);
-          const float ej = __shfl_sync(kAll, e, j);
-          if (rj < 0) continue;
-#pragma unroll
-          for (int i = 0; i < kDPV; ++i) {
-            const int c = lane * kDPV + i;
-            float v;
-            if constexpr (kPaged) v = value(p.v_cache, p.v_scale, rj, c);
-            else v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v)[(x.key0 + rj) * p.v_stride + kvh * D + c]);
-            acc[i] = fmaf(ej, v, acc[i]);
-          }
-        }
-      }
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
-      if (x.part >= 0) {
-        const int64_t at = (int64_t(x.part) * p.units + unit) * p.part_rows + r;
-        for (int i = 0; i < kDPV; ++i) p.acc[at * D + lane * kDPV + i] = acc[i];
-        if (lane == 0) p.ml[at] = make_float2(m, l);
-        continue;
-      }
-      auto* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(x.row0 + tok) * p.out_stride +
-                  (int64_t(kvh) * p.group + head) * D;
-      for (int i = 0; i < kDPV; ++i) out[lane * kDPV + i] = __float2bfloat16_rn(l == 0.0f ? 0.0f : acc[i] / l);
-    }
-  }
-}
-
-template <KvType KV, bool kPaged>
-cudaError_t launch_simple(const PromptParams& p, cudaStream_t stream) {
-  const dim3 grid(p.grid * 4);
-  if (p.head_dim == 128) return launch_pdl(prompt_simple_kernel<KV, 128, kPaged>, grid, dim3(256), 0, stream, p);
-  return launch_pdl(prompt_simple_kernel<KV, 64, kPaged>, grid, dim3(256), 0, stream, p);
-}
-
 }  // namespace
 
 cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream) {
@@ -336,13 +299,6 @@ cudaError_t launch_prompt_join(const PromptParams& p, cudaStream_t stream) {
   const dim3 grid(unsigned(p.grid) * 4);
   if (p.head_dim == 128) return launch_pdl(prompt_join_kernel<128>, grid, dim3(256), 0, stream, p);
   return launch_pdl(prompt_join_kernel<64>, grid, dim3(256), 0, stream, p);
-}
-
-cudaError_t launch_prompt_simple(const PromptParams& p, KvType kv, cudaStream_t stream) {
-  if (!p.paged) return launch_simple<KvType::kBf16, false>(p, stream);
-  return kv == KvType::kBf16  ? launch_simple<KvType::kBf16, true>(p, stream)
-         : kv == KvType::kInt8 ? launch_simple<KvType::kInt8, true>(p, stream)
-                               : launch_simple<KvType::kFp8, true>(p, stream);
 }
 
 }  // namespace pkv

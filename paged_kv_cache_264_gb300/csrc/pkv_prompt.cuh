@@ -2,17 +2,17 @@
 //
 // Sequence b has n_b query tokens, the last n_b of its T_b tokens (packed calls: T_b keys of its
 // own); query i is at position T_b - n_b + i.  A kv head's group of query heads is served in
-// `chunks` of `heads` heads; a row of a chunk is one (token, head), token-major, and an item is up
-// to 2 * kRowTile rows of consecutive tokens of one sequence, in two streams of stream_tokens
-// tokens each, with the range of 128-token tiles that some of its rows sees.  Items are the same for every kv head and chunk, so
-// the list holds them once and work unit w is item w / units, head unit w % units.
+// `chunks` of `heads` heads, each a head unit; a row of a unit is one (token, head), token-major.  An item is
+// up to 2 * stream_tokens consecutive tokens of one sequence, whose rows form two streams of up to kRowTile, and
+// the 128-token tiles that some of its tokens sees.  A unit of work is an item and a head unit; a piece some of its
+// tiles, which leaves a partial softmax state per row.
 #pragma once
 
 #include "pkv_device.cuh"
 
 namespace pkv {
 
-// Tokens that a query at position pos sees: [lo, hi).
+// Tokens that queries at positions first_pos to last_pos see: [lo, hi).
 struct PromptSpan {
   int lo, hi;
 };

@@ -1,5 +1,5 @@
-// pkv_prompt_tc.cuh -- the pass over prompt attention's items on the fifth-generation tensor core: a
-// CTA per SM takes work units (an item and a head unit, pkv_prompt.cuh) off the list until it is empty.
+// pkv_prompt_tc.cuh -- the pass over prompt attention's work on the fifth-generation tensor core: a CTA
+// per SM takes pieces of work (pkv_prompt.cuh), its own of the line or whole units off the list.
 //
 // Two streams of up to 128 query rows run through the CTA, one under the other.  Per stream and tile of 128 tokens:
 //     S = Q K^T    128 x 128 x D, both operands in shared memory, S in tensor memory (fp32)
@@ -7,20 +7,27 @@
 //     O += P V     128 x D x 128, P in tensor memory (bf16, over S's columns), V as it lies in memory
 //                  (token-major, the contracted index outermost: an MN-major operand)
 // One warp issues all products, stream by stream: O of a tile, then S of the next, so that the tensor pipe works
-// on one stream while the other's softmax runs.  Products complete in order, so S may be written over P behind the product that
-// reads it, and a softmax that has its S knows that O is at rest: it rescales O itself where it
-// has to.  That is rare, for the running maximum is lazy (kMaxSlack): it moves only when a row's logits pass it by
-// 2^8.  The weights enter the product over V as bf16, which the product's other operand sets (2^-8 of each at
-// most, as in the paged decode); the softmax sum is over the unrounded ones.
+// on one stream while the other's softmax runs.  Products complete in order, so S may be written over P behind the
+// product that reads it, and a softmax that has its S knows that O is at rest: it rescales O itself where it has to.
+// That is rare, for the running maximum is lazy (kMaxSlack): it moves only when a row's logits pass it by 2^8.  The
+// weights enter the product over V as bf16, which the product's other operand sets (2^-8 of each at most, as in the
+// paged decode); the softmax sum is over the unrounded ones.
 //
-// Warps: a warpgroup of softmax per stream; one that turns finished accumulators into rows of out, so that the
-// next unit's softmax need not wait for that; one warp that takes units off the list and
-// fills Q and the ring of K and V tiles by TMA (over the cache 8 blocks to a tile, each wherever it lies in the
-// pool); one that issues the products.
+// An item of up to 128 rows has both streams hold the same rows and take every other tile; their two states are
+// joined on the way out.
 //
-// What a row does not see is masked in its logits; only tiles that some row of the warp sees in part pay for that.  The product
-// over V takes the steps of 16 tokens that the item sees, and rows of V within those that no row of the item
-// sees are zeroed first, since a weight of 0 would not hide a NaN there.
+// INT8 and FP8 pools: two warpgroups load codes, one K's and one V's, and turn them into bf16 operand tiles, which
+// hold every INT8 and E4M3 code exactly.  The scales stay out of the operands: a token's K scale multiplies its
+// fp32 logit, and its V scale its weight before that is rounded to bf16.
+//
+// Warps: a warpgroup of softmax per stream; over bf16, one that turns finished accumulators into rows of out, so that
+// the next unit's softmax need not wait for that, and one warp that fills the rings of K and V tiles by TMA (over the
+// cache 8 blocks to a tile, each wherever it lies in the pool), which also takes pieces off the list and loads Q; over
+// codes, the softmax warps write out and the two converting warpgroups fill the rings; one warp issues the products.
+//
+// What a row does not see is masked in its logits; only tiles that some row of the warp sees in part pay for that.
+// The product over V takes the steps of 16 tokens that the item sees, and rows of V within those that no row of the
+// item sees are zeroed first, since a weight of 0 would not hide a NaN there.
 //
 // Every wait is bounded; after one that gave up the CTA takes no further work, lets its
 // copies and products land, frees its tensor memory and ends.
@@ -49,48 +56,75 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// A unit of work as the roles of a CTA see it.
+// Loads that stay where they are written: the compiler would sink plain ones to their use.
+__device__ __forceinline__ int load_now(const void* at) {
+  int v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 load_codes(const void* at) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(at));
+  return v;
+}
+
+// A piece of work as the roles of a CTA see it.
 struct PromptPiece {
   int seq, row0, ntok, pos0;  // sequence, first row of q and out, tokens, position of the first
   int len, key0;
-  int tile0, tiles;           // tiles < 0: there are no more units
+  int tile0, tiles;           // tiles < 0: there is no more work
   int lo, hi;                 // tokens that some row of the item sees
   int part, unit;
-  int first[2], count[2];     // each stream's tiles: first[s] .. first[s] + count[s] - 1 of this piece's
+  int twin;                   // both streams hold the same rows and take every other tile
+  int shared;                 // the tiles are read again by other items
+  int first[2], count[2];     // each stream's tiles, from tile0 + first[s] on
 };
 
-template <int D, bool kPaged>
+template <KvType KV, int D, bool kPaged>
 struct PromptCfg {
+  static constexpr bool kQuant = KvTraits<KV>::kQuant;
   static constexpr int kHalves = D / 64;                       // 128-byte spans of a row
   static constexpr int kTileBytes = kPromptTile * D * 2;       // one K, V or Q tile
   static constexpr int kHalfBytes = kPromptTile * 128;         // one span of all its rows
-  static constexpr int kStages = D == 128 ? 4 : 8;
-  static constexpr int kThreads = 512;
-  static constexpr int kOutWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
-  static constexpr int kReaders = 13;                          // warps that take pieces: softmax, out, products
+  static constexpr int kK = (D == 128 ? 2 : 4), kV = (D == 128 ? (kQuant ? 2 : 3) : 4);  // stages of the rings
+  // A tile's scales are read by its softmax.  K of tile n + kSlots takes its stage once S of tile n + kSlots - kK
+  // has been formed, behind the products over V of all tiles two or more before that.
+  static constexpr int kSlots = kQuant ? (D == 128 ? 4 : 8) : 0;
+  static_assert(!kQuant || kSlots >= kK + 2, "a scale slot is free when it is written again");
+  static constexpr int kThreads = kQuant ? 640 : 512;
+  // first warps: of the writers of out, or of the two converting warpgroups (K's and V's); of the others
+  static constexpr int kOutWarp = 8, kConvertWarp = 8, kMmaWarp = kQuant ? 16 : 12, kLoadWarp = kMmaWarp + 1;
+  static constexpr int kReaders = kMmaWarp + 1;                // warps that take pieces
+  // Registers a thread: the launch's, shared out anew by warpgroup.
+  static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 160 : 184, kSideRegs = kQuant ? 56 : 88,
+                       kLoadRegs = kQuant ? 40 : 56;
+  static_assert(2 * kSoftmaxRegs + (kQuant ? 2 : 1) * kSideRegs + kLoadRegs <= kThreads / 128 * kRegs, "registers");
   static constexpr int kRingOff = 2 * kTileBytes;              // Q tiles of both streams first
-  static constexpr int kStageOff = kRingOff + kStages * kTileBytes;  // rows on their way out: 4 KB a warp
-  static constexpr int kMiscOff = kStageOff + 4 * 4096;
+  static constexpr int kVOff = kRingOff + kK * kTileBytes;
+  static constexpr int kSlotOff = kVOff + kV * kTileBytes;     // float [kSlots][2][128]: K's and V's scales
+  static constexpr int kMiscOff = kSlotOff + kSlots * 1024;
   static constexpr int kStatOff = kMiscOff + 1024;             // float2 [2][128]: running max and sum
   static constexpr int kSmemBytes = kStatOff + 2 * 128 * 8;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 };
 
-constexpr int kPieceQueue = 2;   // units handed out ahead
-constexpr int kTileMasks = 16;   // tiles whose masks are kept: more than the ring holds
+constexpr int kPieceQueue = 2;   // pieces handed out
+constexpr int kTileMasks = 16;   // tiles whose masks are kept: more than the rings hold
 
 // Barriers and flags of one CTA.
 struct PromptSync {
-  uint64_t full[8], empty[8];      // ring stages
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];  // ring stages
   uint64_t q_full[2], q_empty[2];  // per stream from here
   uint64_t s_ready[2], p_ready[2];
   uint64_t o_ready[2], o_free[2];
   uint64_t stat_ready[2];
-  uint64_t drain;
+  uint64_t drain, late;
   uint64_t piece_full[kPieceQueue], piece_empty[kPieceQueue];
   PromptPiece piece[kPieceQueue];
-  uint8_t mask[kTileMasks];        // which of a tile's blocks exist, by tile in load order
+  uint32_t mask[kTileMasks];       // which of a tile's blocks exist, by tile in load order: two to a byte
   uint32_t tmem;
   uint32_t abort;
 };
@@ -107,13 +141,6 @@ struct RingAt {  // a place in a ring of N stages: the stage, and the parity of 
   }
 };
 
-// A load that stays where it is written: the compiler would sink a plain one to its use.
-__device__ __forceinline__ int load_now(const void* at) {
-  int v;
-  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
-  return v;
-}
-
 // Bits [lo, hi) of a word.
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   const uint32_t below_hi = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u;
@@ -121,23 +148,30 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   return below_hi & ~below_lo;
 }
 
-template <int D, bool kPaged>
-__global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
+// Bit j: block j of a tile, from the word that holds two to a byte.
+constexpr uint32_t kAllBlocks = 0x03030303u;
+__device__ __forceinline__ uint32_t tile_mask(uint32_t w) { return (w | w >> 6 | w >> 12 | w >> 18) & 0xffu; }
+
+template <KvType KV, int D, bool kPaged>
+__global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, const PromptParams p) {
-  using C = PromptCfg<D, kPaged>;
-  constexpr int S = C::kStages;
+  using C = PromptCfg<KV, D, kPaged>;
   constexpr uint32_t kAll = 0xffffffffu;
   extern __shared__ __align__(1024) unsigned char smem[];  // the swizzled tiles need its alignment
   auto* sy = reinterpret_cast<PromptSync*>(smem + C::kMiscOff);
   auto* stats = reinterpret_cast<float2*>(smem + C::kStatOff);
-  unsigned char* ring = smem + C::kRingOff;
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(sy->full + i, 1);
-      mbar_init(sy->empty + i, 1);
+    constexpr int kFillers = C::kQuant ? 4 : 1;
+    for (int i = 0; i < C::kK; ++i) {
+      mbar_init(sy->k_full + i, kFillers);
+      mbar_init(sy->k_empty + i, 1);
+    }
+    for (int i = 0; i < C::kV; ++i) {
+      mbar_init(sy->v_full + i, kFillers);
+      mbar_init(sy->v_empty + i, 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(sy->q_full + s, 1);
@@ -149,6 +183,7 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
       mbar_init(sy->stat_ready + s, 4);
     }
     mbar_init(&sy->drain, 1);
+    mbar_init(&sy->late, 1);
     for (int i = 0; i < kPieceQueue; ++i) {
       mbar_init(sy->piece_full + i, 1);
       mbar_init(sy->piece_empty + i, C::kReaders);
@@ -156,8 +191,10 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
     sy->abort = 0;
     fence_barrier_init();
     prefetch_tensor_map(&tmap_q);
-    prefetch_tensor_map(&tmap_k);
-    prefetch_tensor_map(&tmap_v);
+    if constexpr (!C::kQuant) {
+      prefetch_tensor_map(&tmap_k);
+      prefetch_tensor_map(&tmap_v);
+    }
   }
   if (warp == C::kMmaWarp) tmem_alloc(&sy->tmem, C::kTmemCols);
   if (threadIdx.x == 0 && (smem_addr(smem) & 1023u)) set_error(p.err, kErrTimeout);  // never: the only shared memory
@@ -192,33 +229,113 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
     if (lane == 0) mbar_arrive(sy->piece_empty + queue.st);
     queue.next();
   };
-  // Tokens of stream s in an item.
-  auto stream_tokens = [&](const PromptPiece& x, int s) { return max(0, min(p.stream_tokens, x.ntok - s * p.stream_tokens)); };
+  // First token and tokens of stream s in an item.
+  auto stream_first = [&](const PromptPiece& x, int s) { return x.twin ? 0 : s * p.stream_tokens; };
+  auto stream_tokens = [&](const PromptPiece& x, int s) { return max(0, min(p.stream_tokens, x.ntok - stream_first(x, s))); };
 
-  if (warp >= 12) {
-    regs_fewer<56>();
+  // Finished rows of stream s (of both streams, where they hold the same): a thread to a row, run by the four
+  // warps of a warpgroup.  used0, used1: the parities of the streams' accumulators of this piece.
+  [[maybe_unused]] auto write_out = [&](const PromptPiece& x, int s, int wq, uint32_t used0, uint32_t used1) {
+    const uint32_t used = s ? used1 : used0;
+    const bool any = x.count[s] > 0, both = x.twin != 0;
+    const int r = wq * 32 + lane, tok = r / p.heads;
+    const int kvh = x.unit / p.chunks, h = (x.unit - kvh * p.chunks) * p.heads + r - tok * p.heads;
+    const int tok0 = stream_first(x, s);
+    const bool live = tok < stream_tokens(x, s) && h < p.group;
+    const uint32_t o_addr = tmem + (uint32_t(wq) << 21) + 256 + s * D;
+    float m = kMaxFloor, l = 0.0f, f0 = 1.0f, f1 = 0.0f;  // the state, and the streams' shares of it
+    bool on0 = false, on1 = false;                        // a state without a weight may have no accumulator
+    if (any) {
+      if (!wait_all(sy->stat_ready + s, used) || !wait_all(sy->o_ready + s, used)) return false;
+      if (both && (!wait_all(sy->stat_ready + 1, used1) || !wait_all(sy->o_ready + 1, used1))) return false;
+      tc_fence_after();
+      const float2 a = stats[s * 128 + r];
+      m = a.x;
+      l = a.y;
+      on0 = a.y != 0.0f;
+      if (both) {
+        const float2 b = stats[128 + r];
+        on1 = b.y != 0.0f;
+        m = fmaxf(a.x, b.x);
+        f0 = fast_exp2(a.x - m);
+        f1 = fast_exp2(b.x - m);
+        l = (on0 ? f0 * a.y : 0.0f) + (on1 ? f1 * b.y : 0.0f);
+      }
+    }
+    const int64_t part = x.part >= 0 ? int64_t(x.part) * p.part_rows + tok0 * p.heads + r : 0;
+    if (x.part >= 0 && live) p.ml[part] = make_float2(m, l);
+    const float inv = x.part >= 0 ? 1.0f : 1.0f / l;
+    f0 *= inv;
+    f1 *= inv;
+    float* acc = p.acc + part * D;
+    auto* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(x.row0 + tok0 + tok) * p.out_stride + (int64_t(kvh) * p.group + h) * D;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 16) {
+      float o[16];
+      if (any) {
+        tmem_ld16(o_addr + c0, o);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = on0 ? o[e] * f0 : 0.0f;
+      if (both) {
+        float o1[16];
+        tmem_ld16(o_addr + D + c0, o1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = on1 ? fmaf(o1[e], f1, o[e]) : o[e];
+      }
+      if (live && x.part >= 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) reinterpret_cast<float4*>(acc + c0)[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+      } else if (live) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          reinterpret_cast<uint4*>(out + c0)[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                                             pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (any && lane == 0) {
+      mbar_arrive(sy->o_free + s);
+      if (both) mbar_arrive(sy->o_free + 1);
+    }
+    return true;
+  };
+
+  if (warp >= C::kMmaWarp) {
+    regs_fewer<C::kLoadRegs>();
     if (warp == C::kLoadWarp) {
-      // ---------------------------------------------------------------- units, Q, K and V tiles
+      // ---------------------------------------------------------------- pieces, Q, and over bf16 K and V tiles
       // The whole warp runs this with warp-uniform values; one elected lane issues.
-      const int64_t total = int64_t(load_now(&p.header->items)) * p.units;
+      const bool line = load_now(&p.header->line) != 0;
+      const int end = line ? load_now(p.cta_first + blockIdx.x + 1) : load_now(&p.header->items) * p.units;
       const uint64_t once = l2_evict_first_policy(), again = l2_evict_last_policy();
-      RingAt<S> at;
-      uint32_t filled = 0, put = 0, tiles = 0;
-      uint32_t q_used[2] = {0, 0};
-      int64_t w = blockIdx.x;
-      unsigned ticket = 0;
-      // an int of the list's entry to a lane
+      [[maybe_unused]] RingAt<C::kK> kr;
+      [[maybe_unused]] RingAt<C::kV> vr;
+      [[maybe_unused]] uint32_t k_filled = 0, v_filled = 0, tiles = 0;
+      uint32_t put = 0, q_used[2] = {0, 0};
+      // an int of a list entry to a lane: entry w of the CTA's own, or unit of work w of the list of whole items
       static_assert(sizeof(PromptItem) == 48, "12 ints");
-      auto fetch = [&](int64_t unit_of_work) {
-        const int* entry = reinterpret_cast<const int*>(p.list + unit_of_work / p.units);
-        return unit_of_work < total && lane < 12 ? load_now(entry + lane) : 0;
+      int w = line ? load_now(p.cta_first + blockIdx.x) : blockIdx.x;
+      auto fetch = [&](int w) {
+        if (w >= end) return 0;
+        const auto* at = reinterpret_cast<const int*>(p.list + (line ? w : w / p.units));
+        int e = lane < 12 ? load_now(at + lane) : 0;
+        if (line) return e;
+        // some entry of the sequence: its units of work are those of a head unit after the other
+        const int first = __shfl_sync(kAll, e, 10), count = __shfl_sync(kAll, e, 11);
+        const int in_seq = w - first * p.units, unit = in_seq / count, index = first + in_seq - unit * count;
+        if (index != w / p.units) e = lane < 12 ? load_now(reinterpret_cast<const int*>(p.list + index) + lane) : 0;
+        return lane == 10 ? unit : e;
       };
       int entry = fetch(w);
       for (;;) {
         PromptPiece x;
         x.tiles = -1;
-        bool shared = false;  // the tiles are read again by the sequence's other items
-        if (w < total) {
+        if (w < end) {
           x.seq = __shfl_sync(kAll, entry, 0);
           x.row0 = __shfl_sync(kAll, entry, 1);
           x.ntok = __shfl_sync(kAll, entry, 2);
@@ -228,8 +345,9 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
           x.tile0 = __shfl_sync(kAll, entry, 6);
           x.tiles = __shfl_sync(kAll, entry, 7);
           x.part = __shfl_sync(kAll, entry, 8);
-          shared = __shfl_sync(kAll, entry, 9) != 0;
-          x.unit = int(w % p.units);
+          x.shared = __shfl_sync(kAll, entry, 9);
+          x.unit = __shfl_sync(kAll, entry, 10);
+          x.twin = x.ntok <= p.stream_tokens && x.tiles > 1;
           const PromptSpan span = prompt_span(p, x.pos0, x.pos0 + x.ntok - 1, x.len);
           x.lo = span.lo;
           x.hi = span.hi;
@@ -239,8 +357,8 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
             int f, c;
             span_tiles(prompt_span(p, pos, pos + n - 1, x.len), f, c);
             const int a = max(f, x.tile0), b = min(f + c, x.tile0 + x.tiles);
-            x.first[s] = a;
-            x.count[s] = n > 0 ? max(0, b - a) : 0;
+            x.first[s] = x.twin ? s : a - x.tile0;
+            x.count[s] = x.twin ? (x.tiles + 1 - s) >> 1 : n > 0 ? max(0, b - a) : 0;
           }
         }
         if (put >= kPieceQueue && !wait_all(sy->piece_empty + queue.st, queue.ph ^ 1u)) {
@@ -256,105 +374,142 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
         ++put;
         if (x.tiles < 0) break;
         const int kvh = x.unit / p.chunks, head = kvh * p.group + (x.unit - kvh * p.chunks) * p.heads;
-        const uint64_t policy = shared ? again : once;
-        const int32_t* table = kPaged ? p.block_tables + int64_t(x.seq) * p.max_blocks_per_seq : nullptr;
-        // Blocks lane % 8 of a tile, asked for a tile ahead.  Only those that hold a token of the item's are read.
-        const int blk0 = x.lo / kBlockSize, blk1 = (x.hi + kBlockSize - 1) / kBlockSize;
-        auto tile_id = [&](int tile) {
-          const int b = tile * (kPromptTile / kBlockSize) + (lane & 7);
-          return b >= blk0 && b < blk1 ? load_now(table + b) : -1;
-        };
-        int next = 0, ids = 0;
-        if (kPaged && x.tiles > 0) next = tile_id(x.tile0);
-        uint32_t have = 0xffu;
-        int64_t w_next = total;
-#pragma unroll 1
-        for (int i = 0; i < 2 * x.tiles && alive; ++i) {
-          const int tile = x.tile0 + (i >> 1);
-          const bool is_v = i & 1;
-          // the next unit: taken late, so that it goes to a CTA that will be free for it
-          if (i == max(0, 2 * x.tiles - 4) && lane == 0) ticket = atomicAdd(&p.header->ticket, 1u);
-          if (kPaged && !is_v) {
-            ids = next;
-            const int b = tile * (kPromptTile / kBlockSize) + (lane & 7);
-            const bool wanted = b >= blk0 && b < blk1, ok = wanted && ids >= 0 && ids < p.num_blocks;
-            if (wanted && !ok && lane < 8) set_error(p.err, kErrBlockId);
-            have = __ballot_sync(kAll, ok) & 0xffu;
-            if ((i >> 1) + 1 < x.tiles) next = tile_id(tile + 1);
-          }
-          if (filled >= S && !wait_all(sy->empty + at.st, at.ph ^ 1u)) {
-            alive = false;
-            break;
-          }
-          const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
-          unsigned char* dst = ring + at.st * C::kTileBytes;
-          uint64_t* bar = sy->full + at.st;
-          if constexpr (kPaged) {
-            int row[8];
+        auto load_q = [&]() {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) row[j] = (__shfl_sync(kAll, ids, j) * p.kv_heads + kvh) * kBlockSize;  // pools with tensor maps have < 2^31 rows
+          for (int s = 0; s < 2; ++s) {
+            if (x.count[s] == 0) continue;
+            if (q_used[s] > 0 && !wait_all(sy->q_empty + s, (q_used[s] - 1) & 1)) {
+              alive = false;
+              return;
+            }
+            ++q_used[s];
             if (elect_one()) {
-              if (!is_v) sy->mask[(tiles + (i >> 1)) % kTileMasks] = uint8_t(have);  // published by the arrival
-              if (have) mbar_arrive_expect_tx(bar, __popc(have) * (C::kHalves * kBlockSize * 128));
-              else mbar_arrive(bar);
+              mbar_arrive_expect_tx(sy->q_full + s, C::kHalves * p.heads * p.stream_tokens * 128);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                if (have >> j & 1) {
+              for (int span = 0; span < C::kHalves; ++span)
+                tma_load_3d(smem + s * C::kTileBytes + span * C::kHalfBytes, &tmap_q, span * 64, head,
+                            x.row0 + stream_first(x, s), sy->q_full + s, once);
+            }
+            __syncwarp();
+          }
+        };
+        // The next piece.  Units off the list are taken late, so that each goes to a CTA that will be free for it.
+        int w_next = w + 1;
+        unsigned ticket = 0;
+        auto ask = [&]() {
+          if (!line && lane == 0) ticket = atomicAdd(&p.header->ticket, 1u);
+        };
+        auto follow = [&]() {
+          if (!line) w_next = int(min(__shfl_sync(kAll, ticket, 0), unsigned(INT_MAX / 2))) + gridDim.x;
+          entry = fetch(w_next);
+        };
+        if constexpr (C::kQuant) {
+          load_q();
+          alive = alive && wait_all(&sy->late, (put - 1) & 1);
+          if (!alive) break;
+          ask();
+          follow();
+        } else {
+          const int lead = x.twin ? 2 : 1;
+          const uint64_t policy = x.shared ? again : once;
+          const int32_t* table = kPaged ? p.block_tables + int64_t(x.seq) * p.max_blocks_per_seq : nullptr;
+          // Blocks lane % 8 of a tile, asked for a tile ahead.  Only those that hold a token of the item's are read.
+          const int blk0 = x.lo / kBlockSize, blk1 = (x.hi + kBlockSize - 1) / kBlockSize;
+          auto tile_id = [&](int tile) {
+            const int b = tile * (kPromptTile / kBlockSize) + (lane & 7);
+            return b >= blk0 && b < blk1 ? load_now(table + b) : -1;
+          };
+          // Of K's tile, and (a tile or two later) of V's: this lane's block, and which of them exist.
+          int next = kPaged && x.tiles > 0 ? tile_id(x.tile0) : 0, ids[3] = {0, 0, 0};
+          uint32_t have[3] = {0xffu, 0xffu, 0xffu};
+          auto copy = [&](const CUtensorMap* map, unsigned char* dst, uint64_t* bar, int tile, int id, uint32_t blocks) {
+            if constexpr (kPaged) {
+              int row[8];
 #pragma unroll
-                  for (int span = 0; span < C::kHalves; ++span)
-                    tma_load_2d(dst + span * C::kHalfBytes + j * (kBlockSize * 128), map, span * 64, row[j], bar, policy);
+              for (int j = 0; j < 8; ++j) row[j] = (__shfl_sync(kAll, id, j) * p.kv_heads + kvh) * kBlockSize;  // pools with tensor maps have < 2^31 rows
+              if (elect_one()) {
+                if (blocks) mbar_arrive_expect_tx(bar, __popc(blocks) * (C::kHalves * kBlockSize * 128));
+                else mbar_arrive(bar);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  if (blocks >> j & 1) {
+#pragma unroll
+                    for (int span = 0; span < C::kHalves; ++span)
+                      tma_load_2d(dst + span * C::kHalfBytes + j * (kBlockSize * 128), map, span * 64, row[j], bar, policy);
+                  }
                 }
               }
-            }
-          } else {
-            if (elect_one()) {
-              if (!is_v) sy->mask[(tiles + (i >> 1)) % kTileMasks] = 0xffu;
+            } else if (elect_one()) {
               mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
               for (int span = 0; span < C::kHalves; ++span)
                 tma_load_3d(dst + span * C::kHalfBytes, map, span * 64, kvh, x.key0 + tile * kPromptTile, bar, policy);
             }
-          }
-          __syncwarp();
-          ++filled;
-          at.next();
-          if (i == 0) {  // Q behind the first K: that need not wait for the last unit's products
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              if (x.count[s] == 0) continue;
-              if (q_used[s] > 0 && !wait_all(sy->q_empty + s, (q_used[s] - 1) & 1)) {
+            __syncwarp();
+          };
+          const int ask_at = max(-lead, x.tiles - 3 - lead), follow_at = max(-lead, x.tiles - 2 - lead);
+#pragma unroll 1
+          for (int j = -lead; j < x.tiles; ++j) {
+            if (j + lead < x.tiles) {
+              const int tile = x.tile0 + j + lead;
+              if constexpr (kPaged) {
+                ids[2] = ids[1];
+                ids[1] = ids[0];
+                ids[0] = next;
+                have[2] = have[1];
+                have[1] = have[0];
+                const int b = tile * (kPromptTile / kBlockSize) + (lane & 7);
+                const bool wanted = b >= blk0 && b < blk1, ok = wanted && next >= 0 && next < p.num_blocks;
+                if (wanted && !ok && lane < 8) set_error(p.err, kErrBlockId);
+                have[0] = __ballot_sync(kAll, ok) & 0xffu;
+                if (j + lead + 1 < x.tiles) next = tile_id(tile + 1);
+              }
+              if (k_filled >= C::kK && !wait_all(sy->k_empty + kr.st, kr.ph ^ 1u)) {
                 alive = false;
                 break;
               }
-              ++q_used[s];
-              if (elect_one()) {
-                mbar_arrive_expect_tx(sy->q_full + s, C::kHalves * p.heads * p.stream_tokens * 128);
-#pragma unroll
-                for (int span = 0; span < C::kHalves; ++span)
-                  tma_load_3d(smem + s * C::kTileBytes + span * C::kHalfBytes, &tmap_q, span * 64, head,
-                              x.row0 + s * p.stream_tokens, sy->q_full + s, once);
+              if (lane == 0) {  // published by the copy's arrival
+                const uint32_t a = have[0];
+                sy->mask[(tiles + j + lead) % kTileMasks] = (a & 3u) | (a & 0xcu) << 6 | (a & 0x30u) << 12 | (a & 0xc0u) << 18;
               }
               __syncwarp();
+              copy(&tmap_k, smem + C::kRingOff + kr.st * C::kTileBytes, sy->k_full + kr.st, tile, ids[0], have[0]);
+              ++k_filled;
+              kr.next();
+            } else if constexpr (kPaged) {  // K is through
+              ids[2] = ids[1];
+              ids[1] = ids[0];
+              have[2] = have[1];
+              have[1] = have[0];
             }
+            if (j == -lead) load_q();  // behind the first K: that need not wait for the last piece's products
+            if (!alive) break;
+            if (j == ask_at) ask();
+            if (j >= 0) {
+              if (v_filled >= C::kV && !wait_all(sy->v_empty + vr.st, vr.ph ^ 1u)) {
+                alive = false;
+                break;
+              }
+              copy(&tmap_v, smem + C::kVOff + vr.st * C::kTileBytes, sy->v_full + vr.st, x.tile0 + j, lead == 1 ? ids[1] : ids[2],
+                   lead == 1 ? have[1] : have[2]);
+              ++v_filled;
+              vr.next();
+            }
+            if (j == follow_at) follow();
           }
-          if (i == 2 * x.tiles - 2) {  // its entry, while the last tile's V is on its way
-            w_next = int64_t(__shfl_sync(kAll, ticket, 0)) + gridDim.x;
-            entry = fetch(w_next);
-          }
-        }
-        tiles += x.tiles;
-        if (!alive) break;
-        if (x.tiles == 0) {
-          if (lane == 0) ticket = atomicAdd(&p.header->ticket, 1u);
-          w_next = int64_t(__shfl_sync(kAll, ticket, 0)) + gridDim.x;
-          entry = fetch(w_next);
+          tiles += x.tiles;
+          if (!alive) break;
         }
         w = w_next;
       }
       // the copies in flight land before the CTA can end (the stages filled last, and Q)
-      for (uint32_t j = 0; j < min(filled, uint32_t(S)); ++j) {
-        const uint32_t n = filled - 1 - j;
-        (void)mbar_wait_bounded(sy->full + n % S, (n / S) & 1);
+      for (uint32_t j = 0; j < min(k_filled, uint32_t(C::kK)); ++j) {
+        const uint32_t n = k_filled - 1 - j;
+        (void)mbar_wait_bounded(sy->k_full + n % C::kK, (n / C::kK) & 1);
+      }
+      for (uint32_t j = 0; j < min(v_filled, uint32_t(C::kV)); ++j) {
+        const uint32_t n = v_filled - 1 - j;
+        (void)mbar_wait_bounded(sy->v_full + n % C::kV, (n / C::kV) & 1);
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s)
@@ -367,30 +522,30 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
       constexpr uint32_t kDescO = mma_bf16_desc(128, D, true);
       constexpr uint32_t kHi = smem_operand_hi(1024);
       const uint32_t q_desc = smem_operand(smem_addr(smem), 16);
-      const uint32_t k_desc = smem_operand(smem_addr(ring), 16), v_desc = smem_operand(smem_addr(ring), C::kHalfBytes);
-      RingAt<S> at;
+      const uint32_t k_desc = smem_operand(smem_addr(smem + C::kRingOff), 16);
+      const uint32_t v_desc = smem_operand(smem_addr(smem + C::kVOff), C::kHalfBytes);
+      RingAt<C::kK> kr;
+      RingAt<C::kV> vr;
       uint32_t tiles = 0;
-      uint32_t steps[2] = {0, 0}, units[2] = {0, 0};  // each stream's tiles and units with tiles before now
+      uint32_t steps[2] = {0, 0}, used[2] = {0, 0};  // each stream's tiles, and pieces with tiles, before now
       for (; take(); done()) {
         const PromptPiece& x = sy->piece[queue.st];
-        const int x_tiles = x.tiles, x_tile0 = x.tile0, x_lo = x.lo, x_hi = x.hi;
+        const int n = x.tiles, tile0 = x.tile0, lo0 = x.lo, hi0 = x.hi;
+        const int twin = x.twin != 0, lead = 1 + twin;
         const int first[2] = {x.first[0], x.first[1]}, count[2] = {x.count[0], x.count[1]};
-        bool fresh[2] = {true, true};  // O holds nothing of this unit yet
+        bool fresh[2] = {true, true};  // O holds nothing of this piece yet
 #pragma unroll 1
-        for (int j = -1; j < x_tiles && alive; ++j) {
-          const int tile = x_tile0 + j;
-          const uint32_t v_st = at.st;
-          uint32_t k_st = 0, vmask = 0;
+        for (int j = -lead; j < n; ++j) {
+          uint32_t vmask = 0;
           if (j >= 0) {
-            if (!(alive = wait_all(sy->full + at.st, at.ph))) break;
-            at.next();
+            if (!(alive = wait_all(sy->v_full + vr.st, vr.ph))) break;
             // steps of 16 tokens that the item sees
-            const int lo = x_lo - tile * kPromptTile, hi = x_hi - tile * kPromptTile;
-            vmask = sy->mask[(tiles + j) % kTileMasks] & bit_range(lo / 16, (hi + 15) / 16);
+            const int lo = lo0 - (tile0 + j) * kPromptTile, hi = hi0 - (tile0 + j) * kPromptTile;
+            vmask = tile_mask(sy->mask[(tiles + j) % kTileMasks]) & bit_range(lo / 16, (hi + 15) / 16);
             // within them, tokens that it does not: zero
             const int z0 = max(0, lo) & ~15, z1 = max(0, lo), z2 = min(kPromptTile, hi), z3 = min(kPromptTile, (hi + 15) & ~15);
             if (z1 > z0 || z3 > z2) {
-              unsigned char* v = ring + v_st * C::kTileBytes;
+              unsigned char* v = smem + C::kVOff + vr.st * C::kTileBytes;
               for (int c = lane; c < (z1 - z0 + z3 - z2) * 8; c += 32) {
                 const int i = c >> 3, row = i < z1 - z0 ? z0 + i : z2 + i - (z1 - z0);
 #pragma unroll
@@ -401,20 +556,19 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
               __syncwarp();
             }
           }
-          if (j + 1 < x_tiles) {
-            if (!(alive = wait_all(sy->full + at.st, at.ph))) break;
-            k_st = at.st;
-            at.next();
-          }
-          const uint32_t vd = __shfl_sync(kAll, v_desc + v_st * (C::kTileBytes >> 4), 0);
-          const uint32_t kd = __shfl_sync(kAll, k_desc + k_st * (C::kTileBytes >> 4), 0);
+          const bool has_k = j + lead < n;
+          if (has_k && !(alive = wait_all(sy->k_full + kr.st, kr.ph))) break;
+          const uint32_t vd = __shfl_sync(kAll, v_desc + vr.st * (C::kTileBytes >> 4), 0);
+          const uint32_t kd = __shfl_sync(kAll, k_desc + kr.st * (C::kTileBytes >> 4), 0);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * D;
-            const int mine = tile - first[s];  // the stream's tile whose product over V is due
-            if (mine >= 0 && mine < count[s]) {
+            const int d = j - first[s];
+            if (twin && (d & 1)) continue;  // the other stream's tile
+            const int at = d >> twin;       // the stream's tile whose product over V is due
+            if (at >= 0 && at < count[s]) {
               alive = alive && wait_all(sy->p_ready + s, steps[s] & 1);
-              if (mine == 0 && units[s] > 0) alive = alive && wait_all(sy->o_free + s, (units[s] - 1) & 1);
+              if (at == 0 && used[s] > 0) alive = alive && wait_all(sy->o_free + s, (used[s] - 1) & 1);
               if (!alive) break;
               ++steps[s];
               tc_fence_after();
@@ -432,15 +586,15 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
                       on = true;
                     }
                 }
-                if (mine == count[s] - 1) tc_commit(sy->o_ready + s);
+                if (at == count[s] - 1) tc_commit(sy->o_ready + s);
               }
               __syncwarp();
               if (vmask != 0) fresh[s] = false;
-              if (mine == count[s] - 1) ++units[s];
+              if (at == count[s] - 1) ++used[s];
             }
-            if (mine + 1 >= 0 && mine + 1 < count[s] && j + 1 < x_tiles) {
-              if (mine + 1 == 0) {
-                alive = alive && wait_all(sy->q_full + s, units[s] & 1);
+            if (at + 1 >= 0 && at + 1 < count[s]) {  // and whose logits
+              if (at + 1 == 0) {
+                alive = alive && wait_all(sy->q_full + s, used[s] & 1);
                 if (!alive) break;
               }
               tc_fence_after();
@@ -451,19 +605,21 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
                   tc_mma_ss(t_s, q_desc + s * (C::kTileBytes >> 4) + o, kd + o, kHi, desc_s, i > 0);
                 }
                 tc_commit(sy->s_ready + s);
-                if (mine + 1 == count[s] - 1) tc_commit(sy->q_empty + s);
+                if (at + 1 == count[s] - 1) tc_commit(sy->q_empty + s);
               }
               __syncwarp();
             }
           }
           if (!alive) break;
           if (elect_one()) {
-            if (j >= 0) tc_commit(sy->empty + v_st);
-            if (j + 1 < x_tiles) tc_commit(sy->empty + k_st);
+            if (j >= 0) tc_commit(sy->v_empty + vr.st);
+            if (has_k) tc_commit(sy->k_empty + kr.st);
           }
           __syncwarp();
+          if (j >= 0) vr.next();
+          if (has_k) kr.next();
         }
-        tiles += x_tiles;
+        tiles += n;
         if (!alive) break;
       }
       if (!alive) {
@@ -473,202 +629,249 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
       }
     }
   } else if (warp >= C::kOutWarp) {
-    // ---------------------------------------------------------------- finished accumulators -> out, or partials
-    regs_fewer<88>();
-    const int wq = warp & 3;
-    const uint32_t lanes = uint32_t(wq) << 21;  // this warp's 32 lanes of tensor memory
-    unsigned char* stage = smem + C::kStageOff + wq * 4096;
-    uint32_t units[2] = {0, 0};
-    for (; take(); done()) {
-      const PromptPiece& x = sy->piece[queue.st];
-      const int kvh = x.unit / p.chunks, head0 = (x.unit - kvh * p.chunks) * p.heads;
+    regs_fewer<C::kSideRegs>();
+    if constexpr (!C::kQuant) {
+      // ---------------------------------------------------------------- finished accumulators -> out, or partials
+      uint32_t used0 = 0, used1 = 0;
+      for (; take(); done()) {
+        const PromptPiece& x = sy->piece[queue.st];
 #pragma unroll 1
-      for (int s = 0; s < 2 && alive; ++s) {
-        const int rows = stream_tokens(x, s) * p.heads;
-        const int r = wq * 32 + lane, tok = r / p.heads, h = head0 + r - tok * p.heads;
-        const bool live = r < rows && h < p.group;
-        const uint32_t o_addr = tmem + lanes + 256 + s * D;
-        float2 st = make_float2(kMaxFloor, 0.0f);
-        const bool any = x.count[s] > 0;
-        if (any) {
-          alive = wait_all(sy->stat_ready + s, units[s] & 1) && wait_all(sy->o_ready + s, units[s] & 1);
-          if (!alive) break;
-          ++units[s];
-          tc_fence_after();
-          st = stats[s * 128 + r];
-        }
-        if (x.part >= 0) {
-          const int64_t row = (int64_t(x.part) * p.units + x.unit) * p.part_rows + s * p.stream_tokens * p.heads;
-          if (live) p.ml[row + r] = st;
-          if (any) {
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              float o[32];
-              tmem_ld32(o_addr + c0, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-              __syncwarp();
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int k = j * 4 + (lane >> 3), e = lane & 7;
-                if (wq * 32 + k < rows)
-                  *reinterpret_cast<float4*>(p.acc + (row + wq * 32 + k) * D + c0 + e * 4) =
-                      *reinterpret_cast<const float4*>(stage + k * 128 + ((e ^ (k & 7)) << 4));
-              }
-              __syncwarp();
-            }
-          }
-        } else {
-          // row of out; -1: none.  A row without a weight is zero, whatever the accumulator holds.
-          const int64_t to = live ? int64_t(x.row0 + s * p.stream_tokens + tok) * p.out_stride + (int64_t(kvh) * p.group + h) * D : -1;
-          const float inv = 1.0f / st.y;
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 64) {
-            uint32_t v[32];
-#pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-              float o[32];
-              if (any) {
-                tmem_ld32(o_addr + c0 + c, o);
-                tmem_wait_ld();
-              }
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[c / 2 + e] = any && st.y != 0.0f ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
-            }
-            if (any && c0 == D - 64) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(sy->o_free + s);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-                  make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int k = j * 4 + (lane >> 3), e = lane & 7;
-              const int64_t row = __shfl_sync(kAll, to, k);
-              if (row >= 0)
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row + c0 + e * 8) =
-                    *reinterpret_cast<const uint4*>(stage + k * 128 + ((e ^ (k & 7)) << 4));
-            }
-            __syncwarp();
-          }
-          continue;
-        }
-        if (any) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sy->o_free + s);
-        }
+        for (int s = 0; s < (x.twin ? 1 : 2) && alive; ++s) alive = write_out(x, s, warp & 3, used0, used1);
+        if (!alive) break;
+        used0 ^= x.count[0] > 0;
+        used1 ^= x.count[1] > 0;
       }
-      if (!alive) break;
+    } else {
+      // ---------------------------------------------------------------- codes -> operand tiles of K, or of V
+      constexpr int kChunks = D / 16;          // 16-byte chunks of a row of codes
+      constexpr int kRows = 32 / kChunks;      // rows that a load of the warp's lanes covers
+      constexpr int kLoads = 32 / kRows;       // for the warp's 32 rows of a tile: two blocks
+      const bool is_v = warp >= C::kConvertWarp + 4;
+      const int wq = warp & 3, chunk = lane % kChunks, sub = lane / kChunks;
+      const auto* cache = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
+      unsigned char* ring = smem + (is_v ? C::kVOff : C::kRingOff);
+      uint64_t* full = is_v ? sy->v_full : sy->k_full;
+      uint64_t* empty = is_v ? sy->v_empty : sy->k_empty;
+      static_assert(C::kK == C::kV, "one ring's place for both");
+      RingAt<C::kK> at;
+      uint32_t filled = 0, tiles = 0;
+      for (; take(); done()) {
+        const PromptPiece& x = sy->piece[queue.st];
+        const int n = x.tiles, tile0 = x.tile0, lo = x.lo, hi = x.hi;
+        const int kvh = x.unit / p.chunks;
+        const int32_t* table = p.block_tables + int64_t(x.seq) * p.max_blocks_per_seq;
+        const int blk0 = lo / kBlockSize, blk1 = (hi + kBlockSize - 1) / kBlockSize;
+        if (n == 0 && warp == C::kConvertWarp && lane == 0) mbar_arrive(&sy->late);
+        // The warp's two blocks of a tile, asked for a tile ahead of their codes: -1 where no token of the item lies in one.
+        int next0 = -1, next1 = -1;
+        auto ask = [&](int tile) {
+          const int b = (tile0 + tile) * (kPromptTile / kBlockSize) + 2 * wq;
+          next0 = tile < n && b >= blk0 && b < blk1 ? load_now(table + b) : -1;
+          next1 = tile < n && b + 1 >= blk0 && b + 1 < blk1 ? load_now(table + b + 1) : -1;
+        };
+        const uint8_t *from0 = nullptr, *from1 = nullptr;  // this lane's first chunk in each
+        uint32_t have = 0;
+        float ks = 0.0f, vs = 0.0f;
+        auto place = [&](int tile) {  // of the blocks that were asked for
+          const bool ok0 = next0 >= 0 && next0 < p.num_blocks, ok1 = next1 >= 0 && next1 < p.num_blocks;
+          const int b = (tile0 + tile) * (kPromptTile / kBlockSize) + 2 * wq;
+          if (!is_v && lane == 0 && ((b >= blk0 && b < blk1 && !ok0) || (b + 1 >= blk0 && b + 1 < blk1 && !ok1)))
+            set_error(p.err, kErrBlockId);
+          have = uint32_t(ok0) | uint32_t(ok1) << 1;
+          const int64_t row0 = (int64_t(next0) * p.kv_heads + kvh) * kBlockSize, row1 = (int64_t(next1) * p.kv_heads + kvh) * kBlockSize;
+          from0 = cache + (row0 + sub) * D + chunk * 16;
+          from1 = cache + (row1 + sub) * D + chunk * 16;
+          if (!is_v) {  // a thread to a token; what the item does not see may hold anything, its scales are 0
+            const int t = (tile0 + tile) * kPromptTile + wq * 32 + lane;
+            const bool ok = (lane < 16 ? ok0 : ok1) && t >= lo && t < hi;
+            const int64_t row = (lane < 16 ? row0 : row1) + (lane & 15);
+            ks = ok ? __int_as_float(load_now(p.k_scale + row)) : 0.0f;
+            vs = ok ? __int_as_float(load_now(p.v_scale + row)) : 0.0f;
+          }
+        };
+        uint4 w[kLoads];
+        auto load = [&](int i) {
+          const bool upper = i >= kLoads / 2;
+          const uint8_t* from = upper ? from1 : from0;
+          w[i] = have >> upper & 1 ? load_codes(from + (i - (upper ? kLoads / 2 : 0)) * kRows * D) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        ask(0);
+        if (n > 0) {
+          place(0);
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) load(i);
+        }
+        ask(1);
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
+          if (filled >= C::kK && !(alive = wait_all(empty + at.st, at.ph ^ 1u))) break;
+          if (!is_v) {
+            if (wq == 0 && lane == 0 && t == max(0, n - 3)) mbar_arrive(&sy->late);
+            auto* slot = reinterpret_cast<float*>(smem + C::kSlotOff + (tiles + t) % C::kSlots * 1024) + wq * 32 + lane;
+            slot[0] = ks;
+            slot[128] = vs;
+            if (lane == 0) reinterpret_cast<uint8_t*>(sy->mask + (tiles + t) % kTileMasks)[wq] = uint8_t(have);
+          }
+          if (t + 1 < n) place(t + 1);
+          ask(t + 2);
+          // Lanes of a row's lower and upper half write different chunks of their spans at a time: no bank twice.
+          unsigned char* dst = ring + at.st * C::kTileBytes + (chunk >> 2) * C::kHalfBytes;
+          const int c0 = 2 * (chunk & 3), swap = D == 128 ? chunk >> 2 : sub & 1;
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            const int row = wq * 32 + i * kRows + sub;
+            uint4 a, b;
+            bf16x4_from_codes<KV>(w[i].x, a.x, a.y);
+            bf16x4_from_codes<KV>(w[i].y, a.z, a.w);
+            bf16x4_from_codes<KV>(w[i].z, b.x, b.y);
+            bf16x4_from_codes<KV>(w[i].w, b.z, b.w);
+            if (t + 1 < n) load(i);
+            *reinterpret_cast<uint4*>(dst + row * 128 + (((c0 + swap) ^ (row & 7)) << 4)) = swap ? b : a;
+            *reinterpret_cast<uint4*>(dst + row * 128 + (((c0 + 1 - swap) ^ (row & 7)) << 4)) = swap ? a : b;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full + at.st);
+          ++filled;
+          at.next();
+        }
+        tiles += n;
+        if (!alive) break;
+      }
     }
   } else {
     // ---------------------------------------------------------------- softmax of stream s, a thread to a row
-    regs_more<184>();
+    regs_more<C::kSoftmaxRegs>();
     const int s = warp >> 2, wq = warp & 3, r = threadIdx.x & 127;
-    const uint32_t lanes = uint32_t(wq) << 21;
+    const uint32_t lanes = uint32_t(wq) << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t s_addr = tmem + lanes + s * 128, o_addr = tmem + lanes + 256 + s * D;
     // a scale of zero becomes one that makes every finite logit 0, and leaves a masked one -inf
     const float scale = p.scale_log2 == 0.0f ? 1e-30f : fabsf(p.scale_log2);
     const uint64_t scale2 = f32x2(scale, scale);
     const int tok = r / p.heads;
-    uint32_t step = 0, units = 0, tiles = 0;
+    uint32_t step = 0, tiles = 0, used0 = 0, used1 = 0;
+    bool before = false;  // the stream has had pieces
     for (; take(); done()) {
       const PromptPiece& x = sy->piece[queue.st];
-      const int n = x.count[s], ntok = stream_tokens(x, s), first = x.first[s];
-      const uint32_t mask0 = tiles - x.tile0;
+      const int n = x.count[s], first = x.first[s], tile0 = x.tile0, stride = x.twin ? 2 : 1;
+      const uint32_t tiles0 = tiles;
       tiles += x.tiles;
-      if (n == 0) continue;
-      const bool dead = tok >= ntok, idle = __all_sync(kAll, dead);
-      const int pos = x.pos0 + s * p.stream_tokens + tok;
-      PromptSpan span = prompt_span(p, pos, pos, x.len);
-      if (dead) span = {0, INT_MAX};  // its values go nowhere
-      float m = kMaxFloor, l = 0.0f;
+      if (n > 0) {
+        const bool dead = tok >= stream_tokens(x, s), idle = __all_sync(kAll, dead);
+        const int pos = x.pos0 + stream_first(x, s) + tok;
+        PromptSpan span = prompt_span(p, pos, pos, x.len);
+        if (dead) span = {0, INT_MAX};  // its values go nowhere
+        float m = kMaxFloor, l = 0.0f;
 #pragma unroll 1
-      for (int i = 0; i < n; ++i, step ^= 1u) {
-        const int tile = first + i;
-        alive = wait_all(sy->s_ready + s, step);
-        if (!alive) break;
-        if (!idle) {
-          tc_fence_after();
-          const uint32_t have = sy->mask[(mask0 + tile) % kTileMasks];
-          const int lo = span.lo - tile * kPromptTile, hi = span.hi - tile * kPromptTile;
-          float y[128];
+        for (int i = 0; i < n; ++i, step ^= 1u) {
+          const int tile = first + i * stride;
+          alive = wait_all(sy->s_ready + s, step);
+          if (!alive) break;
+          if (!idle) {
+            tc_fence_after();
+            const uint32_t have = tile_mask(sy->mask[(tiles0 + tile) % kTileMasks]);
+            const int lo = span.lo - (tile0 + tile) * kPromptTile, hi = span.hi - (tile0 + tile) * kPromptTile;
+            [[maybe_unused]] const auto* ks =
+                reinterpret_cast<const ulonglong2*>(smem + C::kSlotOff + (C::kQuant ? (tiles0 + tile) % (C::kSlots + !C::kQuant) : 0) * 1024);
+            [[maybe_unused]] const auto* vs = ks + kPromptTile / 4;
+            float y[128];
+            const bool cut = __any_sync(kAll, lo > 0 || hi < kPromptTile || have != 0xffu);
+            float mx[4];
+            if constexpr (!C::kQuant) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, y + 32 * c);
-          tmem_wait_ld();
-          if (__any_sync(kAll, lo > 0 || hi < kPromptTile || have != 0xffu)) {
+              for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, y + 32 * c);
+              tmem_wait_ld();
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint32_t w = bit_range(lo - 32 * c, hi - 32 * c) & ((have >> (2 * c) & 1 ? 0xffffu : 0u) | (have >> (2 * c + 1) & 1 ? 0xffff0000u : 0u));
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(w >> j & 1)) y[32 * c + j] = -INFINITY;
-            }
-          }
-          float mx[4] = {y[0], y[1], y[2], y[3]};
-#pragma unroll
-          for (int j = 4; j < 124; j += 8) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], y[j + 2 * u], y[j + 2 * u + 1]);
-          }
-          const float bm = max3(max3(mx[0], y[124], y[125]), max3(mx[1], y[126], y[127]), fmaxf(mx[2], mx[3])) * scale;
-          const bool grow = bm > m + kMaxSlack;
-          if (__any_sync(kAll, grow)) {
-            const float mu = grow ? bm : m, f = fast_exp2(m - mu);
-            m = mu;
-            l *= f;
-            if (i > 0) {
-              // every product into O is done: S was issued after the last
-#pragma unroll 1
-              for (int j = 0; j < D / 16; ++j) {
-                float o[16];
-                tmem_ld16(o_addr + 16 * j, o);
+              float* z = y + 32 * c;
+              if constexpr (C::kQuant) {
+                tmem_ld32(s_addr + 32 * c, z);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] *= f;
-                tmem_st16(o_addr + 16 * j, o);
+                for (int j = 0; j < 8; ++j) {
+                  const ulonglong2 f = ks[8 * c + j];
+                  f32x2_parts(mul2(f32x2(z[4 * j], z[4 * j + 1]), f.x), z[4 * j], z[4 * j + 1]);
+                  f32x2_parts(mul2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y), z[4 * j + 2], z[4 * j + 3]);
+                }
+              }
+              if (cut) {
+                const uint32_t w = bit_range(lo - 32 * c, hi - 32 * c) & ((have >> (2 * c) & 1 ? 0xffffu : 0u) | (have >> (2 * c + 1) & 1 ? 0xffff0000u : 0u));
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!(w >> j & 1)) z[j] = -INFINITY;
+              }
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) mx[u] = c + j == 0 ? fmaxf(z[2 * u], z[2 * u + 1]) : max3(mx[u], z[j + 2 * u], z[j + 2 * u + 1]);
               }
             }
-          }
-          const uint64_t neg = f32x2(-m, -m);
-          uint64_t sum[2] = {0, 0};
+            const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+            const bool grow = bm > m + kMaxSlack;
+            if (__any_sync(kAll, grow)) {
+              const float mu = grow ? bm : m, f = fast_exp2(m - mu);
+              m = mu;
+              l *= f;
+              if (i > 0) {
+                // every product into O is done: S was issued after the last
+#pragma unroll 1
+                for (int j = 0; j < D / 16; ++j) {
+                  float o[16];
+                  tmem_ld16(o_addr + 16 * j, o);
+                  tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float* z = y + 32 * c;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) f32x2_parts(fma2(f32x2(z[2 * j], z[2 * j + 1]), scale2, neg), z[2 * j], z[2 * j + 1]);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) z[j] = fast_exp2(z[j]);
-            float w[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              sum[j & 1] = add2(sum[j & 1], f32x2(z[2 * j], z[2 * j + 1]));
-              w[j] = __uint_as_float(pack_bf16x2(z[2 * j], z[2 * j + 1]));
+                  for (int e = 0; e < 16; ++e) o[e] *= f;
+                  tmem_st16(o_addr + 16 * j, o);
+                }
+              }
             }
-            tmem_st16(s_addr + 16 * c, w);
+            const uint64_t neg = f32x2(-m, -m);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float* z = y + 32 * c;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) f32x2_parts(fma2(f32x2(z[2 * j], z[2 * j + 1]), scale2, neg), z[2 * j], z[2 * j + 1]);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) z[j] = fast_exp2(z[j]);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[j & 1] = add2(sum[j & 1], f32x2(z[2 * j], z[2 * j + 1]));
+              if constexpr (C::kQuant) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const ulonglong2 f = vs[8 * c + j];
+                  f32x2_parts(mul2(f32x2(z[4 * j], z[4 * j + 1]), f.x), z[4 * j], z[4 * j + 1]);
+                  f32x2_parts(mul2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y), z[4 * j + 2], z[4 * j + 3]);
+                }
+              }
+              float w[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = __uint_as_float(pack_bf16x2(z[2 * j], z[2 * j + 1]));
+              tmem_st16(s_addr + 16 * c, w);
+            }
+            float sum_lo, sum_hi;
+            f32x2_parts(add2(sum[0], sum[1]), sum_lo, sum_hi);
+            l += sum_lo + sum_hi;
+            tmem_wait_st();
+            tc_fence_before();
           }
-          float sum_lo, sum_hi;
-          f32x2_parts(add2(sum[0], sum[1]), sum_lo, sum_hi);
-          l += sum_lo + sum_hi;
-          tmem_wait_st();
-          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sy->p_ready + s);
         }
+        if (!alive) break;
+        // the last piece's have been read once its accumulator has
+        if (before && !(alive = wait_all(sy->o_free + s, (s ? used1 : used0) ^ 1u))) break;
+        before = true;
+        stats[s * 128 + r] = make_float2(m, l);
         __syncwarp();
-        if (lane == 0) mbar_arrive(sy->p_ready + s);
+        if (lane == 0) mbar_arrive(sy->stat_ready + s);
       }
-      if (!alive) break;
-      // the last unit's have been read once its accumulator has
-      if (units > 0 && !(alive = wait_all(sy->o_free + s, (units - 1) & 1))) break;
-      stats[s * 128 + r] = make_float2(m, l);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sy->stat_ready + s);
-      ++units;
+      if constexpr (C::kQuant) {
+        if ((s == 0 || !x.twin) && !(alive = write_out(x, s, wq, used0, used1))) break;
+      }
+      used0 ^= x.count[0] > 0;
+      used1 ^= x.count[1] > 0;
     }
   }
   if (!alive && lane == 0) {
@@ -684,11 +887,11 @@ __global__ void __launch_bounds__(PromptCfg<D, kPaged>::kThreads, 1)
   }
 }
 
-template <int D, bool kPaged>
+template <KvType KV, int D, bool kPaged>
 cudaError_t launch_prompt_tc(const PromptParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              cudaStream_t stream) {
-  using C = PromptCfg<D, kPaged>;
-  auto kern = prompt_tc_kernel<D, kPaged>;
+  using C = PromptCfg<KV, D, kPaged>;
+  auto kern = prompt_tc_kernel<KV, D, kPaged>;
   static std::atomic<bool> attr_done[64];  // per device: the shared-memory limit is raised
   int dev = 0;
   cudaGetDevice(&dev);

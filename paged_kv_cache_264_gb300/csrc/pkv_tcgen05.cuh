@@ -125,4 +125,29 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Two codes in the low bytes of each half of `v` (bits 0-7 and 16-23) -> two bf16, exactly: with
+// x = (low seven bits) - 128 (sign), 0x4300 | low bits is 128 + low bits, 0x4300 | sign bit is 128 or
+// 256, and their difference is x.
+__device__ __forceinline__ uint32_t bf16x2_from_i8(uint32_t v) {
+  const uint32_t a = (v & 0x007f007fu) | 0x43004300u, b = (v & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Four codes of a word -> four bf16 in two words.
+template <KvType KV>
+__device__ __forceinline__ void bf16x4_from_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (KV == KvType::kFp8) {
+    uint32_t a, b;
+    f16x2x2_from_e4m3x4(w, a, b);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    lo = pack_bf16x2(x.x, x.y);
+    hi = pack_bf16x2(y.x, y.y);
+  } else {
+    lo = bf16x2_from_i8(__byte_perm(w, 0u, 0x4140u));
+    hi = bf16x2_from_i8(__byte_perm(w, 0u, 0x4342u));
+  }
+}
+
 }  // namespace pkv
