@@ -712,8 +712,6 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             slot[128] = vs;
             if (lane == 0) reinterpret_cast<uint8_t*>(sy->mask + (tiles + t) % kTileMasks)[wq] = uint8_t(have);
           }
-          if (t + 1 < n) place(t + 1);
-          ask(t + 2);
           // Lanes of a row's lower and upper half write different chunks of their spans at a time: no bank twice.
           unsigned char* dst = ring + at.st * C::kTileBytes + (chunk >> 2) * C::kHalfBytes;
           const int c0 = 2 * (chunk & 3), swap = D == 128 ? chunk >> 2 : sub & 1;
@@ -725,10 +723,17 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             bf16x4_from_codes<KV>(w[i].y, a.z, a.w);
             bf16x4_from_codes<KV>(w[i].z, b.x, b.y);
             bf16x4_from_codes<KV>(w[i].w, b.z, b.w);
-            if (t + 1 < n) load(i);
             *reinterpret_cast<uint4*>(dst + row * 128 + (((c0 + swap) ^ (row & 7)) << 4)) = swap ? b : a;
             *reinterpret_cast<uint4*>(dst + row * 128 + (((c0 + 1 - swap) ^ (row & 7)) << 4)) = swap ? a : b;
           }
+          // The next tile's codes, all behind this one's: a wait for one of these would wait for loads issued
+          // before it too.
+          if (t + 1 < n) {
+            place(t + 1);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) load(i);
+          }
+          ask(t + 2);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(full + at.st);
