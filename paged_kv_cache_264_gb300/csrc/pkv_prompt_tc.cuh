@@ -98,8 +98,8 @@ struct PromptCfg {
   static constexpr int kOutWarp = 8, kConvertWarp = 8, kMmaWarp = kQuant ? 16 : 12, kLoadWarp = kMmaWarp + 1;
   static constexpr int kReaders = kMmaWarp + 1;                // warps that take pieces
   // Registers a thread: the launch's, shared out anew by warpgroup.
-  static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 160 : 184, kSideRegs = kQuant ? 56 : 88,
-                       kLoadRegs = kQuant ? 40 : 56;
+  static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 128 : 176, kSideRegs = 80,
+                       kLoadRegs = kQuant ? 56 : 80;
   static_assert(2 * kSoftmaxRegs + (kQuant ? 2 : 1) * kSideRegs + kLoadRegs <= kThreads / 128 * kRegs, "registers");
   static constexpr int kRingOff = 2 * kTileBytes;              // Q tiles of both streams first
   static constexpr int kVOff = kRingOff + kK * kTileBytes;
@@ -779,17 +779,12 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             [[maybe_unused]] const auto* ks =
                 reinterpret_cast<const ulonglong2*>(smem + C::kSlotOff + (C::kQuant ? (tiles0 + tile) % (C::kSlots + !C::kQuant) : 0) * 1024);
             [[maybe_unused]] const auto* vs = ks + kPromptTile / 4;
-            float y[128];
+            // Over codes 32 columns at a time, once for the maximum and once for the weights: all 128 and the
+            // scales would not stay in registers, and spilled ones are far away with shared memory this full.
+            constexpr int kHeld = C::kQuant ? 1 : 4;  // chunks of 32 columns held
+            float y[32 * kHeld];
             const bool cut = __any_sync(kAll, lo > 0 || hi < kPromptTile || have != 0xffu);
-            float mx[4];
-            if constexpr (!C::kQuant) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, y + 32 * c);
-              tmem_wait_ld();
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float* z = y + 32 * c;
+            auto fetch = [&](int c, float* z) {  // a chunk's scaled and masked logits
               if constexpr (C::kQuant) {
                 tmem_ld32(s_addr + 32 * c, z);
                 tmem_wait_ld();
@@ -806,10 +801,21 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                 for (int j = 0; j < 32; ++j)
                   if (!(w >> j & 1)) z[j] = -INFINITY;
               }
+            };
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if constexpr (!C::kQuant) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, y + 32 * c);
+              tmem_wait_ld();
+            }
+#pragma unroll kHeld
+            for (int c = 0; c < 4; ++c) {
+              float* z = y + 32 * (c % kHeld);
+              fetch(c, z);
 #pragma unroll
               for (int j = 0; j < 32; j += 8) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) mx[u] = c + j == 0 ? fmaxf(z[2 * u], z[2 * u + 1]) : max3(mx[u], z[j + 2 * u], z[j + 2 * u + 1]);
+                for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], z[j + 2 * u], z[j + 2 * u + 1]);
               }
             }
             const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
@@ -833,9 +839,10 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             }
             const uint64_t neg = f32x2(-m, -m);
             uint64_t sum[2] = {0, 0};
-#pragma unroll
+#pragma unroll kHeld
             for (int c = 0; c < 4; ++c) {
-              float* z = y + 32 * c;
+              float* z = y + 32 * (c % kHeld);
+              if constexpr (C::kQuant) fetch(c, z);
 #pragma unroll
               for (int j = 0; j < 16; ++j) f32x2_parts(fma2(f32x2(z[2 * j], z[2 * j + 1]), scale2, neg), z[2 * j], z[2 * j + 1]);
 #pragma unroll
