@@ -98,8 +98,8 @@ struct PromptCfg {
   static constexpr int kOutWarp = 8, kConvertWarp = 8, kMmaWarp = kQuant ? 16 : 12, kLoadWarp = kMmaWarp + 1;
   static constexpr int kReaders = kMmaWarp + 1;                // warps that take pieces
   // Registers a thread: the launch's, shared out anew by warpgroup.
-  static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 128 : 176, kSideRegs = 80,
-                       kLoadRegs = kQuant ? 56 : 80;
+  static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 136 : 192, kSideRegs = kQuant ? 72 : 56,
+                       kLoadRegs = kQuant ? 64 : 72;
   static_assert(2 * kSoftmaxRegs + (kQuant ? 2 : 1) * kSideRegs + kLoadRegs <= kThreads / 128 * kRegs, "registers");
   static constexpr int kRingOff = 2 * kTileBytes;              // Q tiles of both streams first
   static constexpr int kVOff = kRingOff + kK * kTileBytes;
@@ -118,7 +118,7 @@ constexpr int kTileMasks = 16;   // tiles whose masks are kept: more than the ri
 struct PromptSync {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];  // ring stages
   uint64_t q_full[2], q_empty[2];  // per stream from here
-  uint64_t s_ready[2], p_ready[2];
+  uint64_t s_ready[2], p_half[2], p_ready[2];  // P's first 64 columns (over bf16), and all
   uint64_t o_ready[2], o_free[2];
   uint64_t stat_ready[2];
   uint64_t drain, late;
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       mbar_init(sy->q_full + s, 1);
       mbar_init(sy->q_empty + s, 1);
       mbar_init(sy->s_ready + s, 1);
+      mbar_init(sy->p_half + s, 4);
       mbar_init(sy->p_ready + s, 4);
       mbar_init(sy->o_ready + s, 1);
       mbar_init(sy->o_free + s, 4);
@@ -567,28 +568,35 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             if (twin && (d & 1)) continue;  // the other stream's tile
             const int at = d >> twin;       // the stream's tile whose product over V is due
             if (at >= 0 && at < count[s]) {
-              alive = alive && wait_all(sy->p_ready + s, steps[s] & 1);
+              alive = alive && wait_all((C::kQuant ? sy->p_ready : sy->p_half) + s, steps[s] & 1);
               if (at == 0 && used[s] > 0) alive = alive && wait_all(sy->o_free + s, (used[s] - 1) & 1);
               if (!alive) break;
-              ++steps[s];
-              tc_fence_after();
-              if (elect_one()) {
-                if (vmask == 0xffu) {
+              bool on = !fresh[s];
 #pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    tc_mma_ts(t_o, t_s + i * 8, vd + i * ((16 * 128) >> 4), kHi, kDescO, i > 0 || !fresh[s]);
-                } else {
-                  bool on = !fresh[s];
+              for (int half = 0; half < 2; ++half) {
+                if (half && !C::kQuant && !(alive = wait_all(sy->p_ready + s, steps[s] & 1))) break;
+                tc_fence_after();
+                if (elect_one()) {
+                  if (vmask == 0xffu) {
+#pragma unroll
+                    for (int i = 4 * half; i < 4 * half + 4; ++i)
+                      tc_mma_ts(t_o, t_s + i * 8, vd + i * ((16 * 128) >> 4), kHi, kDescO, i > 0 || on);
+                  } else {
+                    bool more = on;
 #pragma unroll 1
-                  for (int i = 0; i < 8; ++i)
-                    if (vmask >> i & 1) {
-                      tc_mma_ts(t_o, t_s + i * 8, vd + i * ((16 * 128) >> 4), kHi, kDescO, on);
-                      on = true;
-                    }
+                    for (int i = 4 * half; i < 4 * half + 4; ++i)
+                      if (vmask >> i & 1) {
+                        tc_mma_ts(t_o, t_s + i * 8, vd + i * ((16 * 128) >> 4), kHi, kDescO, more);
+                        more = true;
+                      }
+                  }
+                  if (half && at == count[s] - 1) tc_commit(sy->o_ready + s);
                 }
-                if (at == count[s] - 1) tc_commit(sy->o_ready + s);
+                __syncwarp();
+                on = on || (vmask >> (4 * half) & 0xfu);
               }
-              __syncwarp();
+              if (!alive) break;
+              ++steps[s];
               if (vmask != 0) fresh[s] = false;
               if (at == count[s] - 1) ++used[s];
             }
@@ -779,48 +787,57 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             [[maybe_unused]] const auto* ks =
                 reinterpret_cast<const ulonglong2*>(smem + C::kSlotOff + (C::kQuant ? (tiles0 + tile) % (C::kSlots + !C::kQuant) : 0) * 1024);
             [[maybe_unused]] const auto* vs = ks + kPromptTile / 4;
-            // Over codes 32 columns at a time, once for the maximum and once for the weights: all 128 and the
-            // scales would not stay in registers, and spilled ones are far away with shared memory this full.
-            constexpr int kHeld = C::kQuant ? 1 : 4;  // chunks of 32 columns held
-            float y[32 * kHeld];
             const bool cut = __any_sync(kAll, lo > 0 || hi < kPromptTile || have != 0xffu);
-            auto fetch = [&](int c, float* z) {  // a chunk's scaled and masked logits
-              if constexpr (C::kQuant) {
-                tmem_ld32(s_addr + 32 * c, z);
-                tmem_wait_ld();
+            auto mask = [&](int c, float* z) {  // columns 32 c .. 32 c + 31
+              const uint32_t w = bit_range(lo - 32 * c, hi - 32 * c) & ((have >> (2 * c) & 1 ? 0xffffu : 0u) | (have >> (2 * c + 1) & 1 ? 0xffff0000u : 0u));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const ulonglong2 f = ks[8 * c + j];
-                  f32x2_parts(mul2(f32x2(z[4 * j], z[4 * j + 1]), f.x), z[4 * j], z[4 * j + 1]);
-                  f32x2_parts(mul2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y), z[4 * j + 2], z[4 * j + 3]);
-                }
-              }
-              if (cut) {
-                const uint32_t w = bit_range(lo - 32 * c, hi - 32 * c) & ((have >> (2 * c) & 1 ? 0xffffu : 0u) | (have >> (2 * c + 1) & 1 ? 0xffff0000u : 0u));
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!(w >> j & 1)) z[j] = -INFINITY;
-              }
+              for (int j = 0; j < 32; ++j)
+                if (!(w >> j & 1)) z[j] = -INFINITY;
             };
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if constexpr (!C::kQuant) {
+            auto largest = [&](const float* z, int n, float (&mx)[4]) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, y + 32 * c);
-              tmem_wait_ld();
-            }
-#pragma unroll kHeld
-            for (int c = 0; c < 4; ++c) {
-              float* z = y + 32 * (c % kHeld);
-              fetch(c, z);
-#pragma unroll
-              for (int j = 0; j < 32; j += 8) {
+              for (int j = 0; j < n; j += 8) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], z[j + 2 * u], z[j + 2 * u + 1]);
               }
-            }
-            const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
-            const bool grow = bm > m + kMaxSlack;
-            if (__any_sync(kAll, grow)) {
+            };
+            uint64_t sum[2];
+            // Logits -> weights, 2 n to n registers.  A warp issues in order and is alone with its row's chain, so the
+            // steps of neighbouring groups of 8 are written side by side: exponentials at a time (4 cycles each)
+            // with the products and sums (2) of others.
+            auto weigh = [&](int c, int n, float* z, float* w) {
+              const uint64_t neg = f32x2(-m, -m);
+#pragma unroll
+              for (int g = 0; g < n + 8; g += 4) {
+                if (g < n) {
+#pragma unroll
+                  for (int j = g; j < g + 4; ++j) f32x2_parts(fma2(f32x2(z[2 * j], z[2 * j + 1]), scale2, neg), z[2 * j], z[2 * j + 1]);
+                }
+                if (g >= 4 && g < n + 4) {
+#pragma unroll
+                  for (int j = 2 * g - 8; j < 2 * g; ++j) z[j] = fast_exp2(z[j]);
+                }
+                if (g >= 8) {
+#pragma unroll
+                  for (int j = g - 8; j < g - 4; ++j) sum[j & 1] = add2(sum[j & 1], f32x2(z[2 * j], z[2 * j + 1]));
+                  if constexpr (C::kQuant) {
+#pragma unroll
+                    for (int j = (g - 8) / 2; j < (g - 4) / 2; ++j) {
+                      const ulonglong2 f = vs[8 * c + j];
+                      f32x2_parts(mul2(f32x2(z[4 * j], z[4 * j + 1]), f.x), z[4 * j], z[4 * j + 1]);
+                      f32x2_parts(mul2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y), z[4 * j + 2], z[4 * j + 3]);
+                    }
+                  }
+#pragma unroll
+                  for (int j = g - 8; j < g - 4; ++j) w[j] = __uint_as_float(pack_bf16x2(z[2 * j], z[2 * j + 1]));
+                }
+              }
+            };
+            // The maximum is moved where a row's logits pass it; false where none of the warp's rows' do.
+            auto move = [&](const float (&mx)[4]) {
+              const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+              const bool grow = bm > m + kMaxSlack;
+              if (!__any_sync(kAll, grow)) return false;
               const float mu = grow ? bm : m, f = fast_exp2(m - mu);
               m = mu;
               l *= f;
@@ -836,37 +853,51 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                   tmem_st16(o_addr + 16 * j, o);
                 }
               }
-            }
-            const uint64_t neg = f32x2(-m, -m);
-            uint64_t sum[2] = {0, 0};
-#pragma unroll kHeld
-            for (int c = 0; c < 4; ++c) {
-              float* z = y + 32 * (c % kHeld);
-              if constexpr (C::kQuant) fetch(c, z);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) f32x2_parts(fma2(f32x2(z[2 * j], z[2 * j + 1]), scale2, neg), z[2 * j], z[2 * j + 1]);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) z[j] = fast_exp2(z[j]);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) sum[j & 1] = add2(sum[j & 1], f32x2(z[2 * j], z[2 * j + 1]));
+              return true;
+            };
+            // 32 columns at a time, once for the maximum and once for the weights, in rolled loops: the code of
+            // both streams' softmax stays in the instruction cache.
+            float z[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto fetch = [&](int c) {
+              tmem_ld32(s_addr + 32 * c, z);
+              tmem_wait_ld();
               if constexpr (C::kQuant) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                  const ulonglong2 f = vs[8 * c + j];
+                  const ulonglong2 f = ks[8 * c + j];
                   f32x2_parts(mul2(f32x2(z[4 * j], z[4 * j + 1]), f.x), z[4 * j], z[4 * j + 1]);
                   f32x2_parts(mul2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y), z[4 * j + 2], z[4 * j + 3]);
                 }
               }
+              if (cut) mask(c, z);
+            };
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              fetch(c);
+              largest(z, 32, mx);
+            }
+            move(mx);
+            sum[0] = sum[1] = 0;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
               float w[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) w[j] = __uint_as_float(pack_bf16x2(z[2 * j], z[2 * j + 1]));
+              fetch(c);
+              weigh(c, 16, z, w);
               tmem_st16(s_addr + 16 * c, w);
+              if (!C::kQuant && c == 1) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sy->p_half + s);
+              }
             }
             float sum_lo, sum_hi;
             f32x2_parts(add2(sum[0], sum[1]), sum_lo, sum_hi);
             l += sum_lo + sum_hi;
             tmem_wait_st();
             tc_fence_before();
+          } else if (!C::kQuant && lane == 0) {
+            mbar_arrive(sy->p_half + s);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(sy->p_ready + s);
