@@ -6,8 +6,8 @@
 //     P = 2^(S * scale - m)    a thread to a row
 //     O += P V     128 x D x 128, P in tensor memory (bf16, over S's columns), V as it lies in memory
 //                  (token-major, the contracted index outermost: an MN-major operand)
-// One warp issues all products, stream by stream: O of a tile, then S of the next, so that the tensor pipe works
-// on one stream while the other's softmax runs.  Products complete in order, so S may be written over P behind the
+// A warp per stream issues its products: O of a tile, then S of the next, so that the tensor pipe works on one
+// stream while the other's softmax runs (one warp for both was late with either: 3060 cycles a tile of both streams).  Products complete in order, so S may be written over P behind the
 // product that reads it, and a softmax that has its S knows that O is at rest: it rescales O itself where it has to.
 // That is rare, for the running maximum is lazy (kMaxSlack): it moves only when a row's logits pass it by 2^8.  The
 // weights enter the product over V as bf16, which the product's other operand sets (2^-8 of each at most, as in the
@@ -23,7 +23,7 @@
 // Warps: a warpgroup of softmax per stream; over bf16, one that turns finished accumulators into rows of out, so that
 // the next unit's softmax need not wait for that, and one warp that fills the rings of K and V tiles by TMA (over the
 // cache 8 blocks to a tile, each wherever it lies in the pool), which also takes pieces off the list and loads Q; over
-// codes, the softmax warps write out and the two converting warpgroups fill the rings; one warp issues the products.
+// codes, the softmax warps write out and the two converting warpgroups fill the rings; a warp per stream issues the products.
 //
 // What a row does not see is masked in its logits; only tiles that some row of the warp sees in part pay for that.
 // The product over V takes the steps of 16 tokens that the item sees, and rows of V within those that no row of the
@@ -95,8 +95,8 @@ struct PromptCfg {
   static_assert(!kQuant || kSlots >= kK + 2, "a scale slot is free when it is written again");
   static constexpr int kThreads = kQuant ? 640 : 512;
   // first warps: of the writers of out, or of the two converting warpgroups (K's and V's); of the others
-  static constexpr int kOutWarp = 8, kConvertWarp = 8, kMmaWarp = kQuant ? 16 : 12, kLoadWarp = kMmaWarp + 1;
-  static constexpr int kReaders = kMmaWarp + 1;                // warps that take pieces
+  static constexpr int kOutWarp = 8, kConvertWarp = 8, kMmaWarp = kQuant ? 16 : 12, kLoadWarp = kMmaWarp + 2;
+  static constexpr int kReaders = kMmaWarp + 2;                // warps that take pieces
   // Registers a thread: the launch's, shared out anew by warpgroup.
   static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 136 : 192, kSideRegs = kQuant ? 72 : 56,
                        kLoadRegs = kQuant ? 64 : 72;
@@ -121,7 +121,7 @@ struct PromptSync {
   uint64_t s_ready[2], p_half[2], p_ready[2];  // P's first 64 columns (over bf16), and all
   uint64_t o_ready[2], o_free[2];
   uint64_t stat_ready[2];
-  uint64_t drain, late;
+  uint64_t turn[2], drain[2], late;
   uint64_t piece_full[kPieceQueue], piece_empty[kPieceQueue];
   PromptPiece piece[kPieceQueue];
   uint32_t mask[kTileMasks];       // which of a tile's blocks exist, by tile in load order: two to a byte
@@ -167,11 +167,11 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
     constexpr int kFillers = C::kQuant ? 4 : 1;
     for (int i = 0; i < C::kK; ++i) {
       mbar_init(sy->k_full + i, kFillers);
-      mbar_init(sy->k_empty + i, 1);
+      mbar_init(sy->k_empty + i, 2);
     }
     for (int i = 0; i < C::kV; ++i) {
       mbar_init(sy->v_full + i, kFillers);
-      mbar_init(sy->v_empty + i, 1);
+      mbar_init(sy->v_empty + i, 2);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(sy->q_full + s, 1);
@@ -182,8 +182,9 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       mbar_init(sy->o_ready + s, 1);
       mbar_init(sy->o_free + s, 4);
       mbar_init(sy->stat_ready + s, 4);
+      mbar_init(sy->drain + s, 1);
+      mbar_init(sy->turn + s, 1);
     }
-    mbar_init(&sy->drain, 1);
     mbar_init(&sy->late, 1);
     for (int i = 0; i < kPieceQueue; ++i) {
       mbar_init(sy->piece_full + i, 1);
@@ -515,37 +516,48 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         if (q_used[s] > 0) (void)mbar_wait_bounded(sy->q_full + s, (q_used[s] - 1) & 1);
-    } else if (warp == C::kMmaWarp) {
-      // ---------------------------------------------------------------- products
-      // The whole warp runs this with warp-uniform values; one elected lane issues.
+    } else if (warp == C::kMmaWarp || warp == C::kMmaWarp + 1) {
+      // ---------------------------------------------------------------- products of stream s
+      // The whole warp runs this with warp-uniform values; one elected lane issues.  Both warps wait for and
+      // release every stage, those of tiles that only the other stream takes too: a barrier's wait is for a parity.
+      const int s = warp - C::kMmaWarp;
       const uint32_t negate = p.scale_log2 < 0.0f ? 1u << 13 : 0u;  // -Q: the largest product is the largest logit
       const uint32_t desc_s = mma_bf16_desc(128, kPromptTile, false) | negate;
       constexpr uint32_t kDescO = mma_bf16_desc(128, D, true);
       constexpr uint32_t kHi = smem_operand_hi(1024);
-      const uint32_t q_desc = smem_operand(smem_addr(smem), 16);
+      const uint32_t q_desc = smem_operand(smem_addr(smem + s * C::kTileBytes), 16);
       const uint32_t k_desc = smem_operand(smem_addr(smem + C::kRingOff), 16);
       const uint32_t v_desc = smem_operand(smem_addr(smem + C::kVOff), C::kHalfBytes);
+      const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * D;
       RingAt<C::kK> kr;
       RingAt<C::kV> vr;
-      uint32_t tiles = 0;
-      uint32_t steps[2] = {0, 0}, used[2] = {0, 0};  // each stream's tiles, and pieces with tiles, before now
+      uint32_t tiles = 0, step = 0, used = 0;  // all tiles before the piece's; parities of the stream's tiles and pieces
+      bool before = false;                     // the stream has had pieces
+      uint32_t turns = 0;
       for (; take(); done()) {
         const PromptPiece& x = sy->piece[queue.st];
-        const int n = x.tiles, tile0 = x.tile0, lo0 = x.lo, hi0 = x.hi;
-        const int twin = x.twin != 0, lead = 1 + twin;
-        const int first[2] = {x.first[0], x.first[1]}, count[2] = {x.count[0], x.count[1]};
-        bool fresh[2] = {true, true};  // O holds nothing of this piece yet
+        const int n = x.tiles, tile0 = x.tile0, twin = x.twin != 0, lead = 1 + twin;
+        // the stream's tiles are first, first + lead, ... last
+        const int first = x.first[s], count = x.count[s], last = first + (count - 1) * lead;
+        const int lo0 = x.lo - tile0 * kPromptTile, hi0 = x.hi - tile0 * kPromptTile;
+        bool fresh = true;  // O holds nothing of this piece yet
 #pragma unroll 1
         for (int j = -lead; j < n; ++j) {
-          uint32_t vmask = 0;
-          if (j >= 0) {
-            if (!(alive = wait_all(sy->v_full + vr.st, vr.ph))) break;
-            // steps of 16 tokens that the item sees
-            const int lo = lo0 - (tile0 + j) * kPromptTile, hi = hi0 - (tile0 + j) * kPromptTile;
-            vmask = tile_mask(sy->mask[(tiles + j) % kTileMasks]) & bit_range(lo / 16, (hi + 15) / 16);
-            // within them, tokens that it does not: zero
-            const int z0 = max(0, lo) & ~15, z1 = max(0, lo), z2 = min(kPromptTile, hi), z3 = min(kPromptTile, (hi + 15) & ~15);
-            if (z1 > z0 || z3 > z2) {
+          const bool turn = !twin || !((j ^ first) & 1);
+          const bool has_v = j >= 0, has_k = j + lead < n;
+          const bool pv = turn && j >= first && j <= last, qk = turn && j + lead >= first && j + lead <= last;
+          if (has_k && !(alive = wait_all(sy->k_full + kr.st, kr.ph))) break;
+          if (has_v && !(alive = wait_all(sy->v_full + vr.st, vr.ph))) break;
+          const uint32_t kd = __shfl_sync(kAll, k_desc + kr.st * (C::kTileBytes >> 4), 0);
+          uint32_t vd = 0, vmask = 0;
+          if (pv) {
+            vd = __shfl_sync(kAll, v_desc + vr.st * (C::kTileBytes >> 4), 0);
+            const int lo = lo0 - j * kPromptTile, hi = hi0 - j * kPromptTile;
+            vmask = tile_mask(sy->mask[(tiles + j) % kTileMasks]);
+            if (lo > 0 || hi < kPromptTile) {
+              vmask &= bit_range(lo / 16, (hi + 15) / 16);  // steps of 16 tokens that the item sees
+              // within them, tokens that it does not: zero
+              const int z0 = max(0, lo) & ~15, z1 = max(0, lo), z2 = min(kPromptTile, hi), z3 = min(kPromptTile, (hi + 15) & ~15);
               unsigned char* v = smem + C::kVOff + vr.st * C::kTileBytes;
               for (int c = lane; c < (z1 - z0 + z3 - z2) * 8; c += 32) {
                 const int i = c >> 3, row = i < z1 - z0 ? z0 + i : z2 + i - (z1 - z0);
@@ -556,84 +568,82 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
               fence_proxy_async_smem();
               __syncwarp();
             }
+            if (j == first && before) alive = wait_all(sy->o_free + s, used ^ 1u);
+            alive = alive && wait_all((C::kQuant ? sy->p_ready : sy->p_half) + s, step);
+            if (!alive) break;
           }
-          const bool has_k = j + lead < n;
-          if (has_k && !(alive = wait_all(sy->k_full + kr.st, kr.ph))) break;
-          const uint32_t vd = __shfl_sync(kAll, v_desc + vr.st * (C::kTileBytes >> 4), 0);
-          const uint32_t kd = __shfl_sync(kAll, k_desc + kr.st * (C::kTileBytes >> 4), 0);
+          if (qk && j + lead == first && !(alive = wait_all(sy->q_full + s, used))) break;
+          // Products of the two streams side by side would both be late: the warps issue in turn.
+          if ((s == 1 || turns > 0) && !(alive = wait_all(sy->turn + s, (s == 1 ? turns : turns - 1) & 1))) break;
+          ++turns;
+          tc_fence_after();
+          if (pv) {
+            bool on = !fresh;
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * D;
-            const int d = j - first[s];
-            if (twin && (d & 1)) continue;  // the other stream's tile
-            const int at = d >> twin;       // the stream's tile whose product over V is due
-            if (at >= 0 && at < count[s]) {
-              alive = alive && wait_all((C::kQuant ? sy->p_ready : sy->p_half) + s, steps[s] & 1);
-              if (at == 0 && used[s] > 0) alive = alive && wait_all(sy->o_free + s, (used[s] - 1) & 1);
-              if (!alive) break;
-              bool on = !fresh[s];
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                if (half && !C::kQuant && !(alive = wait_all(sy->p_ready + s, steps[s] & 1))) break;
+            for (int half = 0; half < 2; ++half) {
+              if (half && !C::kQuant) {
+                if (!(alive = wait_all(sy->p_ready + s, step))) break;
                 tc_fence_after();
-                if (elect_one()) {
-                  if (vmask == 0xffu) {
-#pragma unroll
-                    for (int i = 4 * half; i < 4 * half + 4; ++i)
-                      tc_mma_ts(t_o, t_s + i * 8, vd + i * ((16 * 128) >> 4), kHi, kDescO, i > 0 || on);
-                  } else {
-                    bool more = on;
-#pragma unroll 1
-                    for (int i = 4 * half; i < 4 * half + 4; ++i)
-                      if (vmask >> i & 1) {
-                        tc_mma_ts(t_o, t_s + i * 8, vd + i * ((16 * 128) >> 4), kHi, kDescO, more);
-                        more = true;
-                      }
-                  }
-                  if (half && at == count[s] - 1) tc_commit(sy->o_ready + s);
-                }
-                __syncwarp();
-                on = on || (vmask >> (4 * half) & 0xfu);
               }
-              if (!alive) break;
-              ++steps[s];
-              if (vmask != 0) fresh[s] = false;
-              if (at == count[s] - 1) ++used[s];
-            }
-            if (at + 1 >= 0 && at + 1 < count[s]) {  // and whose logits
-              if (at + 1 == 0) {
-                alive = alive && wait_all(sy->q_full + s, used[s] & 1);
-                if (!alive) break;
-              }
-              tc_fence_after();
               if (elect_one()) {
+                if (vmask == 0xffu) {
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                  const uint32_t o = ((i >> 2) * C::kHalfBytes + (i & 3) * 32) >> 4;
-                  tc_mma_ss(t_s, q_desc + s * (C::kTileBytes >> 4) + o, kd + o, kHi, desc_s, i > 0);
+                  for (int i = 4 * half; i < 4 * half + 4; ++i)
+                    tc_mma_ts(t_o, t_s + i * 8, vd + i * ((16 * 128) >> 4), kHi, kDescO, i > 0 || on);
+                } else {
+                  bool more = on;
+#pragma unroll 1
+                  for (int i = 4 * half; i < 4 * half + 4; ++i)
+                    if (vmask >> i & 1) {
+                      tc_mma_ts(t_o, t_s + i * 8, vd + i * ((16 * 128) >> 4), kHi, kDescO, more);
+                      more = true;
+                    }
                 }
-                tc_commit(sy->s_ready + s);
-                if (at + 1 == count[s] - 1) tc_commit(sy->q_empty + s);
               }
               __syncwarp();
+              on = on || (vmask >> (4 * half) & 0xfu);
+            }
+            if (!alive) break;
+            fresh = !on;
+            step ^= 1u;
+          }
+          if (elect_one()) {
+            if (pv) {
+              tc_commit(sy->v_empty + vr.st);
+              if (j == last) tc_commit(sy->o_ready + s);
+            } else if (has_v) {
+              mbar_arrive(sy->v_empty + vr.st);
+            }
+            if (qk) {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint32_t o = ((i >> 2) * C::kHalfBytes + (i & 3) * 32) >> 4;
+                tc_mma_ss(t_s, q_desc + o, kd + o, kHi, desc_s, i > 0);
+              }
+              mbar_arrive(sy->turn + (s ^ 1));
+              tc_commit(sy->s_ready + s);
+              tc_commit(sy->k_empty + kr.st);
+              if (j + lead == last) tc_commit(sy->q_empty + s);
+            } else {
+              mbar_arrive(sy->turn + (s ^ 1));
+              if (has_k) mbar_arrive(sy->k_empty + kr.st);
             }
           }
-          if (!alive) break;
-          if (elect_one()) {
-            if (j >= 0) tc_commit(sy->v_empty + vr.st);
-            if (has_k) tc_commit(sy->k_empty + kr.st);
-          }
           __syncwarp();
-          if (j >= 0) vr.next();
+          if (has_v) vr.next();
           if (has_k) kr.next();
         }
         tiles += n;
         if (!alive) break;
+        if (count > 0) {
+          used ^= 1u;
+          before = true;
+        }
       }
       if (!alive) {
-        if (elect_one()) tc_commit(&sy->drain);  // the products in flight end before their memory is given up
+        if (elect_one()) tc_commit(sy->drain + s);  // the products in flight end before their memory is given up
         __syncwarp();
-        (void)mbar_wait_bounded(&sy->drain, 0);
+        (void)mbar_wait_bounded(sy->drain + s, 0);
       }
     }
   } else if (warp >= C::kOutWarp) {
