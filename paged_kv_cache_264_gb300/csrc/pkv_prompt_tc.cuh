@@ -865,9 +865,12 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
               }
               return true;
             };
+            sum[0] = sum[1] = 0;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if constexpr (C::kQuant) {
             // 32 columns at a time, once for the maximum and once for the weights, in rolled loops: the code of
             // both streams' softmax stays in the instruction cache.
-            float z[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float z[32];
             auto fetch = [&](int c) {
               tmem_ld32(s_addr + 32 * c, z);
               tmem_wait_ld();
@@ -887,7 +890,6 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
               largest(z, 32, mx);
             }
             move(mx);
-            sum[0] = sum[1] = 0;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               float w[16];
@@ -899,6 +901,30 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sy->p_half + s);
+              }
+            }
+            } else {
+              float y[128], w[32];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, y + 32 * c);
+              tmem_wait_ld();
+              if (cut) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mask(c, y + 32 * c);
+              }
+              largest(y, 128, mx);
+              move(mx);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                weigh(2 * h, 32, y + 64 * h, w);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) tmem_st16(s_addr + 32 * h + 16 * c, w + 16 * c);
+                if (h == 0) {
+                  tmem_wait_st();
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(sy->p_half + s);
+                }
               }
             }
             float sum_lo, sum_hi;
