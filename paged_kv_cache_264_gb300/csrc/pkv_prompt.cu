@@ -248,45 +248,56 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
   if (tid == 0) *p.header = PromptHeader{0u, line, items, s_joins};
 }
 
-// Join the pieces' states of cut items: a warp per row, a lane to D / 32 consecutive values.
+// Join the pieces' states of cut units: half a warp per row, a lane to D / 16 consecutive values.  Bound by its chain
+// of loads: the states and accumulators of kAhead pieces are on their way at a time, before it is known what each weighs.
 template <int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p) {
-  constexpr int kDPV = D / 32;
-  constexpr uint32_t kAll = 0xffffffffu;
-  const int lane = threadIdx.x & 31;
+  constexpr int kVec = D / 64;  // float4s of a lane
+  constexpr int kAhead = 4;
+  const int lane = threadIdx.x & 15;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t rows = int64_t(p.header->joins) * p.part_rows;
-  const int64_t warps = int64_t(gridDim.x) * (blockDim.x / 32);
-  for (int64_t w = int64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5); w < rows; w += warps) {
-    const int j = int(w / p.part_rows), r = int(w - int64_t(j) * p.part_rows);
-    const PromptJoin x = p.joins[j];
-    const int tok = r / p.heads, h = r - tok * p.heads;
-    const int kvh = x.unit / p.chunks, head = (x.unit - kvh * p.chunks) * p.heads + h;
-    if (tok >= x.ntok || head >= p.group) continue;
-    auto row = [&](int i) { return int64_t(x.part + i) * p.part_rows + r; };
-    float M = kMaxFloor;
-    for (int i = lane; i < x.parts; i += 32) M = fmaxf(M, p.ml[row(i)].x);
+  const int64_t w = int64_t(blockIdx.x) * (blockDim.x / 16) + (threadIdx.x >> 4);
+  const int j = int(w / p.part_rows), r = int(w - int64_t(j) * p.part_rows);
+  if (j >= p.header->joins) return;
+  const PromptJoin x = p.joins[j];
+  const int tok = r / p.heads, h = r - tok * p.heads;
+  const int kvh = x.unit / p.chunks, head = (x.unit - kvh * p.chunks) * p.heads + h;
+  if (tok >= x.ntok || head >= p.group) return;
+  const int64_t row0 = int64_t(x.part) * p.part_rows + r;
+  float M = kMaxFloor, L = 0.0f, a[4 * kVec] = {};
+  for (int i0 = 0; i0 < x.parts; i0 += kAhead) {
+    float2 s[kAhead];
+    float4 v[kAhead][kVec];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
-    float L = 0.0f, a[kDPV] = {};
-    for (int i = 0; i < x.parts; ++i) {
-      const float2 s = p.ml[row(i)];
-      if (s.y == 0.0f) continue;  // weighs nothing; it may have no accumulator
-      const float f = exp2f(s.x - M);
-      L = fmaf(f, s.y, L);
-      const float* src = p.acc + row(i) * D + lane * kDPV;
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t row = row0 + int64_t(min(i0 + u, x.parts - 1)) * p.part_rows;
+      s[u] = p.ml[row];
 #pragma unroll
-      for (int e = 0; e < kDPV; ++e) a[e] = fmaf(f, src[e], a[e]);
+      for (int e = 0; e < kVec; ++e) v[u][e] = reinterpret_cast<const float4*>(p.acc + row * D)[lane * kVec + e];
     }
-    uint32_t packed[kDPV / 2];
 #pragma unroll
-    for (int e = 0; e < kDPV / 2; ++e) packed[e] = L == 0.0f ? 0u : pack_bf16x2(a[2 * e] / L, a[2 * e + 1] / L);
-    auto* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(x.row0 + tok) * p.out_stride +
-                (int64_t(kvh) * p.group + head) * D + lane * kDPV;
-    if constexpr (kDPV == 4) *reinterpret_cast<uint2*>(out) = make_uint2(packed[0], packed[1]);
-    else *reinterpret_cast<uint32_t*>(out) = packed[0];
+    for (int u = 0; u < kAhead; ++u) {
+      // a sum of 0 weighs nothing, and may have no accumulator
+      if (i0 + u >= x.parts || s[u].y == 0.0f) continue;
+      const float top = fmaxf(M, s[u].x), f0 = exp2f(M - top), f = exp2f(s[u].x - top);
+      M = top;
+      L = L * f0 + s[u].y * f;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        a[4 * e] = a[4 * e] * f0 + v[u][e].x * f;
+        a[4 * e + 1] = a[4 * e + 1] * f0 + v[u][e].y * f;
+        a[4 * e + 2] = a[4 * e + 2] * f0 + v[u][e].z * f;
+        a[4 * e + 3] = a[4 * e + 3] * f0 + v[u][e].w * f;
+      }
+    }
   }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  auto* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(x.row0 + tok) * p.out_stride +
+              (int64_t(kvh) * p.group + head) * D + lane * 4 * kVec;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e)
+    reinterpret_cast<uint2*>(out)[e] = make_uint2(pack_bf16x2(a[4 * e] * inv, a[4 * e + 1] * inv), pack_bf16x2(a[4 * e + 2] * inv, a[4 * e + 3] * inv));
 }
 
 }  // namespace
@@ -296,7 +307,8 @@ cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_prompt_join(const PromptParams& p, cudaStream_t stream) {
-  const dim3 grid(unsigned(p.grid) * 4);
+  // at most a cut unit per CTA of the pass
+  const dim3 grid(unsigned((int64_t(p.grid) * p.part_rows + 15) / 16));
   if (p.head_dim == 128) return launch_pdl(prompt_join_kernel<128>, grid, dim3(256), 0, stream, p);
   return launch_pdl(prompt_join_kernel<64>, grid, dim3(256), 0, stream, p);
 }

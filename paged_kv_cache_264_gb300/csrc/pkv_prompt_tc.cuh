@@ -98,8 +98,8 @@ struct PromptCfg {
   static constexpr int kOutWarp = 8, kConvertWarp = 8, kMmaWarp = kQuant ? 16 : 12, kLoadWarp = kMmaWarp + 2;
   static constexpr int kReaders = kMmaWarp + 2;                // warps that take pieces
   // Registers a thread: the launch's, shared out anew by warpgroup.
-  static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 136 : 192, kSideRegs = kQuant ? 72 : 56,
-                       kLoadRegs = kQuant ? 64 : 72;
+  static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 144 : 192, kSideRegs = kQuant ? 72 : 56,
+                       kLoadRegs = kQuant ? 48 : 72;
   static_assert(2 * kSoftmaxRegs + (kQuant ? 2 : 1) * kSideRegs + kLoadRegs <= kThreads / 128 * kRegs, "registers");
   static constexpr int kRingOff = 2 * kTileBytes;              // Q tiles of both streams first
   static constexpr int kVOff = kRingOff + kK * kTileBytes;
@@ -118,7 +118,7 @@ constexpr int kTileMasks = 16;   // tiles whose masks are kept: more than the ri
 struct PromptSync {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];  // ring stages
   uint64_t q_full[2], q_empty[2];  // per stream from here
-  uint64_t s_ready[2], p_half[2], p_ready[2];  // P's first 64 columns (over bf16), and all
+  uint64_t s_ready[2], p_half[2], p_ready[2];  // P's first 64 columns, and all
   uint64_t o_ready[2], o_free[2];
   uint64_t stat_ready[2];
   uint64_t turn[2], drain[2], late;
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
               __syncwarp();
             }
             if (j == first && before) alive = wait_all(sy->o_free + s, used ^ 1u);
-            alive = alive && wait_all((C::kQuant ? sy->p_ready : sy->p_half) + s, step);
+            alive = alive && wait_all(sy->p_half + s, step);
             if (!alive) break;
           }
           if (qk && j + lead == first && !(alive = wait_all(sy->q_full + s, used))) break;
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             bool on = !fresh;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              if (half && !C::kQuant) {
+              if (half) {
                 if (!(alive = wait_all(sy->p_ready + s, step))) break;
                 tc_fence_after();
               }
@@ -868,41 +868,40 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             sum[0] = sum[1] = 0;
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if constexpr (C::kQuant) {
-            // 32 columns at a time, once for the maximum and once for the weights, in rolled loops: the code of
-            // both streams' softmax stays in the instruction cache.
-            float z[32];
-            auto fetch = [&](int c) {
-              tmem_ld32(s_addr + 32 * c, z);
-              tmem_wait_ld();
-              if constexpr (C::kQuant) {
+              // Half a tile at a time: the upper half for its maximum, the lower one for its maximum and, kept, its
+              // weights, and the upper one again.  All 128 logits and the scales would not stay in registers, and
+              // spilled ones are far away with shared memory this full.  The loop stays rolled: the code of all roles
+              // shares an instruction cache.
+              float z[64], w[32];
+#pragma unroll 1
+              for (int phase = 0; phase < 3; ++phase) {
+                const int h = phase == 1 ? 0 : 1;
+                tmem_ld32(s_addr + 64 * h, z);
+                tmem_ld32(s_addr + 64 * h + 32, z + 32);
+                tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const ulonglong2 f = ks[8 * c + j];
+                for (int j = 0; j < 16; ++j) {
+                  const ulonglong2 f = ks[16 * h + j];
                   f32x2_parts(mul2(f32x2(z[4 * j], z[4 * j + 1]), f.x), z[4 * j], z[4 * j + 1]);
                   f32x2_parts(mul2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y), z[4 * j + 2], z[4 * j + 3]);
                 }
+                if (cut) {
+                  mask(2 * h, z);
+                  mask(2 * h + 1, z + 32);
+                }
+                if (phase < 2) largest(z, 64, mx);
+                if (phase == 0) continue;
+                if (phase == 1) move(mx);
+                weigh(2 * h, 32, z, w);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) tmem_st16(s_addr + 32 * h + 16 * c, w + 16 * c);
+                if (phase == 1) {
+                  tmem_wait_st();
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(sy->p_half + s);
+                }
               }
-              if (cut) mask(c, z);
-            };
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              fetch(c);
-              largest(z, 32, mx);
-            }
-            move(mx);
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              float w[16];
-              fetch(c);
-              weigh(c, 16, z, w);
-              tmem_st16(s_addr + 16 * c, w);
-              if (!C::kQuant && c == 1) {
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sy->p_half + s);
-              }
-            }
             } else {
               float y[128], w[32];
 #pragma unroll
@@ -932,7 +931,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             l += sum_lo + sum_hi;
             tmem_wait_st();
             tc_fence_before();
-          } else if (!C::kQuant && lane == 0) {
+          } else if (lane == 0) {
             mbar_arrive(sy->p_half + s);
           }
           __syncwarp();
