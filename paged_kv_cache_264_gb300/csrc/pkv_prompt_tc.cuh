@@ -665,7 +665,11 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       constexpr int kRows = 32 / kChunks;      // rows that a load of the warp's lanes covers
       constexpr int kLoads = 32 / kRows;       // for the warp's 32 rows of a tile: two blocks
       const bool is_v = warp >= C::kConvertWarp + 4;
-      const int wq = warp & 3, chunk = lane % kChunks, sub = lane / kChunks;
+      // Of a load's rows, this lane has chunk `chunk` of row `sub`.  Eight neighbouring lanes, whose 16-byte stores go
+      // together, hold four chunks of two neighbouring rows: their places in the swizzled tile are all different.
+      const int wq = warp & 3;
+      const int chunk = D == 128 ? (lane & 3) | (lane >> 3 & 1) << 2 : lane & 3;
+      const int sub = D == 128 ? (lane >> 2 & 1) | lane >> 4 << 1 : lane >> 2;
       const auto* cache = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
       unsigned char* ring = smem + (is_v ? C::kVOff : C::kRingOff);
       uint64_t* full = is_v ? sy->v_full : sy->k_full;
@@ -679,6 +683,8 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         const int kvh = x.unit / p.chunks;
         const int32_t* table = p.block_tables + int64_t(x.seq) * p.max_blocks_per_seq;
         const int blk0 = lo / kBlockSize, blk1 = (hi + kBlockSize - 1) / kBlockSize;
+        const uint8_t* mine = cache + (kvh * kBlockSize + sub) * D + chunk * 16;
+        const int block_bytes = p.kv_heads * (kBlockSize * D);
         if (n == 0 && warp == C::kConvertWarp && lane == 0) mbar_arrive(&sy->late);
         // The warp's two blocks of a tile, asked for a tile ahead of their codes: -1 where no token of the item lies in one.
         int next0 = -1, next1 = -1;
@@ -696,13 +702,12 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
           if (!is_v && lane == 0 && ((b >= blk0 && b < blk1 && !ok0) || (b + 1 >= blk0 && b + 1 < blk1 && !ok1)))
             set_error(p.err, kErrBlockId);
           have = uint32_t(ok0) | uint32_t(ok1) << 1;
-          const int64_t row0 = (int64_t(next0) * p.kv_heads + kvh) * kBlockSize, row1 = (int64_t(next1) * p.kv_heads + kvh) * kBlockSize;
-          from0 = cache + (row0 + sub) * D + chunk * 16;
-          from1 = cache + (row1 + sub) * D + chunk * 16;
+          from0 = mine + int64_t(next0) * block_bytes;
+          from1 = mine + int64_t(next1) * block_bytes;
           if (!is_v) {  // a thread to a token; what the item does not see may hold anything, its scales are 0
             const int t = (tile0 + tile) * kPromptTile + wq * 32 + lane;
             const bool ok = (lane < 16 ? ok0 : ok1) && t >= lo && t < hi;
-            const int64_t row = (lane < 16 ? row0 : row1) + (lane & 15);
+            const int64_t row = int64_t(lane < 16 ? next0 : next1) * (p.kv_heads * kBlockSize) + kvh * kBlockSize + (lane & 15);
             ks = ok ? __int_as_float(load_now(p.k_scale + row)) : 0.0f;
             vs = ok ? __int_as_float(load_now(p.v_scale + row)) : 0.0f;
           }
@@ -730,19 +735,18 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             slot[128] = vs;
             if (lane == 0) reinterpret_cast<uint8_t*>(sy->mask + (tiles + t) % kTileMasks)[wq] = uint8_t(have);
           }
-          // Lanes of a row's lower and upper half write different chunks of their spans at a time: no bank twice.
-          unsigned char* dst = ring + at.st * C::kTileBytes + (chunk >> 2) * C::kHalfBytes;
-          const int c0 = 2 * (chunk & 3), swap = D == 128 ? chunk >> 2 : sub & 1;
+          unsigned char* dst = ring + at.st * C::kTileBytes + (chunk >> 2) * C::kHalfBytes + (wq * 32 + sub) * 128;
+          const int c0 = 2 * (chunk & 3);
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) {
-            const int row = wq * 32 + i * kRows + sub;
+            const int row = i * kRows + sub;  // of the warp's 32
             uint4 a, b;
             bf16x4_from_codes<KV>(w[i].x, a.x, a.y);
             bf16x4_from_codes<KV>(w[i].y, a.z, a.w);
             bf16x4_from_codes<KV>(w[i].z, b.x, b.y);
             bf16x4_from_codes<KV>(w[i].w, b.z, b.w);
-            *reinterpret_cast<uint4*>(dst + row * 128 + (((c0 + swap) ^ (row & 7)) << 4)) = swap ? b : a;
-            *reinterpret_cast<uint4*>(dst + row * 128 + (((c0 + 1 - swap) ^ (row & 7)) << 4)) = swap ? a : b;
+            *reinterpret_cast<uint4*>(dst + i * (kRows * 128) + ((c0 ^ (row & 7)) << 4)) = a;
+            *reinterpret_cast<uint4*>(dst + i * (kRows * 128) + (((c0 + 1) ^ (row & 7)) << 4)) = b;
           }
           // The next tile's codes, all behind this one's: a wait for one of these would wait for loads issued
           // before it too.
