@@ -21,7 +21,15 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;  // of sequences' sizes, for the order
-constexpr int kUnitCost = 2;    // a unit's start and end, in tiles
+constexpr int kHeldSeqs = 1024; // of up to this many sequences the plan holds what it needs in shared memory
+// Places on the line: of a tile, of one whose rows both streams hold (up to kRowTile of them), and ahead of a unit's
+// tiles, for its start and end.  Measured on GB300, cycles of a CTA, head_dim 128, 32 query and 8 kv heads: a tile of
+// 256 rows 3400 (codes 4800 to 5000), of 4 and 128 rows 2900 (codes 2700 to 3400), a unit 5500 to 7000 besides.
+constexpr int kTileCost = 8, kTwinCost = 7, kTwinCodesCost = 5, kUnitCost = 12;
+__device__ __forceinline__ int tile_cost(const PromptParams& p, int ntok) {
+  return ntok > p.stream_tokens ? kTileCost : p.k_scale ? kTwinCodesCost : kTwinCost;
+}
+
 template <typename T>
 __device__ __forceinline__ T warp_scan(T v) {  // inclusive
   const int lane = threadIdx.x & 31;
@@ -75,32 +83,45 @@ __device__ __forceinline__ bool prompt_seq(const PromptParams& p, int b, PromptS
   return s.key0 >= 0 && key1 >= s.key0 && key1 <= p.num_keys;
 }
 
-// Item `at` of the call: its sequence, rows and tiles; `index` of the sequence's `count`.
-__device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, int at, int items, int& index) {
-  int lo = 0, hi = p.num_seqs;
-  while (hi - lo > 1) {  // the last sequence whose items start at or before this one
-    const int mid = (lo + hi) >> 1;
-    if (p.item_starts[mid] <= at) lo = mid; else hi = mid;
+// The sequences' items, in shared memory where they fit.
+struct PromptItems {
+  const PromptParams& p;
+  const PromptSeq* held;  // NULL: read again
+  const int* starts;      // [num_seqs] items before each sequence's
+  int items;
+
+  // The sequence that item `at` belongs to, its items and which of them it is.
+  __device__ __forceinline__ int find(int at, int& count, int& index) const {
+    int lo = 0, hi = p.num_seqs;
+    while (hi - lo > 1) {  // the last sequence whose items start at or before this one
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= at) lo = mid; else hi = mid;
+    }
+    count = (lo + 1 < p.num_seqs ? starts[lo + 1] : items) - starts[lo];
+    index = at - starts[lo];
+    return lo;
   }
-  PromptSeq s;
-  bool bad;
-  prompt_seq(p, lo, s, bad);
-  const int per = 2 * p.stream_tokens, start = p.item_starts[lo];
-  index = at - start;
-  const int tok0 = index * per;
-  PromptItem x{};
-  x.seq = lo;
-  x.row0 = s.row0 + tok0;
-  x.ntok = min(per, s.n - tok0);
-  x.pos0 = s.len - s.n + tok0;
-  x.len = s.len;
-  x.key0 = s.key0;
-  x.part = -1;
-  x.count = (lo + 1 < p.num_seqs ? p.item_starts[lo + 1] : items) - start;
-  x.shared = x.count > 1;
-  span_tiles(prompt_span(p, x.pos0, x.pos0 + x.ntok - 1, s.len), x.tile0, x.tiles);
-  return x;
-}
+  // Item `index` of sequence b's `count`.
+  __device__ __forceinline__ PromptItem item(int b, int count, int index) const {
+    PromptSeq s;
+    bool bad;
+    if (held) s = held[b];
+    else prompt_seq(p, b, s, bad);
+    const int per = 2 * p.stream_tokens, tok0 = index * per;
+    PromptItem x{};
+    x.seq = b;
+    x.row0 = s.row0 + tok0;
+    x.ntok = min(per, s.n - tok0);
+    x.pos0 = s.len - s.n + tok0;
+    x.len = s.len;
+    x.key0 = s.key0;
+    x.part = -1;
+    x.count = count;
+    x.shared = count > 1;
+    span_tiles(prompt_span(p, x.pos0, x.pos0 + x.ntok - 1, s.len), x.tile0, x.tiles);
+    return x;
+  }
+};
 
 // CTA c's stretch of a line of `total` places starts here; the CTA whose stretch holds place w.
 __device__ __forceinline__ int64_t line_start(int64_t total, int ctas, int c) { return total * c / ctas; }
@@ -108,15 +129,15 @@ __device__ __forceinline__ int line_owner(int64_t total, int ctas, int64_t w) { 
 
 // A unit's pieces along the line: f(CTA, first tile, tiles) for each that has tiles, or once for a unit that has none.
 template <typename F>
-__device__ __forceinline__ void line_pieces(int64_t total, int ctas, int64_t at, int tiles, F&& f) {
-  const int cost = tiles + kUnitCost;
+__device__ __forceinline__ void line_pieces(int64_t total, int ctas, int64_t at, int tiles, int per, F&& f) {
+  const int64_t cost = int64_t(tiles) * per + kUnitCost;
   if (tiles <= kPromptWhole) {
     f(line_owner(total, ctas, at + cost / 2), 0, tiles);
     return;
   }
   const int c1 = line_owner(total, ctas, at + cost - 1);
   for (int c = line_owner(total, ctas, at), t = 0; c <= c1; ++c) {
-    const int end = c == c1 ? tiles : int(max(line_start(total, ctas, c + 1) - at - kUnitCost, int64_t(0)));
+    const int end = c == c1 ? tiles : int(max(line_start(total, ctas, c + 1) - at - kUnitCost, int64_t(0)) / per);
     if (end > t) {
       f(c, t, end - t);
       t = end;
@@ -128,6 +149,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
   __shared__ int part[32];
   __shared__ int64_t part64[32];
   __shared__ int hist[kBuckets];  // sequences' sizes, or the CTAs' pieces
+  __shared__ PromptSeq held[kHeldSeqs];
+  __shared__ int held_starts[kHeldSeqs];
   __shared__ int s_most, s_joins;
   const int tid = threadIdx.x;
   griddep_wait();
@@ -135,6 +158,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
   if (tid == 0) s_most = s_joins = 0;
   hist[tid] = 0;
   // items of each sequence
+  const bool hold = p.num_seqs <= kHeldSeqs;
+  int* starts = hold ? held_starts : p.item_starts;
   int items = 0;
   bool ok = true;
   for (int b0 = 0; b0 < p.num_seqs; b0 += kPlanThreads) {
@@ -147,10 +172,11 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
       ok &= good;
       if (good && bad_len) set_error(p.err, kErrContextLen);
       if (good) n = (s.n + 2 * p.stream_tokens - 1) / (2 * p.stream_tokens);
+      if (hold) held[b] = s;
     }
     int all;
     const int before = block_scan(n, part, all);
-    if (b < p.num_seqs) p.item_starts[b] = items + before;
+    if (b < p.num_seqs) starts[b] = items + before;
     items += all;
   }
   if (!__syncthreads_and(ok)) {
@@ -160,22 +186,23 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
     }
     return;
   }
-  // the whole call's tiles, and the largest item's
+  const PromptItems call{p, hold ? held : nullptr, starts, items};
+  // the whole call's places, and the largest item's tiles
   int64_t sum = 0;
-  int most = 0, index;
+  int most = 0, count, index;
   for (int i = tid; i < items; i += kPlanThreads) {
-    const int t = prompt_item(p, i, items, index).tiles;
-    sum += t + kUnitCost;
-    most = max(most, t);
+    const int b = call.find(i, count, index);
+    const PromptItem x = call.item(b, count, index);
+    sum += int64_t(x.tiles) * tile_cost(p, x.ntok) + kUnitCost;
+    most = max(most, x.tiles);
   }
+  if (most > 0) atomicMax(&s_most, most);
   int64_t total;
   block_scan(sum, part64, total);
-  atomicMax(&s_most, most);
-  __syncthreads();
   most = s_most;
   total *= p.units;
   const int work = items * p.units;
-  const bool line = work <= kPromptWaves * p.grid || int64_t(most) * kPromptWaves > total / p.grid;
+  const bool line = work <= kPromptWaves * p.grid || int64_t(most) * kTileCost * kPromptWaves > total / p.grid;
   if (line) {
     const int ctas = int(min(total, int64_t(p.grid)));
     int64_t line0 = 0;
@@ -184,27 +211,30 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
       // in order: sequences, their head units, their items
       const int w = w0 + tid;
       PromptItem x{};
-      int pieces = 0;
+      int pieces = 0, per = 0;
       if (w < work) {
-        x = prompt_item(p, w / p.units, items, index);
-        const int in_seq = w - (w / p.units - index) * p.units, unit = in_seq / x.count;
-        x = prompt_item(p, w / p.units - index + in_seq - unit * x.count, items, index);
+        const int b = call.find(w / p.units, count, index);
+        const int in_seq = w - starts[b] * p.units, unit = in_seq / count;
+        x = call.item(b, count, in_seq - unit * count);
         x.unit = unit;
+        per = tile_cost(p, x.ntok);
       }
       int64_t all64;
-      const int64_t at = line0 + block_scan(int64_t(w < work ? x.tiles + kUnitCost : 0), part64, all64);
+      const int64_t at = line0 + block_scan(w < work ? int64_t(x.tiles) * per + kUnitCost : int64_t(0), part64, all64);
       if (w < work)
-        line_pieces(total, ctas, at, x.tiles, [&](int c, int, int) {
+        line_pieces(total, ctas, at, x.tiles, per, [&](int c, int, int) {
           atomicAdd(&hist[c], 1);
           ++pieces;
         });
-      int all_entries, all_parts;
-      int entry = entry0 + block_scan(pieces, part, all_entries);
-      const int first = part0 + block_scan(pieces > 1 ? pieces : 0, part, all_parts);
+      // both counts in one scan: pieces, and those of cut units
+      int64_t all_pieces;
+      const int64_t before = block_scan(int64_t(pieces) | int64_t(pieces > 1 ? pieces : 0) << 32, part64, all_pieces);
+      int entry = entry0 + int(before & 0xffffffff);
+      const int first = part0 + int(before >> 32);
       if (w < work) {
         const int tile0 = x.tile0, tiles = x.tiles;
         int to = first;
-        line_pieces(total, ctas, at, tiles, [&](int, int t, int n) {
+        line_pieces(total, ctas, at, tiles, per, [&](int, int t, int n) {
           x.tile0 = tile0 + t;
           x.tiles = n;
           x.part = pieces > 1 ? to++ : -1;
@@ -213,8 +243,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
         if (pieces > 1) p.joins[atomicAdd(&s_joins, 1)] = PromptJoin{x.row0, x.ntok, x.unit, first, pieces};
       }
       line0 += all64;
-      entry0 += all_entries;
-      part0 += all_parts;
+      entry0 += int(all_pieces & 0xffffffff);
+      part0 += int(all_pieces >> 32);
     }
     __syncthreads();
     int all;
@@ -225,9 +255,9 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
     auto bucket = [&](int tiles) { return kBuckets - 1 - int(int64_t(tiles) * (kBuckets - 1) / max(most, 1)); };
     for (int pass = 0; pass < 2; ++pass) {
       for (int b = tid; b < p.num_seqs; b += kPlanThreads) {
-        const int n = (b + 1 < p.num_seqs ? p.item_starts[b + 1] : items) - p.item_starts[b];
+        const int n = (b + 1 < p.num_seqs ? starts[b + 1] : items) - starts[b];
         if (n == 0) continue;
-        int* at = &hist[bucket(prompt_item(p, p.item_starts[b] + n - 1, items, index).tiles)];
+        int* at = &hist[bucket(call.item(b, n, n - 1).tiles)];
         if (pass == 0) atomicAdd(at, n);
         else p.seq_entry[b] = atomicAdd(at, n);
       }
@@ -240,9 +270,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
       }
     }
     for (int i = tid; i < items; i += kPlanThreads) {
-      PromptItem x = prompt_item(p, i, items, index);
-      x.unit = p.seq_entry[x.seq];
-      p.list[x.unit + x.count - 1 - index] = x;
+      const int b = call.find(i, count, index);
+      PromptItem x = call.item(b, count, index);
+      x.unit = p.seq_entry[b];
+      p.list[x.unit + count - 1 - index] = x;
     }
   }
   if (tid == 0) *p.header = PromptHeader{0u, line, items, s_joins};

@@ -79,7 +79,8 @@ struct PromptPiece {
   int part, unit;
   int twin;                   // both streams hold the same rows and take every other tile
   int shared;                 // the tiles are read again by other items
-  int first[2], count[2];     // each stream's tiles, from tile0 + first[s] on
+  int tok0[2], toks[2];       // each stream's first token and tokens
+  int first[2], count[2];     // and tiles, from tile0 + first[s] on
 };
 
 template <KvType KV, int D, bool kPaged>
@@ -95,8 +96,9 @@ struct PromptCfg {
   static_assert(!kQuant || kSlots >= kK + 2, "a scale slot is free when it is written again");
   static constexpr int kThreads = kQuant ? 640 : 512;
   // first warps: of the writers of out, or of the two converting warpgroups (K's and V's); of the others
-  static constexpr int kOutWarp = 8, kConvertWarp = 8, kMmaWarp = kQuant ? 16 : 12, kLoadWarp = kMmaWarp + 2;
-  static constexpr int kReaders = kMmaWarp + 2;                // warps that take pieces
+  static constexpr int kOutWarp = 8, kConvertWarp = 8, kMmaWarp = kQuant ? 16 : 12, kLoadWarp = kMmaWarp + 2,
+                       kListWarp = kMmaWarp + 3;
+  static constexpr int kReaders = kMmaWarp + 3;                // warps that take pieces
   // Registers a thread: the launch's, shared out anew by warpgroup.
   static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 144 : 192, kSideRegs = kQuant ? 72 : 56,
                        kLoadRegs = kQuant ? 48 : 72;
@@ -111,7 +113,7 @@ struct PromptCfg {
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 };
 
-constexpr int kPieceQueue = 2;   // pieces handed out
+constexpr int kPieceQueue = 4;   // pieces handed out
 constexpr int kTileMasks = 16;   // tiles whose masks are kept: more than the rings hold
 
 // Barriers and flags of one CTA.
@@ -121,7 +123,7 @@ struct PromptSync {
   uint64_t s_ready[2], p_half[2], p_ready[2];  // P's first 64 columns, and all
   uint64_t o_ready[2], o_free[2];
   uint64_t stat_ready[2];
-  uint64_t turn[2], drain[2], late;
+  uint64_t turn[2], drain[2];
   uint64_t piece_full[kPieceQueue], piece_empty[kPieceQueue];
   PromptPiece piece[kPieceQueue];
   uint32_t mask[kTileMasks];       // which of a tile's blocks exist, by tile in load order: two to a byte
@@ -185,7 +187,6 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       mbar_init(sy->drain + s, 1);
       mbar_init(sy->turn + s, 1);
     }
-    mbar_init(&sy->late, 1);
     for (int i = 0; i < kPieceQueue; ++i) {
       mbar_init(sy->piece_full + i, 1);
       mbar_init(sy->piece_empty + i, C::kReaders);
@@ -231,10 +232,6 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
     if (lane == 0) mbar_arrive(sy->piece_empty + queue.st);
     queue.next();
   };
-  // First token and tokens of stream s in an item.
-  auto stream_first = [&](const PromptPiece& x, int s) { return x.twin ? 0 : s * p.stream_tokens; };
-  auto stream_tokens = [&](const PromptPiece& x, int s) { return max(0, min(p.stream_tokens, x.ntok - stream_first(x, s))); };
-
   // Finished rows of stream s (of both streams, where they hold the same): a thread to a row, run by the four
   // warps of a warpgroup.  used0, used1: the parities of the streams' accumulators of this piece.
   [[maybe_unused]] auto write_out = [&](const PromptPiece& x, int s, int wq, uint32_t used0, uint32_t used1) {
@@ -242,8 +239,8 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
     const bool any = x.count[s] > 0, both = x.twin != 0;
     const int r = wq * 32 + lane, tok = r / p.heads;
     const int kvh = x.unit / p.chunks, h = (x.unit - kvh * p.chunks) * p.heads + r - tok * p.heads;
-    const int tok0 = stream_first(x, s);
-    const bool live = tok < stream_tokens(x, s) && h < p.group;
+    const int tok0 = x.tok0[s];
+    const bool live = tok < x.toks[s] && h < p.group;
     const uint32_t o_addr = tmem + (uint32_t(wq) << 21) + 256 + s * D;
     float m = kMaxFloor, l = 0.0f, f0 = 1.0f, f1 = 0.0f;  // the state, and the streams' shares of it
     bool on0 = false, on1 = false;                        // a state without a weight may have no accumulator
@@ -309,35 +306,29 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
 
   if (warp >= C::kMmaWarp) {
     regs_fewer<C::kLoadRegs>();
-    if (warp == C::kLoadWarp) {
-      // ---------------------------------------------------------------- pieces, Q, and over bf16 K and V tiles
-      // The whole warp runs this with warp-uniform values; one elected lane issues.
+    if (warp == C::kListWarp) {
+      // ---------------------------------------------------------------- list -> pieces
       const bool line = load_now(&p.header->line) != 0;
       const int end = line ? load_now(p.cta_first + blockIdx.x + 1) : load_now(&p.header->items) * p.units;
-      const uint64_t once = l2_evict_first_policy(), again = l2_evict_last_policy();
-      [[maybe_unused]] RingAt<C::kK> kr;
-      [[maybe_unused]] RingAt<C::kV> vr;
-      [[maybe_unused]] uint32_t k_filled = 0, v_filled = 0, tiles = 0;
-      uint32_t put = 0, q_used[2] = {0, 0};
       // an int of a list entry to a lane: entry w of the CTA's own, or unit of work w of the list of whole items
       static_assert(sizeof(PromptItem) == 48, "12 ints");
       int w = line ? load_now(p.cta_first + blockIdx.x) : blockIdx.x;
-      auto fetch = [&](int w) {
-        if (w >= end) return 0;
-        const auto* at = reinterpret_cast<const int*>(p.list + (line ? w : w / p.units));
-        int e = lane < 12 ? load_now(at + lane) : 0;
-        if (line) return e;
-        // some entry of the sequence: its units of work are those of a head unit after the other
-        const int first = __shfl_sync(kAll, e, 10), count = __shfl_sync(kAll, e, 11);
-        const int in_seq = w - first * p.units, unit = in_seq / count, index = first + in_seq - unit * count;
-        if (index != w / p.units) e = lane < 12 ? load_now(reinterpret_cast<const int*>(p.list + index) + lane) : 0;
-        return lane == 10 ? unit : e;
-      };
-      int entry = fetch(w);
-      for (;;) {
+      uint32_t solo = 0;  // the stream of the next piece that only needs one
+      for (uint32_t put = 0;;) {
         PromptPiece x;
         x.tiles = -1;
+        unsigned ticket = 0;
+        if (!line && w < end && lane == 0) ticket = atomicAdd(&p.header->ticket, 1u);  // the unit after this one
         if (w < end) {
+          int entry = lane < 12 ? load_now(reinterpret_cast<const int*>(p.list + (line ? w : w / p.units)) + lane) : 0;
+          x.unit = __shfl_sync(kAll, entry, 10);
+          if (!line) {
+            // some entry of the sequence: its units of work are those of a head unit after the other
+            const int first = x.unit, count = __shfl_sync(kAll, entry, 11), in_seq = w - first * p.units;
+            x.unit = in_seq / count;
+            const int index = first + in_seq - x.unit * count;
+            if (index != w / p.units) entry = lane < 12 ? load_now(reinterpret_cast<const int*>(p.list + index) + lane) : 0;
+          }
           x.seq = __shfl_sync(kAll, entry, 0);
           x.row0 = __shfl_sync(kAll, entry, 1);
           x.ntok = __shfl_sync(kAll, entry, 2);
@@ -348,20 +339,25 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
           x.tiles = __shfl_sync(kAll, entry, 7);
           x.part = __shfl_sync(kAll, entry, 8);
           x.shared = __shfl_sync(kAll, entry, 9);
-          x.unit = __shfl_sync(kAll, entry, 10);
-          x.twin = x.ntok <= p.stream_tokens && x.tiles > 1;
           const PromptSpan span = prompt_span(p, x.pos0, x.pos0 + x.ntok - 1, x.len);
           x.lo = span.lo;
           x.hi = span.hi;
+          // Up to one stream's rows: both streams' over several tiles; over one, those of either stream in turn, so that
+          // the next piece need not wait for this one.
+          const bool single = x.ntok <= p.stream_tokens;
+          x.twin = single && x.tiles > 1;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            const int n = stream_tokens(x, s), pos = x.pos0 + s * p.stream_tokens;
+            x.tok0[s] = single ? 0 : s * p.stream_tokens;
+            x.toks[s] = single ? (x.twin || uint32_t(s) == solo ? x.ntok : 0) : min(p.stream_tokens, x.ntok - x.tok0[s]);
+            const int pos = x.pos0 + x.tok0[s];
             int f, c;
-            span_tiles(prompt_span(p, pos, pos + n - 1, x.len), f, c);
+            span_tiles(prompt_span(p, pos, pos + x.toks[s] - 1, x.len), f, c);
             const int a = max(f, x.tile0), b = min(f + c, x.tile0 + x.tiles);
             x.first[s] = x.twin ? s : a - x.tile0;
-            x.count[s] = x.twin ? (x.tiles + 1 - s) >> 1 : n > 0 ? max(0, b - a) : 0;
+            x.count[s] = x.twin ? (x.tiles + 1 - s) >> 1 : x.toks[s] > 0 ? max(0, b - a) : 0;
           }
+          if (single && !x.twin) solo ^= 1u;
         }
         if (put >= kPieceQueue && !wait_all(sy->piece_empty + queue.st, queue.ph ^ 1u)) {
           alive = false;
@@ -375,6 +371,18 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         queue.next();
         ++put;
         if (x.tiles < 0) break;
+        w = line ? w + 1 : int(min(__shfl_sync(kAll, ticket, 0), unsigned(INT_MAX / 2))) + int(gridDim.x);
+      }
+    } else if (warp == C::kLoadWarp) {
+      // ---------------------------------------------------------------- Q, and over bf16 K and V tiles
+      // The whole warp runs this with warp-uniform values; one elected lane issues.
+      const uint64_t once = l2_evict_first_policy(), again = l2_evict_last_policy();
+      [[maybe_unused]] RingAt<C::kK> kr;
+      [[maybe_unused]] RingAt<C::kV> vr;
+      [[maybe_unused]] uint32_t k_filled = 0, v_filled = 0, tiles = 0;
+      uint32_t q_used[2] = {0, 0};
+      for (; take(); done()) {
+        const PromptPiece x = sy->piece[queue.st];
         const int kvh = x.unit / p.chunks, head = kvh * p.group + (x.unit - kvh * p.chunks) * p.heads;
         auto load_q = [&]() {
 #pragma unroll
@@ -389,28 +397,15 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
               mbar_arrive_expect_tx(sy->q_full + s, C::kHalves * p.heads * p.stream_tokens * 128);
 #pragma unroll
               for (int span = 0; span < C::kHalves; ++span)
-                tma_load_3d(smem + s * C::kTileBytes + span * C::kHalfBytes, &tmap_q, span * 64, head,
-                            x.row0 + stream_first(x, s), sy->q_full + s, once);
+                tma_load_3d(smem + s * C::kTileBytes + span * C::kHalfBytes, &tmap_q, span * 64, head, x.row0 + x.tok0[s],
+                            sy->q_full + s, once);
             }
             __syncwarp();
           }
         };
-        // The next piece.  Units off the list are taken late, so that each goes to a CTA that will be free for it.
-        int w_next = w + 1;
-        unsigned ticket = 0;
-        auto ask = [&]() {
-          if (!line && lane == 0) ticket = atomicAdd(&p.header->ticket, 1u);
-        };
-        auto follow = [&]() {
-          if (!line) w_next = int(min(__shfl_sync(kAll, ticket, 0), unsigned(INT_MAX / 2))) + gridDim.x;
-          entry = fetch(w_next);
-        };
         if constexpr (C::kQuant) {
           load_q();
-          alive = alive && wait_all(&sy->late, (put - 1) & 1);
           if (!alive) break;
-          ask();
-          follow();
         } else {
           const int lead = x.twin ? 2 : 1;
           const uint64_t policy = x.shared ? again : once;
@@ -449,7 +444,6 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             }
             __syncwarp();
           };
-          const int ask_at = max(-lead, x.tiles - 3 - lead), follow_at = max(-lead, x.tiles - 2 - lead);
 #pragma unroll 1
           for (int j = -lead; j < x.tiles; ++j) {
             if (j + lead < x.tiles) {
@@ -486,7 +480,6 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             }
             if (j == -lead) load_q();  // behind the first K: that need not wait for the last piece's products
             if (!alive) break;
-            if (j == ask_at) ask();
             if (j >= 0) {
               if (v_filled >= C::kV && !wait_all(sy->v_empty + vr.st, vr.ph ^ 1u)) {
                 alive = false;
@@ -497,12 +490,10 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
               ++v_filled;
               vr.next();
             }
-            if (j == follow_at) follow();
           }
           tiles += x.tiles;
           if (!alive) break;
         }
-        w = w_next;
       }
       // the copies in flight land before the CTA can end (the stages filled last, and Q)
       for (uint32_t j = 0; j < min(k_filled, uint32_t(C::kK)); ++j) {
@@ -654,7 +645,8 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       for (; take(); done()) {
         const PromptPiece& x = sy->piece[queue.st];
 #pragma unroll 1
-        for (int s = 0; s < (x.twin ? 1 : 2) && alive; ++s) alive = write_out(x, s, warp & 3, used0, used1);
+        for (int s = 0; s < (x.twin ? 1 : 2) && alive; ++s)
+          if (x.toks[s] > 0) alive = write_out(x, s, warp & 3, used0, used1);
         if (!alive) break;
         used0 ^= x.count[0] > 0;
         used1 ^= x.count[1] > 0;
@@ -685,7 +677,6 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         const int blk0 = lo / kBlockSize, blk1 = (hi + kBlockSize - 1) / kBlockSize;
         const uint8_t* mine = cache + (kvh * kBlockSize + sub) * D + chunk * 16;
         const int block_bytes = p.kv_heads * (kBlockSize * D);
-        if (n == 0 && warp == C::kConvertWarp && lane == 0) mbar_arrive(&sy->late);
         // The warp's two blocks of a tile, asked for a tile ahead of their codes: -1 where no token of the item lies in one.
         int next0 = -1, next1 = -1;
         auto ask = [&](int tile) {
@@ -729,7 +720,6 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         for (int t = 0; t < n; ++t) {
           if (filled >= C::kK && !(alive = wait_all(empty + at.st, at.ph ^ 1u))) break;
           if (!is_v) {
-            if (wq == 0 && lane == 0 && t == max(0, n - 3)) mbar_arrive(&sy->late);
             auto* slot = reinterpret_cast<float*>(smem + C::kSlotOff + (tiles + t) % C::kSlots * 1024) + wq * 32 + lane;
             slot[0] = ks;
             slot[128] = vs;
@@ -784,8 +774,8 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       const uint32_t tiles0 = tiles;
       tiles += x.tiles;
       if (n > 0) {
-        const bool dead = tok >= stream_tokens(x, s), idle = __all_sync(kAll, dead);
-        const int pos = x.pos0 + stream_first(x, s) + tok;
+        const bool dead = tok >= x.toks[s], idle = __all_sync(kAll, dead);
+        const int pos = x.pos0 + x.tok0[s] + tok;
         PromptSpan span = prompt_span(p, pos, pos, x.len);
         if (dead) span = {0, INT_MAX};  // its values go nowhere
         float m = kMaxFloor, l = 0.0f;
@@ -950,7 +940,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         if (lane == 0) mbar_arrive(sy->stat_ready + s);
       }
       if constexpr (C::kQuant) {
-        if ((s == 0 || !x.twin) && !(alive = write_out(x, s, wq, used0, used1))) break;
+        if (x.toks[s] > 0 && (s == 0 || !x.twin) && !(alive = write_out(x, s, wq, used0, used1))) break;
       }
       used0 ^= x.count[0] > 0;
       used1 ^= x.count[1] > 0;
