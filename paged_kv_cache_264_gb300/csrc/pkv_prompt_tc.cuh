@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         // the stream's tiles are first, first + lead, ... last
         const int first = x.first[s], count = x.count[s], last = first + (count - 1) * lead;
         const int lo0 = x.lo - tile0 * kPromptTile, hi0 = x.hi - tile0 * kPromptTile;
+        const bool both = count > 0 && x.count[s ^ 1] > 0;
         bool fresh = true;  // O holds nothing of this piece yet
 #pragma unroll 1
         for (int j = -lead; j < n; ++j) {
@@ -565,8 +566,10 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
           }
           if (qk && j + lead == first && !(alive = wait_all(sy->q_full + s, used))) break;
           // Products of the two streams side by side would both be late: the warps issue in turn.
-          if ((s == 1 || turns > 0) && !(alive = wait_all(sy->turn + s, (s == 1 ? turns : turns - 1) & 1))) break;
-          ++turns;
+          if (both) {
+            if ((s == 1 || turns > 0) && !(alive = wait_all(sy->turn + s, (s == 1 ? turns : turns - 1) & 1))) break;
+            ++turns;
+          }
           tc_fence_after();
           if (pv) {
             bool on = !fresh;
@@ -611,12 +614,12 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                 const uint32_t o = ((i >> 2) * C::kHalfBytes + (i & 3) * 32) >> 4;
                 tc_mma_ss(t_s, q_desc + o, kd + o, kHi, desc_s, i > 0);
               }
-              mbar_arrive(sy->turn + (s ^ 1));
+              if (both) mbar_arrive(sy->turn + (s ^ 1));
               tc_commit(sy->s_ready + s);
               tc_commit(sy->k_empty + kr.st);
               if (j + lead == last) tc_commit(sy->q_empty + s);
             } else {
-              mbar_arrive(sy->turn + (s ^ 1));
+              if (both) mbar_arrive(sy->turn + (s ^ 1));
               if (has_k) mbar_arrive(sy->k_empty + kr.st);
             }
           }
