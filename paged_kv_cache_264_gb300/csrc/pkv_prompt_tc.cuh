@@ -76,7 +76,7 @@ struct PromptPiece {
   int len, key0;
   int tile0, tiles;           // tiles < 0: there is no more work
   int lo, hi;                 // tokens that some row of the item sees
-  int part, unit;
+  int part, kvh, head0;       // partial (-1: none), kv head, first of its query heads
   int twin;                   // both streams hold the same rows and take every other tile
   int shared;                 // the tiles are read again by other items
   int tok0[2], toks[2];       // each stream's first token and tokens
@@ -89,7 +89,7 @@ struct PromptCfg {
   static constexpr int kHalves = D / 64;                       // 128-byte spans of a row
   static constexpr int kTileBytes = kPromptTile * D * 2;       // one K, V or Q tile
   static constexpr int kHalfBytes = kPromptTile * 128;         // one span of all its rows
-  static constexpr int kK = (D == 128 ? 2 : 4), kV = (D == 128 ? (kQuant ? 2 : 3) : 4);  // stages of the rings
+  static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 && !kQuant ? 3 : kK;  // stages of the rings
   // A tile's scales are read by its softmax.  K of tile n + kSlots takes its stage once S of tile n + kSlots - kK
   // has been formed, behind the products over V of all tiles two or more before that.
   static constexpr int kSlots = kQuant ? (D == 128 ? 4 : 8) : 0;
@@ -100,8 +100,8 @@ struct PromptCfg {
                        kListWarp = kMmaWarp + 3;
   static constexpr int kReaders = kMmaWarp + 3;                // warps that take pieces
   // Registers a thread: the launch's, shared out anew by warpgroup.
-  static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 144 : 192, kSideRegs = kQuant ? 72 : 56,
-                       kLoadRegs = kQuant ? 48 : 72;
+  static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 160 : 192, kSideRegs = kQuant ? 56 : 64,
+                       kLoadRegs = kQuant ? 48 : 64;
   static_assert(2 * kSoftmaxRegs + (kQuant ? 2 : 1) * kSideRegs + kLoadRegs <= kThreads / 128 * kRegs, "registers");
   static constexpr int kRingOff = 2 * kTileBytes;              // Q tiles of both streams first
   static constexpr int kVOff = kRingOff + kK * kTileBytes;
@@ -232,15 +232,14 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
     if (lane == 0) mbar_arrive(sy->piece_empty + queue.st);
     queue.next();
   };
-  // Finished rows of stream s (of both streams, where they hold the same): a thread to a row, run by the four
-  // warps of a warpgroup.  used0, used1: the parities of the streams' accumulators of this piece.
-  [[maybe_unused]] auto write_out = [&](const PromptPiece& x, int s, int wq, uint32_t used0, uint32_t used1) {
+  // Finished rows of stream s (of both streams, where they hold the same): a thread to a row of the accumulator, run by
+  // the four warps of a warpgroup.  Each thread stores its own: turned through shared memory first, so that an
+  // instruction's stores lie in 8 lines and not 32, was no faster.
+  // used0, used1: the parities of the streams' accumulators of this piece; tok, h: this thread's row.
+  [[maybe_unused]] auto write_out = [&](const PromptPiece& x, int s, int wq, int tok, int h, uint32_t used0, uint32_t used1) {
     const uint32_t used = s ? used1 : used0;
     const bool any = x.count[s] > 0, both = x.twin != 0;
-    const int r = wq * 32 + lane, tok = r / p.heads;
-    const int kvh = x.unit / p.chunks, h = (x.unit - kvh * p.chunks) * p.heads + r - tok * p.heads;
-    const int tok0 = x.tok0[s];
-    const bool live = tok < x.toks[s] && h < p.group;
+    const bool live = tok < x.toks[s] && x.head0 + h < p.group;
     const uint32_t o_addr = tmem + (uint32_t(wq) << 21) + 256 + s * D;
     float m = kMaxFloor, l = 0.0f, f0 = 1.0f, f1 = 0.0f;  // the state, and the streams' shares of it
     bool on0 = false, on1 = false;                        // a state without a weight may have no accumulator
@@ -248,6 +247,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       if (!wait_all(sy->stat_ready + s, used) || !wait_all(sy->o_ready + s, used)) return false;
       if (both && (!wait_all(sy->stat_ready + 1, used1) || !wait_all(sy->o_ready + 1, used1))) return false;
       tc_fence_after();
+      const int r = wq * 32 + lane;
       const float2 a = stats[s * 128 + r];
       m = a.x;
       l = a.y;
@@ -261,39 +261,45 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         l = (on0 ? f0 * a.y : 0.0f) + (on1 ? f1 * b.y : 0.0f);
       }
     }
-    const int64_t part = x.part >= 0 ? int64_t(x.part) * p.part_rows + tok0 * p.heads + r : 0;
-    if (x.part >= 0 && live) p.ml[part] = make_float2(m, l);
-    const float inv = x.part >= 0 ? 1.0f : 1.0f / l;
-    f0 *= inv;
-    f1 *= inv;
-    float* acc = p.acc + part * D;
-    auto* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(x.row0 + tok0 + tok) * p.out_stride + (int64_t(kvh) * p.group + h) * D;
-#pragma unroll 1
-    for (int c0 = 0; c0 < D; c0 += 16) {
-      float o[16];
-      if (any) {
-        tmem_ld16(o_addr + c0, o);
-        tmem_wait_ld();
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] = on0 ? o[e] * f0 : 0.0f;
-      if (both) {
-        float o1[16];
-        tmem_ld16(o_addr + D + c0, o1);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = on1 ? fmaf(o1[e], f1, o[e]) : o[e];
-      }
-      if (live && x.part >= 0) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) reinterpret_cast<float4*>(acc + c0)[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+    if (__any_sync(kAll, live)) {
+      const bool partial = x.part >= 0;
+      float* acc = p.acc;
+      auto* out = static_cast<__nv_bfloat16*>(p.out);
+      if (live && partial) {
+        const int64_t row = int64_t(x.part) * p.part_rows + x.tok0[s] * p.heads + wq * 32 + lane;
+        p.ml[row] = make_float2(m, l);
+        acc += row * D;
       } else if (live) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          reinterpret_cast<uint4*>(out + c0)[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                                             pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+        out += int64_t(x.row0 + x.tok0[s] + tok) * p.out_stride + (x.kvh * p.group + x.head0 + h) * D;
+        const float inv = 1.0f / l;
+        f0 *= inv;
+        f1 *= inv;
       }
-      __syncwarp();
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 16) {
+        float o[16], o1[16];
+        if (any) {
+          tmem_ld16(o_addr + c0, o);
+          if (both) tmem_ld16(o_addr + D + c0, o1);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = on0 ? o[e] * f0 : 0.0f;
+        if (both) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = on1 ? fmaf(o1[e], f1, o[e]) : o[e];
+        }
+        if (live && partial) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) reinterpret_cast<float4*>(acc + c0)[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else if (live) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            reinterpret_cast<uint4*>(out + c0)[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                                               pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+        }
+        __syncwarp();
+      }
     }
     tc_fence_before();
     __syncwarp();
@@ -321,12 +327,12 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         if (!line && w < end && lane == 0) ticket = atomicAdd(&p.header->ticket, 1u);  // the unit after this one
         if (w < end) {
           int entry = lane < 12 ? load_now(reinterpret_cast<const int*>(p.list + (line ? w : w / p.units)) + lane) : 0;
-          x.unit = __shfl_sync(kAll, entry, 10);
+          int unit = __shfl_sync(kAll, entry, 10);
           if (!line) {
             // some entry of the sequence: its units of work are those of a head unit after the other
-            const int first = x.unit, count = __shfl_sync(kAll, entry, 11), in_seq = w - first * p.units;
-            x.unit = in_seq / count;
-            const int index = first + in_seq - x.unit * count;
+            const int first = unit, count = __shfl_sync(kAll, entry, 11), in_seq = w - first * p.units;
+            unit = in_seq / count;
+            const int index = first + in_seq - unit * count;
             if (index != w / p.units) entry = lane < 12 ? load_now(reinterpret_cast<const int*>(p.list + index) + lane) : 0;
           }
           x.seq = __shfl_sync(kAll, entry, 0);
@@ -339,6 +345,8 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
           x.tiles = __shfl_sync(kAll, entry, 7);
           x.part = __shfl_sync(kAll, entry, 8);
           x.shared = __shfl_sync(kAll, entry, 9);
+          x.kvh = unit / p.chunks;
+          x.head0 = (unit - x.kvh * p.chunks) * p.heads;
           const PromptSpan span = prompt_span(p, x.pos0, x.pos0 + x.ntok - 1, x.len);
           x.lo = span.lo;
           x.hi = span.hi;
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       uint32_t q_used[2] = {0, 0};
       for (; take(); done()) {
         const PromptPiece x = sy->piece[queue.st];
-        const int kvh = x.unit / p.chunks, head = kvh * p.group + (x.unit - kvh * p.chunks) * p.heads;
+        const int kvh = x.kvh, head = kvh * p.group + x.head0;
         auto load_q = [&]() {
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
@@ -645,11 +653,12 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
     if constexpr (!C::kQuant) {
       // ---------------------------------------------------------------- finished accumulators -> out, or partials
       uint32_t used0 = 0, used1 = 0;
+      const int wq = warp & 3, r = wq * 32 + lane, tok = r / p.heads, h = r - tok * p.heads;
       for (; take(); done()) {
         const PromptPiece& x = sy->piece[queue.st];
 #pragma unroll 1
         for (int s = 0; s < (x.twin ? 1 : 2) && alive; ++s)
-          if (x.toks[s] > 0) alive = write_out(x, s, warp & 3, used0, used1);
+          if (x.toks[s] > 0) alive = write_out(x, s, wq, tok, h, used0, used1);
         if (!alive) break;
         used0 ^= x.count[0] > 0;
         used1 ^= x.count[1] > 0;
@@ -675,7 +684,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       for (; take(); done()) {
         const PromptPiece& x = sy->piece[queue.st];
         const int n = x.tiles, tile0 = x.tile0, lo = x.lo, hi = x.hi;
-        const int kvh = x.unit / p.chunks;
+        const int kvh = x.kvh;
         const int32_t* table = p.block_tables + int64_t(x.seq) * p.max_blocks_per_seq;
         const int blk0 = lo / kBlockSize, blk1 = (hi + kBlockSize - 1) / kBlockSize;
         const uint8_t* mine = cache + (kvh * kBlockSize + sub) * D + chunk * 16;
@@ -943,7 +952,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         if (lane == 0) mbar_arrive(sy->stat_ready + s);
       }
       if constexpr (C::kQuant) {
-        if (x.toks[s] > 0 && (s == 0 || !x.twin) && !(alive = write_out(x, s, wq, used0, used1))) break;
+        if (x.toks[s] > 0 && (s == 0 || !x.twin) && !(alive = write_out(x, s, wq, tok, r - tok * p.heads, used0, used1))) break;
       }
       used0 ^= x.count[0] > 0;
       used1 ^= x.count[1] > 0;
