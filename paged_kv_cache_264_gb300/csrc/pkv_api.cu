@@ -446,6 +446,7 @@ void prompt_heads(int group, int* heads, int* chunks) {
 // Layout of a prompt attention call's workspace, and its parameters that follow from the shape.
 struct PromptPlan {
   int heads, chunks, units, stream_tokens, max_parts, part_rows;
+  int direct;  // units of work that a call without a plan may have (0: it has one)
   size_t list, joins, ctas, starts, entries, acc, ml, bytes;  // offsets (the header sits at 0), size
 };
 
@@ -459,11 +460,12 @@ pkv_status make_prompt_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
   x->units = pool->kv_heads * x->chunks;
   x->stream_tokens = pkv::kRowTile / x->heads;
   const int64_t per = 2 * x->stream_tokens;
+  const int64_t items = num_seqs + num_tokens / per, work = items * x->units, tiles = ceil_div(max_context_len, pkv::kPromptTile);
+  // Without a plan a short call is one launch of three.  DIRECT_FIGURES
+  x->direct = num_seqs <= pkv::kDirectSeqs && work <= pool->sm_count && tiles <= pkv::kDirectTiles ? static_cast<int>(work) : 0;
   // A CTA's stretch of the line holds pieces of at most two units that are cut.
-  const bool cut = ceil_div(max_context_len, pkv::kPromptTile) > pkv::kPromptWhole;
-  x->max_parts = cut ? 2 * pool->sm_count : 0;
+  x->max_parts = tiles > pkv::kPromptWhole && !x->direct ? 2 * pool->sm_count : 0;
   x->part_rows = static_cast<int>(std::min(per, num_tokens)) * x->heads;
-  const int64_t items = num_seqs + num_tokens / per, work = items * x->units;
   if (work > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -571,7 +573,8 @@ pkv_status prompt_attention(const pkv_pool* pool, const pkv_prefill* a, bool pag
   p.chunks = plan.chunks;
   p.units = plan.units;
   p.stream_tokens = plan.stream_tokens;
-  p.grid = pool->sm_count;
+  p.grid = plan.direct ? plan.direct : pool->sm_count;
+  p.direct = plan.direct != 0;
   p.max_parts = plan.max_parts;
   p.part_rows = plan.part_rows;
   p.header = reinterpret_cast<pkv::PromptHeader*>(ws);
@@ -595,12 +598,12 @@ pkv_status prompt_attention(const pkv_pool* pool, const pkv_prefill* a, bool pag
     return PKV_ERR_UNSUPPORTED;
   }
   const auto s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = pkv::launch_prompt_plan(p, s);
+  cudaError_t e = plan.direct ? cudaSuccess : pkv::launch_prompt_plan(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention: plan launch");
   e = paged && pool->dtype != PKV_KV_BF16 ? pkv::launch_prompt_quant(p, tq, static_cast<pkv::KvType>(pool->dtype), s)
                                           : pkv::launch_prompt_bf16(p, tq, tk, tv, s);
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
-  g_launches.fetch_add(2, std::memory_order_relaxed);
+  g_launches.fetch_add(plan.direct ? 1 : 2, std::memory_order_relaxed);
   if (plan.max_parts == 0) return PKV_OK;
   e = pkv::launch_prompt_join(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention: join launch");

@@ -11,13 +11,17 @@ namespace {
 
 constexpr int kGatherThreads = 256;
 
-// A CTA takes a tile of tokens at a time, finds each one's place in the pool, and then a thread moves
-// 8 values at a time.
+// A CTA takes 32 tokens at a time (of a long sequence: whole blocks, which lie in one piece in the pool) and finds
+// the next ones' places meanwhile.  A thread moves 16 bytes of K and of V at a time, kAhead of each on their way.
+// Bound by memory.  MEASURED
 template <KvType KV, int D>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p) {
-  constexpr int kChunks = D / 8;  // per (token, head) row
-  constexpr int kTile = 32;       // tokens
-  __shared__ int64_t place[kTile];   // block * 16 + offset; -1: rows of zeros, -2: no token
+  constexpr bool kQuant = KV != KvType::kBf16;
+  constexpr int kValues = kQuant ? 16 : 8;   // of a 16-byte load
+  constexpr int kChunks = D / kValues;       // per (token, head) row
+  constexpr int kTile = 32;                  // tokens
+  constexpr int kAhead = kQuant ? 2 : 4;
+  __shared__ int64_t places[2][kTile];       // block * 16 + offset; -1: rows of zeros, -2: no token
   griddep_wait();
   griddep_launch_dependents();
   // The starts are checked by every CTA: one that writes must know that all are valid.
@@ -31,68 +35,95 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
     return;
   }
   const int first = __ldg(p.token_starts), last = __ldg(p.token_starts + p.num_seqs);
-  for (int64_t t0 = first + int64_t(blockIdx.x) * kTile; t0 < last; t0 += int64_t(gridDim.x) * kTile) {
-    __syncthreads();
-    if (threadIdx.x < kTile) {
-      const int64_t t = t0 + threadIdx.x;
-      int64_t at = -2;
-      if (t < last) {
-        int lo = 0, hi = p.num_seqs;
-        while (hi - lo > 1) {  // the last sequence that starts at or before t
-          const int mid = (lo + hi) >> 1;
-          if (__ldg(p.token_starts + mid) <= t) lo = mid; else hi = mid;
-        }
-        const int from = p.first_positions ? __ldg(p.first_positions + lo) : 0;
-        const int64_t pos = int64_t(from) + (t - __ldg(p.token_starts + lo));
-        at = -1;
-        if (from < 0 || pos >= int64_t(p.max_blocks_per_seq) * kBlockSize) {
-          set_error(p.err, kErrContextLen);
-        } else {
-          const int id = __ldg(p.block_tables + int64_t(lo) * p.max_blocks_per_seq + pos / kBlockSize);
-          if (id < 0 || id >= p.num_blocks) set_error(p.err, kErrBlockId);
-          else at = int64_t(id) * kBlockSize + pos % kBlockSize;
-        }
-      }
-      place[threadIdx.x] = at;
+  auto find = [&](int64_t t) -> int64_t {
+    if (t >= last) return -2;
+    int lo = 0, hi = p.num_seqs;
+    while (hi - lo > 1) {  // the last sequence that starts at or before t
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.token_starts + mid) <= t) lo = mid; else hi = mid;
     }
-    __syncthreads();
-    const int per_token = p.kv_heads * kChunks;
-    for (int i = threadIdx.x; i < kTile * per_token; i += kGatherThreads) {
-      const int tok = i / per_token, rest = i - tok * per_token, h = rest / kChunks, c = rest - h * kChunks;
-      const int64_t at = place[tok];
-      if (at == -2) continue;
-      const int64_t block = at / kBlockSize, row = (block * p.kv_heads + h) * kBlockSize + (at - block * kBlockSize);
-      auto move = [&](const void* cache, const float* scale, void* to, int64_t stride) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    const int from = p.first_positions ? __ldg(p.first_positions + lo) : 0;
+    const int64_t pos = int64_t(from) + (t - __ldg(p.token_starts + lo));
+    if (from < 0 || pos >= int64_t(p.max_blocks_per_seq) * kBlockSize) {
+      set_error(p.err, kErrContextLen);
+      return -1;
+    }
+    const int id = __ldg(p.block_tables + int64_t(lo) * p.max_blocks_per_seq + pos / kBlockSize);
+    if (id < 0 || id >= p.num_blocks) {
+      set_error(p.err, kErrBlockId);
+      return -1;
+    }
+    return int64_t(id) * kBlockSize + pos % kBlockSize;
+  };
+  // this thread's chunks: (token, rest) of chunk i = threadIdx.x + j * kGatherThreads, rest = head * kChunks + chunk
+  const int per_token = p.kv_heads * kChunks, all = kTile * per_token;
+  const int step_tok = kGatherThreads / per_token, step_rest = kGatherThreads - step_tok * per_token;
+  const int tok0 = int(threadIdx.x) / per_token, rest0 = int(threadIdx.x) - tok0 * per_token;
+  int64_t t0 = first + int64_t(blockIdx.x) * kTile;
+  if (threadIdx.x < kTile) places[0][threadIdx.x] = find(t0 + threadIdx.x);
+  for (int buf = 0; t0 < last; t0 += int64_t(gridDim.x) * kTile, buf ^= 1) {
+    __syncthreads();  // places are there, and the last tile's have been read
+    const int64_t t1 = t0 + int64_t(gridDim.x) * kTile;
+    if (threadIdx.x < kTile && t1 < last) places[buf ^ 1][threadIdx.x] = find(t1 + threadIdx.x);
+    int tok = tok0, rest = rest0;
+    for (int i = threadIdx.x; i < all; i += kAhead * kGatherThreads) {
+      uint4 kw[kAhead], vw[kAhead];
+      float ks[kAhead], vs[kAhead];
+      int64_t to[kAhead];  // row of the output; -1: none
+      int off[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int64_t at = i + u * kGatherThreads < all ? places[buf][tok] : -2;
+        const int h = rest / kChunks, c = rest - h * kChunks;
+        to[u] = at == -2 ? -1 : t0 + tok;
+        off[u] = h * D + c * kValues;
+        kw[u] = vw[u] = make_uint4(0u, 0u, 0u, 0u);
+        ks[u] = vs[u] = 0.0f;
         if (at >= 0) {
-          if constexpr (KV == KvType::kBf16) {
-            w = __ldg(reinterpret_cast<const uint4*>(cache) + row * kChunks + c);
-          } else {
-            const uint2 codes = __ldg(reinterpret_cast<const uint2*>(cache) + row * kChunks + c);
-            const float s = __ldg(scale + row);
-            float f[8];
-            if constexpr (KV == KvType::kFp8) {
-              float a[4], b[4];
-              e4m3x4_to_f32(codes.x, a);
-              e4m3x4_to_f32(codes.y, b);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                f[e] = a[e];
-                f[4 + e] = b[e];
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] = i8_from_flipped((e < 4 ? codes.x : codes.y) ^ 0x80808080u, e & 3);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= s;
-            w = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+          const int64_t block = at / kBlockSize, row = (block * p.kv_heads + h) * kBlockSize + (at - block * kBlockSize);
+          kw[u] = __ldcs(static_cast<const uint4*>(p.k_cache) + row * kChunks + c);
+          vw[u] = __ldcs(static_cast<const uint4*>(p.v_cache) + row * kChunks + c);
+          if constexpr (kQuant) {
+            ks[u] = __ldg(p.k_scale + row);
+            vs[u] = __ldg(p.v_scale + row);
           }
         }
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(to) + (t0 + tok) * stride + h * D + c * 8) = w;
-      };
-      move(p.k_cache, p.k_scale, p.k, p.k_stride);
-      move(p.v_cache, p.v_scale, p.v, p.v_stride);
+        tok += step_tok;
+        rest += step_rest;
+        if (rest >= per_token) {
+          rest -= per_token;
+          ++tok;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (to[u] < 0) continue;
+        auto put = [&](void* base, int64_t stride, const uint4& w, float s) {
+          auto* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + to[u] * stride + off[u]);
+          if constexpr (!kQuant) {
+            __stcs(dst, w);
+          } else {
+            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+            uint32_t out[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float f[4];
+              if constexpr (KV == KvType::kFp8) {
+                e4m3x4_to_f32(words[q], f);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = i8_from_flipped(words[q] ^ 0x80808080u, e);
+              }
+              out[2 * q] = pack_bf16x2(f[0] * s, f[1] * s);
+              out[2 * q + 1] = pack_bf16x2(f[2] * s, f[3] * s);
+            }
+            __stcs(dst, make_uint4(out[0], out[1], out[2], out[3]));
+            __stcs(dst + 1, make_uint4(out[4], out[5], out[6], out[7]));
+          }
+        };
+        put(p.k, p.k_stride, kw[u], ks[u]);
+        put(p.v, p.v_stride, vw[u], vs[u]);
+      }
     }
   }
 }

@@ -265,6 +265,7 @@ struct PromptParams {
   int heads, chunks, units;     // heads of a chunk, chunks of a kv head, units = kv_heads * chunks
   int stream_tokens;            // tokens of a stream's rows
   int grid;
+  int direct;                   // no plan: at most a unit of work per CTA
   int max_parts;                // partials that there is room for
   int part_rows;                // rows of a partial
   // workspace
@@ -279,6 +280,8 @@ struct PromptParams {
 };
 constexpr int kPromptTile = 128;  // tokens of one tile
 constexpr int kRowTile = 128;     // rows of one stream
+constexpr int kDirectSeqs = 32;   // calls of up to this many sequences, of up to this many tiles each, and of
+constexpr int kDirectTiles = 4;   // at most a unit of work per CTA have no plan
 constexpr int kPromptWhole = 3;   // units of up to this many tiles are not cut
 constexpr int kPromptWaves = 8;   // up to this many units of work a CTA are shared out piece by piece
 cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream);

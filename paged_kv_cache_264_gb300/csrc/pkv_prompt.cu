@@ -58,31 +58,6 @@ __device__ __forceinline__ T block_scan(T v, T* part, T& total) {
   return r;
 }
 
-struct PromptSeq {
-  int row0, n, len, key0;
-};
-// Sequence b; false where its starts are invalid.  len is 0 where its length is.
-__device__ __forceinline__ bool prompt_seq(const PromptParams& p, int b, PromptSeq& s, bool& bad_len) {
-  s.row0 = __ldg(p.query_starts + b);
-  const int end = __ldg(p.query_starts + b + 1);
-  s.n = end - s.row0;
-  s.key0 = 0;
-  bad_len = false;
-  if (s.row0 < 0 || end < s.row0 || end > p.num_tokens) return false;
-  if (p.paged) {
-    s.len = __ldg(p.context_lens + b);
-    if (s.n > 0 && (s.len < s.n || s.len > p.max_context_len)) {
-      bad_len = true;
-      s.len = 0;
-    }
-    return true;
-  }
-  s.key0 = __ldg(p.key_starts + b);
-  const int key1 = __ldg(p.key_starts + b + 1);
-  s.len = key1 - s.key0;
-  return s.key0 >= 0 && key1 >= s.key0 && key1 <= p.num_keys;
-}
-
 // The sequences' items, in shared memory where they fit.
 struct PromptItems {
   const PromptParams& p;
@@ -107,19 +82,7 @@ struct PromptItems {
     bool bad;
     if (held) s = held[b];
     else prompt_seq(p, b, s, bad);
-    const int per = 2 * p.stream_tokens, tok0 = index * per;
-    PromptItem x{};
-    x.seq = b;
-    x.row0 = s.row0 + tok0;
-    x.ntok = min(per, s.n - tok0);
-    x.pos0 = s.len - s.n + tok0;
-    x.len = s.len;
-    x.key0 = s.key0;
-    x.part = -1;
-    x.count = count;
-    x.shared = count > 1;
-    span_tiles(prompt_span(p, x.pos0, x.pos0 + x.ntok - 1, s.len), x.tile0, x.tiles);
-    return x;
+    return sequence_item(p, s, b, count, index);
   }
 };
 

@@ -314,11 +314,18 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
     regs_fewer<C::kLoadRegs>();
     if (warp == C::kListWarp) {
       // ---------------------------------------------------------------- list -> pieces
-      const bool line = load_now(&p.header->line) != 0;
-      const int end = line ? load_now(p.cta_first + blockIdx.x + 1) : load_now(&p.header->items) * p.units;
-      // an int of a list entry to a lane: entry w of the CTA's own, or unit of work w of the list of whole items
+      // an int of a list entry to a lane
       static_assert(sizeof(PromptItem) == 48, "12 ints");
-      int w = line ? load_now(p.cta_first + blockIdx.x) : blockIdx.x;
+      bool line = true;
+      int w = 0, end = 0, entry = 0;
+      if (p.direct) {  // few units, at most one per CTA: no list, a lane to a sequence
+        entry = direct_entry(p, lane);
+        end = __shfl_sync(kAll, entry, 12);
+      } else {
+        line = load_now(&p.header->line) != 0;
+        end = line ? load_now(p.cta_first + blockIdx.x + 1) : load_now(&p.header->items) * p.units;
+        w = line ? load_now(p.cta_first + blockIdx.x) : blockIdx.x;
+      }
       uint32_t solo = 0;  // the stream of the next piece that only needs one
       for (uint32_t put = 0;;) {
         PromptPiece x;
@@ -326,7 +333,8 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         unsigned ticket = 0;
         if (!line && w < end && lane == 0) ticket = atomicAdd(&p.header->ticket, 1u);  // the unit after this one
         if (w < end) {
-          int entry = lane < 12 ? load_now(reinterpret_cast<const int*>(p.list + (line ? w : w / p.units)) + lane) : 0;
+          // entry w of the CTA's own, or unit of work w of the list of whole items
+          if (!p.direct) entry = lane < 12 ? load_now(reinterpret_cast<const int*>(p.list + (line ? w : w / p.units)) + lane) : 0;
           int unit = __shfl_sync(kAll, entry, 10);
           if (!line) {
             // some entry of the sequence: its units of work are those of a head unit after the other
