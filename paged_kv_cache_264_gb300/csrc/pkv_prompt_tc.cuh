@@ -857,11 +857,13 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                 }
               }
             };
-            // The maximum is moved where a row's logits pass it; false where none of the warp's rows' do.
+            // The maximum moves where a row's logits pass it by kMaxSlack: what was weighed with the old one counts this
+            // much of it now.
             auto move = [&](const float (&mx)[4]) {
-              const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+              float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+              if constexpr (C::kQuant) bm = ceilf(bm);
               const bool grow = bm > m + kMaxSlack;
-              if (!__any_sync(kAll, grow)) return false;
+              if (!__any_sync(kAll, grow)) return 1.0f;
               const float mu = grow ? bm : m, f = fast_exp2(m - mu);
               m = mu;
               l *= f;
@@ -877,45 +879,72 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                   tmem_st16(o_addr + 16 * j, o);
                 }
               }
-              return true;
+              return f;
             };
             sum[0] = sum[1] = 0;
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if constexpr (C::kQuant) {
-              // Half a tile at a time: the upper half for its maximum, the lower one for its maximum and, kept, its
-              // weights, and the upper one again.  All 128 logits and the scales would not stay in registers, and
-              // spilled ones are far away with shared memory this full.  The loop stays rolled: the code of all roles
-              // shares an instruction cache.
+              // Half a tile at a time, once: weights are floating point, so a maximum that logits have passed by far does
+              // no harm until they overflow.  It is looked for in the first half of a row's tiles, and again where a
+              // half's weights add up to more than 2^64; it moves by whole powers of two, so that weights handed over
+              // already can be rescaled exactly.  (All 128 logits and the scales would not stay in registers, and
+              // spilled ones are far away with shared memory this full.  The loop stays rolled: the code of all roles shares an
+              // instruction cache.)
               float z[64], w[32];
 #pragma unroll 1
-              for (int phase = 0; phase < 3; ++phase) {
-                const int h = phase == 1 ? 0 : 1;
-                tmem_ld32(s_addr + 64 * h, z);
-                tmem_ld32(s_addr + 64 * h + 32, z + 32);
-                tmem_wait_ld();
+              for (int h = 0; h < 2; ++h) {
+                bool look = i == 0 && h == 0;
+                for (;;) {
+                  tmem_ld32(s_addr + 64 * h, z);
+                  tmem_ld32(s_addr + 64 * h + 32, z + 32);
+                  tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const ulonglong2 f = ks[16 * h + j];
-                  f32x2_parts(mul2(f32x2(z[4 * j], z[4 * j + 1]), f.x), z[4 * j], z[4 * j + 1]);
-                  f32x2_parts(mul2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y), z[4 * j + 2], z[4 * j + 3]);
+                  for (int j = 0; j < 16; ++j) {
+                    const ulonglong2 f = ks[16 * h + j];
+                    f32x2_parts(mul2(f32x2(z[4 * j], z[4 * j + 1]), f.x), z[4 * j], z[4 * j + 1]);
+                    f32x2_parts(mul2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y), z[4 * j + 2], z[4 * j + 3]);
+                  }
+                  if (cut) {
+                    mask(2 * h, z);
+                    mask(2 * h + 1, z + 32);
+                  }
+                  if (look) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mx[u] = -INFINITY;
+                    largest(z, 64, mx);
+                    const float f = move(mx);
+                    if (h == 1) {  // the lower half's weights
+                      const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
+#pragma unroll 1
+                      for (int c = 0; c < 32; c += 16) {
+                        float o[16];
+                        tmem_ld16(s_addr + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                          const uint32_t bits = __float_as_uint(o[e]);
+                          const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&bits), f2);
+                          o[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&r));
+                        }
+                        tmem_st16(s_addr + c, o);
+                      }
+                    }
+                  }
+                  sum[0] = sum[1] = 0;
+                  weigh(2 * h, 32, z, w);
+                  float lo_sum, hi_sum;
+                  f32x2_parts(add2(sum[0], sum[1]), lo_sum, hi_sum);
+                  lo_sum += hi_sum;
+                  if (look || !__any_sync(kAll, lo_sum > 0x1p64f)) {
+                    l += lo_sum;
+                    break;
+                  }
+                  look = true;
                 }
-                if (cut) {
-                  mask(2 * h, z);
-                  mask(2 * h + 1, z + 32);
-                }
-                if (phase < 2) largest(z, 64, mx);
-                if (phase == 0) continue;
-                if (phase == 1) move(mx);
-                weigh(2 * h, 32, z, w);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) tmem_st16(s_addr + 32 * h + 16 * c, w + 16 * c);
-                if (phase == 1) {
-                  tmem_wait_st();
-                  tc_fence_before();
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive(sy->p_half + s);
-                }
               }
+              sum[0] = sum[1] = 0;
             } else {
               float y[128], w[32];
 #pragma unroll
@@ -945,11 +974,12 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             l += sum_lo + sum_hi;
             tmem_wait_st();
             tc_fence_before();
-          } else if (lane == 0) {
-            mbar_arrive(sy->p_half + s);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(sy->p_ready + s);
+          if (lane == 0) {
+            if (C::kQuant || idle) mbar_arrive(sy->p_half + s);
+            mbar_arrive(sy->p_ready + s);
+          }
         }
         if (!alive) break;
         // the last piece's have been read once its accumulator has

@@ -154,6 +154,31 @@ def test_prefill_growing_logits():
     pool.close()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("jump", [3.0, 40.0, 300.0, 20000.0])
+def test_prefill_jumping_logits(jump, kv):
+    """Logits that jump by any amount at any column: within a tile, between its halves, after thousands."""
+    gen = torch.Generator(device="cuda").manual_seed(int(jump))
+    t, n, d = 1100, 70, 64
+    pool, tables = make_cache(gen, [t], 1, d, kv)
+    k = 0.05 * _randn(gen, t, 1, d)
+    k[:, 0, 0] = 0
+    at = [3, 70, 130, 200, 270, 700, 701, 1000]  # tokens whose logit is a jump above all before
+    for i, pos in enumerate(at):
+        k[pos, 0, 0] = (i + 1) * jump
+    v = _randn(gen, t, 1, d)
+    pos = torch.arange(t, device="cuda")
+    pool.reshape_and_cache(k.to(torch.bfloat16), v.to(torch.bfloat16), (tables[0, pos // 16] * 16 + pos % 16).to(torch.int32))
+    q = _randn(gen, n, 4, d)
+    q[:, :, 0] = torch.tensor([1.0, -1.0, 0.0, 0.125], device="cuda")
+    q = q.to(torch.bfloat16)
+    out = pool.prefill(q, tables, ints([t]), starts_of([n]), 1.0, t)
+    check_prefill(pool, tables, q, out, [n], [t], 1.0, 0, ("jump", jump, kv))
+    out = pool.prefill(q, tables, ints([300]), starts_of([n]), -1.0, t)
+    check_prefill(pool, tables, q, out, [n], [300], -1.0, 0, ("jump", jump, kv))
+    pool.close()
+
+
 def test_prefill_matches_decode_for_single_tokens():
     gen = torch.Generator(device="cuda").manual_seed(6)
     lens = [1, 17, 200, 1025, 3000]
