@@ -87,8 +87,10 @@ struct PromptItems {
 };
 
 // CTA c's stretch of a line of `total` places starts here; the CTA whose stretch holds place w.
-__device__ __forceinline__ int64_t line_start(int64_t total, int ctas, int c) { return total * c / ctas; }
-__device__ __forceinline__ int line_owner(int64_t total, int ctas, int64_t w) { return int(((w + 1) * ctas - 1) / total); }
+// (Lines are short enough for 32 bits as a rule, and a 64-bit division is some hundred instructions.)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) { return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b; }
+__device__ __forceinline__ int64_t line_start(int64_t total, int ctas, int c) { return divide(total * c, ctas); }
+__device__ __forceinline__ int line_owner(int64_t total, int ctas, int64_t w) { return int(divide((w + 1) * ctas - 1, total)); }
 
 // A unit's pieces along the line: f(CTA, first tile, tiles) for each that has tiles, or once for a unit that has none.
 template <typename F>
@@ -100,7 +102,7 @@ __device__ __forceinline__ void line_pieces(int64_t total, int ctas, int64_t at,
   }
   const int c1 = line_owner(total, ctas, at + cost - 1);
   for (int c = line_owner(total, ctas, at), t = 0; c <= c1; ++c) {
-    const int end = c == c1 ? tiles : int(max(line_start(total, ctas, c + 1) - at - kUnitCost, int64_t(0)) / per);
+    const int end = c == c1 ? tiles : int(divide(max(line_start(total, ctas, c + 1) - at - kUnitCost, int64_t(0)), per));
     if (end > t) {
       f(c, t, end - t);
       t = end;

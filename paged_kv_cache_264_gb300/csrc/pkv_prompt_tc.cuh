@@ -121,8 +121,10 @@ struct PromptSync {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];  // ring stages
   uint64_t q_full[2], q_empty[2];  // per stream from here
   uint64_t s_ready[2], p_half[2], p_ready[2];  // P's first 64 columns, and all
-  uint64_t o_ready[2], o_free[2];
-  uint64_t stat_ready[2];
+  uint64_t o_free[2];
+  // An accumulator and its state are complete: stream 0's; stream 1's; and stream 1's of a piece whose rows both hold,
+  // which others wait for (a parity wait has to see every phase).
+  uint64_t o_ready[3], stat_ready[3];
   uint64_t turn[2], drain[2];
   uint64_t piece_full[kPieceQueue], piece_empty[kPieceQueue];
   PromptPiece piece[kPieceQueue];
@@ -181,11 +183,13 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       mbar_init(sy->s_ready + s, 1);
       mbar_init(sy->p_half + s, 4);
       mbar_init(sy->p_ready + s, 4);
-      mbar_init(sy->o_ready + s, 1);
       mbar_init(sy->o_free + s, 4);
-      mbar_init(sy->stat_ready + s, 4);
       mbar_init(sy->drain + s, 1);
       mbar_init(sy->turn + s, 1);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(sy->o_ready + i, 1);
+      mbar_init(sy->stat_ready + i, 4);
     }
     for (int i = 0; i < kPieceQueue; ++i) {
       mbar_init(sy->piece_full + i, 1);
@@ -232,20 +236,23 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
     if (lane == 0) mbar_arrive(sy->piece_empty + queue.st);
     queue.next();
   };
+  // Which of o_ready and stat_ready a piece completes.
+  auto piece_done = [&](const PromptPiece& x) {
+    return uint32_t(x.count[0] > 0) | uint32_t(x.count[1] > 0) << (x.twin ? 2 : 1);
+  };
   // Finished rows of stream s (of both streams, where they hold the same): a thread to a row of the accumulator, run by
   // the four warps of a warpgroup.  Each thread stores its own: turned through shared memory first, so that an
   // instruction's stores lie in 8 lines and not 32, was no faster.
-  // used0, used1: the parities of the streams' accumulators of this piece; tok, h: this thread's row.
-  [[maybe_unused]] auto write_out = [&](const PromptPiece& x, int s, int wq, int tok, int h, uint32_t used0, uint32_t used1) {
-    const uint32_t used = s ? used1 : used0;
+  // done3: the parities of o_ready and stat_ready, a bit each; tok, h: this thread's row.
+  [[maybe_unused]] auto write_out = [&](const PromptPiece& x, int s, int wq, int tok, int h, uint32_t done3) {
     const bool any = x.count[s] > 0, both = x.twin != 0;
     const bool live = tok < x.toks[s] && x.head0 + h < p.group;
     const uint32_t o_addr = tmem + (uint32_t(wq) << 21) + 256 + s * D;
     float m = kMaxFloor, l = 0.0f, f0 = 1.0f, f1 = 0.0f;  // the state, and the streams' shares of it
     bool on0 = false, on1 = false;                        // a state without a weight may have no accumulator
     if (any) {
-      if (!wait_all(sy->stat_ready + s, used) || !wait_all(sy->o_ready + s, used)) return false;
-      if (both && (!wait_all(sy->stat_ready + 1, used1) || !wait_all(sy->o_ready + 1, used1))) return false;
+      if (!wait_all(sy->stat_ready + s, done3 >> s & 1) || !wait_all(sy->o_ready + s, done3 >> s & 1)) return false;
+      if (both && (!wait_all(sy->stat_ready + 2, done3 >> 2) || !wait_all(sy->o_ready + 2, done3 >> 2))) return false;
       tc_fence_after();
       const int r = wq * 32 + lane;
       const float2 a = stats[s * 128 + r];
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
           if (elect_one()) {
             if (pv) {
               tc_commit(sy->v_empty + vr.st);
-              if (j == last) tc_commit(sy->o_ready + s);
+              if (j == last) tc_commit(sy->o_ready + (s + (s & twin)));
             } else if (has_v) {
               mbar_arrive(sy->v_empty + vr.st);
             }
@@ -660,16 +667,15 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
     regs_fewer<C::kSideRegs>();
     if constexpr (!C::kQuant) {
       // ---------------------------------------------------------------- finished accumulators -> out, or partials
-      uint32_t used0 = 0, used1 = 0;
+      uint32_t done3 = 0;
       const int wq = warp & 3, r = wq * 32 + lane, tok = r / p.heads, h = r - tok * p.heads;
       for (; take(); done()) {
         const PromptPiece& x = sy->piece[queue.st];
 #pragma unroll 1
         for (int s = 0; s < (x.twin ? 1 : 2) && alive; ++s)
-          if (x.toks[s] > 0) alive = write_out(x, s, wq, tok, h, used0, used1);
+          if (x.toks[s] > 0) alive = write_out(x, s, wq, tok, h, done3);
         if (!alive) break;
-        used0 ^= x.count[0] > 0;
-        used1 ^= x.count[1] > 0;
+        done3 ^= piece_done(x);
       }
     } else {
       // ---------------------------------------------------------------- codes -> operand tiles of K, or of V
@@ -786,7 +792,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
     const float scale = p.scale_log2 == 0.0f ? 1e-30f : fabsf(p.scale_log2);
     const uint64_t scale2 = f32x2(scale, scale);
     const int tok = r / p.heads;
-    uint32_t step = 0, tiles = 0, used0 = 0, used1 = 0;
+    uint32_t step = 0, tiles = 0, done3 = 0, used = 0;
     bool before = false;  // the stream has had pieces
     for (; take(); done()) {
       const PromptPiece& x = sy->piece[queue.st];
@@ -983,17 +989,17 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         }
         if (!alive) break;
         // the last piece's have been read once its accumulator has
-        if (before && !(alive = wait_all(sy->o_free + s, (s ? used1 : used0) ^ 1u))) break;
+        if (before && !(alive = wait_all(sy->o_free + s, used ^ 1u))) break;
         before = true;
+        used ^= 1u;
         stats[s * 128 + r] = make_float2(m, l);
         __syncwarp();
-        if (lane == 0) mbar_arrive(sy->stat_ready + s);
+        if (lane == 0) mbar_arrive(sy->stat_ready + (s && x.twin ? 2 : s));
       }
       if constexpr (C::kQuant) {
-        if (x.toks[s] > 0 && (s == 0 || !x.twin) && !(alive = write_out(x, s, wq, tok, r - tok * p.heads, used0, used1))) break;
+        if (x.toks[s] > 0 && (s == 0 || !x.twin) && !(alive = write_out(x, s, wq, tok, r - tok * p.heads, done3))) break;
       }
-      used0 ^= x.count[0] > 0;
-      used1 ^= x.count[1] > 0;
+      done3 ^= piece_done(x);
     }
   }
   if (!alive && lane == 0) {

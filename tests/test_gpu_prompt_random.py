@@ -1,0 +1,105 @@
+"""paged_attention_prefill and prompt_attention over batches drawn at random: sequences without queries, single
+tokens, chunks of any size and long contexts side by side, against 64-bit torch; the same call again gives the
+same bits."""
+
+import random
+
+import pytest
+import torch
+
+import paged_kv_cache_264_gb300 as pkv
+from paged_kv_cache_264_gb300 import build
+from prompt_reference import ints, starts_of
+from test_gpu_prompt import check_prefill, make_cache, run_prompt
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(8, 2, 64), (4, 4, 128), (28, 4, 128), (16, 1, 64), (5, 1, 128), (32, 32, 64)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+def _batch(rng):
+    seqs = rng.choice([1, 2, 5, 20, 60])
+    new, before = [], []
+    for _ in range(seqs):
+        kind = rng.choice(["one", "one", "none", "few", "chunk", "long"])
+        n = {"one": 1, "none": 0, "few": rng.randint(2, 40), "chunk": rng.randint(60, 400), "long": rng.randint(1, 30)}[kind]
+        t = rng.randint(3000, 9000) if kind == "long" and seqs < 20 else rng.choice([0, rng.randint(0, 600)])
+        new.append(n)
+        before.append(t)
+    return new, before
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("seed", range(12))
+def test_prefill_batches(seed, kv):
+    rng = random.Random(seed * 3 + len(kv))
+    new, before = _batch(rng)
+    hq, hkv, d = rng.choice(HEADS)
+    window = rng.choice([0, 0, 0, rng.randint(1, 700)])
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    lens = [a + b for a, b in zip(new, before)]
+    pool, tables = make_cache(gen, lens, hkv, d, kv)
+    q = (1.5 * torch.randn(sum(new) + 1, hq, d, generator=gen, device="cuda")).to(torch.bfloat16)
+    args = (q, tables, ints(lens), starts_of(new), d ** -0.5, max(lens + [1]))
+    out = pool.prefill(*args, window=window)
+    torch.cuda.synchronize()
+    assert pool.device_error() == 0
+    check_prefill(pool, tables, q, out, new, lens, d ** -0.5, window, (seed, kv, new, before, hq, hkv, d, window))
+    n = sum(new)
+    for _ in range(3):
+        assert torch.equal(pool.prefill(*args, window=window)[:n], out[:n])
+    pool.close()
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_prompt_batches(seed):
+    rng = random.Random(100 + seed)
+    new, before = _batch(rng)
+    hq, hkv, d = rng.choice(HEADS)
+    keys = None if rng.random() < 0.4 else [max(0, n + b - rng.choice([0, 0, 50])) for n, b in zip(new, before)]
+    causal = rng.random() < 0.7
+    run_prompt(seed, new, keys, hq, hkv, d, causal=causal, window=rng.choice([0, rng.randint(1, 300)]) if causal else 0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_many_units_of_every_kind_many_times(kv):
+    """More units of work than CTAs take at once, some of one stream, some of both, some of the same rows in both:
+    whatever their order in time, the same bits."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    new = [1, 40, 130, 2, 0, 70] * 40
+    lens = [1 + n + (i * 37) % 300 for i, n in enumerate(new)]
+    pool, tables = make_cache(gen, lens, 8, 64, kv)
+    q = torch.randn(sum(new), 32, 64, generator=gen, device="cuda").to(torch.bfloat16)
+    args = (q, tables, ints(lens), starts_of(new), 0.125, max(lens))
+    out = pool.prefill(*args)
+    check_prefill(pool, tables, q, out, new[:12], lens[:12], 0.125, 0, kv)
+    for _ in range(20):
+        assert torch.equal(pool.prefill(*args), out)
+    assert pool.device_error() == 0
+    pool.close()
+
+
+def test_two_calls_at_once():
+    """Two pools, two streams, two workspaces: calls that overlap on the GPU."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    sides = []
+    for kv, hkv, d in (("bf16", 4, 128), ("int8", 8, 64)):
+        new, lens = [300, 1, 40], [900, 2000, 40]
+        pool, tables = make_cache(gen, lens, hkv, d, kv)
+        q = torch.randn(sum(new), 16, d, generator=gen, device="cuda").to(torch.bfloat16)
+        args = (q, tables, ints(lens), starts_of(new), d ** -0.5, 2000)
+        ws = torch.empty(pkv.prefill_workspace_bytes(pool, 3, 16, sum(new), 2000), dtype=torch.uint8, device="cuda")
+        sides.append((pool, args, pool.prefill(*args), torch.empty_like(q), ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for pool, args, _, out, ws, stream in sides:
+            pool.prefill(*args, out=out, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for pool, _, expect, out, _, _ in sides:
+        assert torch.equal(out, expect) and pool.device_error() == 0
+        pool.close()
