@@ -16,9 +16,11 @@
 // An item of up to 128 rows has both streams hold the same rows and take every other tile; their two states are
 // joined on the way out.
 //
-// INT8 and FP8 pools: two warpgroups load codes, one K's and one V's, and turn them into bf16 operand tiles, which
-// hold every INT8 and E4M3 code exactly.  The scales stay out of the operands: a token's K scale multiplies its
-// fp32 logit, and its V scale its weight before that is rounded to bf16.
+// INT8 and FP8 pools: two warpgroups load codes, one K's and one V's, and turn them into operand tiles, bf16 and
+// fp16, which hold every INT8 and E4M3 code exactly.  The scales stay out of the operands.  A token's K scale multiplies
+// its fp32 logit, and its V scale goes into its weight before that is rounded, as a term of the exponent: with
+// y = logit + log2(V scale) and m the running maximum of y, the weight w = 2^(y - m) is near 1 where it matters, so that
+// fp16 holds it (2^-11 of it; below 2^-14 of the row's largest an absolute 2^-25), and the softmax sum adds w / (V scale).
 //
 // Warps: a warpgroup of softmax per stream; over bf16, one that turns finished accumulators into rows of out, so that
 // the next unit's softmax need not wait for that, and one warp that fills the rings of K and V tiles by TMA (over the
@@ -100,13 +102,15 @@ struct PromptCfg {
                        kListWarp = kMmaWarp + 3;
   static constexpr int kReaders = kMmaWarp + 3;                // warps that take pieces
   // Registers a thread: the launch's, shared out anew by warpgroup.
-  static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 160 : 192, kSideRegs = kQuant ? 56 : 64,
+  static constexpr int kRegs = kQuant ? 96 : 128, kSoftmaxRegs = kQuant ? 152 : 192, kSideRegs = 64,
                        kLoadRegs = kQuant ? 48 : 64;
   static_assert(2 * kSoftmaxRegs + (kQuant ? 2 : 1) * kSideRegs + kLoadRegs <= kThreads / 128 * kRegs, "registers");
   static constexpr int kRingOff = 2 * kTileBytes;              // Q tiles of both streams first
   static constexpr int kVOff = kRingOff + kK * kTileBytes;
-  static constexpr int kSlotOff = kVOff + kV * kTileBytes;     // float [kSlots][2][128]: K's and V's scales
-  static constexpr int kMiscOff = kSlotOff + kSlots * 1024;
+  // float [3][128] and [2][4] to a slot: K's scale times the softmax's, log2 of V's, and 1 / V's; V's smallest scale of
+  // each warp's tokens and the largest of those so far
+  static constexpr int kSlotOff = kVOff + kV * kTileBytes, kSlotBytes = 3 * kPromptTile * 4 + 32;
+  static constexpr int kMiscOff = kSlotOff + kSlots * kSlotBytes;
   static constexpr int kStatOff = kMiscOff + 1024;             // float2 [2][128]: running max and sum
   static constexpr int kSmemBytes = kStatOff + 2 * 128 * 8;
   static constexpr uint32_t kTmemCols = 512;
@@ -537,7 +541,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       const int s = warp - C::kMmaWarp;
       const uint32_t negate = p.scale_log2 < 0.0f ? 1u << 13 : 0u;  // -Q: the largest product is the largest logit
       const uint32_t desc_s = mma_bf16_desc(128, kPromptTile, false) | negate;
-      constexpr uint32_t kDescO = mma_bf16_desc(128, D, true);
+      constexpr uint32_t kDescO = C::kQuant ? mma_f16_desc(128, D, true) : mma_bf16_desc(128, D, true);
       constexpr uint32_t kHi = smem_operand_hi(1024);
       const uint32_t q_desc = smem_operand(smem_addr(smem + s * C::kTileBytes), 16);
       const uint32_t k_desc = smem_operand(smem_addr(smem + C::kRingOff), 16);
@@ -688,6 +692,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
       const int wq = warp & 3;
       const int chunk = D == 128 ? (lane & 3) | (lane >> 3 & 1) << 2 : lane & 3;
       const int sub = D == 128 ? (lane >> 2 & 1) | lane >> 4 << 1 : lane >> 2;
+      const float scale = p.scale_log2 == 0.0f ? 1e-30f : fabsf(p.scale_log2);  // as the softmax takes it
       const auto* cache = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
       unsigned char* ring = smem + (is_v ? C::kVOff : C::kRingOff);
       uint64_t* full = is_v ? sy->v_full : sy->k_full;
@@ -712,7 +717,8 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         };
         const uint8_t *from0 = nullptr, *from1 = nullptr;  // this lane's first chunk in each
         uint32_t have = 0;
-        float ks = 0.0f, vs = 0.0f;
+        float ks = 0.0f, vs = 1.0f;
+        [[maybe_unused]] uint32_t most = 0;
         auto place = [&](int tile) {  // of the blocks that were asked for
           const bool ok0 = next0 >= 0 && next0 < p.num_blocks, ok1 = next1 >= 0 && next1 < p.num_blocks;
           const int b = (tile0 + tile) * (kPromptTile / kBlockSize) + 2 * wq;
@@ -721,12 +727,12 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
           have = uint32_t(ok0) | uint32_t(ok1) << 1;
           from0 = mine + int64_t(next0) * block_bytes;
           from1 = mine + int64_t(next1) * block_bytes;
-          if (!is_v) {  // a thread to a token; what the item does not see may hold anything, its scales are 0
+          if (!is_v) {  // a thread to a token; what the item does not see may hold anything, its scales are 0 and 1
             const int t = (tile0 + tile) * kPromptTile + wq * 32 + lane;
             const bool ok = (lane < 16 ? ok0 : ok1) && t >= lo && t < hi;
             const int64_t row = int64_t(lane < 16 ? next0 : next1) * (p.kv_heads * kBlockSize) + kvh * kBlockSize + (lane & 15);
             ks = ok ? __int_as_float(load_now(p.k_scale + row)) : 0.0f;
-            vs = ok ? __int_as_float(load_now(p.v_scale + row)) : 0.0f;
+            vs = ok ? __int_as_float(load_now(p.v_scale + row)) : 1.0f;
           }
         };
         uint4 w[kLoads];
@@ -746,9 +752,16 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         for (int t = 0; t < n; ++t) {
           if (filled >= C::kK && !(alive = wait_all(empty + at.st, at.ph ^ 1u))) break;
           if (!is_v) {
-            auto* slot = reinterpret_cast<float*>(smem + C::kSlotOff + (tiles + t) % C::kSlots * 1024) + wq * 32 + lane;
-            slot[0] = ks;
-            slot[128] = vs;
+            auto* slot = reinterpret_cast<float*>(smem + C::kSlotOff + (tiles + t) % C::kSlots * C::kSlotBytes) + wq * 32 + lane;
+            // A scale of 0, whose codes are 0, counts as 2^-60: the token's logit has to bound the exponent, and its
+            // weight must not hide others'.
+            const float size = vs == 0.0f ? 0x1p-60f : vs, lv = log2f(size);
+            slot[0] = ks * scale;
+            slot[128] = lv;
+            slot[256] = exp2f(-lv);
+            const uint32_t smallest = __reduce_min_sync(kAll, __float_as_uint(size));
+            most = max(most, __reduce_max_sync(kAll, __float_as_uint(size)));
+            if (lane < 2) (slot - lane - wq * 32)[384 + lane * 4 + wq] = __uint_as_float(lane ? most : smallest);
             if (lane == 0) reinterpret_cast<uint8_t*>(sy->mask + (tiles + t) % kTileMasks)[wq] = uint8_t(have);
           }
           unsigned char* dst = ring + at.st * C::kTileBytes + (chunk >> 2) * C::kHalfBytes + (wq * 32 + sub) * 128;
@@ -757,10 +770,17 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
           for (int i = 0; i < kLoads; ++i) {
             const int row = i * kRows + sub;  // of the warp's 32
             uint4 a, b;
-            bf16x4_from_codes<KV>(w[i].x, a.x, a.y);
-            bf16x4_from_codes<KV>(w[i].y, a.z, a.w);
-            bf16x4_from_codes<KV>(w[i].z, b.x, b.y);
-            bf16x4_from_codes<KV>(w[i].w, b.z, b.w);
+            if (is_v) {
+              f16x4_from_codes<KV>(w[i].x, a.x, a.y);
+              f16x4_from_codes<KV>(w[i].y, a.z, a.w);
+              f16x4_from_codes<KV>(w[i].z, b.x, b.y);
+              f16x4_from_codes<KV>(w[i].w, b.z, b.w);
+            } else {
+              bf16x4_from_codes<KV>(w[i].x, a.x, a.y);
+              bf16x4_from_codes<KV>(w[i].y, a.z, a.w);
+              bf16x4_from_codes<KV>(w[i].z, b.x, b.y);
+              bf16x4_from_codes<KV>(w[i].w, b.z, b.w);
+            }
             *reinterpret_cast<uint4*>(dst + i * (kRows * 128) + ((c0 ^ (row & 7)) << 4)) = a;
             *reinterpret_cast<uint4*>(dst + i * (kRows * 128) + (((c0 + 1) ^ (row & 7)) << 4)) = b;
           }
@@ -815,8 +835,8 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             const uint32_t have = tile_mask(sy->mask[(tiles0 + tile) % kTileMasks]);
             const int lo = span.lo - (tile0 + tile) * kPromptTile, hi = span.hi - (tile0 + tile) * kPromptTile;
             [[maybe_unused]] const auto* ks =
-                reinterpret_cast<const ulonglong2*>(smem + C::kSlotOff + (C::kQuant ? (tiles0 + tile) % (C::kSlots + !C::kQuant) : 0) * 1024);
-            [[maybe_unused]] const auto* vs = ks + kPromptTile / 4;
+                reinterpret_cast<const ulonglong2*>(smem + C::kSlotOff + (C::kQuant ? (tiles0 + tile) % (C::kSlots + !C::kQuant) : 0) * C::kSlotBytes);
+            [[maybe_unused]] const auto *lv = ks + kPromptTile / 4, *iv = lv + kPromptTile / 4;
             const bool cut = __any_sync(kAll, lo > 0 || hi < kPromptTile || have != 0xffu);
             auto mask = [&](int c, float* z) {  // columns 32 c .. 32 c + 31
               const uint32_t w = bit_range(lo - 32 * c, hi - 32 * c) & ((have >> (2 * c) & 1 ? 0xffffu : 0u) | (have >> (2 * c + 1) & 1 ? 0xffff0000u : 0u));
@@ -835,39 +855,50 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             // Logits -> weights, 2 n to n registers.  A warp issues in order and is alone with its row's chain, so the
             // steps of neighbouring groups of 8 are written side by side: exponentials at a time (4 cycles each)
             // with the products and sums (2) of others.
+            [[maybe_unused]] __half2 halves[2];
             auto weigh = [&](int c, int n, float* z, float* w) {
               const uint64_t neg = f32x2(-m, -m);
 #pragma unroll
               for (int g = 0; g < n + 8; g += 4) {
                 if (g < n) {
 #pragma unroll
-                  for (int j = g; j < g + 4; ++j) f32x2_parts(fma2(f32x2(z[2 * j], z[2 * j + 1]), scale2, neg), z[2 * j], z[2 * j + 1]);
+                  for (int j = g; j < g + 4; ++j) {
+                    const uint64_t y = f32x2(z[2 * j], z[2 * j + 1]);
+                    f32x2_parts(C::kQuant ? add2(y, neg) : fma2(y, scale2, neg), z[2 * j], z[2 * j + 1]);
+                  }
                 }
                 if (g >= 4 && g < n + 4) {
 #pragma unroll
                   for (int j = 2 * g - 8; j < 2 * g; ++j) z[j] = fast_exp2(z[j]);
                 }
                 if (g >= 8) {
-#pragma unroll
-                  for (int j = g - 8; j < g - 4; ++j) sum[j & 1] = add2(sum[j & 1], f32x2(z[2 * j], z[2 * j + 1]));
                   if constexpr (C::kQuant) {
 #pragma unroll
                     for (int j = (g - 8) / 2; j < (g - 4) / 2; ++j) {
-                      const ulonglong2 f = vs[8 * c + j];
-                      f32x2_parts(mul2(f32x2(z[4 * j], z[4 * j + 1]), f.x), z[4 * j], z[4 * j + 1]);
-                      f32x2_parts(mul2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y), z[4 * j + 2], z[4 * j + 3]);
+                      const ulonglong2 f = iv[8 * c + j];
+                      sum[0] = fma2(f32x2(z[4 * j], z[4 * j + 1]), f.x, sum[0]);
+                      sum[1] = fma2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y, sum[1]);
                     }
                   }
 #pragma unroll
-                  for (int j = g - 8; j < g - 4; ++j) w[j] = __uint_as_float(pack_bf16x2(z[2 * j], z[2 * j + 1]));
+                  for (int j = g - 8; j < g - 4; ++j) {
+                    if constexpr (C::kQuant) {
+                      const __half2 v = __floats2half2_rn(z[2 * j], z[2 * j + 1]);
+                      halves[j & 1] = __hadd2(halves[j & 1], v);
+                      w[j] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&v));
+                    } else {
+                      sum[j & 1] = add2(sum[j & 1], f32x2(z[2 * j], z[2 * j + 1]));
+                      w[j] = __uint_as_float(pack_bf16x2(z[2 * j], z[2 * j + 1]));
+                    }
+                  }
                 }
               }
             };
             // The maximum moves where a row's logits pass it by kMaxSlack: what was weighed with the old one counts this
             // much of it now.
             auto move = [&](const float (&mx)[4]) {
-              float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
-              if constexpr (C::kQuant) bm = ceilf(bm);
+              float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+              bm = C::kQuant ? ceilf(bm) : bm * scale;
               const bool grow = bm > m + kMaxSlack;
               if (!__any_sync(kAll, grow)) return 1.0f;
               const float mu = grow ? bm : m, f = fast_exp2(m - mu);
@@ -890,12 +921,15 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             sum[0] = sum[1] = 0;
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if constexpr (C::kQuant) {
-              // Half a tile at a time, once: weights are floating point, so a maximum that logits have passed by far does
-              // no harm until they overflow.  It is looked for in the first half of a row's tiles, and again where a
-              // half's weights add up to more than 2^64; it moves by whole powers of two, so that weights handed over
-              // already can be rescaled exactly.  (All 128 logits and the scales would not stay in registers, and
-              // spilled ones are far away with shared memory this full.  The loop stays rolled: the code of all roles shares an
-              // instruction cache.)
+              // Half a tile at a time, once.  The maximum is looked for in the first half of a row's tiles, and again where
+              // a half's weights do not add up within fp16's range (a row that passes it has one of at least 2^9).  It moves by
+              // whole powers of two, so that weights handed over already can be rescaled exactly.  (All 128 logits and
+              // the scales would not stay in registers, and spilled ones are far away with shared memory this full.  The
+              // loop stays rolled: the code of all roles shares an instruction cache.)
+              // Scales of V that lie 2^90 apart: weights (and with them w / scale) of small values would vanish beside large
+              // ones', so the sum is formed by itself.
+              const float4 least = *reinterpret_cast<const float4*>(iv + kPromptTile / 4), most = *(reinterpret_cast<const float4*>(iv + kPromptTile / 4) + 1);
+              const bool wide = fminf(fminf(least.x, least.y), fminf(least.z, least.w)) < 0x1p-90f * fmaxf(fmaxf(most.x, most.y), fmaxf(most.z, most.w));
               float z[64], w[32];
 #pragma unroll 1
               for (int h = 0; h < 2; ++h) {
@@ -906,9 +940,9 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                   tmem_wait_ld();
 #pragma unroll
                   for (int j = 0; j < 16; ++j) {
-                    const ulonglong2 f = ks[16 * h + j];
-                    f32x2_parts(mul2(f32x2(z[4 * j], z[4 * j + 1]), f.x), z[4 * j], z[4 * j + 1]);
-                    f32x2_parts(mul2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y), z[4 * j + 2], z[4 * j + 3]);
+                    const ulonglong2 f = ks[16 * h + j], g = lv[16 * h + j];
+                    f32x2_parts(fma2(f32x2(z[4 * j], z[4 * j + 1]), f.x, g.x), z[4 * j], z[4 * j + 1]);
+                    f32x2_parts(fma2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y, g.y), z[4 * j + 2], z[4 * j + 3]);
                   }
                   if (cut) {
                     mask(2 * h, z);
@@ -920,7 +954,8 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                     largest(z, 64, mx);
                     const float f = move(mx);
                     if (h == 1) {  // the lower half's weights
-                      const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
+                      tmem_wait_st();
+                      const __half2 f2 = __float2half2_rn(f);
 #pragma unroll 1
                       for (int c = 0; c < 32; c += 16) {
                         float o[16];
@@ -929,7 +964,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                           const uint32_t bits = __float_as_uint(o[e]);
-                          const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&bits), f2);
+                          const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&bits), f2);
                           o[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&r));
                         }
                         tmem_st16(s_addr + c, o);
@@ -937,12 +972,27 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                     }
                   }
                   sum[0] = sum[1] = 0;
+                  halves[0] = halves[1] = __float2half2_rn(0.0f);
                   weigh(2 * h, 32, z, w);
-                  float lo_sum, hi_sum;
-                  f32x2_parts(add2(sum[0], sum[1]), lo_sum, hi_sum);
-                  lo_sum += hi_sum;
-                  if (look || !__any_sync(kAll, lo_sum > 0x1p64f)) {
-                    l += lo_sum;
+                  const float2 both = __half22float2(__hadd2(halves[0], halves[1]));
+                  if (look || !__any_sync(kAll, fmaxf(both.x, both.y) > 30000.0f)) {
+                    if (wide) {
+                      sum[0] = sum[1] = 0;
+#pragma unroll 1
+                      for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                        tmem_ld32(s_addr + 32 * c, z);
+                        tmem_wait_ld();
+                        const float* f = reinterpret_cast<const float*>(ks) + 32 * c;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) z[j] *= f[j];
+                        if (cut) mask(c, z);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sum[j & 1] = add2(sum[j & 1], f32x2(fast_exp2(z[2 * j] - m), fast_exp2(z[2 * j + 1] - m)));
+                      }
+                    }
+                    float lo_sum, hi_sum;
+                    f32x2_parts(add2(sum[0], sum[1]), lo_sum, hi_sum);
+                    l += lo_sum + hi_sum;
                     break;
                   }
                   look = true;

@@ -46,6 +46,8 @@ constexpr uint32_t smem_operand_hi(uint32_t sbo) { return (sbo & 0x3ffffu) >> 4 
 constexpr uint32_t mma_bf16_desc(int m, int n, bool b_mn_major) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn_major ? 1u << 16 : 0u) | uint32_t(n >> 3) << 17 | uint32_t(m >> 4) << 24;
 }
+// The same with fp16 operands.
+constexpr uint32_t mma_f16_desc(int m, int n, bool b_mn_major) { return mma_bf16_desc(m, n, b_mn_major) & ~(1u << 7 | 1u << 10); }
 
 // D (+)= A B^T over 16 contracted values; A and B in shared memory (low descriptor words).
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool accumulate) {
@@ -150,6 +152,21 @@ __device__ __forceinline__ void bf16x4_from_codes(uint32_t w, uint32_t& lo, uint
     const uint32_t u = w ^ 0x80808080u;
     lo = bf16x2_from_i8(__byte_perm(u, 0x43434343u, 0x4140u));
     hi = bf16x2_from_i8(__byte_perm(u, 0x43434343u, 0x4342u));
+  }
+}
+
+// Four codes of a word -> four fp16 in two words, exactly.
+template <KvType KV>
+__device__ __forceinline__ void f16x4_from_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (KV == KvType::kFp8) {
+    f16x2x2_from_e4m3x4(w, lo, hi);
+  } else {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 offset = __float2half2_rn(1152.0f);
+    const uint32_t a = f16x2_biased(u, 0x4140u), b = f16x2_biased(u, 0x4342u);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), offset), y = __hsub2(*reinterpret_cast<const __half2*>(&b), offset);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
   }
 }
 
