@@ -750,18 +750,24 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         ask(1);
 #pragma unroll 1
         for (int t = 0; t < n; ++t) {
-          if (filled >= C::kK && !(alive = wait_all(empty + at.st, at.ph ^ 1u))) break;
+          float lv = 0.0f, iv = 0.0f;
+          uint32_t least = 0;
           if (!is_v) {
-            auto* slot = reinterpret_cast<float*>(smem + C::kSlotOff + (tiles + t) % C::kSlots * C::kSlotBytes) + wq * 32 + lane;
             // A scale of 0, whose codes are 0, counts as 2^-60: the token's logit has to bound the exponent, and its
             // weight must not hide others'.
-            const float size = vs == 0.0f ? 0x1p-60f : vs, lv = log2f(size);
-            slot[0] = ks * scale;
-            slot[128] = lv;
-            slot[256] = exp2f(-lv);
-            const uint32_t smallest = __reduce_min_sync(kAll, __float_as_uint(size));
+            const float size = vs == 0.0f ? 0x1p-60f : vs;
+            lv = __log2f(size);
+            iv = fast_exp2(-lv);
+            least = __reduce_min_sync(kAll, __float_as_uint(size));
             most = max(most, __reduce_max_sync(kAll, __float_as_uint(size)));
-            if (lane < 2) (slot - lane - wq * 32)[384 + lane * 4 + wq] = __uint_as_float(lane ? most : smallest);
+          }
+          if (filled >= C::kK && !(alive = wait_all(empty + at.st, at.ph ^ 1u))) break;
+          if (!is_v) {
+            auto* slot = reinterpret_cast<float*>(smem + C::kSlotOff + (tiles + t) % C::kSlots * C::kSlotBytes) + wq * 32;
+            slot[lane] = ks * scale;
+            slot[128 + lane] = lv;
+            slot[256 + lane] = iv;
+            if (lane < 2) slot[384 - wq * 32 + lane * 4 + wq] = __uint_as_float(lane ? most : least);
             if (lane == 0) reinterpret_cast<uint8_t*>(sy->mask + (tiles + t) % kTileMasks)[wq] = uint8_t(have);
           }
           unsigned char* dst = ring + at.st * C::kTileBytes + (chunk >> 2) * C::kHalfBytes + (wq * 32 + sub) * 128;
