@@ -219,52 +219,57 @@ def test_prefill_matches_decode_for_single_tokens():
     pool.close()
 
 
-def test_prefill_bad_lengths_and_blocks():
+@pytest.mark.parametrize("most", [300, 5000])  # short calls run without a plan
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_prefill_bad_lengths_and_blocks(kv, most):
     gen = torch.Generator(device="cuda").manual_seed(7)
     new, lens = [10, 4, 6, 0, 30], [100, 40, 50, 33, 300]
-    pool, tables = make_cache(gen, lens, 2, 64, "bf16")
+    pool, tables = make_cache(gen, lens, 2, 64, kv)
+    tables = torch.cat([tables, torch.full((5, 400), -1, dtype=torch.int32, device="cuda")], 1)
     q = _randn(gen, sum(new), 4, 64).to(torch.bfloat16)
     qs = starts_of(new)
     # lengths: fewer tokens than queries, more than max_context_len, negative for a sequence without queries
-    given = [100, 3, 301, -5, 300]
+    given = [100, 3, most + 1, -5, 300]
     out = torch.full_like(q, 7.0)
-    pool.prefill(q, tables, ints(given), qs, 0.125, 300, out=out)
+    pool.prefill(q, tables, ints(given), qs, 0.125, most, out=out)
     assert pool.device_error() == pkv.DEVERR_CONTEXT_LEN
     assert (out[10:20] == 0).all()
     check_prefill(pool, tables, q[:10], out[:10], [10], [100], 0.125, 0, "good one")
-    k, v, _ = cached(pool, tables[4], 300)
-    check(out[20:], *attend(q[20:].double(), k, v, 0.125), 300, "last one")
+    check_prefill(pool, tables[4:], q[20:], out[20:], [30], [300], 0.125, 0, "last one")
     # blocks that are not there
     tables[0, 2] = -1
     tables[4, 18] = pool.num_blocks  # the last, partly filled one
     tables[4, 0] = 2 ** 31 - 1
     out.fill_(7.0)
-    pool.prefill(q, tables, ints(lens), qs, 0.125, 300, out=out)
+    pool.prefill(q, tables, ints(lens), qs, 0.125, most, out=out)
     assert pool.device_error() == pkv.DEVERR_BLOCK_ID
     check_prefill(pool, tables, q, out, new, lens, 0.125, 0, "missing blocks")
     # all of a sequence's blocks missing: nothing to see
     tables[1] = -1
-    pool.prefill(q, tables, ints(lens), qs, 0.125, 300, out=out)
+    pool.prefill(q, tables, ints(lens), qs, 0.125, most, out=out)
     assert pool.device_error() == pkv.DEVERR_BLOCK_ID
     assert (out[10:14] == 0).all()
     pool.close()
 
 
+@pytest.mark.parametrize("most", [20, 5000])
 @pytest.mark.parametrize("starts", [[0, 4, 3, 12], [-1, 4, 8, 12], [0, 4, 8, 13], [0, 2 ** 31 - 1, 8, 12]])
-def test_invalid_starts_write_nothing(starts):
+def test_invalid_starts_write_nothing(starts, most):
     gen = torch.Generator(device="cuda").manual_seed(8)
     pool, tables = make_cache(gen, [20, 20, 20], 2, 64, "bf16")
-    x = _randn(gen, 12, 4, 64).to(torch.bfloat16)
+    wide = torch.cat([tables, torch.full((3, 400), -1, dtype=torch.int32, device="cuda")], 1)
+    x = _randn(gen, max(12, most), 4, 64).to(torch.bfloat16)
     out = torch.full_like(x, 7.0)
-    pool.prefill(x, tables, ints([20] * 3), ints(starts), 0.125, 20, out=out)
+    bad = ints([s if s != 13 else max(13, most + 1) for s in starts])
+    pool.prefill(x, wide, ints([20] * 3), bad, 0.125, most, out=out)
     assert pool.device_error() == pkv.DEVERR_QUERY
-    pool.prompt_attention(x, x[:, :2], x[:, 2:], ints(starts), 0.125, out=out)
+    pool.prompt_attention(x, x[:, :2], x[:, 2:], bad, 0.125, out=out)
     assert pool.device_error() == pkv.DEVERR_QUERY
-    pool.prompt_attention(x, x[:, :2], x[:, 2:], starts_of([4, 4, 4]), 0.125, key_starts=ints(starts), out=out)
+    pool.prompt_attention(x, x[:, :2], x[:, 2:], starts_of([4, 4, 4]), 0.125, key_starts=bad, out=out)
     assert pool.device_error() == pkv.DEVERR_QUERY
     assert (out == 7.0).all()
     k, v = torch.full_like(x[:, :2].contiguous(), 7.0), torch.full_like(x[:, :2].contiguous(), 7.0)
-    pool.gather_cache(tables, ints(starts), 12, k=k, v=v)
+    pool.gather_cache(tables, bad, x.shape[0], k=k, v=v)
     assert pool.device_error() == pkv.DEVERR_QUERY
     assert (k == 7.0).all() and (v == 7.0).all()
     pool.close()

@@ -84,6 +84,40 @@ def test_many_units_of_every_kind_many_times(kv):
     pool.close()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_one_long_context_among_thousands_of_units(kv):
+    """A unit of work that is large beside a CTA's share, among more units than one pass of the plan takes."""
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    new, lens = [1] * 400, [1 + (i * 29) % 60 for i in range(400)]
+    new[217], lens[217] = 30, 20000
+    pool, tables = make_cache(gen, lens, 8, 64, kv)
+    q = torch.randn(sum(new), 16, 64, generator=gen, device="cuda").to(torch.bfloat16)
+    out = pool.prefill(q, tables, ints(lens), starts_of(new), 0.125, 20000)
+    assert pool.device_error() == 0
+    check_prefill(pool, tables[210:225], q[210:254], out[210:254], new[210:225], lens[210:225], 0.125, 0, kv)
+    check_prefill(pool, tables[:3], q[:3], out[:3], new[:3], lens[:3], 0.125, 0, kv)
+    check_prefill(pool, tables[-3:], q[-3:], out[-3:], new[-3:], lens[-3:], 0.125, 0, kv)
+    pool.close()
+
+
+@pytest.mark.parametrize("seqs", [1024, 1025, 3000])
+def test_more_sequences_than_the_plan_holds(seqs):
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    new = [(i * 7) % 4 for i in range(seqs)]
+    lens = [n + (i * 13) % 40 for i, n in enumerate(new)]
+    pool, tables = make_cache(gen, lens, 1, 64, "bf16")
+    q = torch.randn(sum(new), 4, 64, generator=gen, device="cuda").to(torch.bfloat16)
+    out = pool.prefill(q, tables, ints(lens), starts_of(new), 0.125, 5 * 16)
+    assert pool.device_error() == 0
+    at = 0
+    for b, n in enumerate(new):
+        if b % 41 == 0 or b > seqs - 3:
+            check_prefill(pool, tables[b:b + 1], q[at:at + n], out[at:at + n], [n], [lens[b]], 0.125, 0, b)
+        at += n
+    assert not out.isnan().any()
+    pool.close()
+
+
 def test_two_calls_at_once():
     """Two pools, two streams, two workspaces: calls that overlap on the GPU."""
     gen = torch.Generator(device="cuda").manual_seed(4)
