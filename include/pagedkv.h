@@ -645,16 +645,19 @@ PKV_API pkv_status pkv_prefill_workspace_bytes(const pkv_pool* pool, int num_seq
  * queries, as many of each sequence as it has).  Query i of sequence b's n, at position p = T_b - n + i:
  *   out[row][h][:] = sum_{t <= p} softmax_t(scale * q[row][h] . K_b[t]) V_b[t]
  * with T_b = context_lens[b] >= n and query heads grouped as there.  INT8 and FP8 pools: K and V are the
- * dequantised values s * value(code).  Accumulation is fp32, weights enter the product over V as bf16 (INT8 and
- * FP8 pools: times V's scale), which moves an output by at most 2^-8 (sum of weight |v| + |output|) before its
- * own rounding to bf16.
+ * dequantised values s * value(code).  Accumulation is fp32 and the softmax sum is over unrounded weights.  Over
+ * bf16 pools weights enter the product over V as bf16, which moves an output by at most 2^-8 (sum of weight |v|)
+ * before its own rounding.  Over INT8 and FP8 pools weight * V's scale enters as fp16: at most 2^-11 of that sum,
+ * and 2^-24 of the row's largest weight |v| for each token.  A scale of V counts as at least 2^-98 (one of 0, whose
+ * codes are 0, as 2^-60, beside which values far below it vanish); beside ordinary values one beyond 2^90 costs precision.
  * A sequence whose T_b is out of range gets zero rows and sets PKV_DEVERR_CONTEXT_LEN; an invalid
  * query_starts entry sets PKV_DEVERR_QUERY and nothing is written; a block id out of range is skipped and
  * sets PKV_DEVERR_BLOCK_ID.  Cache slots that no query of the call sees may hold anything; a NaN or infinite
  * value (not a key) of a token that only some of a sequence's queries see may reach the others.
  * num_seqs == 0 or num_tokens == 0 is a no-op.
- * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (2^30 rows or more, a pool of 2^31 or more rows of
- * head_dim), PKV_ERR_WORKSPACE, PKV_ERR_CUDA.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (2^30 rows or more, some 2^30 units of work or more: a kv
+ * head of up to 256 rows of (token, query head), a pool of 2^31 or more rows of head_dim), PKV_ERR_WORKSPACE,
+ * PKV_ERR_CUDA.
  */
 PKV_API pkv_status pkv_paged_attention_prefill(const pkv_pool* pool, const pkv_prefill* args, void* stream);
 

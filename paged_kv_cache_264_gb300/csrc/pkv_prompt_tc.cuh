@@ -754,8 +754,9 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
           uint32_t least = 0;
           if (!is_v) {
             // A scale of 0, whose codes are 0, counts as 2^-60: the token's logit has to bound the exponent, and its
-            // weight must not hide others'.
-            const float size = vs == 0.0f ? 0x1p-60f : vs;
+            // weight must not hide others'.  Any other counts as at least 2^-98 (values move by less than 2^-89), so that a
+            // sum of weights of up to 2^15 over it stays finite for 2^15 half-tiles.
+            const float size = vs == 0.0f ? 0x1p-60f : vs < 0x1p-98f ? 0x1p-98f : vs;
             lv = __log2f(size);
             iv = fast_exp2(-lv);
             least = __reduce_min_sync(kAll, __float_as_uint(size));

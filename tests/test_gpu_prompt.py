@@ -203,6 +203,27 @@ def test_prefill_values_of_any_size(kv):
     pool.close()
 
 
+@pytest.mark.parametrize("t,tiny", [(700, 400), (700, 700), (6000, 3000)])
+@pytest.mark.parametrize("kv", ["bf16", "int8", "fp8"])
+def test_prefill_smallest_values_ahead_of_others(kv, t, tiny):
+    """The smallest values that there are, a tile of them and more, must not cost the ones behind them their weights.
+    Over codes V's scales count as at least 2^-98: a value of such a row moves by at most 448 * 2^-98 < 2^-89."""
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    n, hkv, d = 40, 2, 128
+    pool, tables = make_cache(gen, [t], hkv, d, kv)
+    k, v = _randn(gen, t, hkv, d), _randn(gen, t, hkv, d)
+    v[:tiny] *= torch.exp2(torch.randint(-124, -90, (tiny, hkv, 1), generator=gen, device="cuda").float())
+    pos = torch.arange(t, device="cuda")
+    pool.reshape_and_cache(k.to(torch.bfloat16), v.to(torch.bfloat16), (tables[0, pos // 16] * 16 + pos % 16).to(torch.int32))
+    q = _randn(gen, n, 8, d).to(torch.bfloat16)
+    out = pool.prefill(q, tables, ints([t]), starts_of([n]), 0.125, t)
+    kc, vc, _ = cached(pool, tables[0], t)
+    ref = attend(q.double(), kc, vc, 0.125)
+    tol = tolerance(*ref, t, d, kv != "bf16") + 2.0 ** -89
+    assert ((out.double() - ref[0]).abs() <= tol).all()
+    pool.close()
+
+
 def test_prefill_matches_decode_for_single_tokens():
     gen = torch.Generator(device="cuda").manual_seed(6)
     lens = [1, 17, 200, 1025, 3000]
