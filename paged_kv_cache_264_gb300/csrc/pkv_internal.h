@@ -233,14 +233,13 @@ struct PromptHeader {    // of the workspace
   int items, joins;
 };
 struct PromptParams {
-  const void* q;                // bf16 rows of [Hq, D] at token stride q_stride
-  void* out;
+  void* out;                    // bf16 rows of [Hq, D] at token stride out_stride (elements); q, k and v come as maps
   const int32_t* query_starts;  // [B + 1]
   uint32_t* err;
-  int64_t q_stride, out_stride; // elements
+  int64_t out_stride;
   int num_tokens;               // rows of q and out
   int num_seqs;
-  int num_q_heads, kv_heads, group, head_dim;
+  int kv_heads, group, head_dim;
   int window;                   // tokens each query sees back from its own position (kNoWindow: all)
   int causal;
   float scale_log2;
@@ -256,17 +255,13 @@ struct PromptParams {
   int max_blocks_per_seq;
   int max_context_len;
   // over packed rows
-  const void* k;                // bf16 rows of [Hkv, D]
-  const void* v;
   const int32_t* key_starts;    // [B + 1]
-  int64_t k_stride, v_stride;
   int num_keys;
   // head units and items
   int heads, chunks, units;     // heads of a chunk, chunks of a kv head, units = kv_heads * chunks
   int stream_tokens;            // tokens of a stream's rows
   int grid;
   int direct;                   // no plan: at most a unit of work per CTA
-  int max_parts;                // partials that there is room for
   int part_rows;                // rows of a partial
   // workspace
   PromptHeader* header;
@@ -280,8 +275,9 @@ struct PromptParams {
 };
 constexpr int kPromptTile = 128;  // tokens of one tile
 constexpr int kRowTile = 128;     // rows of one stream
-constexpr int kDirectSeqs = 32;   // calls of up to this many sequences, of up to this many tiles each, and of
-constexpr int kDirectTiles = 4;   // at most a unit of work per CTA have no plan
+constexpr int kDirectSeqs = 32;   // calls of up to this many sequences and at most a unit of work per CTA have no plan
+constexpr int kDirectTiles = 16;  // where no sequence has more tiles than this,
+constexpr int kDirectCodesTiles = 12;  // or, on INT8 and FP8 pools, than this
 constexpr int kPromptWhole = 3;   // units of up to this many tiles are not cut
 constexpr int kPromptWaves = 8;   // up to this many units of work a CTA are shared out piece by piece
 cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream);

@@ -84,6 +84,27 @@ def test_many_units_of_every_kind_many_times(kv):
     pool.close()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("seed", range(4))
+def test_short_calls_with_and_without_a_plan(kv, seed):
+    """A bound on the lengths that is far above them makes a short call one with a plan."""
+    rng = random.Random(seed + 50)
+    new = [rng.choice([0, 1, 1, 2, 17, 40]) for _ in range(rng.randint(1, 12))]
+    lens = [n + rng.choice([0, 5, 130, 600, 1400]) for n in new]
+    hq, hkv, d = rng.choice([(8, 2, 128), (14, 2, 64), (4, 4, 64), (40, 1, 128)])
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    pool, tables = make_cache(gen, lens, hkv, d, kv)
+    tables = torch.cat([tables, torch.full((len(new), 640), -1, dtype=torch.int32, device="cuda")], 1)
+    q = (2 * torch.randn(max(1, sum(new)), hq, d, generator=gen, device="cuda")).to(torch.bfloat16)
+    for most in (max(lens), 10000):
+        out = pool.prefill(q, tables, ints(lens), starts_of(new), d ** -0.5, most)
+        assert pool.device_error() == 0
+        check_prefill(pool, tables, q, out, new, lens, d ** -0.5, 0, (kv, seed, most))
+        for _ in range(3):
+            assert torch.equal(pool.prefill(q, tables, ints(lens), starts_of(new), d ** -0.5, most)[:sum(new)], out[:sum(new)])
+    pool.close()
+
+
 @pytest.mark.parametrize("kv", ["bf16", "int8"])
 def test_one_long_context_among_thousands_of_units(kv):
     """A unit of work that is large beside a CTA's share, among more units than one pass of the plan takes."""
