@@ -18,9 +18,9 @@
 //
 // INT8 and FP8 pools: two warpgroups load codes, one K's and one V's, and turn them into operand tiles, bf16 and
 // fp16, which hold every INT8 and E4M3 code exactly.  The scales stay out of the operands.  A token's K scale multiplies
-// its fp32 logit, and its V scale goes into its weight before that is rounded, as a term of the exponent: with
-// y = logit + log2(V scale) and m the running maximum of y, the weight w = 2^(y - m) is near 1 where it matters, so that
-// fp16 holds it (2^-11 of it; below 2^-14 of the row's largest an absolute 2^-25), and the softmax sum adds w / (V scale).
+// its fp32 logit, and its V scale its weight before that is rounded: with m the running maximum of logit + log2(V scale),
+// p = 2^(logit - m) goes into the softmax sum and w = p * (V scale) is near 1 where it matters, so that fp16 holds it
+// (2^-11 of it; below 2^-14 of the row's largest an absolute 2^-25).
 //
 // Warps: a warpgroup of softmax per stream; over bf16, one that turns finished accumulators into rows of out, so that
 // the next unit's softmax need not wait for that, and one warp that fills the rings of K and V tiles by TMA (over the
@@ -107,9 +107,8 @@ struct PromptCfg {
   static_assert(2 * kSoftmaxRegs + (kQuant ? 2 : 1) * kSideRegs + kLoadRegs <= kThreads / 128 * kRegs, "registers");
   static constexpr int kRingOff = 2 * kTileBytes;              // Q tiles of both streams first
   static constexpr int kVOff = kRingOff + kK * kTileBytes;
-  // float [3][128] and [2][4] to a slot: K's scale times the softmax's, log2 of V's, and 1 / V's; V's smallest scale of
-  // each warp's tokens and the largest of those so far
-  static constexpr int kSlotOff = kVOff + kV * kTileBytes, kSlotBytes = 3 * kPromptTile * 4 + 32;
+  // float [3][128] to a slot: K's scale times the softmax's, V's, and its log2
+  static constexpr int kSlotOff = kVOff + kV * kTileBytes, kSlotBytes = 3 * kPromptTile * 4;
   static constexpr int kMiscOff = kSlotOff + kSlots * kSlotBytes;
   static constexpr int kStatOff = kMiscOff + 1024;             // float2 [2][128]: running max and sum
   static constexpr int kSmemBytes = kStatOff + 2 * 128 * 8;
@@ -718,7 +717,6 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         const uint8_t *from0 = nullptr, *from1 = nullptr;  // this lane's first chunk in each
         uint32_t have = 0;
         float ks = 0.0f, vs = 1.0f;
-        [[maybe_unused]] uint32_t most = 0;
         auto place = [&](int tile) {  // of the blocks that were asked for
           const bool ok0 = next0 >= 0 && next0 < p.num_blocks, ok1 = next1 >= 0 && next1 < p.num_blocks;
           const int b = (tile0 + tile) * (kPromptTile / kBlockSize) + 2 * wq;
@@ -750,25 +748,20 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
         ask(1);
 #pragma unroll 1
         for (int t = 0; t < n; ++t) {
-          float lv = 0.0f, iv = 0.0f;
-          uint32_t least = 0;
+          float size = 1.0f, lv = 0.0f;
           if (!is_v) {
             // A scale of 0, whose codes are 0, counts as 2^-60: the token's logit has to bound the exponent, and its
             // weight must not hide others'.  Any other counts as at least 2^-98 (values move by less than 2^-89), so that a
             // sum of weights of up to 2^15 over it stays finite for 2^15 half-tiles.
-            const float size = vs == 0.0f ? 0x1p-60f : vs < 0x1p-98f ? 0x1p-98f : vs;
+            size = vs == 0.0f ? 0x1p-60f : vs < 0x1p-98f ? 0x1p-98f : vs;
             lv = __log2f(size);
-            iv = fast_exp2(-lv);
-            least = __reduce_min_sync(kAll, __float_as_uint(size));
-            most = max(most, __reduce_max_sync(kAll, __float_as_uint(size)));
           }
           if (filled >= C::kK && !(alive = wait_all(empty + at.st, at.ph ^ 1u))) break;
           if (!is_v) {
             auto* slot = reinterpret_cast<float*>(smem + C::kSlotOff + (tiles + t) % C::kSlots * C::kSlotBytes) + wq * 32;
             slot[lane] = ks * scale;
-            slot[128 + lane] = lv;
-            slot[256 + lane] = iv;
-            if (lane < 2) slot[384 - wq * 32 + lane * 4 + wq] = __uint_as_float(lane ? most : least);
+            slot[128 + lane] = size;
+            slot[256 + lane] = lv;
             if (lane == 0) reinterpret_cast<uint8_t*>(sy->mask + (tiles + t) % kTileMasks)[wq] = uint8_t(have);
           }
           unsigned char* dst = ring + at.st * C::kTileBytes + (chunk >> 2) * C::kHalfBytes + (wq * 32 + sub) * 128;
@@ -843,7 +836,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
             const int lo = span.lo - (tile0 + tile) * kPromptTile, hi = span.hi - (tile0 + tile) * kPromptTile;
             [[maybe_unused]] const auto* ks =
                 reinterpret_cast<const ulonglong2*>(smem + C::kSlotOff + (C::kQuant ? (tiles0 + tile) % (C::kSlots + !C::kQuant) : 0) * C::kSlotBytes);
-            [[maybe_unused]] const auto *lv = ks + kPromptTile / 4, *iv = lv + kPromptTile / 4;
+            [[maybe_unused]] const auto *vs = ks + kPromptTile / 4, *lv = vs + kPromptTile / 4;
             const bool cut = __any_sync(kAll, lo > 0 || hi < kPromptTile || have != 0xffu);
             auto mask = [&](int c, float* z) {  // columns 32 c .. 32 c + 31
               const uint32_t w = bit_range(lo - 32 * c, hi - 32 * c) & ((have >> (2 * c) & 1 ? 0xffffu : 0u) | (have >> (2 * c + 1) & 1 ? 0xffff0000u : 0u));
@@ -859,7 +852,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
               }
             };
             uint64_t sum[2];
-            // Logits -> weights, 2 n to n registers.  A warp issues in order and is alone with its row's chain, so the
+            // Logits (over codes: less the maximum) -> weights, 2 n to n registers.  A warp issues in order and is alone with its row's chain, so the
             // steps of neighbouring groups of 8 are written side by side: exponentials at a time (4 cycles each)
             // with the products and sums (2) of others.
             [[maybe_unused]] __half2 halves[2];
@@ -867,34 +860,25 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
               const uint64_t neg = f32x2(-m, -m);
 #pragma unroll
               for (int g = 0; g < n + 8; g += 4) {
-                if (g < n) {
+                if (!C::kQuant && g < n) {
 #pragma unroll
-                  for (int j = g; j < g + 4; ++j) {
-                    const uint64_t y = f32x2(z[2 * j], z[2 * j + 1]);
-                    f32x2_parts(C::kQuant ? add2(y, neg) : fma2(y, scale2, neg), z[2 * j], z[2 * j + 1]);
-                  }
+                  for (int j = g; j < g + 4; ++j) f32x2_parts(fma2(f32x2(z[2 * j], z[2 * j + 1]), scale2, neg), z[2 * j], z[2 * j + 1]);
                 }
                 if (g >= 4 && g < n + 4) {
 #pragma unroll
                   for (int j = 2 * g - 8; j < 2 * g; ++j) z[j] = fast_exp2(z[j]);
                 }
                 if (g >= 8) {
-                  if constexpr (C::kQuant) {
-#pragma unroll
-                    for (int j = (g - 8) / 2; j < (g - 4) / 2; ++j) {
-                      const ulonglong2 f = iv[8 * c + j];
-                      sum[0] = fma2(f32x2(z[4 * j], z[4 * j + 1]), f.x, sum[0]);
-                      sum[1] = fma2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y, sum[1]);
-                    }
-                  }
 #pragma unroll
                   for (int j = g - 8; j < g - 4; ++j) {
+                    sum[j & 1] = add2(sum[j & 1], f32x2(z[2 * j], z[2 * j + 1]));
                     if constexpr (C::kQuant) {
+                      const ulonglong2 f = vs[8 * c + j / 2];
+                      f32x2_parts(mul2(f32x2(z[2 * j], z[2 * j + 1]), j & 1 ? f.y : f.x), z[2 * j], z[2 * j + 1]);
                       const __half2 v = __floats2half2_rn(z[2 * j], z[2 * j + 1]);
                       halves[j & 1] = __hadd2(halves[j & 1], v);
                       w[j] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&v));
                     } else {
-                      sum[j & 1] = add2(sum[j & 1], f32x2(z[2 * j], z[2 * j + 1]));
                       w[j] = __uint_as_float(pack_bf16x2(z[2 * j], z[2 * j + 1]));
                     }
                   }
@@ -913,6 +897,7 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
               l *= f;
               if (i > 0) {
                 // every product into O is done: S was issued after the last
+                tmem_wait_st();  // and so is a move's in the tile's first half
 #pragma unroll 1
                 for (int j = 0; j < D / 16; ++j) {
                   float o[16];
@@ -933,23 +918,22 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
               // whole powers of two, so that weights handed over already can be rescaled exactly.  (All 128 logits and
               // the scales would not stay in registers, and spilled ones are far away with shared memory this full.  The
               // loop stays rolled: the code of all roles shares an instruction cache.)
-              // Scales of V that lie 2^90 apart: weights (and with them w / scale) of small values would vanish beside large
-              // ones', so the sum is formed by itself.
-              const float4 least = *reinterpret_cast<const float4*>(iv + kPromptTile / 4), most = *(reinterpret_cast<const float4*>(iv + kPromptTile / 4) + 1);
-              const bool wide = fminf(fminf(least.x, least.y), fminf(least.z, least.w)) < 0x1p-90f * fmaxf(fmaxf(most.x, most.y), fmaxf(most.z, most.w));
               float z[64], w[32];
 #pragma unroll 1
               for (int h = 0; h < 2; ++h) {
-                bool look = i == 0 && h == 0;
+                // A search is a turn of its own, so that the weights of a row are the same whether or not another row of the
+                // warp asked for one.
+                bool look = i == 0 && h == 0, looked = false;
                 for (;;) {
                   tmem_ld32(s_addr + 64 * h, z);
                   tmem_ld32(s_addr + 64 * h + 32, z + 32);
                   tmem_wait_ld();
+                  const uint64_t neg = look ? 0 : f32x2(-m, -m);
 #pragma unroll
                   for (int j = 0; j < 16; ++j) {
-                    const ulonglong2 f = ks[16 * h + j], g = lv[16 * h + j];
-                    f32x2_parts(fma2(f32x2(z[4 * j], z[4 * j + 1]), f.x, g.x), z[4 * j], z[4 * j + 1]);
-                    f32x2_parts(fma2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y, g.y), z[4 * j + 2], z[4 * j + 3]);
+                    const ulonglong2 f = ks[16 * h + j];
+                    f32x2_parts(fma2(f32x2(z[4 * j], z[4 * j + 1]), f.x, neg), z[4 * j], z[4 * j + 1]);
+                    f32x2_parts(fma2(f32x2(z[4 * j + 2], z[4 * j + 3]), f.y, neg), z[4 * j + 2], z[4 * j + 3]);
                   }
                   if (cut) {
                     mask(2 * h, z);
@@ -958,7 +942,12 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                   if (look) {
 #pragma unroll
                     for (int u = 0; u < 4; ++u) mx[u] = -INFINITY;
-                    largest(z, 64, mx);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                      const float4 f = reinterpret_cast<const float4*>(lv)[16 * h + j];
+                      mx[2 * (j & 1)] = max3(mx[2 * (j & 1)], z[4 * j] + f.x, z[4 * j + 1] + f.y);
+                      mx[2 * (j & 1) + 1] = max3(mx[2 * (j & 1) + 1], z[4 * j + 2] + f.z, z[4 * j + 3] + f.w);
+                    }
                     const float f = move(mx);
                     if (h == 1) {  // the lower half's weights
                       tmem_wait_st();
@@ -977,26 +966,15 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                         tmem_st16(s_addr + c, o);
                       }
                     }
+                    look = false;
+                    looked = true;
+                    continue;
                   }
                   sum[0] = sum[1] = 0;
                   halves[0] = halves[1] = __float2half2_rn(0.0f);
                   weigh(2 * h, 32, z, w);
                   const float2 both = __half22float2(__hadd2(halves[0], halves[1]));
-                  if (look || !__any_sync(kAll, fmaxf(both.x, both.y) > 30000.0f)) {
-                    if (wide) {
-                      sum[0] = sum[1] = 0;
-#pragma unroll 1
-                      for (int c = 2 * h; c < 2 * h + 2; ++c) {
-                        tmem_ld32(s_addr + 32 * c, z);
-                        tmem_wait_ld();
-                        const float* f = reinterpret_cast<const float*>(ks) + 32 * c;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) z[j] *= f[j];
-                        if (cut) mask(c, z);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) sum[j & 1] = add2(sum[j & 1], f32x2(fast_exp2(z[2 * j] - m), fast_exp2(z[2 * j + 1] - m)));
-                      }
-                    }
+                  if (looked || !__any_sync(kAll, !dead && fmaxf(both.x, both.y) > 30000.0f)) {
                     float lo_sum, hi_sum;
                     f32x2_parts(add2(sum[0], sum[1]), lo_sum, hi_sum);
                     l += lo_sum + hi_sum;
