@@ -224,6 +224,28 @@ def test_prefill_smallest_values_ahead_of_others(kv, t, tiny):
     pool.close()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8", "fp8"])
+def test_blocks_behind_two_to_the_31_elements(kv):
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    t, n, hkv, d, blocks = 200, 9, 16, 128, 70000
+    assert (blocks - 20) * 16 * hkv * d > 2 ** 31
+    pool = pkv.PagedKVPool(blocks, hkv, d, kv)
+    tables = (blocks - 1 - torch.randperm(13, generator=gen, device="cuda")).to(torch.int32)[None]
+    k, v = (_randn(gen, t, hkv, d).to(torch.bfloat16) for _ in range(2))
+    pos = torch.arange(t, device="cuda")
+    pool.reshape_and_cache(k, v, (tables[0, pos // 16] * 16 + pos % 16).to(torch.int32))
+    q = _randn(gen, n, 32, d).to(torch.bfloat16)
+    wide = torch.cat([tables, torch.full((1, 400), -1, dtype=torch.int32, device="cuda")], 1)
+    for most in (t, 5000):
+        out = pool.prefill(q, wide, ints([t]), starts_of([n]), d ** -0.5, most)
+        check_prefill(pool, tables, q, out, [n], [t], d ** -0.5, 0, (kv, most))
+    for got, ref in zip(pool.gather_cache(tables, starts_of([t]), t), cached(pool, tables[0], t)):
+        # over codes a product rounded to fp32 and to bf16
+        assert ((got.double() - ref).abs() <= (0 if kv == "bf16" else 2.0 ** -8 + 2.0 ** -23) * ref.abs()).all()
+    assert pool.device_error() == 0
+    pool.close()
+
+
 def test_prefill_matches_decode_for_single_tokens():
     gen = torch.Generator(device="cuda").manual_seed(6)
     lens = [1, 17, 200, 1025, 3000]
