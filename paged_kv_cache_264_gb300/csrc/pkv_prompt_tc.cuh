@@ -35,9 +35,9 @@
 // Measured, 32 query and 8 kv heads of 128: a causal prompt of 16384 tokens 1240 us in a short burst (1.77 PFLOP/s of
 // its unmasked logits), 1376 in a loop that draws 1370 of 1400 W; the tensor pipe is busy for 72 % of a prompt of 8192.
 // A tile of two full streams takes 3350 cycles of 2048 that its products need: the rest is the hand-over between
-// softmax and products.  Over INT8 and FP8 it takes 5400 to 5700: the streams' chain again, longer by the scales and by
+// softmax and products.  Over INT8 and FP8 it takes 5000 to 5400: the streams' chain again, longer by the scales and by
 // the converting warps beside it (issue slots 53 % busy, shared memory about 73 %: scales, codes and operands).  Over
-// bf16 a call of single tokens reads the cache at 5.9 TB/s.
+// bf16 24 tokens of 32 kv heads behind 32744 read the cache at 5.9 TB/s.
 //
 // Every wait is bounded; after one that gave up the CTA takes no further work, lets its
 // copies and products land, frees its tensor memory and ends.

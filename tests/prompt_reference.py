@@ -52,14 +52,13 @@ def tolerance(out, weight, size, peak, tokens, d, codes):
     - exponentials, the sums over the tokens and the rescaling: 2^-22 and `tokens` steps of 2^-23 of W;
     - over codes a weight times its token's scale is held relative to the row's largest such, which is at least 2^-1:
       below 2^-14 fp16's steps are 2^-24, off by half a step, 2^-25, so 2^-24 of the largest, for each token; a
-      token's largest value is its scale times 127 or 448, so in values it is 2^-24 of the row's largest weight |v|.
-      The logarithm of the scale is off by 2^-18 at most (up to 2^7, steps of 2^-17), and the weight by that share;
+      token's largest value is its scale times 127 or 448, so in values it is 2^-24 of the row's largest weight |v|;
     - exponentials below 2^-126 are 0, 2^-117 of the largest at most: the maximum may stand 2^8 too low."""
     move = 2.0 ** -23 * (d + 8) * size
     tol = (2.0 ** -8 * (weight + 2 * out.abs()) * (1 + 2.0 ** -7)
            + (torch.expm1(2 * move) + 2.0 ** -20 + tokens * 2.0 ** -23) * (weight + out.abs()) + 1e-30)
     if codes:
-        tol = tol + 2.0 ** -24 * tokens * peak[..., :1] + 2.0 ** -17 * (weight + out.abs())
+        tol = tol + 2.0 ** -24 * tokens * peak[..., :1]
     return tol + 2.0 ** -117 * tokens * peak[..., 1:]
 
 
