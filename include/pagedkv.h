@@ -603,8 +603,9 @@ PKV_API pkv_status pkv_shared_prefix_decode(const pkv_pool* pool, const void* q,
  *   key_starts (device): int32 [num_seqs + 1], not decreasing, within [0, num_keys]: sequence b's keys are
  *             rows key_starts[b] .. key_starts[b + 1] - 1.  NULL: query_starts.
  *   num_keys: rows of k and v.
- *   bidirectional: 0: query i of n sees the keys t <= T - n + i of its sequence's T; else all of them
- *             (window must be 0 then).
+ *   bidirectional: 0: query i of n sees the keys t <= T - n + i of its sequence's T; else later ones too.  With a
+ *             window only those with t > T - n + i - window, either way; a bidirectional call with a window has to
+ *             give key_starts (query_starts again, where the keys are the queries' own).
  *   workspace (device): at least pkv_prefill_workspace_bytes(...) bytes, 16-byte aligned.
  */
 typedef struct pkv_prefill {

@@ -592,9 +592,10 @@ def prompt_attention(pool: PagedKVPool, q: torch.Tensor, k: torch.Tensor, v: tor
     v bf16 [M, Hkv, d], all possibly slices of one projection's output.  Sequence b's queries are rows
     query_starts[b] .. query_starts[b + 1] - 1, its keys rows key_starts[b] .. key_starts[b + 1] - 1 (int32 [B + 1];
     None: the queries' rows).  Query i of n sees the keys up to T - n + i of its sequence's T, with ``window`` W > 0
-    the last W of them; with ``causal`` false all T.  A query that sees none gets zeros.  The pool gives the kv heads,
-    head_dim and device; its blocks are not touched.  Returns out, bf16 [N, Hq, d]; its rows outside all sequences are
-    not written.  ``workspace`` (a uint8 CUDA tensor) is allocated here when not given."""
+    the last W of them; with ``causal`` false the later ones too, all T or with a window those from T - n + i - W + 1 on
+    (which takes key_starts, query_starts again where the keys are the queries' own).  A query that sees none gets zeros.
+    The pool gives the kv heads, head_dim and device; its blocks are not touched.  Returns out, bf16 [N, Hq, d]; its rows
+    outside all sequences are not written.  ``workspace`` (a uint8 CUDA tensor) is allocated here when not given."""
     k_stride = _head_rows(k, "k", None, pool.kv_heads, pool)
     v_stride = _head_rows(v, "v", k.shape[0], pool.kv_heads, pool)
     if key_starts is not None:

@@ -520,7 +520,8 @@ pkv_status prompt_attention(const pkv_pool* pool, const pkv_prefill* a, bool pag
                                          paged ? a->max_context_len : a->num_keys, &plan);
   if (st != PKV_OK) return st;
   if (a->window < 0 || !(a->scale == a->scale)) return PKV_ERR_INVALID_ARG;
-  if (!paged && a->bidirectional && a->window != 0) return PKV_ERR_INVALID_ARG;
+  // Where queries and keys are the same rows, a window to one side beside no limit on the other is taken for a mistake.
+  if (!paged && a->bidirectional && a->window != 0 && !a->key_starts) return PKV_ERR_INVALID_ARG;
   if (a->num_seqs == 0 || a->num_tokens == 0) return PKV_OK;
   const int64_t q_width = int64_t(a->num_q_heads) * pool->head_dim, k_width = int64_t(pool->kv_heads) * pool->head_dim;
   if (!a->query_starts || !valid_rows(a->q, a->q_stride, a->num_tokens, q_width) ||
