@@ -657,7 +657,7 @@ PKV_API pkv_status pkv_prefill_workspace_bytes(const pkv_pool* pool, int num_seq
  * value (not a key) of a token that only some of a sequence's queries see may reach the others.
  * num_seqs == 0 or num_tokens == 0 is a no-op.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (2^30 rows or more, some 2^30 units of work or more: a kv
- * head of up to 256 rows of (token, query head), a pool of 2^31 or more rows of head_dim), PKV_ERR_WORKSPACE,
+ * head of up to 256 rows of (token, query head), a bf16 pool of 2^31 or more rows of head_dim), PKV_ERR_WORKSPACE,
  * PKV_ERR_CUDA.
  */
 PKV_API pkv_status pkv_paged_attention_prefill(const pkv_pool* pool, const pkv_prefill* args, void* stream);

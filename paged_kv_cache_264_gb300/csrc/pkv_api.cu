@@ -530,7 +530,7 @@ pkv_status prompt_attention(const pkv_pool* pool, const pkv_prefill* a, bool pag
   if (paged) {
     if (!a->block_tables || !a->context_lens || a->max_context_len < 1 || a->max_blocks_per_seq < 1) return PKV_ERR_INVALID_ARG;
     if (int64_t(a->max_context_len) > int64_t(a->max_blocks_per_seq) * pkv::kBlockSize) return PKV_ERR_INVALID_ARG;
-    if (!pool->has_tmaps) return PKV_ERR_UNSUPPORTED;
+    if (pool->dtype == PKV_KV_BF16 && !pool->has_tmaps) return PKV_ERR_UNSUPPORTED;  // codes come by plain loads
   } else if (a->num_keys > 0 && (!valid_rows(a->k, a->k_stride, a->num_keys, k_width) ||
                                  !valid_rows(a->v, a->v_stride, a->num_keys, k_width))) {
     return PKV_ERR_INVALID_ARG;
