@@ -76,6 +76,11 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _int32(value) -> int:
+    """``value``, or the 32-bit number next to it: ctypes would keep its low bits."""
+    return max(-2 ** 31, min(int(value), 2 ** 31 - 1))
+
+
 _KERNELS = {0: 0, "auto": 0, 1: 1, "cuda_core": 1, 2: 2, "tensor_core": 2}
 _SCHEDULES = {0: 0, "auto": 0, 1: 1, "grid": 1, 2: 2, "persistent": 2}
 
@@ -92,7 +97,7 @@ def _options(partition_blocks: int = 0, kernel=0, schedule=0, stages=0,
     o.stages = int(stages)
     o.blocks_per_stage = int(blocks_per_stage)
     o.num_queries = int(num_queries)
-    o.window = int(window)
+    o.window = _int32(window)
     return ctypes.pointer(o)
 
 
@@ -533,7 +538,7 @@ def prefill_workspace_bytes(pool: PagedKVPool, num_seqs: int, num_q_heads: int, 
                             max_context_len: int) -> int:
     """Workspace of ``paged_attention_prefill`` and ``prompt_attention`` (there max_context_len is k's rows)."""
     n = ctypes.c_size_t()
-    check(_lib.load().pkv_prefill_workspace_bytes(_handle(pool), num_seqs, num_q_heads, num_tokens, int(max_context_len),
+    check(_lib.load().pkv_prefill_workspace_bytes(_handle(pool), num_seqs, num_q_heads, num_tokens, _int32(max_context_len),
                                                   ctypes.byref(n)), "prefill_workspace_bytes")
     return n.value
 
@@ -556,7 +561,7 @@ def _prefill_args(pool, q, query_starts, scale, max_context_len, window, out, wo
     a = Prefill()
     a.q, a.q_stride, a.out, a.out_stride = q.data_ptr(), q_stride, out.data_ptr(), out_stride
     a.query_starts, a.num_tokens, a.num_seqs, a.num_q_heads = query_starts.data_ptr(), n, b, hq
-    a.scale, a.window = float(scale), int(window)
+    a.scale, a.window = float(scale), _int32(window)
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.nbytes
     return a, out, workspace
 
@@ -578,7 +583,7 @@ def paged_attention_prefill(pool: PagedKVPool, q: torch.Tensor, block_tables: to
     if rows != a.num_seqs or context_lens.shape[0] != rows:
         raise ValueError("query_starts, block_tables and context_lens disagree in shape")
     a.block_tables, a.context_lens = block_tables.data_ptr(), context_lens.data_ptr()
-    a.max_blocks_per_seq, a.max_context_len = width, int(max_context_len)
+    a.max_blocks_per_seq, a.max_context_len = width, _int32(max_context_len)
     st = _lib.load().pkv_paged_attention_prefill(pool.handle, ctypes.byref(a), _pool_stream(pool, stream))
     if st:
         check(st, "paged_attention_prefill")
