@@ -656,7 +656,7 @@ PKV_API pkv_status pkv_prefill_workspace_bytes(const pkv_pool* pool, int num_seq
  * sets PKV_DEVERR_BLOCK_ID.  Cache slots that no query of the call sees may hold anything; a NaN or infinite
  * value (not a key) of a token that only some of a sequence's queries see may reach the others.
  * num_seqs == 0 or num_tokens == 0 is a no-op.
- * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (2^30 rows or more, some 2^30 units of work or more: a kv
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (2^30 rows or more, rows of 2^27 values or more, some 2^30 units of work or more: a kv
  * head of up to 256 rows of (token, query head), a bf16 pool of 2^31 or more rows of head_dim), PKV_ERR_WORKSPACE,
  * PKV_ERR_CUDA.
  */
@@ -683,7 +683,7 @@ PKV_API pkv_status pkv_prompt_attention(const pkv_pool* pool, const pkv_prefill*
  * A token past the table's row, or at a negative position, becomes a row of zeros and sets
  * PKV_DEVERR_CONTEXT_LEN; one whose block id is out of range does and sets PKV_DEVERR_BLOCK_ID; an invalid
  * token_starts entry sets PKV_DEVERR_QUERY and nothing is written.  num_seqs == 0 or num_tokens == 0 is a no-op.
- * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (2^30 rows or more), PKV_ERR_CUDA.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (2^30 rows or more, rows of 2^27 values or more), PKV_ERR_CUDA.
  */
 PKV_API pkv_status pkv_gather_cache(const pkv_pool* pool, const int32_t* block_tables, int max_blocks_per_seq,
                                     const int32_t* token_starts, const int32_t* first_positions, int num_seqs,

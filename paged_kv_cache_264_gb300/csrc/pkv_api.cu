@@ -443,6 +443,10 @@ void prompt_heads(int group, int* heads, int* chunks) {
   }
 }
 
+// A token's rows of all heads that the prompt operators take: 32-bit places of a head within a token, of a value within
+// a block of codes (16 tokens) and of 16 bytes within the 32 tokens of a tile that is read back.
+bool valid_width(int64_t heads, int head_dim) { return heads * head_dim < int64_t(1) << 27; }
+
 // Layout of a prompt attention call's workspace, and its parameters that follow from the shape.
 struct PromptPlan {
   int heads, chunks, units, stream_tokens, max_parts, part_rows;
@@ -455,6 +459,7 @@ pkv_status make_prompt_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
   if (!pool || num_seqs < 0 || num_q_heads < 1 || num_tokens < 0 || max_context_len < 0) return PKV_ERR_INVALID_ARG;
   if (num_q_heads % pool->kv_heads != 0) return PKV_ERR_INVALID_ARG;
   if (num_tokens >= pkv::kNoWindow || max_context_len >= pkv::kNoWindow) return PKV_ERR_UNSUPPORTED;
+  if (!valid_width(num_q_heads, pool->head_dim)) return PKV_ERR_UNSUPPORTED;
   if (pool->sm_count >= 1024) return PKV_ERR_UNSUPPORTED;  // the plan holds a value per CTA
   prompt_heads(num_q_heads / pool->kv_heads, &x->heads, &x->chunks);
   x->units = pool->kv_heads * x->chunks;
@@ -1076,7 +1081,7 @@ pkv_status pkv_gather_cache(const pkv_pool* pool, const int32_t* block_tables, i
                             const int32_t* token_starts, const int32_t* first_positions, int num_seqs,
                             int64_t num_tokens, void* k, int64_t k_stride, void* v, int64_t v_stride, void* stream) {
   if (!pool || num_seqs < 0 || num_tokens < 0) return PKV_ERR_INVALID_ARG;
-  if (num_tokens >= pkv::kNoWindow) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens >= pkv::kNoWindow || !valid_width(pool->kv_heads, pool->head_dim)) return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
   if (!block_tables || max_blocks_per_seq < 1 || !token_starts) return PKV_ERR_INVALID_ARG;
   const int64_t width = int64_t(pool->kv_heads) * pool->head_dim;
