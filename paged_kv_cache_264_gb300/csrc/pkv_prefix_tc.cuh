@@ -170,10 +170,16 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
   using C = PrefixCfg<KV, D>;
   constexpr int S = C::kStages;
   constexpr uint32_t kFull = 0xffffffffu;
-  extern __shared__ __align__(1024) unsigned char smem[];  // the swizzled tiles need its alignment
+  extern __shared__ __align__(1024) unsigned char tile_smem[];  // the swizzled tiles need its alignment
+  unsigned char* smem = tile_smem;
   auto* sy = reinterpret_cast<PrefixSync*>(smem + C::kMiscOff);
   unsigned char* ring = smem + C::kRingOff;
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (smem_addr(smem) & 1023u) {  // never, since it is the kernel's only shared memory: no work, the error
+    griddep_wait();
+    if (threadIdx.x == 0) set_error(p.err, kErrTimeout);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -205,7 +211,6 @@ __global__ void __launch_bounds__(PrefixCfg<KV, D>::kThreads, 1)
     prefetch_tensor_map(&tmap_v);
   }
   if (warp == C::kMmaWarp) tmem_alloc(&sy->tmem, C::kTmemCols);
-  if (threadIdx.x == 0 && (smem_addr(smem) & 1023u)) set_error(p.err, kErrTimeout);  // never: the only shared memory
   griddep_wait();  // inputs may come from the previous kernel in the stream
   // The scan of up to 32 groups is the walking warp's own; that of many lies where the ring will be,
   // and all warps describe the sequences from it first.

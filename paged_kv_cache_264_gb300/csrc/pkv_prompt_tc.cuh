@@ -173,10 +173,16 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
                      const __grid_constant__ CUtensorMap tmap_v, const PromptParams p) {
   using C = PromptCfg<KV, D, kPaged>;
   constexpr uint32_t kAll = 0xffffffffu;
-  extern __shared__ __align__(1024) unsigned char smem[];  // the swizzled tiles need its alignment
+  extern __shared__ __align__(1024) unsigned char tile_smem[];  // the swizzled tiles need its alignment
+  unsigned char* smem = tile_smem;
   auto* sy = reinterpret_cast<PromptSync*>(smem + C::kMiscOff);
   auto* stats = reinterpret_cast<float2*>(smem + C::kStatOff);
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (smem_addr(smem) & 1023u) {  // never, since it is the kernel's only shared memory: no work, the error
+    griddep_wait();
+    if (threadIdx.x == 0) set_error(p.err, kErrTimeout);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     constexpr int kFillers = C::kQuant ? 4 : 1;
@@ -215,7 +221,6 @@ __global__ void __launch_bounds__(PromptCfg<KV, D, kPaged>::kThreads, 1)
     }
   }
   if (warp == C::kMmaWarp) tmem_alloc(&sy->tmem, C::kTmemCols);
-  if (threadIdx.x == 0 && (smem_addr(smem) & 1023u)) set_error(p.err, kErrTimeout);  // never: the only shared memory
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
