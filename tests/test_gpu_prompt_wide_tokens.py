@@ -55,7 +55,7 @@ def test_the_widest_tokens():
     pool.v_scale.uniform_(0.005, 0.02, generator=gen)
     q = torch.randn(2, heads, D, generator=gen, device="cuda").to(torch.bfloat16)
     out = pool.prefill(q, ints([[0]]), ints([t]), ints([0, 2]), 0.125, 16)
-    k, v = pool.gather_cache(ints([[0]]), ints([0, 2]), 2)  # a tile of 32 tokens is one CTA's: some seconds
+    k, v = pool.gather_cache(ints([[0]]), ints([0, 2]), 2)
     packed = pool.prompt_attention(q, k, v, ints([0, 2]), 0.125)
     assert pool.device_error() == 0
     for lo in (0, heads // 2, heads - 4096):
