@@ -164,7 +164,6 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
 }
 
 // Bit j: block j of a tile, from the word that holds two to a byte.
-constexpr uint32_t kAllBlocks = 0x03030303u;
 __device__ __forceinline__ uint32_t tile_mask(uint32_t w) { return (w | w >> 6 | w >> 12 | w >> 18) & 0xffu; }
 
 template <KvType KV, int D, bool kPaged>
