@@ -467,9 +467,24 @@ pkv_status make_prompt_plan(const pkv_pool* pool, int num_seqs, int num_q_heads,
   const int64_t per = 2 * x->stream_tokens;
   const int64_t items = num_seqs + num_tokens / per, work = items * x->units, tiles = ceil_div(max_context_len, pkv::kPromptTile);
   // Without a plan a short call is one launch of three, and its units are not cut.  Measured in a graph, 32 query and 8
-  // kv heads of 128, us without / with a plan: bf16, one token of 1, 4, 16 sequences behind 1024 tokens 13 / 26, 14 / 21,
-  // 14 / 26, behind 2048 21 / 28, 22 / 23, 28 / 35; INT8 behind 1024 19 / 27, 19 / 24, 22 / 37, behind 2048 31 / 30,
-  // 31 / 29, 37 / 51.
+  // kv heads of 128, us without / with a plan, sequences x new tokens (64 fill a unit's 256 rows), by tiles of a sequence:
+  //                     8 tiles        12             16             24
+  //   bf16  1 x 1       13.2 / 25.4    17.2 / 27.0    21.2 / 28.3    29.3 / 30.0
+  //         4 x 1       13.7 / 20.9    17.7 / 21.4    21.8 / 22.8    29.9 / 25.0
+  //         16 x 1      14.7 / 26.6    20.7 / 31.3    28.2 / 38.6    39.2 / 49.1
+  //         1 x 64      18.7 / 30.7    23.2 / 32.4    28.4 / 37.2    38.8 / 40.6
+  //         4 x 64      18.7 / 27.9    23.8 / 29.6    28.9 / 32.8    39.6 / 35.7
+  //         2 x 512     19.9 / 41.3    24.9 / 46.4    30.0 / 50.5    40.2 / 59.8
+  //   INT8  1 x 1       17.6 / 27.1    23.2 / 27.8    28.7 / 29.2    39.8 / 31.1
+  //         4 x 1       18.4 / 22.7    24.2 / 25.2    29.9 / 27.9    41.4 / 30.7
+  //         16 x 1      21.0 / 36.0    27.4 / 43.3    35.5 / 49.0    51.5 / 64.1
+  //         1 x 64      29.3 / 32.8    39.5 / 34.3    50.1 / 39.5    71.4 / 43.4
+  //         4 x 64      29.5 / 30.7    40.1 / 33.2    50.6 / 37.3    71.7 / 42.7
+  //         2 x 512     30.2 / 50.4    41.1 / 60.6    51.5 / 69.4    72.7 / 89.3
+  // FP8 is within 2 to 6 us of INT8; at head_dim 64 both sides are shorter and the borders the same (bf16 4 x 64, 16 tiles:
+  // 25.2 / 25.1; INT8 1 x 64, 12: 31.9 / 29.7).  So a bf16 call of up to 16 tiles is faster without a plan whatever its
+  // units.  On codes 12 tiles are too many where full units leave most CTAs idle (up to 7 us of 33), and too few where they
+  // do not (20 of 61); which it is lies in the lengths, on the device.
   // (A pool's type counts for packed keys too: both calls have one size of workspace.)
   const int64_t direct_tiles = pool->dtype != PKV_KV_BF16 ? pkv::kDirectCodesTiles : pkv::kDirectTiles;
   x->direct = num_seqs <= pkv::kDirectSeqs && work <= pool->sm_count && tiles <= direct_tiles ? static_cast<int>(work) : 0;

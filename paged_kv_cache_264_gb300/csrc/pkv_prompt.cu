@@ -24,7 +24,9 @@ constexpr int kBuckets = 1024;  // of sequences' sizes, for the order
 constexpr int kHeldSeqs = 1024; // of up to this many sequences the plan holds what it needs in shared memory
 // Places on the line: of a tile, of one whose rows both streams hold (up to kRowTile of them), and ahead of a unit's
 // tiles, for its start and end.  Measured on GB300, cycles of a CTA, head_dim 128, 32 query and 8 kv heads: a tile of
-// 256 rows 3400 (codes 5000 to 5400), of 4 and 128 rows 2900 (codes 3100 to 3700), a unit 5000 to 7000 besides.
+// 256 rows 3400 (codes 5000 to 5400), of 4 and 128 rows 2900 (codes 3100 to 3700), a unit 5000 to 7000 besides.  At
+// head_dim 64 a tile takes 2400 and 1800 (codes 4400 and 2450) and a unit as long, some 8 : 6 : 17, and its line is shared
+// out by the same weights: stretches with more units of few tiles than others end later.
 constexpr int kTileCost = 8, kTwinCost = 7, kTwinCodesCost = 5, kUnitCost = 12;
 __device__ __forceinline__ int tile_cost(const PromptParams& p, int ntok) {
   return ntok > p.stream_tokens ? kTileCost : p.k_scale ? kTwinCodesCost : kTwinCost;
