@@ -27,10 +27,11 @@ def memory():
     need = BLOCKS * HKV * 16 * (D + 4)
     if torch.cuda.mem_get_info()[0] < need + (8 << 30):
         pytest.skip(f"{need >> 30} GiB of device memory")
-    codes = torch.empty(BLOCKS, HKV, 16, D, dtype=torch.uint8, device="cuda")
-    yield codes, torch.empty(BLOCKS, HKV, 16, dtype=torch.float32, device="cuda")
-    del codes
-    torch.cuda.empty_cache()
+    held = [torch.empty(BLOCKS, HKV, 16, D, dtype=torch.uint8, device="cuda"),
+            torch.empty(BLOCKS, HKV, 16, dtype=torch.float32, device="cuda")]
+    yield held
+    held.clear()
+    torch.cuda.empty_cache()  # other processes of the tests need it
 
 
 @pytest.mark.parametrize("kv", ["int8", "fp8"])
